@@ -455,12 +455,182 @@ QMUON_API qmuon_status qmuon_step_prepare(const qmuon_plan* plan, float* const* 
 QMUON_API qmuon_status qmuon_sync_status(void* ws, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Beside the Muon step: the parameters that are not matrices.  Gradient
+ * clipping over all tensors, AdamW over many tensors, and the RMS norm whose
+ * gains are such parameters and whose output can leave as an MXFP8 carrier.
+ * The pages have no counterpart: these entries exist so that a training step
+ * can run on this library's kernels from the norms to the weights.
+ *
+ * Pointers here need only their elements' alignment, except where a comment
+ * says more; 16-byte alignment of every array of a tensor is faster.  The
+ * entries keep no tallies in qmuon_counters and record nothing in a
+ * workspace's header.
+ * ------------------------------------------------------------------------- */
+
+/* One gradient of a clipping plan: `numel` elements of `dtype` (D). */
+typedef struct {
+  void* grad;
+  int64_t numel;
+  int32_t dtype;               /* qmuon_dtype; the plan's tensors may differ */
+  int32_t reserved;
+} qmuon_grad;
+
+typedef struct qmuon_clip_plan qmuon_clip_plan;
+
+/* A reusable plan over n gradients (H array, copied) of at most 2^40 elements
+ * each.  Empty ones are skipped, but there must be at least one element.
+ * Allocates a small device table on the current device, and uploads it. */
+QMUON_API qmuon_status qmuon_clip_plan_create(const qmuon_grad* grads, int32_t n, qmuon_clip_plan** out);
+QMUON_API void qmuon_clip_plan_destroy(qmuon_clip_plan* plan);
+/* Workspace bytes of qmuon_grad_clip (0 for a NULL plan). */
+QMUON_API size_t qmuon_clip_workspace_size(const qmuon_clip_plan* plan);
+
+/* The 2-norm of all gradients of the plan together and the factor that brings
+ * it to at most max_norm:
+ *   norm[0] = sqrt(sum g^2)     norm[1] = min(1, max_norm / (norm[0] + 1e-6))
+ * or NaN in norm[1] where norm[0] is not finite.
+ *   max_norm  > 0 (infinity: the norm alone)
+ *   apply     0: leaves the gradients as they are, for an optimizer that takes
+ *                norm[1] (qmuon_adamw_step's grad_scale)
+ *             1: g <- norm[1] g, rounded to nearest, where norm[1] < 1
+ *   norm      D  two fp32
+ *   ws        D  256-byte aligned, of qmuon_clip_workspace_size(plan)
+ * Squares are taken in fp32 and summed in fp64 in a fixed order, so the same
+ * gradients give the same bits.  Calls with one plan must not overlap on the
+ * GPU (enqueue them on one stream). */
+QMUON_API qmuon_status qmuon_grad_clip(const qmuon_clip_plan* plan, float max_norm, int32_t apply, float* norm, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+typedef enum { QMUON_STATE_F32 = 0, QMUON_STATE_E4M3 = 1 } qmuon_state_kind;
+
+/* One tensor of an AdamW plan (all pointers D).
+ *   param   fp32 parameters, updated in place
+ *   grad    gradient of `grad_dtype`, read only
+ *   copy    the updated parameters rounded to `copy_dtype` (QMUON_BF16 or
+ *           QMUON_FP16), written; or NULL
+ *   m, v    QMUON_STATE_F32: fp32 first and second moments
+ *           QMUON_STATE_E4M3: one E4M3 code per element, 16-byte aligned, of
+ *           the first moment and of the SQUARE ROOT of the second; an element
+ *           is code * (absmax / 448)
+ *   m_absmax, v_absmax   QMUON_STATE_E4M3: ceil(numel/256) fp32, the largest
+ *           magnitude of each 256 elements (of the root, for v)
+ * A first step starts from zero bytes in all of the state. */
+typedef struct {
+  float* param;
+  const void* grad;
+  void* copy;
+  void* m;
+  void* v;
+  float* m_absmax;
+  float* v_absmax;
+  int64_t numel;
+  float lr_scale;              /* this tensor's factor on the step's lr */
+  float weight_decay;
+  int32_t grad_dtype;          /* qmuon_dtype */
+  int32_t copy_dtype;          /* looked at only with a copy */
+} qmuon_adamw_tensor;
+
+typedef struct qmuon_adamw_plan qmuon_adamw_plan;
+
+/* A reusable plan over n tensors (H array, copied); limits as in
+ * qmuon_clip_plan_create. */
+QMUON_API qmuon_status qmuon_adamw_plan_create(const qmuon_adamw_tensor* tensors, int32_t n, qmuon_state_kind state,
+                                               qmuon_adamw_plan** out);
+QMUON_API void qmuon_adamw_plan_destroy(qmuon_adamw_plan* plan);
+
+/* One AdamW step of every tensor of the plan in one launch.  With g' = s g,
+ * lr' = lr * lr_scale, fp32, one rounding per operation:
+ *   m <- beta1 m + (1 - beta1) g'       v <- beta2 v + (1 - beta2) g'^2
+ *   p <- p (1 - lr' weight_decay) - (lr' / (1 - beta1^t)) * u
+ *   u = m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * 8-bit states are then requantised to the nearest code of their block's new
+ * maximum (the update above uses the unrounded ones).  A NaN or infinity in a
+ * block leaves NaN codes, so that it is not lost.
+ *   t           >= 1, the step's index; fixed in captured launches
+ *   eps         > 0 in fp32
+ *   grad_scale  D  one fp32 s (a clipping coefficient, an inverse loss scale),
+ *                  or NULL for 1.  Where s is not finite the step changes
+ *                  nothing.
+ * Needs no workspace and allocates nothing. */
+QMUON_API qmuon_status qmuon_adamw_step(const qmuon_adamw_plan* plan, int64_t t, double lr, double beta1, double beta2,
+                                        double eps, const float* grad_scale, void* stream);
+
+/* qmuon_adamw_step with stochastic requantisation (QMUON_STATE_E4M3 plans; else
+ * QMUON_ERR_UNSUPPORTED).  To nearest, a second moment that changes by less
+ * than half a code's step (1/32 to 1/16) against its block's maximum stays;
+ * rounded up or down at random, in proportion, it follows on average.
+ * Element e of tensor i takes word w = word (e mod 4) of Philox4x32-10 with
+ * key (seed mod 2^32, seed >> 32) and counter (e/4 mod 2^32, e/2^34, i, t mod
+ * 2^32); m is rounded up in magnitude where its remainder's fraction of a step
+ * plus (w mod 2^16) 2^-16 reaches 1, the root of v likewise with w >> 16. */
+QMUON_API qmuon_status qmuon_adamw_step_sr(const qmuon_adamw_plan* plan, int64_t t, double lr, double beta1, double beta2,
+                                           double eps, uint64_t seed, const float* grad_scale, void* stream);
+
+/* RMS norm of `rows` rows of `cols` elements, with the residual's addition:
+ *   h = x + residual (fp32)        y = h / sqrt(mean(h^2) + eps) * gain
+ * All matrices are of `dtype`, row-major, rows ld_* >= cols elements apart.
+ *   residual   or NULL: h = x
+ *   gain       cols fp32
+ *   sum        h rounded to dtype, or NULL; may be x or residual itself
+ *   y          y rounded to dtype, or NULL
+ *   payload,   y as an MXFP8 carrier (rows x cols E4M3 codes and rows x
+ *   scale_inv    (cols/32) E8M0 exponents, contiguous, as
+ *                qmuon_update_mxfp8_carrier writes them), or both NULL;
+ *                cols % 32 != 0 is QMUON_ERR_UNSUPPORTED
+ * One of y and payload at least.  The MXFP8 codes are taken from the fp32 y.
+ * rows may be 0; cols at most 2^30, rows * cols at most 2^40. */
+typedef struct {
+  const void* x;
+  const void* residual;
+  const float* gain;
+  void* sum;
+  void* y;
+  uint8_t* payload;
+  uint8_t* scale_inv;
+  int64_t rows, cols;
+  int64_t ld_x, ld_residual, ld_sum, ld_y;
+  float eps;                   /* >= 0 */
+  int32_t dtype;               /* qmuon_dtype */
+} qmuon_rmsnorm;
+
+QMUON_API qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* norm, void* stream);
+
+/* Its backward pass, from the stored sum h:
+ *   inv = 1 / sqrt(mean(h^2) + eps)    n = h inv    a = dy gain
+ *   dx = inv (a - n mean(a n)) + dsum        dgain = sum over rows of dy n
+ *   dsum       gradient that reaches h from elsewhere (the residual stream),
+ *              or NULL
+ *   dx         gradient of h, that is of x and of residual alike; may be dy or
+ *              dsum itself
+ *   dgain      cols fp32, overwritten
+ *   ws         D  256-byte aligned, of qmuon_rmsnorm_workspace_size(rows, cols)
+ * Sums over rows are taken in an order that depends on the shape and the GPU's
+ * SM count alone. */
+typedef struct {
+  const void* dy;
+  const void* h;
+  const void* dsum;
+  const float* gain;
+  void* dx;
+  float* dgain;
+  int64_t rows, cols;
+  int64_t ld_dy, ld_h, ld_dsum, ld_dx;
+  float eps;
+  int32_t dtype;
+} qmuon_rmsnorm_grad;
+
+/* Workspace bytes of qmuon_rmsnorm_backward (0 for sizes it rejects). */
+QMUON_API size_t qmuon_rmsnorm_workspace_size(int64_t rows, int64_t cols);
+
+QMUON_API qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Path and dtype audit.  "Quantized Muon Momentum", §Wave18B MXFP8 Carrier
  * Probe, checks a run with counters: calls of the carrier update and the
  * dtypes of the tensors it read and wrote (uint8 payload and scales, fp32
  * inverse norm, the gradient's dtype), and whether a bf16 path was taken.
- * The library keeps the same kind of tallies for every entry point that
- * computes, process-wide: a caller can check which paths ran, for example
+ * The library keeps the same kind of tallies for every entry point of the
+ * Muon path that computes, process-wide: a caller can check which paths ran, for example
  * that Newton-Schulz was fed from MXFP8 carriers and how many bytes of bf16
  * the carrier expansion wrote on the way (ns_bf16_handoff_bytes; the
  * expansion is the bf16 hand-off that the page's probe still needs).

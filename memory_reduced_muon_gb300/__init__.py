@@ -33,9 +33,11 @@ QMUON_Q8_INT8, QMUON_Q8_UINT8 = 0, 1
 QMUON_BF16, QMUON_FP16, QMUON_FP32 = 0, 1, 2
 QMUON_WS_UPDATE, QMUON_WS_STEP = 0, 1
 QMUON_NS_BF16, QMUON_NS_MXFP8 = 0, 1
+QMUON_STATE_F32, QMUON_STATE_E4M3 = 0, 1
 
 Q8_KINDS = {"int8": QMUON_Q8_INT8, "uint8": QMUON_Q8_UINT8}
 DTYPES = {"bf16": QMUON_BF16, "f16": QMUON_FP16, "f32": QMUON_FP32}
+STATE_KINDS = {"f32": QMUON_STATE_F32, "e4m3": QMUON_STATE_E4M3}
 
 
 class QmuonError(RuntimeError):
@@ -71,6 +73,31 @@ class qmuon_grasp_matrix(C.Structure):
                 ("r", C.c_void_p), ("r_rmax", C.c_void_p), ("r_cmax", C.c_void_p), ("grad", C.c_void_p)]
 
 
+class qmuon_grad(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("numel", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class qmuon_adamw_tensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("copy", C.c_void_p), ("m", C.c_void_p),
+                ("v", C.c_void_p), ("m_absmax", C.c_void_p), ("v_absmax", C.c_void_p), ("numel", C.c_int64),
+                ("lr_scale", C.c_float), ("weight_decay", C.c_float), ("grad_dtype", C.c_int32),
+                ("copy_dtype", C.c_int32)]
+
+
+class qmuon_rmsnorm(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("residual", C.c_void_p), ("gain", C.c_void_p), ("sum", C.c_void_p),
+                ("y", C.c_void_p), ("payload", C.c_void_p), ("scale_inv", C.c_void_p), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("ld_x", C.c_int64), ("ld_residual", C.c_int64), ("ld_sum", C.c_int64),
+                ("ld_y", C.c_int64), ("eps", C.c_float), ("dtype", C.c_int32)]
+
+
+class qmuon_rmsnorm_grad(C.Structure):
+    _fields_ = [("dy", C.c_void_p), ("h", C.c_void_p), ("dsum", C.c_void_p), ("gain", C.c_void_p),
+                ("dx", C.c_void_p), ("dgain", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("ld_dy", C.c_int64), ("ld_h", C.c_int64), ("ld_dsum", C.c_int64), ("ld_dx", C.c_int64),
+                ("eps", C.c_float), ("dtype", C.c_int32)]
+
+
 GRASP_RANK, GRASP_BLOCK = 8, 64
 
 COUNTER_FIELDS = (
@@ -97,6 +124,7 @@ def lib() -> C.CDLL:
                            "run `python -m memory_reduced_muon_gb300.build`")
     L = C.CDLL(LIB_PATH)
     vp, i32, i64, f32, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
+    f64 = C.c_double
     sig = {
         "qmuon_plan_create": (i32, [C.POINTER(qmuon_tensor), i32, i32, i32, C.POINTER(qmuon_norm_segment),
                                     i32, i32, i32, i32, C.POINTER(vp)]),
@@ -126,6 +154,17 @@ def lib() -> C.CDLL:
         "qmuon_plan_set_nonfinite_counter": (i32, [vp, vp]),
         "qmuon_noalloc_sync_status": (i32, [vp]),
         "qmuon_noalloc_inject_status": (i32, [i32, C.c_uint32]),
+        "qmuon_clip_plan_create": (i32, [C.POINTER(qmuon_grad), i32, C.POINTER(vp)]),
+        "qmuon_clip_plan_destroy": (None, [vp]),
+        "qmuon_clip_workspace_size": (sz, [vp]),
+        "qmuon_grad_clip": (i32, [vp, f32, i32, vp, vp, sz, vp]),
+        "qmuon_adamw_plan_create": (i32, [C.POINTER(qmuon_adamw_tensor), i32, i32, C.POINTER(vp)]),
+        "qmuon_adamw_plan_destroy": (None, [vp]),
+        "qmuon_adamw_step": (i32, [vp, i64, f64, f64, f64, f64, vp, vp]),
+        "qmuon_adamw_step_sr": (i32, [vp, i64, f64, f64, f64, f64, C.c_uint64, vp, vp]),
+        "qmuon_rmsnorm_forward": (i32, [C.POINTER(qmuon_rmsnorm), vp]),
+        "qmuon_rmsnorm_workspace_size": (sz, [i64, i64]),
+        "qmuon_rmsnorm_backward": (i32, [C.POINTER(qmuon_rmsnorm_grad), vp, sz, vp]),
         "qmuon_get_counters": (i32, [C.POINTER(qmuon_counters), sz]),
         "qmuon_reset_counters": (None, []),
     }
@@ -146,7 +185,10 @@ def exported_symbols() -> list:
             "qmuon_plan_set_stochastic_rounding", "qmuon_update_mxfp8_carrier_multi",
             "qmuon_grasp_workspace_size", "qmuon_grasp_step", "qmuon_step_from_host",
             "qmuon_plan_set_nonfinite_counter", "qmuon_noalloc_sync_status", "qmuon_noalloc_inject_status",
-            "qmuon_get_counters", "qmuon_reset_counters", "qmuon_plan_set_host_ingest"]
+            "qmuon_get_counters", "qmuon_reset_counters", "qmuon_plan_set_host_ingest",
+            "qmuon_clip_plan_create", "qmuon_clip_plan_destroy", "qmuon_clip_workspace_size", "qmuon_grad_clip",
+            "qmuon_adamw_plan_create", "qmuon_adamw_plan_destroy", "qmuon_adamw_step", "qmuon_adamw_step_sr",
+            "qmuon_rmsnorm_forward", "qmuon_rmsnorm_workspace_size", "qmuon_rmsnorm_backward"]
 
 
 # --------------------------------------------------------------------------
@@ -435,3 +477,119 @@ def qmuon_grasp_step(matrices: Sequence, mu: float, ws, ws_bytes: Optional[int] 
     arr, n = _grasp_array(matrices)
     _check(lib().qmuon_grasp_step(arr, n, float(mu), _ptr(ws), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
                                   _stream(stream)), "qmuon_grasp_step")
+
+
+# --------------------------------------------------------------------------
+# beside the Muon step: gradient clipping, AdamW, RMS norm
+# --------------------------------------------------------------------------
+
+class ClipPlan:
+    """An owned ``qmuon_clip_plan*`` (destroyed with the object)."""
+
+    def __init__(self, handle: int, keepalive):
+        self.handle = handle
+        self._keep = keepalive
+
+    def __del__(self):
+        qmuon_clip_plan_destroy(self)
+
+
+def qmuon_clip_plan_create(grads: Sequence) -> ClipPlan:
+    """``grads``: ``qmuon_grad`` or ``(gradient tensor, dtype name)`` tuples."""
+    descs = [g if isinstance(g, qmuon_grad) else
+             qmuon_grad(_ptr(g[0]), int(g[0].numel()), DTYPES.get(g[1], g[1]), 0) for g in grads]
+    arr = (qmuon_grad * max(1, len(descs)))(*descs)
+    out = C.c_void_p()
+    _check(lib().qmuon_clip_plan_create(arr, len(descs), C.byref(out)), "qmuon_clip_plan_create")
+    return ClipPlan(out.value, grads)
+
+
+def qmuon_clip_plan_destroy(plan: ClipPlan):
+    h, plan.handle = getattr(plan, "handle", None), None
+    if h and _lib_handle is not None:
+        _lib_handle.qmuon_clip_plan_destroy(h)
+
+
+def qmuon_clip_workspace_size(plan: ClipPlan) -> int:
+    return int(lib().qmuon_clip_workspace_size(plan.handle))
+
+
+def qmuon_grad_clip(plan: ClipPlan, max_norm: float, apply: bool, norm, ws, ws_bytes: Optional[int] = None, stream=None):
+    """``norm``: a device fp32 tensor of two: the norm and the coefficient."""
+    st = lib().qmuon_grad_clip(plan.handle, float(max_norm), int(apply), _ptr(norm), _ptr(ws),
+                               _nbytes(ws) if ws_bytes is None else int(ws_bytes), _stream(stream))
+    _check(st, "qmuon_grad_clip")
+
+
+class AdamwPlan:
+    """An owned ``qmuon_adamw_plan*`` (destroyed with the object)."""
+
+    def __init__(self, handle: int, keepalive):
+        self.handle = handle
+        self._keep = keepalive
+
+    def __del__(self):
+        qmuon_adamw_plan_destroy(self)
+
+
+def adamw_tensor(param, grad, m, v, numel: int, grad_dtype="bf16", m_absmax=None, v_absmax=None, copy=None,
+                 copy_dtype="bf16", weight_decay: float = 0.0, lr_scale: float = 1.0) -> qmuon_adamw_tensor:
+    t = qmuon_adamw_tensor(_ptr(param), _ptr(grad), _ptr(copy), _ptr(m), _ptr(v), _ptr(m_absmax), _ptr(v_absmax),
+                           int(numel), float(lr_scale), float(weight_decay), DTYPES.get(grad_dtype, grad_dtype),
+                           DTYPES.get(copy_dtype, copy_dtype))
+    t._keep = (param, grad, copy, m, v, m_absmax, v_absmax)
+    return t
+
+
+def qmuon_adamw_plan_create(tensors: Sequence, state="f32") -> AdamwPlan:
+    """``tensors``: ``adamw_tensor(...)``; ``state``: "f32" or "e4m3"."""
+    arr = (qmuon_adamw_tensor * max(1, len(tensors)))(*tensors)
+    out = C.c_void_p()
+    st = lib().qmuon_adamw_plan_create(arr, len(tensors), STATE_KINDS.get(state, state), C.byref(out))
+    _check(st, "qmuon_adamw_plan_create")
+    return AdamwPlan(out.value, tensors)
+
+
+def qmuon_adamw_plan_destroy(plan: AdamwPlan):
+    h, plan.handle = getattr(plan, "handle", None), None
+    if h and _lib_handle is not None:
+        _lib_handle.qmuon_adamw_plan_destroy(h)
+
+
+def qmuon_adamw_step(plan: AdamwPlan, t: int, lr: float, beta1: float, beta2: float, eps: float, grad_scale=None,
+                     stream=None):
+    """``grad_scale``: a device fp32 tensor of one (a clipping coefficient), or None."""
+    _check(lib().qmuon_adamw_step(plan.handle, int(t), lr, beta1, beta2, eps, _ptr(grad_scale), _stream(stream)),
+           "qmuon_adamw_step")
+
+
+def qmuon_adamw_step_sr(plan: AdamwPlan, t: int, lr: float, beta1: float, beta2: float, eps: float, seed: int,
+                        grad_scale=None, stream=None):
+    _check(lib().qmuon_adamw_step_sr(plan.handle, int(t), lr, beta1, beta2, eps, int(seed) & 0xFFFFFFFFFFFFFFFF,
+                                     _ptr(grad_scale), _stream(stream)), "qmuon_adamw_step_sr")
+
+
+def qmuon_rmsnorm_forward(x, gain, rows: int, cols: int, dtype, eps: float, y=None, residual=None, sum=None,
+                          payload=None, scale_inv=None, ld_x: Optional[int] = None, ld_residual: Optional[int] = None,
+                          ld_sum: Optional[int] = None, ld_y: Optional[int] = None, stream=None):
+    """The ``ld_*`` default to ``cols`` (rows next to one another)."""
+    n = qmuon_rmsnorm(_ptr(x), _ptr(residual), _ptr(gain), _ptr(sum), _ptr(y), _ptr(payload), _ptr(scale_inv),
+                           rows, cols, cols if ld_x is None else ld_x, cols if ld_residual is None else ld_residual,
+                           cols if ld_sum is None else ld_sum, cols if ld_y is None else ld_y, eps,
+                           DTYPES.get(dtype, dtype))
+    _check(lib().qmuon_rmsnorm_forward(C.byref(n), _stream(stream)), "qmuon_rmsnorm_forward")
+
+
+def qmuon_rmsnorm_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().qmuon_rmsnorm_workspace_size(int(rows), int(cols)))
+
+
+def qmuon_rmsnorm_backward(dy, h, gain, rows: int, cols: int, dtype, eps: float, dx, dgain, ws, dsum=None,
+                           ld_dy: Optional[int] = None, ld_h: Optional[int] = None, ld_dsum: Optional[int] = None,
+                           ld_dx: Optional[int] = None, ws_bytes: Optional[int] = None, stream=None):
+    n = qmuon_rmsnorm_grad(_ptr(dy), _ptr(h), _ptr(dsum), _ptr(gain), _ptr(dx), _ptr(dgain), rows, cols,
+                           cols if ld_dy is None else ld_dy, cols if ld_h is None else ld_h,
+                           cols if ld_dsum is None else ld_dsum, cols if ld_dx is None else ld_dx, eps,
+                           DTYPES.get(dtype, dtype))
+    _check(lib().qmuon_rmsnorm_backward(C.byref(n), _ptr(ws), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
+                                        _stream(stream)), "qmuon_rmsnorm_backward")
