@@ -547,7 +547,7 @@ QMUON_API void qmuon_adamw_plan_destroy(qmuon_adamw_plan* plan);
  * maximum (the update above uses the unrounded ones).  A NaN or infinity in a
  * block leaves NaN codes, so that it is not lost.
  *   t           >= 1, the step's index; fixed in captured launches
- *   eps         > 0 in fp32
+ *   eps         at least 2^-126 (the smallest normal fp32)
  *   grad_scale  D  one fp32 s (a clipping coefficient, an inverse loss scale),
  *                  or NULL for 1.  Where s is not finite the step changes
  *                  nothing.

@@ -4,10 +4,13 @@
 // table says which tensor each chunk belongs to, and one CTA takes one chunk
 // (or, in the norm, every gridDim.x-th one).  There is no work per tensor, so
 // hundreds of short vectors cost what one tensor of their total size costs.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <memory>
+#include <type_traits>
 #include <vector>
 
 #include "qm_elem.h"
@@ -44,7 +47,7 @@ struct ClipLaunch {
 template <int DT>
 __device__ __forceinline__ float chunk_sumsq(const ClipTensor& T, int64_t e0, int n, int tid) {
   constexpr int K = Vec16<DT>::kElems;
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float2 s[2] = {};
   int done = 0;
   const unsigned char* base = static_cast<const unsigned char*>(T.grad) + e0 * elem_size(DT);
   if (T.vec) {
@@ -52,18 +55,18 @@ __device__ __forceinline__ float chunk_sumsq(const ClipTensor& T, int64_t e0, in
     const int nv = n / K;
 #pragma unroll 4
     for (int i = tid; i < nv; i += kThreads) {
-      float f[K];
+      float2 f[K / 2];
       Vec16<DT>::unpack(__ldg(p + i), f);
 #pragma unroll
-      for (int j = 0; j < K; ++j) s[j & 3] = fmaf(f[j], f[j], s[j & 3]);
+      for (int j = 0; j < K / 2; ++j) s[j & 1] = fma2(f[j], f[j], s[j & 1]);
     }
     done = nv * K;
   }
   for (int i = done + tid; i < n; i += kThreads) {
     const float f = load_elem<DT>(base, i);
-    s[0] = fmaf(f, f, s[0]);
+    s[0].x = fmaf(f, f, s[0].x);
   }
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  return (s[0].x + s[0].y) + (s[1].x + s[1].y);
 }
 
 __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const ClipLaunch L) {
@@ -122,10 +125,10 @@ __device__ __forceinline__ void chunk_scale(const ClipTensor& T, int64_t e0, int
     const int nv = n / K;
 #pragma unroll 4
     for (int i = tid; i < nv; i += kThreads) {
-      float f[K];
+      float2 f[K / 2];
       Vec16<DT>::unpack(p[i], f);
 #pragma unroll
-      for (int j = 0; j < K; ++j) f[j] *= c;
+      for (int j = 0; j < K / 2; ++j) f[j] = mul2(f[j], c);
       p[i] = Vec16<DT>::pack(f);
     }
     done = nv * K;
@@ -151,7 +154,11 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const ClipLaunch L
 // With g' = c g (c the clipping coefficient), every operation rounded once:
 //   m <- b1 m + (1 - b1) g'          v <- b2 v + (1 - b2) g'^2
 //   p <- p (1 - lr wd) - (lr / (1 - b1^t)) (m / (sqrt(v) / sqrt(1 - b2^t) + eps))
-constexpr int kAdamChunk = 2048;   // elements: 8 per thread, or one 256-element block per warp
+constexpr int kWarps = kThreads / 32;
+constexpr int kAdamChunk = 2048;   // elements with fp32 states: 8 per thread
+// With 8-bit states a chunk is J blocks of 256 per warp: 3, or 1 where 3 would
+// leave SMs without a CTA (fewer than two chunks per SM).
+constexpr int kManyBlocks = 3;
 
 struct AdamTensor {
   float* param;
@@ -161,13 +168,13 @@ struct AdamTensor {
   void* v;
   float* m_absmax;     // 8-bit states
   float* v_absmax;
-  int64_t numel;
-  float lr_scale, weight_decay;
+  int64_t end;         // elements are [begin, end) of the arrays, which point `begin` elements
+  int32_t begin;       //   before the caller's: 0..3, so that quads of elements are aligned
   int32_t first_chunk;
+  float lr_scale, weight_decay;
   int32_t index;       // in the caller's list: the stochastic rounding's counter
   int16_t grad_dtype, copy_dtype;
-  int16_t vec;         // four elements of every array can be moved at once
-  int16_t pad;
+  int32_t vec;         // quads are aligned in every array
 };
 
 struct AdamLaunch {
@@ -175,7 +182,8 @@ struct AdamLaunch {
   const int32_t* chunk_tensor;
   const float* grad_scale;   // D, or null
   float lr, b1, omb1, b2, omb2, rbc1, rbc2, eps;
-  uint32_t key0, key1, step;
+  uint32_t step;
+  PhiloxKeys keys;
 };
 
 struct AdamCoef {
@@ -187,205 +195,416 @@ __device__ __forceinline__ AdamCoef adam_coef(const AdamLaunch& L, const AdamTen
   return {scale, __fsub_rn(1.0f, __fmul_rn(lr, T.weight_decay)), __fmul_rn(lr, L.rbc1)};
 }
 
-// New momentum, second moment and parameter of one element; returns sqrt(v).
-__device__ __forceinline__ float adam_elem(const AdamLaunch& L, const AdamCoef& C, float g, float& p, float& m, float& v) {
-  g = __fmul_rn(g, C.scale);
-  m = __fadd_rn(__fmul_rn(m, L.b1), __fmul_rn(g, L.omb1));
-  v = __fadd_rn(__fmul_rn(v, L.b2), __fmul_rn(__fmul_rn(g, g), L.omb2));
-  const float r = __fsqrt_rn(v);
-  const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, L.rbc2), L.eps));
-  p = __fsub_rn(__fmul_rn(p, C.decay), __fmul_rn(C.step, u));
+// 1 / x to 1 ulp for normal x below 2^126 (zero above).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// Four elements from e, of which the first n exist.
-__device__ __forceinline__ void load4(const float* p, int64_t e, int n, bool vec, float* f) {
-  if (vec && n == 4) {
-    const float4 t = __ldcs(reinterpret_cast<const float4*>(p + e));
-    f[0] = t.x, f[1] = t.y, f[2] = t.z, f[3] = t.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = j < n ? p[e + j] : 0.0f;
+// Two elements: the new momentum, parameter and square root of the new second
+// moment, from the old momentum, parameter and second moment.  Only the
+// quotient is not correctly rounded (2 ulp): it reaches the parameter alone,
+// scaled by the step size.
+__device__ __forceinline__ void adam_pair(const AdamLaunch& L, const AdamCoef& C, float2 g, float2& p, float2& m, float2& v,
+                                          float2& r) {
+  g = mul2(g, C.scale);
+  const float2 mb = mul2(m, L.b1), mg = mul2(g, L.omb1);
+  const float2 vb = mul2(v, L.b2), vg = mul2(mul2(g, g), L.omb2);
+  m = make_float2(__fadd_rn(mb.x, mg.x), __fadd_rn(mb.y, mg.y));
+  v = make_float2(__fadd_rn(vb.x, vg.x), __fadd_rn(vb.y, vg.y));
+  r = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+  const float2 d = mul2(r, L.rbc2);
+  const float2 u = mul2(mul2(m, make_float2(rcp_approx(__fadd_rn(d.x, L.eps)), rcp_approx(__fadd_rn(d.y, L.eps)))), C.step);
+  const float2 q = mul2(p, C.decay);
+  p = make_float2(__fsub_rn(q.x, u.x), __fsub_rn(q.y, u.y));
+}
+
+// One CTA per chunk, two quads of elements per thread.  A CTA that takes its
+// chunk and leaves keeps DRAM busier than one that stays: the same traffic
+// without any arithmetic runs at 7.06 TB/s with one CTA per 2048 elements and at
+// 6.4 with the resident CTAs looping over chunks (2^28 elements), rings of
+// asynchronous copies ahead of them or not.  Chunks that lie wholly inside a
+// tensor whose arrays are aligned (AdamTensor::vec) move in vectors; in the
+// chunks at a tensor's ends, and in all of an unaligned one, quads that are not
+// whole move element by element.
+struct Quad {
+  float2 a, b;
+};
+
+__device__ __forceinline__ Quad as_quad(const float4& t) { return {make_float2(t.x, t.y), make_float2(t.z, t.w)}; }
+__device__ __forceinline__ Quad load_quad(const float* p) { return as_quad(__ldcs(reinterpret_cast<const float4*>(p))); }
+template <int GDT>
+__device__ __forceinline__ Quad load_grad(const void* g, int64_t e) {
+  if constexpr (GDT == QMUON_FP32) return load_quad(static_cast<const float*>(g) + e);
+  else {
+    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + e));
+    return {unpack2<GDT>(w.x), unpack2<GDT>(w.y)};
   }
 }
-__device__ __forceinline__ void store4(float* p, int64_t e, int n, bool vec, const float* f) {
-  if (vec && n == 4) {
-    __stcs(reinterpret_cast<float4*>(p + e), make_float4(f[0], f[1], f[2], f[3]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < n) p[e + j] = f[j];
-  }
+__device__ __forceinline__ Quad load_grad(const AdamTensor& T, int64_t e) {
+  return T.grad_dtype == QMUON_FP32   ? load_grad<QMUON_FP32>(T.grad, e)
+         : T.grad_dtype == QMUON_BF16 ? load_grad<QMUON_BF16>(T.grad, e)
+                                      : load_grad<QMUON_FP16>(T.grad, e);
 }
-template <int DT>
-__device__ __forceinline__ void load4_16(const void* p, int64_t e, int n, bool vec, float* f) {
-  if (vec && n == 4) {
-    const uint2 t = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + e));
-    const float2 a = unpack2<DT>(t.x), b = unpack2<DT>(t.y);
-    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = j < n ? load_elem<DT>(p, e + j) : 0.0f;
-  }
+__device__ __forceinline__ float grad_elem(const AdamTensor& T, int64_t e) {
+  if (T.grad_dtype == QMUON_FP32) return load_elem<QMUON_FP32>(T.grad, e);
+  if (T.grad_dtype == QMUON_BF16) return load_elem<QMUON_BF16>(T.grad, e);
+  return load_elem<QMUON_FP16>(T.grad, e);
 }
-__device__ __forceinline__ void load_grad4(const AdamTensor& T, int64_t e, int n, float* f) {
-  if (T.grad_dtype == QMUON_FP32) load4(static_cast<const float*>(T.grad), e, n, T.vec, f);
-  else if (T.grad_dtype == QMUON_BF16) load4_16<QMUON_BF16>(T.grad, e, n, T.vec, f);
-  else load4_16<QMUON_FP16>(T.grad, e, n, T.vec, f);
+constexpr int kNoCopy = -1;
+template <int CDT>
+__device__ __forceinline__ void store_copy_quad(uint16_t* c, const Quad& p) {
+  if constexpr (CDT != kNoCopy)
+    __stcs(reinterpret_cast<uint2*>(c), make_uint2(pack2<CDT>(p.a.x, p.a.y), pack2<CDT>(p.b.x, p.b.y)));
 }
-template <int DT>
-__device__ __forceinline__ void store4_16(void* p, int64_t e, int n, bool vec, const float* f) {
-  if (vec && n == 4) {
-    __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + e),
-           make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < n) store_elem<DT>(p, e + j, f[j]);
-  }
+__device__ __forceinline__ void store_quad(float* d, const Quad& q) {
+  __stcs(reinterpret_cast<float4*>(d), make_float4(q.a.x, q.a.y, q.b.x, q.b.y));
 }
-__device__ __forceinline__ void store_copy4(const AdamTensor& T, int64_t e, int n, const float* f) {
+__device__ __forceinline__ void store_param_quad(const AdamTensor& T, int64_t e, const Quad& p) {
+  store_quad(T.param + e, p);
+  uint16_t* c = static_cast<uint16_t*>(T.copy) + e;
   if (!T.copy) return;
-  if (T.copy_dtype == QMUON_BF16) store4_16<QMUON_BF16>(T.copy, e, n, T.vec, f);
-  else store4_16<QMUON_FP16>(T.copy, e, n, T.vec, f);
+  if (T.copy_dtype == QMUON_BF16) store_copy_quad<QMUON_BF16>(c, p);
+  else store_copy_quad<QMUON_FP16>(c, p);
+}
+__device__ __forceinline__ void store_param_elem(const AdamTensor& T, int64_t e, float p) {
+  T.param[e] = p;
+  if (!T.copy) return;
+  if (T.copy_dtype == QMUON_BF16) store_elem<QMUON_BF16>(T.copy, e, p);
+  else store_elem<QMUON_FP16>(T.copy, e, p);
 }
 
-__global__ void __launch_bounds__(kThreads) adamw_f32_kernel(const __grid_constant__ AdamLaunch L) {
-  const float scale = L.grad_scale ? __ldg(L.grad_scale) : 1.0f;
-  if (!isfinite(scale)) return;
+// One element with fp32 states, from and to memory.
+__device__ __forceinline__ void adam_single(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int64_t e) {
+  float* mp = static_cast<float*>(T.m) + e;
+  float* vp = static_cast<float*>(T.v) + e;
+  float2 p = make_float2(T.param[e], 0.0f), m = make_float2(*mp, 0.0f), v = make_float2(*vp, 0.0f), r;
+  adam_pair(L, C, make_float2(grad_elem(T, e), 0.0f), p, m, v, r);
+  store_param_elem(T, e, p.x);
+  *mp = m.x;
+  *vp = v.x;
+}
+
+// Calls f with the gradient's and the copy's type as constants.
+template <class F>
+__device__ __forceinline__ void with_types(const AdamTensor& T, F&& f) {
+  auto copy = [&](auto g) {
+    if (!T.copy) f(g, std::integral_constant<int, kNoCopy>{});
+    else if (T.copy_dtype == QMUON_BF16) f(g, std::integral_constant<int, QMUON_BF16>{});
+    else f(g, std::integral_constant<int, QMUON_FP16>{});
+  };
+  if (T.grad_dtype == QMUON_FP32) copy(std::integral_constant<int, QMUON_FP32>{});
+  else if (T.grad_dtype == QMUON_BF16) copy(std::integral_constant<int, QMUON_BF16>{});
+  else copy(std::integral_constant<int, QMUON_FP16>{});
+}
+
+// Calls f(T, C, c) for this CTA's chunk: chunk c of tensor T.
+template <class F>
+__device__ __forceinline__ void for_chunk(const AdamLaunch& L, F&& f) {
   const AdamTensor T = L.tensors[__ldg(L.chunk_tensor + blockIdx.x)];
-  const AdamCoef C = adam_coef(L, T, scale);
-  const int64_t e0 = (int64_t)((int)blockIdx.x - T.first_chunk) * kAdamChunk + threadIdx.x * 4;
-  float p[2][4], m[2][4], v[2][4], g[2][4];
-  int n[2];
+  const float scale = L.grad_scale ? __ldg(L.grad_scale) : 1.0f;
+  if (isfinite(scale)) f(T, adam_coef(L, T, scale), (int)blockIdx.x - T.first_chunk);
+}
+
+// ---- fp32 states ----
+template <int GDT, int CDT>
+__device__ __forceinline__ void f32_fast(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int c) {
+  constexpr int kHalf = kThreads * 4;
+  const int64_t e = (int64_t)c * kAdamChunk + threadIdx.x * 4;   // of the first quad; the second is kHalf on
+  float* p = T.param + e;
+  float* m = static_cast<float*>(T.m) + e;
+  float* v = static_cast<float*>(T.v) + e;
+  Quad P[2], M[2], V[2], G[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int64_t e = e0 + k * kThreads * 4;
-    n[k] = (int)max((int64_t)0, min((int64_t)4, T.numel - e));
-    load_grad4(T, e, n[k], g[k]);
-    load4(T.param, e, n[k], T.vec, p[k]);
-    load4(static_cast<const float*>(T.m), e, n[k], T.vec, m[k]);
-    load4(static_cast<const float*>(T.v), e, n[k], T.vec, v[k]);
+    G[k] = load_grad<GDT>(T.grad, e + k * kHalf);
+    P[k] = load_quad(p + k * kHalf);
+    M[k] = load_quad(m + k * kHalf);
+    V[k] = load_quad(v + k * kHalf);
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int64_t e = e0 + k * kThreads * 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) adam_elem(L, C, g[k][j], p[k][j], m[k][j], v[k][j]);
-    store4(T.param, e, n[k], T.vec, p[k]);
-    store4(static_cast<float*>(T.m), e, n[k], T.vec, m[k]);
-    store4(static_cast<float*>(T.v), e, n[k], T.vec, v[k]);
-    store_copy4(T, e, n[k], p[k]);
+    float2 r;
+    adam_pair(L, C, G[k].a, P[k].a, M[k].a, V[k].a, r);
+    adam_pair(L, C, G[k].b, P[k].b, M[k].b, V[k].b, r);
+    store_quad(p + k * kHalf, P[k]);
+    store_quad(m + k * kHalf, M[k]);
+    store_quad(v + k * kHalf, V[k]);
+    store_copy_quad<CDT>(static_cast<uint16_t*>(T.copy) + e + k * kHalf, P[k]);
   }
 }
 
-// 8-bit states.  m and r = sqrt(v) are E4M3 codes with one fp32 maximum per
-// 256 elements: x = code * (max / 448).  The root is stored, not v: its codes
-// then cover as many powers of two as the momentum's, so that where r rounds
-// to zero m does too, and no element divides a momentum by eps alone.
+__device__ __noinline__ void f32_slow(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int c) {
+  const int t = threadIdx.x;
+  const int64_t e0 = (int64_t)c * kAdamChunk;
+  if (!T.vec) {   // neighbouring threads on neighbouring elements
+#pragma unroll 4
+    for (int j = 0; j < kAdamChunk / kThreads; ++j) {
+      const int64_t e = e0 + j * kThreads + t;
+      if (e < T.end) adam_single(L, T, C, e);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t e = e0 + (k * kThreads + t) * 4;
+    if (e >= T.begin && e + 4 <= T.end) {
+      float4* mp = reinterpret_cast<float4*>(static_cast<float*>(T.m) + e);
+      float4* vp = reinterpret_cast<float4*>(static_cast<float*>(T.v) + e);
+      Quad P = load_quad(T.param + e), M = as_quad(__ldcs(mp)), V = as_quad(__ldcs(vp));
+      const Quad G = load_grad(T, e);
+      float2 r;
+      adam_pair(L, C, G.a, P.a, M.a, V.a, r);
+      adam_pair(L, C, G.b, P.b, M.b, V.b, r);
+      store_param_quad(T, e, P);
+      store_quad(reinterpret_cast<float*>(mp), M);
+      store_quad(reinterpret_cast<float*>(vp), V);
+    } else {
+      for (int j = 0; j < 4; ++j)
+        if (e + j >= T.begin && e + j < T.end) adam_single(L, T, C, e + j);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 4) adamw_f32_kernel(const __grid_constant__ AdamLaunch L) {
+  for_chunk(L, [&](const AdamTensor& T, const AdamCoef& C, int c) {
+    if (T.vec && (c > 0 || T.begin == 0) && (int64_t)(c + 1) * kAdamChunk <= T.end)
+      with_types(T, [&](auto g, auto k) { f32_fast<decltype(g)::value, decltype(k)::value>(L, T, C, c); });
+    else
+      f32_slow(L, T, C, c);
+  });
+}
+
+// ---- 8-bit states ----
+// m and r = sqrt(v) are E4M3 codes with one fp32 maximum per 256 elements:
+// x = code * (max / 448).  The root is stored, not v: its codes then cover as
+// many powers of two as the momentum's, so that where r rounds to zero m does
+// too, and no element divides a momentum by eps alone.
 //
-// A warp takes a block: lane l holds elements 4l..4l+3 and 128+4l..128+4l+3,
-// so every load and store of the warp is one contiguous run.
-__device__ __forceinline__ uint32_t load_codes4(const uint8_t* p, int64_t e, int n) {
-  if (n == 4) return __ldcs(reinterpret_cast<const uint32_t*>(p + e));   // block starts are 16-byte aligned
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < n) w |= (uint32_t)p[e + j] << (8 * j);
-  return w;
-}
-__device__ __forceinline__ void store_codes4(uint8_t* p, int64_t e, int n, uint32_t w) {
-  if (n == 4) {
-    __stcs(reinterpret_cast<uint32_t*>(p + e), w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < n) p[e + j] = (uint8_t)(w >> (8 * j));
-  }
-}
-__device__ __forceinline__ uint32_t encode4(const float* x, float sc) {
-  return e4m3x2_of(__fmul_rn(x[0], sc), __fmul_rn(x[1], sc)) |
-         (e4m3x2_of(__fmul_rn(x[2], sc), __fmul_rn(x[3], sc)) << 16);
-}
-// E4M3 of x with 16 random bits u: rounded up in magnitude with probability
-// (remainder / step) to 2^-16.  2^-120 |x| has its exponent field where the
-// code's is, subnormals included, so the bits above the lowest 20 are the code.
-__device__ __forceinline__ uint32_t encode_sr(float x, uint32_t u) {
-  const uint32_t b = __float_as_uint(__fmul_rn(fabsf(x), 7.52316384526264e-37f));
-  const uint32_t c = min((b + (u << 4)) >> 20, 0x7Eu) | ((__float_as_uint(x) >> 24) & 0x80u);
-  return x != x ? 0x7Fu : c;
+// A warp takes a block, lane l its elements 4l..4l+3 and 128+4l..128+4l+3: every
+// load and store of the warp is one contiguous run, and a quad of elements
+// shares a random counter.
+
+// E4M3 of four scaled values with 16 random bits each: rounded up in magnitude
+// with probability (remainder / step) to 2^-16.  2^-120 |x| has its exponent
+// field where the code's is, subnormals included, so the bits above the lowest
+// 20 are the code.  The largest value's code, 0x7E with all lower bits zero (up
+// to an ulp), cannot be carried to 0x7F by random bits of which the lowest four
+// are zero: 0x7F remains for NaN alone.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t encode_sr4(const Quad& x, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
+  constexpr float kShift = 7.52316384526264e-37f;   // 2^-120
+  const float2 a = mul2(x.a, kShift), b = mul2(x.b, kShift);
+  auto code = [](float y, uint32_t u) { return min(__float_as_uint(fabsf(y)) + u, 0x7F00000u) << 4; };
+  const uint32_t c0 = code(a.x, u0), c1 = code(a.y, u1), c2 = code(b.x, u2), c3 = code(b.y, u3);
+  const uint32_t w = __byte_perm(__byte_perm(c0, c1, 0x0073u), __byte_perm(c2, c3, 0x0073u), 0x5410u);
+  if constexpr (!SIGNED) return w;
+  const uint32_t s = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0073u),
+                                 __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0073u), 0x5410u);
+  return w | (s & 0x80808080u);
 }
 
-template <bool SR>
-__global__ void __launch_bounds__(kThreads) adamw_e4m3_kernel(const __grid_constant__ AdamLaunch L) {
-  const float scale = L.grad_scale ? __ldg(L.grad_scale) : 1.0f;
-  if (!isfinite(scale)) return;
-  const AdamTensor T = L.tensors[__ldg(L.chunk_tensor + blockIdx.x)];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t blk = (int64_t)((int)blockIdx.x - T.first_chunk) * (kAdamChunk / kBlock) + warp;
-  const int64_t b0 = blk * kBlock;
-  if (b0 >= T.numel) return;   // the whole warp
-  const AdamCoef C = adam_coef(L, T, scale);
-  float p[2][4], m[2][4], v[2][4], g[2][4];
+// Two quads of a block in a lane.
+struct E4m3Quads {
+  Quad p[2], g[2], m[2], r[2];
   uint32_t mc[2], vc[2];
-  int n[2];
-  const float m_unit = __fdiv_rn(T.m_absmax[blk], 448.0f), r_unit = __fdiv_rn(T.v_absmax[blk], 448.0f);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t e = b0 + k * 128 + lane * 4;
-    n[k] = (int)max((int64_t)0, min((int64_t)4, T.numel - e));
-    load_grad4(T, e, n[k], g[k]);
-    load4(T.param, e, n[k], T.vec, p[k]);
-    mc[k] = load_codes4(static_cast<const uint8_t*>(T.m), e, n[k]);
-    vc[k] = load_codes4(static_cast<const uint8_t*>(T.v), e, n[k]);
-  }
+  float m_max, r_max;
+};
+
+// Decodes, updates and, for the n[k] elements of each quad that exist, takes
+// part in the block's maxima; m and r leave scaled for encoding, mc and vc as
+// the new codes.
+template <bool SR, bool WHOLE>
+__device__ __forceinline__ void e4m3_update(const AdamLaunch& L, const AdamCoef& C, E4m3Quads& q, const int* n, int64_t e0,
+                                            int32_t index) {
+  const float m_unit = __fdiv_rn(q.m_max, 448.0f), r_unit = __fdiv_rn(q.r_max, 448.0f);
   float m_max = 0.0f, r_max = 0.0f;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const float2 ma = e4m3x2_to(mc[k]), mb = e4m3x2_to(mc[k] >> 16), va = e4m3x2_to(vc[k]), vb = e4m3x2_to(vc[k] >> 16);
-    const float mo[4] = {ma.x, ma.y, mb.x, mb.y}, ro[4] = {va.x, va.y, vb.x, vb.y};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      m[k][j] = __fmul_rn(mo[j], m_unit);
-      const float r = __fmul_rn(ro[j], r_unit);
-      v[k][j] = __fmul_rn(r, r);
-      v[k][j] = adam_elem(L, C, g[k][j], p[k][j], m[k][j], v[k][j]);   // the root from here on
-      if (j >= n[k]) m[k][j] = v[k][j] = 0.0f;
-      m_max = fmaxf(m_max, fabsf(m[k][j]));
-      r_max = fmaxf(r_max, v[k][j]);
+    Quad &m = q.m[k], &r = q.r[k];
+    m.a = mul2(e4m3x2_to(q.mc[k]), m_unit);
+    m.b = mul2(e4m3x2_to(q.mc[k] >> 16), m_unit);
+    const float2 ra = mul2(e4m3x2_to(q.vc[k]), r_unit), rb = mul2(e4m3x2_to(q.vc[k] >> 16), r_unit);
+    float2 va = mul2(ra, ra), vb = mul2(rb, rb);
+    adam_pair(L, C, q.g[k].a, q.p[k].a, m.a, va, r.a);
+    adam_pair(L, C, q.g[k].b, q.p[k].b, m.b, vb, r.b);
+    if constexpr (!WHOLE) {
+      if (n[k] < 1) m.a.x = r.a.x = 0.0f;
+      if (n[k] < 2) m.a.y = r.a.y = 0.0f;
+      if (n[k] < 3) m.b.x = r.b.x = 0.0f;
+      if (n[k] < 4) m.b.y = r.b.y = 0.0f;
     }
+    m_max = fmaxf(m_max, fmaxf(fmaxf(fabsf(m.a.x), fabsf(m.a.y)), fmaxf(fabsf(m.b.x), fabsf(m.b.y))));
+    r_max = fmaxf(r_max, fmaxf(fmaxf(r.a.x, r.a.y), fmaxf(r.b.x, r.b.y)));
   }
-  m_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m_max)));   // not negative: ordered as integers
-  r_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r_max)));
+  q.m_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m_max)));   // not negative: ordered as integers
+  q.r_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r_max)));
   constexpr float kMax = 3.402823466e+38f;   // a zero or tiny maximum: no infinite factor
-  const float m_sc = fminf(__fdiv_rn(448.0f, m_max), kMax), r_sc = fminf(__fdiv_rn(448.0f, r_max), kMax);
+  const float m_sc = fminf(__fdiv_rn(448.0f, q.m_max), kMax), r_sc = fminf(__fdiv_rn(448.0f, q.r_max), kMax);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int64_t e = b0 + k * 128 + lane * 4;
-    uint32_t mo, vo;
+    const float2 ma = mul2(q.m[k].a, m_sc), mb = mul2(q.m[k].b, m_sc), ra = mul2(q.r[k].a, r_sc), rb = mul2(q.r[k].b, r_sc);
     if constexpr (SR) {
-      const uint64_t j = (uint64_t)e >> 2;
-      const uint4 w = philox(make_uint4((uint32_t)j, (uint32_t)(j >> 32), (uint32_t)T.index, L.step), L.key0, L.key1);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      mo = vo = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mo |= encode_sr(__fmul_rn(m[k][i], m_sc), u[i] & 0xFFFFu) << (8 * i);
-        vo |= encode_sr(__fmul_rn(v[k][i], r_sc), u[i] >> 16) << (8 * i);
-      }
+      const uint64_t j = (uint64_t)(e0 + 128 * k) >> 2;
+      const uint4 w = philox(make_uint4((uint32_t)j, (uint32_t)(j >> 32), (uint32_t)index, L.step), L.keys);
+      // per element: the word's low half for m, its high half for r, above four zero bits
+      auto lo = [](uint32_t x) { return (x << 4) & 0xFFFF0u; };
+      auto hi = [](uint32_t x) { return (x >> 12) & 0xFFFF0u; };
+      q.mc[k] = encode_sr4<true>({ma, mb}, lo(w.x), lo(w.y), lo(w.z), lo(w.w));
+      q.vc[k] = encode_sr4<false>({ra, rb}, hi(w.x), hi(w.y), hi(w.z), hi(w.w));
     } else {
-      mo = encode4(m[k], m_sc);
-      vo = encode4(v[k], r_sc);
+      q.mc[k] = e4m3x2_of(ma.x, ma.y) | (e4m3x2_of(mb.x, mb.y) << 16);
+      q.vc[k] = e4m3x2_of(ra.x, ra.y) | (e4m3x2_of(rb.x, rb.y) << 16);
     }
-    store_codes4(static_cast<uint8_t*>(T.m), e, n[k], mo);
-    store_codes4(static_cast<uint8_t*>(T.v), e, n[k], vo);
-    store4(T.param, e, n[k], T.vec, p[k]);
-    store_copy4(T, e, n[k], p[k]);
+  }
+}
+
+// One block's inputs in shared memory, as its warp's asynchronous copies
+// bring them: all in 16-byte pieces but the two maxima.
+template <int GDT>
+struct __align__(16) E4m3Stage {
+  float p[kBlock];
+  unsigned char g[kBlock * elem_size(GDT)];
+  uint8_t codes[2][kBlock];   // m, v
+  float maxima[4];
+};
+
+// J whole blocks per warp, all of their loads in flight from the start: the
+// copies need no registers while they are (64 registers' worth of blocks in
+// flight per thread were too few for the arithmetic's length).
+template <int GDT, int CDT, bool SR, int J>
+__device__ __forceinline__ void e4m3_fast(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int64_t first, int n,
+                                          unsigned char* smem) {
+  constexpr int kGs = elem_size(GDT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  E4m3Stage<GDT>* ring = reinterpret_cast<E4m3Stage<GDT>*>(smem) + warp;
+  n = (n - warp + kWarps - 1) / kWarps;   // this warp's: blocks first + warp, first + warp + 8, ..
+  int64_t blk = first + warp;
+  const unsigned char* code_src = static_cast<const unsigned char*>(lane < 16 ? T.m : T.v) + (lane & 15) * 16;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (j < n) {
+      E4m3Stage<GDT>& S = ring[j * kWarps];
+      const int64_t e = (blk + j * kWarps) * kBlock;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) async16(&S.p[(k * 32 + lane) * 4], T.param + e + (k * 32 + lane) * 4);
+#pragma unroll
+      for (int k = 0; k < kGs / 2; ++k)
+        async16(&S.g[(k * 32 + lane) * 16], static_cast<const unsigned char*>(T.grad) + e * kGs + (k * 32 + lane) * 16);
+      async16(&S.codes[0][lane * 16], code_src + e);
+      if (lane < 2) async4(&S.maxima[lane], (lane == 0 ? T.m_absmax : T.v_absmax) + blk + j * kWarps);
+    }
+    async_commit();
+  }
+#pragma unroll 1
+  for (int j = 0; j < n; ++j, blk += kWarps) {
+    if (J == 1 || j == J - 1) async_wait<0>();
+    else if (j == J - 2) async_wait<1>();
+    else if (j == J - 3) async_wait<2>();
+    else async_wait<3>();
+    __syncwarp();   // the other lanes' copies
+    const E4m3Stage<GDT>& S = ring[j * kWarps];
+    const int64_t e = blk * kBlock + 4 * lane;   // of the first quad; the second is 128 on
+    E4m3Quads q;
+    q.m_max = S.maxima[0];
+    q.r_max = S.maxima[1];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 128 * k + 4 * lane;
+      q.p[k] = as_quad(*reinterpret_cast<const float4*>(&S.p[i]));
+      if constexpr (kGs == 4) {
+        q.g[k] = as_quad(*reinterpret_cast<const float4*>(&S.g[i * 4]));
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(&S.g[i * 2]);
+        q.g[k] = {unpack2<GDT>(w.x), unpack2<GDT>(w.y)};
+      }
+      q.mc[k] = *reinterpret_cast<const uint32_t*>(&S.codes[0][i]);
+      q.vc[k] = *reinterpret_cast<const uint32_t*>(&S.codes[1][i]);
+    }
+    e4m3_update<SR, true>(L, C, q, nullptr, e, T.index);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(T.m) + e + 128 * k), q.mc[k]);
+      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(T.v) + e + 128 * k), q.vc[k]);
+      store_quad(T.param + e + 128 * k, q.p[k]);
+      store_copy_quad<CDT>(static_cast<uint16_t*>(T.copy) + e + 128 * k, q.p[k]);
+    }
+    if (lane < 2) (lane == 0 ? T.m_absmax : T.v_absmax)[blk] = lane == 0 ? q.m_max : q.r_max;
+  }
+}
+
+// One block, whole or not, by the calling warp.
+template <bool SR>
+__device__ __noinline__ void e4m3_slow(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int64_t blk) {
+  const int lane = threadIdx.x & 31;
+  const int64_t e0 = blk * kBlock + 4 * lane;
+  uint8_t* mp = static_cast<uint8_t*>(T.m) + e0;
+  uint8_t* vp = static_cast<uint8_t*>(T.v) + e0;
+  E4m3Quads q;
+  int n[2];
+  q.m_max = T.m_absmax[blk];
+  q.r_max = T.v_absmax[blk];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t e = e0 + 128 * k;
+    n[k] = (int)max((int64_t)0, min((int64_t)4, T.end - e));
+    if (T.vec && n[k] == 4) {
+      q.p[k] = load_quad(T.param + e);
+      q.g[k] = load_grad(T, e);
+      q.mc[k] = *reinterpret_cast<const uint32_t*>(mp + 128 * k);
+      q.vc[k] = *reinterpret_cast<const uint32_t*>(vp + 128 * k);
+    } else {
+      float pe[4], ge[4];
+      q.mc[k] = q.vc[k] = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        pe[j] = ge[j] = 0.0f;
+        if (j >= n[k]) continue;
+        pe[j] = T.param[e + j];
+        ge[j] = grad_elem(T, e + j);
+        q.mc[k] |= (uint32_t)mp[128 * k + j] << (8 * j);
+        q.vc[k] |= (uint32_t)vp[128 * k + j] << (8 * j);
+      }
+      q.p[k] = {make_float2(pe[0], pe[1]), make_float2(pe[2], pe[3])};
+      q.g[k] = {make_float2(ge[0], ge[1]), make_float2(ge[2], ge[3])};
+    }
+  }
+  e4m3_update<SR, false>(L, C, q, n, e0, T.index);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (T.vec && n[k] == 4) {
+      *reinterpret_cast<uint32_t*>(mp + 128 * k) = q.mc[k];
+      *reinterpret_cast<uint32_t*>(vp + 128 * k) = q.vc[k];
+      store_param_quad(T, e0 + 128 * k, q.p[k]);
+    } else {
+      const float pe[4] = {q.p[k].a.x, q.p[k].a.y, q.p[k].b.x, q.p[k].b.y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= n[k]) continue;
+        mp[128 * k + j] = (uint8_t)(q.mc[k] >> (8 * j));
+        vp[128 * k + j] = (uint8_t)(q.vc[k] >> (8 * j));
+        store_param_elem(T, e0 + 128 * k + j, pe[j]);
+      }
+    }
   }
   if (lane == 0) {
-    T.m_absmax[blk] = m_max;
-    T.v_absmax[blk] = r_max;
+    T.m_absmax[blk] = q.m_max;
+    T.v_absmax[blk] = q.r_max;
   }
+}
+
+template <bool SR, int J>
+__global__ void __launch_bounds__(kThreads, 4) adamw_e4m3_kernel(const __grid_constant__ AdamLaunch L) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  for_chunk(L, [&](const AdamTensor& T, const AdamCoef& C, int c) {
+    constexpr int kPer = J * kWarps;
+    const int64_t first = (int64_t)c * kPer, nb = (T.end + kBlock - 1) / kBlock;
+    const int whole = T.vec ? (int)min((int64_t)kPer, T.end / kBlock - first) : 0, all = (int)min((int64_t)kPer, nb - first);
+    if (whole > 0)
+      with_types(T, [&](auto g, auto k) { e4m3_fast<decltype(g)::value, decltype(k)::value, SR, J>(L, T, C, first, whole, smem); });
+    for (int b = whole + (int)(threadIdx.x >> 5); b < all; b += kWarps) e4m3_slow<SR>(L, T, C, first + b);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -394,6 +613,12 @@ __global__ void __launch_bounds__(kThreads) adamw_e4m3_kernel(const __grid_const
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool is_dtype(int v) { return v == QMUON_BF16 || v == QMUON_FP16 || v == QMUON_FP32; }
 
+using AdamKernel = void (*)(AdamLaunch);
+AdamKernel adam_kernel(qmuon_state_kind state, bool sr, int per_warp) {
+  if (state == QMUON_STATE_F32) return adamw_f32_kernel;
+  if (per_warp == 1) return sr ? adamw_e4m3_kernel<true, 1> : adamw_e4m3_kernel<false, 1>;
+  return sr ? adamw_e4m3_kernel<true, kManyBlocks> : adamw_e4m3_kernel<false, kManyBlocks>;
+}
 // The chunks' table: for each chunk of `chunk` elements, the position of its
 // tensor among the non-empty ones.
 struct Chunks {
@@ -449,6 +674,8 @@ struct qmuon_adamw_plan {
   AdamTensor* tensors = nullptr;
   int32_t* chunk_tensor = nullptr;
   int32_t n_chunks = 0;
+  int32_t per_warp = 0;    // J
+  int32_t smem = 0;
   qmuon_state_kind state = QMUON_STATE_F32;
 };
 
@@ -523,7 +750,7 @@ extern "C" qmuon_status qmuon_adamw_plan_create(const qmuon_adamw_tensor* tensor
     *out = nullptr;
     if (!tensors || n <= 0 || (state != QMUON_STATE_F32 && state != QMUON_STATE_E4M3)) return QMUON_ERR_INVALID_ARGUMENT;
     const bool f32 = state == QMUON_STATE_F32;
-    Chunks ch;
+    bool f32_grads = false;
     std::vector<AdamTensor> ts;
     for (int32_t i = 0; i < n; ++i) {
       const qmuon_adamw_tensor& t = tensors[i];
@@ -537,31 +764,64 @@ extern "C" qmuon_status qmuon_adamw_plan_create(const qmuon_adamw_tensor* tensor
       if (!is_aligned(t.m, f32 ? 4 : 16) || !is_aligned(t.v, f32 ? 4 : 16)) return QMUON_ERR_INVALID_ARGUMENT;
       if (!f32 && (!t.m_absmax || !t.v_absmax || !is_aligned(t.m_absmax, 4) || !is_aligned(t.v_absmax, 4)))
         return QMUON_ERR_INVALID_ARGUMENT;
-      if (!ch.add(t.numel, kAdamChunk)) return QMUON_ERR_INVALID_ARGUMENT;
+      // fp32 states: arrays that are slices of flat buffers at one element offset become aligned together after a
+      // head of up to three elements (8-bit blocks count from the first element and start on 16 bytes)
+      int begin = 0;
+      bool vec = false;
+      for (; !vec && begin < (f32 ? 4 : 1); ++begin) {
+        auto at = [&](const void* p, size_t es) { return reinterpret_cast<uintptr_t>(p) - begin * es; };
+        vec = at(t.param, 4) % 16 == 0 && at(t.grad, gs) % (f32 ? 4 * gs : 16) == 0 && (!t.copy || at(t.copy, 2) % 8 == 0) &&
+              (!f32 || (at(t.m, 4) % 16 == 0 && at(t.v, 4) % 16 == 0));
+      }
+      begin = vec ? begin - 1 : 0;
+      auto back = [&](auto* p, size_t es) {
+        return p ? reinterpret_cast<decltype(p)>(reinterpret_cast<uintptr_t>(p) - begin * es) : nullptr;
+      };
       AdamTensor a{};
-      a.param = t.param;
-      a.grad = t.grad;
-      a.copy = t.copy;
-      a.m = t.m;
-      a.v = t.v;
+      a.param = back(t.param, 4);
+      a.grad = back(t.grad, gs);
+      a.copy = back(t.copy, 2);
+      a.m = back(t.m, 4);
+      a.v = back(t.v, 4);
       a.m_absmax = t.m_absmax;
       a.v_absmax = t.v_absmax;
-      a.numel = t.numel;
+      a.begin = begin;
+      a.end = t.numel + begin;
       a.lr_scale = t.lr_scale;
       a.weight_decay = t.weight_decay;
-      a.first_chunk = ch.first.back();
       a.index = i;
       a.grad_dtype = (int16_t)t.grad_dtype;
       a.copy_dtype = (int16_t)t.copy_dtype;
-      a.vec = is_aligned(t.param, 16) && is_aligned(t.grad, 4 * gs) && is_aligned(t.copy, 8) && is_aligned(t.m, 16) &&
-              is_aligned(t.v, 16);
+      a.vec = vec;
+      f32_grads = f32_grads || t.grad_dtype == QMUON_FP32;
       ts.push_back(a);
     }
     if (ts.empty()) return QMUON_ERR_INVALID_ARGUMENT;
     std::unique_ptr<qmuon_adamw_plan> P(new qmuon_adamw_plan);
     P->state = state;
+    int64_t chunk = kAdamChunk;
+    cudaError_t e = cudaSuccess;
+    if (!f32) {
+      int dev = 0, sms = 0;
+      e = cudaGetDevice(&dev);
+      if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+      int64_t many = 0;
+      for (const AdamTensor& a : ts) many += (a.end + kManyBlocks * kWarps * kBlock - 1) / (kManyBlocks * kWarps * kBlock);
+      P->per_warp = many >= 2 * (int64_t)sms ? kManyBlocks : 1;
+      chunk = (int64_t)P->per_warp * kWarps * kBlock;
+      P->smem = P->per_warp * kWarps * (int)(f32_grads ? sizeof(E4m3Stage<QMUON_FP32>) : sizeof(E4m3Stage<QMUON_BF16>));
+      for (int sr = 0; sr < 2 && e == cudaSuccess; ++sr)
+        e = cudaFuncSetAttribute(adam_kernel(state, sr != 0, P->per_warp), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kManyBlocks * kWarps * (int)sizeof(E4m3Stage<QMUON_FP32>));
+      if (e != cudaSuccess) return set_error("qmuon_adamw_plan_create (device)", e);
+    }
+    Chunks ch;
+    for (AdamTensor& a : ts) {
+      if (!ch.add(a.end, chunk)) return QMUON_ERR_INVALID_ARGUMENT;
+      a.first_chunk = ch.first.back();
+    }
     P->n_chunks = (int32_t)ch.tensor.size();
-    const cudaError_t e = upload(ts, ch.tensor, &P->table, &P->tensors, &P->chunk_tensor);
+    e = upload(ts, ch.tensor, &P->table, &P->tensors, &P->chunk_tensor);
     if (e != cudaSuccess) return set_error("qmuon_adamw_plan_create (tables)", e);
     *out = P.release();
     return QMUON_OK;
@@ -581,7 +841,7 @@ qmuon_status adamw_step(const char* where, const qmuon_adamw_plan* plan, int64_t
   if (!plan || t < 1 || !is_aligned(grad_scale, 4)) return QMUON_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
     return QMUON_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(eps) || !((float)eps > 0.0f)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(eps) || !((float)eps >= FLT_MIN)) return QMUON_ERR_INVALID_ARGUMENT;
   if (sr && plan->state != QMUON_STATE_E4M3) return QMUON_ERR_UNSUPPORTED;
   AdamLaunch L{};
   L.tensors = plan->tensors;
@@ -595,13 +855,10 @@ qmuon_status adamw_step(const char* where, const qmuon_adamw_plan* plan, int64_t
   L.rbc1 = (float)(1.0 / (1.0 - std::pow(beta1, (double)t)));
   L.rbc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)t)));
   L.eps = (float)eps;
-  L.key0 = (uint32_t)seed;
-  L.key1 = (uint32_t)(seed >> 32);
+  L.keys.set(seed);
   L.step = (uint32_t)t;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (plan->state == QMUON_STATE_F32) adamw_f32_kernel<<<plan->n_chunks, kThreads, 0, s>>>(L);
-  else if (sr) adamw_e4m3_kernel<true><<<plan->n_chunks, kThreads, 0, s>>>(L);
-  else adamw_e4m3_kernel<false><<<plan->n_chunks, kThreads, 0, s>>>(L);
+  adam_kernel(plan->state, sr, plan->per_warp)<<<plan->n_chunks, kThreads, plan->smem, s>>>(L);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QMUON_OK : set_error(where, e);
 }

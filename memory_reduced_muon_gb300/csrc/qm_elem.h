@@ -42,33 +42,72 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A 16-byte vector of DT as fp32 values: 8 of a 16-bit type, 4 of fp32.
+// A 16-byte vector of DT as fp32 pairs: 8 values of a 16-bit type, 4 of fp32.
 template <int DT>
 struct Vec16 {
   static constexpr int kElems = 16 / elem_size(DT);
-  __device__ __forceinline__ static void unpack(const uint4& v, float* f) {
+  static constexpr int kPairs = kElems / 2;
+  __device__ __forceinline__ static void unpack(const uint4& v, float2* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == QMUON_FP32) {
+      f[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      f[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == QMUON_FP32) {
-        f[i] = __uint_as_float(w[i]);
-      } else {
-        const float2 t = unpack2<DT>(w[i]);
-        f[2 * i] = t.x;
-        f[2 * i + 1] = t.y;
-      }
+      for (int i = 0; i < 4; ++i) f[i] = unpack2<DT>(w[i]);
     }
   }
-  __device__ __forceinline__ static uint4 pack(const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == QMUON_FP32) w[i] = __float_as_uint(f[i]);
-      else w[i] = pack2<DT>(f[2 * i], f[2 * i + 1]);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  __device__ __forceinline__ static uint4 pack(const float2* f) {
+    if constexpr (DT == QMUON_FP32)
+      return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    else
+      return make_uint4(pack2<DT>(f[0].x, f[0].y), pack2<DT>(f[1].x, f[1].y), pack2<DT>(f[2].x, f[2].y),
+                        pack2<DT>(f[3].x, f[3].y));
   }
 };
+
+// Products of fp32 pairs in one instruction, each rounded to nearest as
+// __fmul_rn rounds it.  A packed product is never added packed: that sum could
+// be contracted into one rounding.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+      "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return mul2(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+      "add.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\tmov.b64 pc, {%6, %7};\n\t"
+      "fma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// Asynchronous copies of the calling thread into shared memory.
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Two E4M3 codes (the low one first) from fp32, nearest even, |x| > 448
 // saturating, NaN to 0x7F; and back, exactly.
@@ -98,15 +137,22 @@ __device__ __forceinline__ float e8m0_inverse(int byte) {
 }
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
-// easy as 1, 2, 3", SC'11).
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+// easy as 1, 2, 3", SC'11) under the round keys of a seed, made on the host.
+struct PhiloxKeys {
+  uint32_t k[10][2];
+  void set(uint64_t seed) {
+    for (int r = 0; r < 10; ++r) {
+      k[r][0] = (uint32_t)seed + (uint32_t)r * 0x9E3779B9u;
+      k[r][1] = (uint32_t)(seed >> 32) + (uint32_t)r * 0xBB67AE85u;
+    }
+  }
+};
+__device__ __forceinline__ uint4 philox(uint4 c, const PhiloxKeys& key) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint32_t hi0 = __umulhi(0xD2511F53u, c.x), lo0 = 0xD2511F53u * c.x;
-    const uint32_t hi1 = __umulhi(0xCD9E8D57u, c.z), lo1 = 0xCD9E8D57u * c.z;
-    c = make_uint4(hi1 ^ c.y ^ k0, lo1, hi0 ^ c.w ^ k1, lo0);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+    const uint64_t p0 = (uint64_t)0xD2511F53u * c.x, p1 = (uint64_t)0xCD9E8D57u * c.z;
+    c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ key.k[r][0], (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ key.k[r][1],
+                   (uint32_t)p0);
   }
   return c;
 }

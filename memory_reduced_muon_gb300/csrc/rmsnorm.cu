@@ -5,20 +5,23 @@
 //   a = dy * gain, n = h inv: dx = inv (a - n mean(a n)) + dsum
 //                             dgain = sum over rows of dy n
 //
-// A row is held in registers by T threads (a power of two up to a warp, or
-// whole warps), V vectors of 16 bytes each, from its loads to its stores, so
-// that every array crosses HBM once.  Rows that start off a 16-byte boundary
-// are moved element by element; rows longer than the registers of 1024
-// threads hold are read twice.
+// A row belongs to T threads: a power of two up to a warp (and a CTA then takes
+// several rows), or whole warps.  Rows that start on 16 bytes and fit their
+// threads' registers cross HBM once ("rows" kernels).  All others are walked
+// twice by the "walk" kernels, the second time out of the caches: in 16-byte
+// vectors where they are only long, in pairs of 16-bit elements where all
+// arrays' rows start alike within 4 bytes, else by single elements.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <set>
+#include <type_traits>
+#include <utility>
 
 #include "qm_elem.h"
 
 namespace qm {
 namespace {
-
-constexpr int kMaxT = 1024;
 
 struct FwdArgs {
   const void* x;
@@ -29,7 +32,7 @@ struct FwdArgs {
   uint8_t* payload;       // MXFP8 output, or null
   uint8_t* scale;
   int64_t rows, ld_x, ld_residual, ld_sum, ld_y;
-  int32_t cols;
+  int32_t cols, vec;
   float eps, inv_cols;
 };
 
@@ -41,270 +44,361 @@ struct BwdArgs {
   void* dx;
   float* partial;         // [grid][cols]
   int64_t rows, ld_dy, ld_h, ld_dsum, ld_dx;
-  int32_t cols;
+  int32_t cols, vec;
   float eps, inv_cols;
 };
 
-// VEC consecutive elements (one 16-byte vector, or one element) at index i.
-template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const void* row, int i, float* f) {
-  if constexpr (VEC == 1) f[0] = load_elem<DT>(row, i);
-  else Vec16<DT>::unpack(reinterpret_cast<const uint4*>(row)[i], f);
-}
-template <int DT, int VEC>
-__device__ __forceinline__ void store_vec(void* row, int i, const float* f) {
-  if constexpr (VEC == 1) store_elem<DT>(row, i, f[0]);
-  else reinterpret_cast<uint4*>(row)[i] = Vec16<DT>::pack(f);
-}
-template <int DT>
-__device__ __forceinline__ const void* row_of(const void* base, int64_t row, int64_t ld) {
-  return static_cast<const unsigned char*>(base) + row * ld * elem_size(DT);
-}
-template <int DT>
-__device__ __forceinline__ void* row_of(void* base, int64_t row, int64_t ld) {
-  return static_cast<unsigned char*>(base) + row * ld * elem_size(DT);
-}
-template <int VEC>
-__device__ __forceinline__ void load_gain(const float* gain, int i, float* f) {
-  if constexpr (VEC == 1) {
-    f[0] = __ldg(gain + i);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC; j += 4) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(gain + (int64_t)i * VEC + j));
-      f[j] = t.x, f[j + 1] = t.y, f[j + 2] = t.z, f[j + 3] = t.w;
-    }
-  }
+template <int DT, class P>
+__device__ __forceinline__ auto row_of(P* base, int64_t row, int64_t ld) {
+  using B = std::conditional_t<std::is_const_v<P>, const unsigned char, unsigned char>;
+  return static_cast<B*>(base) + row * ld * elem_size(DT);
 }
 
-// Sum of v over the T threads of a row (the same in all of them).  T > 32:
-// `part` is one float per warp; the caller alternates two of them, so that one
+// Sum of v over the T threads of a row, the same bits in all of them.  T > 32:
+// `part` is one value per warp; callers alternate two of them, so that one
 // barrier per sum is enough.
-__device__ __forceinline__ float row_sum(float v, int T, float* part) {
-  for (int o = min(T, 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float lane_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ float2 lane_xor(float2 v, int o) { return make_float2(lane_xor(v.x, o), lane_xor(v.y, o)); }
+
+template <class S>
+__device__ __forceinline__ S row_sum(S v, int T, S* part) {
+  for (int o = min(T, 32) >> 1; o > 0; o >>= 1) v = plus(v, lane_xor(v, o));
   if (T <= 32) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = T >> 5;
   if (lane == 0) part[warp] = v;
   __syncthreads();
-  v = lane < nw ? part[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  v = lane < nw ? part[lane] : S{};
+  for (int o = 16; o > 0; o >>= 1) v = plus(v, lane_xor(v, o));
   return v;
 }
 
-// The MXFP8 codes of VEC values held by a thread whose neighbours hold the
-// rest of the 32-element block; every thread of the warp calls it.
-template <int DT, int VEC>
+__device__ __forceinline__ float inverse_norm(float sumsq, float inv_cols, float eps) {
+  return __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sumsq, inv_cols, eps)));
+}
+
+// The MXFP8 codes of N values held by a thread whose neighbours hold the rest
+// of the 32-element block; every thread of the warp calls it.
+template <int N>
 __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t e, uint8_t* payload, uint8_t* scale) {
   float amax = 0.0f;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) amax = fmaxf(amax, valid ? fabsf(y[j]) : 0.0f);
+  for (int j = 0; j < N; ++j) amax = fmaxf(amax, fabsf(y[j]));
+  if (!valid) amax = 0.0f;
 #pragma unroll
-  for (int o = 16 / VEC; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 16 / N; o > 0; o >>= 1) amax = fmaxf(amax, lane_xor(amax, o));
   const int byte = e8m0_byte(amax);
   const float mult = e8m0_inverse(byte);
   if (!valid) return;
-  if constexpr (VEC == 1) {
+  if constexpr (N == 1) {
     payload[e] = (uint8_t)e4m3x2_of(__fmul_rn(y[0], mult), 0.0f);
   } else {
-    uint32_t w[VEC / 4];
+    uint32_t w[N / 4];
 #pragma unroll
-    for (int j = 0; j < VEC / 4; ++j)
-      w[j] = e4m3x2_of(__fmul_rn(y[4 * j], mult), __fmul_rn(y[4 * j + 1], mult)) |
-             (e4m3x2_of(__fmul_rn(y[4 * j + 2], mult), __fmul_rn(y[4 * j + 3], mult)) << 16);
-    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(payload + e) = make_uint2(w[0], w[1]);
+    for (int j = 0; j < N / 4; ++j) {
+      const float2 a = mul2(make_float2(y[4 * j], y[4 * j + 1]), mult), b = mul2(make_float2(y[4 * j + 2], y[4 * j + 3]), mult);
+      w[j] = e4m3x2_of(a.x, a.y) | (e4m3x2_of(b.x, b.y) << 16);
+    }
+    if constexpr (N == 8) *reinterpret_cast<uint2*>(payload + e) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(payload + e) = w[0];
   }
   if ((e & 31) == 0) scale[e >> 5] = (uint8_t)byte;
 }
 
-// blockDim = (T, rows per CTA); T > 32 has one row per CTA.
-template <int DT, int VEC, int V, bool MX>
-__global__ void __launch_bounds__(kMaxT) rmsnorm_fwd_kernel(const __grid_constant__ FwdArgs A) {
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+// blockDim = (T, rows per CTA); V 16-byte vectors per thread.
+constexpr int fwd_max_threads(int V) { return V == 4 ? 512 : 1024; }
+
+template <int DT, int V, bool RES, bool MX>
+__global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(const __grid_constant__ FwdArgs A) {
+  using X = Vec16<DT>;
+  constexpr int P = X::kPairs;
   __shared__ float part[2][32];
   const int T = blockDim.x, t = threadIdx.x;
-  const int nv = A.cols / VEC;
+  const int nv = A.cols / X::kElems;
   int flip = 0;
-  // rows per pass are the same for the whole grid, so every thread of a warp leaves the loop together
-  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
-    const int64_t row = r0 + threadIdx.y;
-    const bool live = row < A.rows;
-    const int n = live ? nv : 0;
-    const void* x = row_of<DT>(A.x, row, A.ld_x);
-    float h[V][VEC];
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int k = i * T + t;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) h[i][j] = 0.0f;
-      if (k < n) load_vec<DT, VEC>(x, k, h[i]);
-    }
-    if (A.residual) {
-      const void* res = row_of<DT>(A.residual, row, A.ld_residual);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int k = i * T + t;
-        if (k < n) {
-          float f[VEC];
-          load_vec<DT, VEC>(res, k, f);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) h[i][j] += f[j];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss = fmaf(h[i][j], h[i][j], ss);
-    if (A.sum) {
-      void* sum = row_of<DT>(A.sum, row, A.ld_sum);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i * T + t < n) store_vec<DT, VEC>(sum, i * T + t, h[i]);
-    }
-    ss = row_sum(ss, T, part[flip]);
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, A.inv_cols, A.eps)));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int k = i * T + t;
-      float g[VEC];
-      if (k < n) {
-        load_gain<VEC>(A.gain, k, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i][j] = h[i][j] * inv * g[j];
-        if (A.y) store_vec<DT, VEC>(row_of<DT>(A.y, row, A.ld_y), k, h[i]);
-      }
-      if constexpr (MX) store_mxfp8<DT, VEC>(h[i], k < n, row * A.cols + (int64_t)k * VEC, A.payload, A.scale);
-    }
-  }
-}
-
-// Rows that do not fit the registers of a CTA: read for the sum, and again for the output.
-template <int DT, int VEC, bool MX>
-__global__ void __launch_bounds__(kMaxT) rmsnorm_fwd_long_kernel(const __grid_constant__ FwdArgs A) {
-  __shared__ float part[2][32];
-  const int T = blockDim.x, t = threadIdx.x;
-  const int nv = A.cols / VEC;
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
-    const void* x = row_of<DT>(A.x, row, A.ld_x);
-    const void* res = row_of<DT>(A.residual, row, A.ld_residual);
-    auto load = [&](int k, float* h) {
-      load_vec<DT, VEC>(x, k, h);
-      if (A.residual) {
-        float f[VEC];
-        load_vec<DT, VEC>(res, k, f);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] += f[j];
-      }
-    };
-    float ss = 0.0f;
-    for (int k = t; k < nv; k += T) {
-      float h[VEC];
-      load(k, h);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss = fmaf(h[j], h[j], ss);
-    }
-    ss = row_sum(ss, T, part[flip]);
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, A.inv_cols, A.eps)));
-    for (int k0 = 0; k0 < nv; k0 += T) {   // the same number of passes in every thread
-      const int k = k0 + t;
-      float h[VEC] = {}, g[VEC];
-      if (k < nv) {
-        load(k, h);
-        if (A.sum) store_vec<DT, VEC>(row_of<DT>(A.sum, row, A.ld_sum), k, h);
-        load_gain<VEC>(A.gain, k, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = h[j] * inv * g[j];
-        if (A.y) store_vec<DT, VEC>(row_of<DT>(A.y, row, A.ld_y), k, h);
-      }
-      if constexpr (MX) store_mxfp8<DT, VEC>(h, k < nv, row * A.cols + (int64_t)k * VEC, A.payload, A.scale);
-    }
-  }
-}
-
-// Two sums over the T threads of a row.
-__device__ __forceinline__ float2 row_sum2(float2 v, int T, float2* part) {
-  for (int o = min(T, 32) >> 1; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if (T <= 32) return v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = T >> 5;
-  if (lane == 0) part[warp] = v;
-  __syncthreads();
-  v = lane < nw ? part[lane] : make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  return v;
-}
-
-// The backward pass: a CTA's threads keep the gain of their columns and its
-// gradient over all rows of the CTA, which then leaves as one row of
-// `partial`; dgain_kernel adds those rows in order.
-template <int DT, int VEC, int V>
-__global__ void __launch_bounds__(V * VEC >= 16 ? 512 : kMaxT) rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs A) {
-  __shared__ float2 part[2][32];
-  extern __shared__ float s_gain[];   // T <= 32: [rows per CTA][cols]
-  const int T = blockDim.x, t = threadIdx.x;
-  const int nv = A.cols / VEC;
-  float acc[V][VEC], gain[V][VEC];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[i][j] = gain[i][j] = 0.0f;
-    if (i * T + t < nv) load_gain<VEC>(A.gain, i * T + t, gain[i]);
-  }
-  int flip = 0;
+  // every thread of a warp leaves the loop together: the CTA's rows of one pass are one step of it
   for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
     const int64_t row = r0 + threadIdx.y;
     const int n = row < A.rows ? nv : 0;
-    const void* hp = row_of<DT>(A.h, row, A.ld_h);
-    const void* dp = row_of<DT>(A.dy, row, A.ld_dy);
-    float h[V][VEC], d[V][VEC];
-    float2 s = make_float2(0.0f, 0.0f);   // sum h^2, sum a h
+    const uint4* x = reinterpret_cast<const uint4*>(row_of<DT>(A.x, row, A.ld_x)) + t;
+    const uint4* res = reinterpret_cast<const uint4*>(row_of<DT>(A.residual, row, A.ld_residual)) + t;
+    uint4 rx[V], rr[RES ? V : 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) rx[i] = i * T + t < n ? x[i * T] : make_uint4(0, 0, 0, 0);
+    if constexpr (RES)
+#pragma unroll
+      for (int i = 0; i < V; ++i) rr[i] = i * T + t < n ? res[i * T] : make_uint4(0, 0, 0, 0);
+    float2 h[V][P], ss = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      X::unpack(rx[i], h[i]);
+      if constexpr (RES) {
+        float2 f[P];
+        X::unpack(rr[i], f);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) h[i][j] = d[i][j] = 0.0f;
-      if (i * T + t < n) {
-        load_vec<DT, VEC>(hp, i * T + t, h[i]);
-        load_vec<DT, VEC>(dp, i * T + t, d[i]);
+        for (int j = 0; j < P; ++j) h[i][j] = add2(h[i][j], f[j]);
       }
+#pragma unroll
+      for (int j = 0; j < P; ++j) ss = fma2(h[i][j], h[i][j], ss);
     }
+    if (A.sum) {
+      uint4* sum = reinterpret_cast<uint4*>(row_of<DT>(A.sum, row, A.ld_sum)) + t;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i * T + t < n) sum[i * T] = X::pack(h[i]);
+    }
+    const float inv = inverse_norm(row_sum(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
+    const float4* gain = reinterpret_cast<const float4*>(A.gain) + t * (P / 2);
+    uint4* y = reinterpret_cast<uint4*>(row_of<DT>(A.y, row, A.ld_y)) + t;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool in = i * T + t < n;
+      if (in) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+          const float4 g = __ldg(gain + i * T * (P / 2) + j / 2);
+          h[i][j] = mul2(mul2(h[i][j], inv), make_float2(g.x, g.y));
+          h[i][j + 1] = mul2(mul2(h[i][j + 1], inv), make_float2(g.z, g.w));
+        }
+        if (!MX || A.y) y[i * T] = X::pack(h[i]);
+      }
+      if constexpr (MX)
+        store_mxfp8<2 * P>(reinterpret_cast<const float*>(h[i]), in, row * A.cols + (int64_t)(i * T + t) * X::kElems, A.payload,
+                           A.scale);
+    }
+  }
+}
+
+// N consecutive elements of a row at column c, moved at once.
+template <int DT, int N>
+__device__ __forceinline__ void load_n(const void* row, int c, float* f) {
+  if constexpr (N == 1) {
+    f[0] = load_elem<DT>(row, c);
+  } else if constexpr (N == 2) {
+    const float2 t = unpack2<DT>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + c));
+    f[0] = t.x, f[1] = t.y;
+  } else {
+    Vec16<DT>::unpack(reinterpret_cast<const uint4*>(row)[c / N], reinterpret_cast<float2*>(f));
+  }
+}
+template <int DT, int N>
+__device__ __forceinline__ void store_n(void* row, int c, const float* f) {
+  if constexpr (N == 1) store_elem<DT>(row, c, f[0]);
+  else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(row) + c) = pack2<DT>(f[0], f[1]);
+  else reinterpret_cast<uint4*>(row)[c / N] = Vec16<DT>::pack(reinterpret_cast<const float2*>(f));
+}
+
+// Calls f(column, constant count) for the pieces of a row that thread t of T
+// moves: vectors; pairs from column `head` (0 or 1) on, with single elements at
+// the ends; or single elements.  `how`: 0 single, 1 pairs, 2 vectors.
+template <int DT, class F>
+__device__ __forceinline__ void walk_row(int cols, int how, int head, int T, int t, F&& f) {
+  constexpr int K = Vec16<DT>::kElems;
+  if (cols == 0) return;   // a row past the last one: its ends are not there either
+  if (how == 2) {
+#pragma unroll 4
+    for (int c = t * K; c < cols; c += T * K) f(c, std::integral_constant<int, K>{});
+    return;
+  }
+  if constexpr (DT != QMUON_FP32) {
+    if (how == 1) {
+#pragma unroll 4
+      for (int c = head + 2 * t; c + 1 < cols; c += 2 * T) f(c, std::integral_constant<int, 2>{});
+      if (t == 0 && head) f(0, std::integral_constant<int, 1>{});
+      if (t == T - 1 && ((cols - head) & 1)) f(cols - 1, std::integral_constant<int, 1>{});
+      return;
+    }
+  }
+#pragma unroll 4
+  for (int c = t; c < cols; c += T) f(c, std::integral_constant<int, 1>{});
+}
+
+// How a row whose arrays start at these addresses can be walked: `how` for
+// walk_row, and in `head` the column where pairs start.
+template <int DT>
+__device__ __forceinline__ int row_kind(bool vec, int* head, const void* a, const void* b, const void* c, const void* d) {
+  *head = 0;
+  if (vec) return 2;
+  if (DT == QMUON_FP32) return 0;
+  auto bits = [](const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p) & 3u; };
+  const uint32_t k = bits(a);
+  if ((b && bits(b) != k) || (c && bits(c) != k) || (d && bits(d) != k)) return 0;
+  *head = (int)(k >> 1);
+  return 1;
+}
+
+template <int DT, bool MX>
+__global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_constant__ FwdArgs A) {
+  __shared__ float part[2][32];
+  const int T = blockDim.x, t = threadIdx.x;
+  int flip = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
+    const int64_t row = r0 + threadIdx.y;
+    const int cols = row < A.rows ? A.cols : 0;
+    const void* x = row_of<DT>(A.x, row, A.ld_x);
+    const void* res = A.residual ? row_of<DT>(A.residual, row, A.ld_residual) : nullptr;
+    void* sum = A.sum ? row_of<DT>(A.sum, row, A.ld_sum) : nullptr;
+    void* y = A.y ? row_of<DT>(A.y, row, A.ld_y) : nullptr;
+    int head = 0;
+    const int how = MX ? (A.vec ? 2 : 0) : row_kind<DT>(A.vec, &head, x, res, sum, y);
+    auto load = [&](int c, auto n, float* h) {
+      constexpr int N = decltype(n)::value;
+      load_n<DT, N>(x, c, h);
+      if (res) {
+        float f[N];
+        load_n<DT, N>(res, c, f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[j] += f[j];
+      }
+    };
+    float ss = 0.0f;
+    walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
+      constexpr int N = decltype(n)::value;
+      float h[N];
+      load(c, n, h);
+#pragma unroll
+      for (int j = 0; j < N; ++j) ss = fmaf(h[j], h[j], ss);
+    });
+    const float inv = inverse_norm(row_sum(ss, T, part[flip]), A.inv_cols, A.eps);
+    auto finish = [&](int c, auto n, float* h) {
+      constexpr int N = decltype(n)::value;
+      load(c, n, h);
+      if (sum) store_n<DT, N>(sum, c, h);
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[j] = h[j] * inv * __ldg(A.gain + c + j);
+      if (y) store_n<DT, N>(y, c, h);
+    };
+    if constexpr (!MX) {
+      walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
+      constexpr int N = decltype(n)::value;
+        float h[N];
+        finish(c, n, h);
+      });
+    } else {
+      // the same number of passes in every thread of a warp: its lanes share scales
+      constexpr int K = Vec16<DT>::kElems;
+      auto pass = [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        for (int c0 = 0; c0 < A.cols; c0 += T * N) {
+          const int c = c0 + t * N;
+          float h[N] = {};
+          if (c < cols) finish(c, n, h);
+          store_mxfp8<N>(h, c < cols, row * A.cols + c, A.payload, A.scale);
+        }
+      };
+      if (how == 2) pass(std::integral_constant<int, K>{});
+      else pass(std::integral_constant<int, 1>{});
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// A CTA walks over rows and keeps the gradient of the gain of its threads'
+// columns, which leaves as one row of `partial`; dgain_kernel adds those rows
+// in order.  The next rows come through a ring of shared-memory slots, each
+// thread's own, `stages` rows ahead.
+constexpr int bwd_max_threads(int V) { return V == 8 ? 512 : 256; }
+
+__device__ __forceinline__ void wait_rows(int pending) {
+  if (pending >= 2) async_wait<2>();
+  else if (pending == 1) async_wait<1>();
+  else async_wait<0>();
+}
+
+template <int DT, int V, bool DSUM>
+__global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(const __grid_constant__ BwdArgs A, int stages) {
+  using X = Vec16<DT>;
+  constexpr int P = X::kPairs;
+  constexpr int kArrays = DSUM ? 3 : 2;
+  constexpr bool kKeepGain = V <= 4;   // in registers; else read again for each row
+  __shared__ float2 part[2][32];
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int T = blockDim.x, t = threadIdx.x, threads = T * blockDim.y, me = threadIdx.y * T + t;
+  uint4* ring = reinterpret_cast<uint4*>(smem) + me;   // [stages][kArrays][V][threads]
+  const int nv = A.cols / X::kElems;
+  const float4* gain = reinterpret_cast<const float4*>(A.gain) + t * (P / 2);
+  auto load_gain = [&](int i, float2* g) {
+#pragma unroll
+    for (int j = 0; j < P; j += 2) {
+      const float4 q = i * T + t < nv ? __ldg(gain + i * T * (P / 2) + j / 2) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      g[j] = make_float2(q.x, q.y);
+      g[j + 1] = make_float2(q.z, q.w);
+    }
+  };
+  float2 acc[V][P], kept[kKeepGain ? V : 1][P];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int j = 0; j < P; ++j) acc[i][j] = make_float2(0.0f, 0.0f);
+    if constexpr (kKeepGain) load_gain(i, kept[i]);
+  }
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  auto issue = [&](int64_t row, uint4* slot) {
+    if (row < A.rows) {
+      const uint4* src[3] = {reinterpret_cast<const uint4*>(row_of<DT>(A.h, row, A.ld_h)),
+                             reinterpret_cast<const uint4*>(row_of<DT>(A.dy, row, A.ld_dy)),
+                             DSUM ? reinterpret_cast<const uint4*>(row_of<DT>(A.dsum, row, A.ld_dsum)) : nullptr};
+#pragma unroll
+      for (int a = 0; a < kArrays; ++a)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i * T + t < nv) async16(slot + (a * V + i) * threads, src[a] + i * T + t);
+    }
+    async_commit();   // one group per row, empty past the end
+  };
+  const int64_t r0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  for (int s = 0; s < stages; ++s) issue(r0 + s * step, ring + s * kArrays * V * threads);
+  int flip = 0, s = 0;
+  // the same number of passes in every thread of the CTA
+  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < A.rows; base += step, flip ^= 1) {
+    const int64_t row = base + threadIdx.y;
+    const int n = row < A.rows ? nv : 0;
+    uint4* slot = ring + s * kArrays * V * threads;
+    wait_rows(stages - 1);
+    float2 sh = make_float2(0.0f, 0.0f), sa = sh;   // sums of h^2 and a h
 #pragma unroll
     for (int i = 0; i < V; ++i)
+      if (i * T + t < n) {
+        float2 h[P], d[P], g[P];
+        X::unpack(slot[i * threads], h);
+        X::unpack(slot[(V + i) * threads], d);
+        if constexpr (!kKeepGain) load_gain(i, g);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        s.x = fmaf(h[i][j], h[i][j], s.x);
-        s.y = fmaf(d[i][j] * gain[i][j], h[i][j], s.y);
-      }
-    s = row_sum2(s, T, part[flip]);
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(s.x, A.inv_cols, A.eps)));
-    const float c = s.y * A.inv_cols * inv * inv;   // mean(a h) inv^2
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int k = i * T + t;
-      if (k < n) {
-        float o[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          o[j] = inv * (d[i][j] * gain[i][j] - h[i][j] * c);
-          acc[i][j] = fmaf(d[i][j], h[i][j] * inv, acc[i][j]);
+        for (int j = 0; j < P; ++j) {
+          sh = fma2(h[j], h[j], sh);
+          sa = fma2(mul2(d[j], kKeepGain ? kept[i % V][j] : g[j]), h[j], sa);
         }
-        if (A.dsum) {
-          float f[VEC];
-          load_vec<DT, VEC>(row_of<DT>(A.dsum, row, A.ld_dsum), k, f);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) o[j] += f[j];
-        }
-        store_vec<DT, VEC>(row_of<DT>(A.dx, row, A.ld_dx), k, o);
       }
-    }
+    const float2 sum = row_sum(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
+    const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
+    const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
+    uint4* dx = reinterpret_cast<uint4*>(row_of<DT>(A.dx, row, A.ld_dx)) + t;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i * T + t < n) {
+        float2 h[P], d[P], o[P], g[P];
+        X::unpack(slot[i * threads], h);
+        X::unpack(slot[(V + i) * threads], d);
+        if constexpr (DSUM) X::unpack(slot[(2 * V + i) * threads], o);
+        if constexpr (!kKeepGain) load_gain(i, g);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float2 a = mul2(d[j], kKeepGain ? kept[i % V][j] : g[j]);
+          const float2 e = fma2(h[j], make_float2(c, c), a);
+          if constexpr (DSUM) o[j] = fma2(e, make_float2(inv, inv), o[j]);
+          else o[j] = mul2(e, inv);
+          acc[i][j] = fma2(d[j], mul2(h[j], inv), acc[i][j]);
+        }
+        dx[i * T] = X::pack(o);
+      }
+    issue(row + stages * step, slot);
+    s = s + 1 == stages ? 0 : s + 1;
   }
   float* out = A.partial + (int64_t)blockIdx.x * A.cols;
   if (T > 32) {
@@ -312,69 +406,92 @@ __global__ void __launch_bounds__(V * VEC >= 16 ? 512 : kMaxT) rmsnorm_bwd_kerne
     for (int i = 0; i < V; ++i)
       if (i * T + t < nv)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) out[(i * T + t) * VEC + j] = acc[i][j];
+        for (int j = 0; j < P; j += 2)
+          reinterpret_cast<float4*>(out)[(i * T + t) * (P / 2) + j / 2] =
+              make_float4(acc[i][j].x, acc[i][j].y, acc[i][j + 1].x, acc[i][j + 1].y);
     return;
   }
+  async_wait<0>();
+  __syncthreads();   // the ring is free
+  float* rows = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if (i * T + t < nv)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s_gain[threadIdx.y * A.cols + (i * T + t) * VEC + j] = acc[i][j];
+      for (int j = 0; j < P; ++j)
+        *reinterpret_cast<float2*>(rows + (size_t)threadIdx.y * A.cols + (i * T + t) * X::kElems + 2 * j) = acc[i][j];
   __syncthreads();
-  for (int c = threadIdx.y * T + t; c < A.cols; c += T * blockDim.y) {
+  for (int k = me; k < A.cols; k += threads) {
     float v = 0.0f;
-    for (int y = 0; y < blockDim.y; ++y) v += s_gain[y * A.cols + c];
-    out[c] = v;
+    for (int y = 0; y < (int)blockDim.y; ++y) v += rows[(size_t)y * A.cols + k];
+    out[k] = v;
   }
 }
 
-// Longer rows: each is read twice, and the CTA's row of `partial` holds its sums.
-template <int DT, int VEC>
-__global__ void __launch_bounds__(kMaxT) rmsnorm_bwd_long_kernel(const __grid_constant__ BwdArgs A) {
+// The gain's gradient lies in shared memory, a row for each of the CTA's, or,
+// where it does not fit, in the CTA's row of `partial`.
+template <int DT>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_constant__ BwdArgs A, int in_smem) {
   __shared__ float2 part[2][32];
+  extern __shared__ __align__(16) unsigned char smem[];
   const int T = blockDim.x, t = threadIdx.x;
-  const int nv = A.cols / VEC;
   float* out = A.partial + (int64_t)blockIdx.x * A.cols;
+  float* acc = in_smem ? reinterpret_cast<float*>(smem) + (size_t)threadIdx.y * A.cols : out;
+  for (int c = t; c < A.cols; c += T) acc[c] = 0.0f;
+  if (T > 32) __syncthreads();
+  else __syncwarp();
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
+  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < A.rows; base += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
+    const int64_t row = base + threadIdx.y;
+    const int cols = row < A.rows ? A.cols : 0;
     const void* hp = row_of<DT>(A.h, row, A.ld_h);
     const void* dp = row_of<DT>(A.dy, row, A.ld_dy);
-    float2 s = make_float2(0.0f, 0.0f);
-    for (int k = t; k < nv; k += T) {
-      float h[VEC], d[VEC], g[VEC];
-      load_vec<DT, VEC>(hp, k, h);
-      load_vec<DT, VEC>(dp, k, d);
-      load_gain<VEC>(A.gain, k, g);
+    const void* sp = A.dsum ? row_of<DT>(A.dsum, row, A.ld_dsum) : nullptr;
+    void* dx = row_of<DT>(A.dx, row, A.ld_dx);
+    int head = 0;
+    const int how = row_kind<DT>(A.vec, &head, hp, dp, sp, dx);
+    float2 s = make_float2(0.0f, 0.0f);   // sums of h^2 and a h
+    walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
+      constexpr int N = decltype(n)::value;
+      float h[N], d[N];
+      load_n<DT, N>(hp, c, h);
+      load_n<DT, N>(dp, c, d);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < N; ++j) {
         s.x = fmaf(h[j], h[j], s.x);
-        s.y = fmaf(d[j] * g[j], h[j], s.y);
+        s.y = fmaf(d[j] * __ldg(A.gain + c + j), h[j], s.y);
       }
-    }
-    s = row_sum2(s, T, part[flip]);
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(s.x, A.inv_cols, A.eps)));
-    const float c = s.y * A.inv_cols * inv * inv;
-    const bool first = row == blockIdx.x;
-    for (int k = t; k < nv; k += T) {
-      float h[VEC], d[VEC], g[VEC], o[VEC];
-      load_vec<DT, VEC>(hp, k, h);
-      load_vec<DT, VEC>(dp, k, d);
-      load_gain<VEC>(A.gain, k, g);
+    });
+    // A column may be another thread's than in the row before: the barrier (the shuffles, within a warp) orders the two.
+    s = row_sum(s, T, part[flip]);
+    if (T <= 32) __syncwarp();
+    const float inv = inverse_norm(s.x, A.inv_cols, A.eps);
+    const float k = s.y * A.inv_cols * inv * inv;
+    walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
+      constexpr int N = decltype(n)::value;
+      float h[N], d[N], o[N];
+      load_n<DT, N>(hp, c, h);
+      load_n<DT, N>(dp, c, d);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        o[j] = inv * (d[j] * g[j] - h[j] * c);
-        const float v = d[j] * (h[j] * inv);
-        float* a = out + (int64_t)k * VEC + j;
-        *a = first ? v : *a + v;   // this thread's column in every row
+      for (int j = 0; j < N; ++j) {
+        o[j] = inv * (d[j] * __ldg(A.gain + c + j) - h[j] * k);
+        acc[c + j] = fmaf(d[j], h[j] * inv, acc[c + j]);
       }
-      if (A.dsum) {
-        float f[VEC];
-        load_vec<DT, VEC>(row_of<DT>(A.dsum, row, A.ld_dsum), k, f);
+      if (sp) {
+        float f[N];
+        load_n<DT, N>(sp, c, f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] += f[j];
+        for (int j = 0; j < N; ++j) o[j] += f[j];
       }
-      store_vec<DT, VEC>(row_of<DT>(A.dx, row, A.ld_dx), k, o);
-    }
+      store_n<DT, N>(dx, c, o);
+    });
+  }
+  if (!in_smem) return;
+  __syncthreads();
+  for (int c = threadIdx.y * T + t; c < A.cols; c += T * blockDim.y) {
+    float v = 0.0f;
+    for (int y = 0; y < (int)blockDim.y; ++y) v += reinterpret_cast<const float*>(smem)[(size_t)y * A.cols + c];
+    out[c] = v;
   }
 }
 
@@ -400,27 +517,37 @@ __global__ void __launch_bounds__(1024) dgain_kernel(const float* partial, int32
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool is_dtype(int v) { return v == QMUON_BF16 || v == QMUON_FP16 || v == QMUON_FP32; }
 
-// Threads of a row and vectors per thread for nv vectors; V == 0: a long row.
+// Threads of a row and 16-byte vectors per thread, V being the largest allowed
+// that leaves a row at least eight threads (128 contiguous bytes per access),
+// or the smallest that fits.  V == 0: it does not fit.
 struct Shape {
   int T, V;
-  int rows_per_cta() const { return T >= 256 || T > 32 ? 1 : 256 / T; }
+  dim3 block() const { return dim3(T, T > 32 ? 1 : 256 / T); }
 };
 
-Shape pick_shape(int nv, const int* vs, int n_vs, int min_t, int want_v) {
-  for (int i = 0; i < n_vs; ++i) {
-    const int V = vs[i];
-    if (V < want_v && i + 1 < n_vs) continue;
+template <class MaxThreads>
+Shape pick_shape(int nv, int want, int most, MaxThreads max_threads) {
+  int V = want;
+  while (V > 1 && nv / V < 8) V /= 2;
+  for (; V <= most; V *= 2) {
     int T = (nv + V - 1) / V;
-    if (T <= 32) {
-      int p = min_t;
+    if (T > 32) {
+      T = (T + 31) / 32 * 32;
+    } else {
+      int p = 8;
       while (p < T) p *= 2;
       T = p;
-    } else {
-      T = (T + 31) / 32 * 32;
     }
-    if (T <= kMaxT) return {T, V};
+    if (T <= max_threads(V)) return {T, V};
   }
-  return {kMaxT, 0};
+  return {0, 0};
+}
+
+// Threads of a row that is walked in pieces: about four pieces per thread.
+int walk_threads(int64_t pieces) {
+  int T = 32;
+  while (T < 1024 && T * 4 < pieces) T *= 2;
+  return T;
 }
 
 int device_sms() {
@@ -430,62 +557,74 @@ int device_sms() {
   return sms;
 }
 
-template <int DT, int VEC, bool MX>
+// Lets a kernel have kMaxSmem bytes of dynamic shared memory on the current
+// device: once per kernel and device, so that calls can be captured.
+constexpr int kMaxSmem = 224 * 1024;
+cudaError_t allow_smem(const void* kernel) {
+  static std::mutex mu;
+  static std::set<std::pair<const void*, int>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({kernel, dev})) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess) done.insert({kernel, dev});
+  return e;
+}
+
+template <int DT, bool RES, bool MX>
 void launch_fwd(const FwdArgs& A, cudaStream_t s) {
-  const int nv = A.cols / VEC;
-  static const int vs16[] = {1, 2, 4}, vs1[] = {1, 4, 8};
-  const int min_t = !MX ? 1 : VEC == 1 ? 32 : 32 / VEC;
-  const Shape S = VEC == 1 ? pick_shape(nv, vs1, 3, min_t, 8) : pick_shape(nv, vs16, 3, min_t, 4);
-  const dim3 block(S.T, S.rows_per_cta());
-  const int64_t groups = (A.rows + block.y - 1) / block.y;
-  const unsigned grid = (unsigned)std::min<int64_t>(groups, ((int64_t)1 << 31) - 1);
-  if (S.V == 0) rmsnorm_fwd_long_kernel<DT, VEC, MX><<<grid, block, 0, s>>>(A);
-  else if (S.V == 1) rmsnorm_fwd_kernel<DT, VEC, 1, MX><<<grid, block, 0, s>>>(A);
-  else if constexpr (VEC == 1) {
-    if (S.V == 4) rmsnorm_fwd_kernel<DT, VEC, 4, MX><<<grid, block, 0, s>>>(A);
-    else rmsnorm_fwd_kernel<DT, VEC, 8, MX><<<grid, block, 0, s>>>(A);
-  } else {
-    if (S.V == 2) rmsnorm_fwd_kernel<DT, VEC, 2, MX><<<grid, block, 0, s>>>(A);
-    else rmsnorm_fwd_kernel<DT, VEC, 4, MX><<<grid, block, 0, s>>>(A);
-  }
+  const Shape S = A.vec ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 4, fwd_max_threads) : Shape{0, 0};
+  const dim3 block = S.V ? S.block() : Shape{walk_threads(A.cols / (A.vec ? Vec16<DT>::kElems : 2)), 0}.block();
+  const unsigned grid = (unsigned)std::min<int64_t>((A.rows + block.y - 1) / block.y, ((int64_t)1 << 31) - 1);
+  if (S.V == 1) rmsnorm_fwd_rows_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
+  else if (S.V == 2) rmsnorm_fwd_rows_kernel<DT, 2, RES, MX><<<grid, block, 0, s>>>(A);
+  else if (S.V == 4) rmsnorm_fwd_rows_kernel<DT, 4, RES, MX><<<grid, block, 0, s>>>(A);
+  else rmsnorm_fwd_walk_kernel<DT, MX><<<grid, block, 0, s>>>(A);
 }
-
 template <int DT>
-void launch_fwd_dt(const FwdArgs& A, bool vec, cudaStream_t s) {
-  constexpr int K = Vec16<DT>::kElems;
-  if (A.payload) {
-    if (vec) launch_fwd<DT, K, true>(A, s);
-    else launch_fwd<DT, 1, true>(A, s);
-  } else {
-    if (vec) launch_fwd<DT, K, false>(A, s);
-    else launch_fwd<DT, 1, false>(A, s);
-  }
+void launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
+  if (A.payload) A.residual ? launch_fwd<DT, true, true>(A, s) : launch_fwd<DT, false, true>(A, s);
+  else A.residual ? launch_fwd<DT, true, false>(A, s) : launch_fwd<DT, false, false>(A, s);
 }
 
-// CTAs of the backward pass: one row of `partial` each.
+// CTAs of the backward pass, each with its row of `partial`: at most four per SM.
 constexpr int kBwdPerSm = 4;
-int bwd_grid(int64_t rows, int sms) { return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), (int64_t)sms * kBwdPerSm); }
+int bwd_grid(int64_t groups, int sms, int per_sm) {
+  return (int)std::min<int64_t>(std::max<int64_t>(groups, 1), (int64_t)sms * std::min(std::max(per_sm, 1), kBwdPerSm));
+}
 
-template <int DT, int VEC>
-int launch_bwd(const BwdArgs& A, int sms, cudaStream_t s) {
-  const int nv = A.cols / VEC;
-  static const int vs16[] = {1, 2, 4}, vs1[] = {1, 4, 8};
-  const Shape S = VEC == 1 ? pick_shape(nv, vs1, 3, 1, 4) : pick_shape(nv, vs16, 3, 1, 2);
-  const bool too_wide = S.V * VEC >= 16 && S.T > 512;
-  const dim3 block(S.T, S.rows_per_cta());
-  const int64_t groups = (A.rows + block.y - 1) / block.y;
-  const int grid = bwd_grid(groups, sms);
-  const size_t smem = S.T > 32 ? 0 : (size_t)block.y * A.cols * 4;
-  if (S.V == 0 || too_wide) rmsnorm_bwd_long_kernel<DT, VEC><<<bwd_grid(A.rows, sms), kMaxT, 0, s>>>(A);
-  else if (S.V == 1) rmsnorm_bwd_kernel<DT, VEC, 1><<<grid, block, smem, s>>>(A);
-  else if constexpr (VEC == 1) {
-    if (S.V == 4) rmsnorm_bwd_kernel<DT, VEC, 4><<<grid, block, smem, s>>>(A);
-    else rmsnorm_bwd_kernel<DT, VEC, 8><<<grid, block, smem, s>>>(A);
-  } else {
-    if (S.V == 2) rmsnorm_bwd_kernel<DT, VEC, 2><<<grid, block, smem, s>>>(A);
-    else rmsnorm_bwd_kernel<DT, VEC, 4><<<grid, block, smem, s>>>(A);
-  }
-  return (S.V == 0 || too_wide) ? bwd_grid(A.rows, sms) : grid;
+template <int DT, int V, bool DSUM>
+cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* grid, cudaStream_t s) {
+  const int threads = block.x * block.y;
+  const int row = (DSUM ? 3 : 2) * V * threads * 16;
+  const int stages = std::min(3, std::max(1, kMaxSmem / row));
+  const int smem = std::max(stages * row, block.y > 1 ? (int)block.y * A.cols * 4 : 0);
+  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, kMaxSmem / smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_rows_kernel<DT, V, DSUM>));
+  if (e == cudaSuccess) rmsnorm_bwd_rows_kernel<DT, V, DSUM><<<*grid, block, smem, s>>>(A, stages);
+  return e;
+}
+
+template <int DT, bool DSUM>
+cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
+  const Shape S = A.vec ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 8, bwd_max_threads) : Shape{0, 0};
+  if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(), sms, grid, s);
+  if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(), sms, grid, s);
+  if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(), sms, grid, s);
+  if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(), sms, grid, s);
+  const dim3 block = Shape{walk_threads(A.cols / (A.vec ? Vec16<DT>::kElems : 2)), 0}.block();
+  const int64_t bytes = (int64_t)block.y * A.cols * 4;
+  const int in_smem = bytes <= kMaxSmem ? 1 : 0;
+  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, in_smem ? (int)(kMaxSmem / bytes) : 1);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_walk_kernel<DT>));
+  if (e == cudaSuccess) rmsnorm_bwd_walk_kernel<DT><<<*grid, block, in_smem ? (size_t)bytes : 0, s>>>(A, in_smem);
+  return e;
+}
+template <int DT>
+cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
+  return A.dsum ? launch_bwd<DT, true>(A, sms, grid, s) : launch_bwd<DT, false>(A, sms, grid, s);
 }
 
 // A matrix argument: non-null, aligned to its elements, rows at least cols
@@ -520,11 +659,11 @@ extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stre
   if (n->y && !check_matrix(n->y, n->ld_y, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
   if (n->rows == 0) return QMUON_OK;
   FwdArgs A{n->x,    n->residual,    n->gain,   n->sum,  n->y,    n->payload, n->scale_inv, n->rows,
-            n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, n->eps,    1.0f / (float)n->cols};
+            n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n->dtype == QMUON_BF16) launch_fwd_dt<QMUON_BF16>(A, vec, s);
-  else if (n->dtype == QMUON_FP16) launch_fwd_dt<QMUON_FP16>(A, vec, s);
-  else launch_fwd_dt<QMUON_FP32>(A, vec, s);
+  if (n->dtype == QMUON_BF16) launch_fwd_dt<QMUON_BF16>(A, s);
+  else if (n->dtype == QMUON_FP16) launch_fwd_dt<QMUON_FP16>(A, s);
+  else launch_fwd_dt<QMUON_FP32>(A, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_forward (launch)", e);
 }
@@ -532,7 +671,7 @@ extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stre
 extern "C" size_t qmuon_rmsnorm_workspace_size(int64_t rows, int64_t cols) {
   if (!check_sizes(rows, cols, QMUON_FP32, 0.0f)) return 0;
   const int sms = device_sms();
-  return ((size_t)bwd_grid(rows, sms > 0 ? sms : 1) * (size_t)cols * 4 + 255) / 256 * 256;
+  return ((size_t)bwd_grid(rows, sms > 0 ? sms : 1, kBwdPerSm) * (size_t)cols * 4 + 255) / 256 * 256;
 }
 
 extern "C" qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* n, void* ws, size_t ws_bytes, void* stream) {
@@ -553,14 +692,15 @@ extern "C" qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* n, void
   const int sms = device_sms();
   if (sms <= 0) return set_error_msg("qmuon_rmsnorm_backward: SM count query failed", QMUON_ERR_CUDA);
   if (ws_bytes < qmuon_rmsnorm_workspace_size(n->rows, n->cols)) return QMUON_ERR_WORKSPACE_TOO_SMALL;
-  BwdArgs A{n->dy,   n->h,    n->dsum,    n->gain,  n->dx,            static_cast<float*>(ws), n->rows,
-            n->ld_dy, n->ld_h, n->ld_dsum, n->ld_dx, (int32_t)n->cols, n->eps,                  1.0f / (float)n->cols};
-  constexpr int kHalf = 8, kFull = 4;   // elements of a 16-byte vector
+  BwdArgs A{n->dy,    n->h,    n->dsum,    n->gain,  n->dx,            static_cast<float*>(ws), n->rows,
+            n->ld_dy, n->ld_h, n->ld_dsum, n->ld_dx, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
   int grid = 0;
-  if (n->dtype == QMUON_BF16) grid = vec ? launch_bwd<QMUON_BF16, kHalf>(A, sms, s) : launch_bwd<QMUON_BF16, 1>(A, sms, s);
-  else if (n->dtype == QMUON_FP16) grid = vec ? launch_bwd<QMUON_FP16, kHalf>(A, sms, s) : launch_bwd<QMUON_FP16, 1>(A, sms, s);
-  else grid = vec ? launch_bwd<QMUON_FP32, kFull>(A, sms, s) : launch_bwd<QMUON_FP32, 1>(A, sms, s);
-  dgain_kernel<<<(unsigned)((n->cols + 31) / 32), dim3(32, 32), 0, s>>>(A.partial, grid, A.cols, n->dgain);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = n->dtype == QMUON_BF16   ? launch_bwd_dt<QMUON_BF16>(A, sms, &grid, s)
+                  : n->dtype == QMUON_FP16 ? launch_bwd_dt<QMUON_FP16>(A, sms, &grid, s)
+                                           : launch_bwd_dt<QMUON_FP32>(A, sms, &grid, s);
+  if (e == cudaSuccess) {
+    dgain_kernel<<<(unsigned)((n->cols + 31) / 32), dim3(32, 32), 0, s>>>(A.partial, grid, A.cols, n->dgain);
+    e = cudaGetLastError();
+  }
   return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (launch)", e);
 }
