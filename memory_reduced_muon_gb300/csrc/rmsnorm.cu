@@ -6,13 +6,13 @@
 //                             dgain = sum over rows of dy n
 //
 // A row belongs to T threads: a power of two up to a warp (and a CTA then takes
-// several rows), or whole warps.  Rows that start on 16 bytes and fit their
-// threads' registers cross HBM once ("rows" kernels).  All others are walked
-// twice by the "walk" kernels, the second time out of the caches: in 16-byte
-// vectors where they are only long, in pairs of 16-bit elements where all
-// arrays' rows start alike within 4 bytes, else by single elements.
+// several rows), or whole warps.  Rows that fit their threads' registers cross
+// HBM once: in 16-byte vectors where all arrays' rows start on 16 bytes ("rows"
+// kernels), else in pairs of 16-bit elements or single elements ("pieces").
+// Longer ones are walked twice, the second time out of the caches ("walk").
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <set>
 #include <type_traits>
@@ -173,82 +173,116 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
   }
 }
 
-// N consecutive elements of a row at column c, moved at once.
+// A row whose arrays are not aligned, in pieces of one element or, where all
+// arrays' rows start alike within 4 bytes, of a pair of 16-bit elements; these
+// start at column `head` (0 or 1) and leave one element at either end, which
+// the first and the last thread hold besides.
 template <int DT, int N>
-__device__ __forceinline__ void load_n(const void* row, int c, float* f) {
-  if constexpr (N == 1) {
-    f[0] = load_elem<DT>(row, c);
-  } else if constexpr (N == 2) {
-    const float2 t = unpack2<DT>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + c));
-    f[0] = t.x, f[1] = t.y;
-  } else {
-    Vec16<DT>::unpack(reinterpret_cast<const uint4*>(row)[c / N], reinterpret_cast<float2*>(f));
+struct Piece {
+  using Raw = std::conditional_t<N == 2 || DT == QMUON_FP32, uint32_t, uint16_t>;
+  __device__ __forceinline__ static Raw load(const void* row, int c) {
+    return *reinterpret_cast<const Raw*>(static_cast<const unsigned char*>(row) + c * elem_size(DT));
   }
-}
-template <int DT, int N>
-__device__ __forceinline__ void store_n(void* row, int c, const float* f) {
-  if constexpr (N == 1) store_elem<DT>(row, c, f[0]);
-  else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(row) + c) = pack2<DT>(f[0], f[1]);
-  else reinterpret_cast<uint4*>(row)[c / N] = Vec16<DT>::pack(reinterpret_cast<const float2*>(f));
-}
-
-// Calls f(column, constant count) for the pieces of a row that thread t of T
-// moves: vectors; pairs from column `head` (0 or 1) on, with single elements at
-// the ends; or single elements.  `how`: 0 single, 1 pairs, 2 vectors.
-template <int DT, class F>
-__device__ __forceinline__ void walk_row(int cols, int how, int head, int T, int t, F&& f) {
-  constexpr int K = Vec16<DT>::kElems;
-  if (cols == 0) return;   // a row past the last one: its ends are not there either
-  if (how == 2) {
-#pragma unroll 4
-    for (int c = t * K; c < cols; c += T * K) f(c, std::integral_constant<int, K>{});
-    return;
+  __device__ __forceinline__ static float2 unpack(Raw w) {
+    if constexpr (N == 2) return unpack2<DT>(w);
+    else if constexpr (DT == QMUON_FP32) return make_float2(__uint_as_float(w), 0.0f);
+    else return make_float2(unpack2<DT>(w).x, 0.0f);
   }
-  if constexpr (DT != QMUON_FP32) {
-    if (how == 1) {
-#pragma unroll 4
-      for (int c = head + 2 * t; c + 1 < cols; c += 2 * T) f(c, std::integral_constant<int, 2>{});
-      if (t == 0 && head) f(0, std::integral_constant<int, 1>{});
-      if (t == T - 1 && ((cols - head) & 1)) f(cols - 1, std::integral_constant<int, 1>{});
-      return;
-    }
+  __device__ __forceinline__ static void store(void* row, int c, float2 f) {
+    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(row) + c * 2) = pack2<DT>(f.x, f.y);
+    else store_elem<DT>(row, c, f.x);
   }
-#pragma unroll 4
-  for (int c = t; c < cols; c += T) f(c, std::integral_constant<int, 1>{});
-}
+};
 
-// How a row whose arrays start at these addresses can be walked: `how` for
-// walk_row, and in `head` the column where pairs start.
-template <int DT>
-__device__ __forceinline__ int row_kind(bool vec, int* head, const void* a, const void* b, const void* c, const void* d) {
-  *head = 0;
-  if (vec) return 2;
-  if (DT == QMUON_FP32) return 0;
-  auto bits = [](const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p) & 3u; };
-  const uint32_t k = bits(a);
-  if ((b && bits(b) != k) || (c && bits(c) != k) || (d && bits(d) != k)) return 0;
-  *head = (int)(k >> 1);
-  return 1;
-}
+constexpr int kPieces = 8;   // per thread
 
-template <int DT, bool MX>
-__global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_constant__ FwdArgs A) {
+template <int DT, int N, bool RES, bool MX>
+__global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_constant__ FwdArgs A) {
+  using One = Piece<DT, 1>;
+  using Some = Piece<DT, N>;
   __shared__ float part[2][32];
   const int T = blockDim.x, t = threadIdx.x;
   int flip = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
     const int64_t row = r0 + threadIdx.y;
-    const int cols = row < A.rows ? A.cols : 0;
+    const bool live = row < A.rows;
     const void* x = row_of<DT>(A.x, row, A.ld_x);
-    const void* res = A.residual ? row_of<DT>(A.residual, row, A.ld_residual) : nullptr;
-    void* sum = A.sum ? row_of<DT>(A.sum, row, A.ld_sum) : nullptr;
-    void* y = A.y ? row_of<DT>(A.y, row, A.ld_y) : nullptr;
-    int head = 0;
-    const int how = MX ? (A.vec ? 2 : 0) : row_kind<DT>(A.vec, &head, x, res, sum, y);
-    auto load = [&](int c, auto n, float* h) {
-      constexpr int N = decltype(n)::value;
+    const void* res = row_of<DT>(A.residual, row, A.ld_residual);
+    const int head = N == 2 ? (int)(reinterpret_cast<uintptr_t>(x) >> 1) & 1 : 0;
+    const int n = live ? (A.cols - head) / N : 0;   // whole pieces, from column head on
+    // the single elements of the first and the last thread (one thread's, where T is 1: never, T is 32 or more)
+    const int edge = N == 1 || !live         ? -1
+                     : t == 0 && head        ? 0
+                     : t == T - 1 && ((A.cols - head) & 1) ? A.cols - 1
+                                             : -1;
+    typename Some::Raw rx[kPieces], rr[RES ? kPieces : 1];
+    typename One::Raw ex = 0, er = 0;
+    if (edge >= 0) {
+      ex = One::load(x, edge);
+      if constexpr (RES) er = One::load(res, edge);
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int k = i * T + t;
+      rx[i] = k < n ? Some::load(x, head + N * k) : 0;
+      if constexpr (RES) rr[i] = k < n ? Some::load(res, head + N * k) : 0;
+    }
+    float2 h[kPieces], ss = make_float2(0.0f, 0.0f);
+    float he = One::unpack(ex).x;
+    if constexpr (RES) he += One::unpack(er).x;
+    ss.x = he * he;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      h[i] = Some::unpack(rx[i]);
+      if constexpr (RES) h[i] = add2(h[i], Some::unpack(rr[i]));
+      ss = fma2(h[i], h[i], ss);
+    }
+    const float inv = inverse_norm(row_sum(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
+    void* sum = row_of<DT>(A.sum, row, A.ld_sum);
+    void* y = row_of<DT>(A.y, row, A.ld_y);
+    if (edge >= 0) {
+      if (A.sum) One::store(sum, edge, make_float2(he, 0.0f));
+      One::store(y, edge, make_float2(he * inv * __ldg(A.gain + edge), 0.0f));
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int k = i * T + t, c = head + N * k;
+      if (k < n) {
+        if (A.sum) Some::store(sum, c, h[i]);
+        h[i] = mul2(mul2(h[i], inv), make_float2(__ldg(A.gain + c), N == 2 ? __ldg(A.gain + c + N - 1) : 0.0f));
+        if (!MX || A.y) Some::store(y, c, h[i]);
+      }
+      if constexpr (MX) store_mxfp8<1>(&h[i].x, k < n, row * A.cols + c, A.payload, A.scale);
+    }
+  }
+}
+
+// N consecutive elements of a row at column c, moved at once: one, or a
+// 16-byte vector.
+template <int DT, int N>
+__device__ __forceinline__ void load_n(const void* row, int c, float* f) {
+  if constexpr (N == 1) f[0] = load_elem<DT>(row, c);
+  else Vec16<DT>::unpack(reinterpret_cast<const uint4*>(row)[c / N], reinterpret_cast<float2*>(f));
+}
+template <int DT, int N>
+__device__ __forceinline__ void store_n(void* row, int c, const float* f) {
+  if constexpr (N == 1) store_elem<DT>(row, c, f[0]);
+  else reinterpret_cast<uint4*>(row)[c / N] = Vec16<DT>::pack(reinterpret_cast<const float2*>(f));
+}
+
+// Rows longer than a CTA holds: read for the sum, and again, out of the
+// caches, for the output.
+template <int DT, int N, bool MX>
+__global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_constant__ FwdArgs A) {
+  __shared__ float part[2][32];
+  const int T = blockDim.x, t = threadIdx.x;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
+    const void* x = row_of<DT>(A.x, row, A.ld_x);
+    const void* res = row_of<DT>(A.residual, row, A.ld_residual);
+    auto load = [&](int c, float* h) {
       load_n<DT, N>(x, c, h);
-      if (res) {
+      if (A.residual) {
         float f[N];
         load_n<DT, N>(res, c, f);
 #pragma unroll
@@ -256,42 +290,26 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_con
       }
     };
     float ss = 0.0f;
-    walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
-      constexpr int N = decltype(n)::value;
+#pragma unroll 4
+    for (int c = t * N; c < A.cols; c += T * N) {
       float h[N];
-      load(c, n, h);
+      load(c, h);
 #pragma unroll
       for (int j = 0; j < N; ++j) ss = fmaf(h[j], h[j], ss);
-    });
+    }
     const float inv = inverse_norm(row_sum(ss, T, part[flip]), A.inv_cols, A.eps);
-    auto finish = [&](int c, auto n, float* h) {
-      constexpr int N = decltype(n)::value;
-      load(c, n, h);
-      if (sum) store_n<DT, N>(sum, c, h);
+#pragma unroll 2
+    for (int c0 = 0; c0 < A.cols; c0 += T * N) {   // the same number of passes in every thread: lanes share scales
+      const int c = c0 + t * N;
+      float h[N] = {};
+      if (c < A.cols) {
+        load(c, h);
+        if (A.sum) store_n<DT, N>(row_of<DT>(A.sum, row, A.ld_sum), c, h);
 #pragma unroll
-      for (int j = 0; j < N; ++j) h[j] = h[j] * inv * __ldg(A.gain + c + j);
-      if (y) store_n<DT, N>(y, c, h);
-    };
-    if constexpr (!MX) {
-      walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
-      constexpr int N = decltype(n)::value;
-        float h[N];
-        finish(c, n, h);
-      });
-    } else {
-      // the same number of passes in every thread of a warp: its lanes share scales
-      constexpr int K = Vec16<DT>::kElems;
-      auto pass = [&](auto n) {
-        constexpr int N = decltype(n)::value;
-        for (int c0 = 0; c0 < A.cols; c0 += T * N) {
-          const int c = c0 + t * N;
-          float h[N] = {};
-          if (c < cols) finish(c, n, h);
-          store_mxfp8<N>(h, c < cols, row * A.cols + c, A.payload, A.scale);
-        }
-      };
-      if (how == 2) pass(std::integral_constant<int, K>{});
-      else pass(std::integral_constant<int, 1>{});
+        for (int j = 0; j < N; ++j) h[j] = h[j] * inv * __ldg(A.gain + c + j);
+        if (A.y) store_n<DT, N>(row_of<DT>(A.y, row, A.ld_y), c, h);
+      }
+      if constexpr (MX) store_mxfp8<N>(h, c < A.cols, row * A.cols + c, A.payload, A.scale);
     }
   }
 }
@@ -428,31 +446,140 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
   }
 }
 
-// The gain's gradient lies in shared memory, a row for each of the CTA's, or,
-// where it does not fit, in the CTA's row of `partial`.
-template <int DT>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_constant__ BwdArgs A, int in_smem) {
+// Rows in pieces (see the forward pass); the next row's are loaded while one is
+// computed.  Pairs start at column 0 or 1, by the row, so that a thread's
+// columns differ between the two kinds of rows: it sums each kind's apart.
+constexpr int bwd_piece_threads = 512;
+
+template <int DT, int N, bool DSUM>
+__global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(const __grid_constant__ BwdArgs A) {
+  using One = Piece<DT, 1>;
+  using Some = Piece<DT, N>;
+  constexpr int kKinds = N;   // 1, or pairs from column 0 and pairs from column 1
   __shared__ float2 part[2][32];
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols]
   const int T = blockDim.x, t = threadIdx.x;
-  float* out = A.partial + (int64_t)blockIdx.x * A.cols;
-  float* acc = in_smem ? reinterpret_cast<float*>(smem) + (size_t)threadIdx.y * A.cols : out;
-  for (int c = t; c < A.cols; c += T) acc[c] = 0.0f;
-  if (T > 32) __syncthreads();
-  else __syncwarp();
+  struct Raw {
+    typename Some::Raw h[kPieces], d[kPieces], s[DSUM ? kPieces : 1];
+    typename One::Raw he, de, se;
+    int head, n, edge;
+  };
+  auto load = [&](int64_t row, Raw& r) {
+    const bool live = row < A.rows;
+    const void* h = row_of<DT>(A.h, row, A.ld_h);
+    const void* d = row_of<DT>(A.dy, row, A.ld_dy);
+    const void* s = row_of<DT>(A.dsum, row, A.ld_dsum);
+    r.head = N == 2 ? (int)(reinterpret_cast<uintptr_t>(h) >> 1) & 1 : 0;
+    r.n = live ? (A.cols - r.head) / N : 0;
+    r.edge = N == 1 || !live                        ? -1
+             : t == 0 && r.head                     ? 0
+             : t == T - 1 && ((A.cols - r.head) & 1) ? A.cols - 1
+                                                    : -1;
+    r.he = r.de = r.se = 0;
+    if (r.edge >= 0) {
+      r.he = One::load(h, r.edge);
+      r.de = One::load(d, r.edge);
+      if constexpr (DSUM) r.se = One::load(s, r.edge);
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int k = i * T + t, c = r.head + N * k;
+      r.h[i] = r.d[i] = 0;
+      if constexpr (DSUM) r.s[i] = 0;
+      if (k < r.n) {
+        r.h[i] = Some::load(h, c);
+        r.d[i] = Some::load(d, c);
+        if constexpr (DSUM) r.s[i] = Some::load(s, c);
+      }
+    }
+  };
+  float2 acc[kKinds][kPieces] = {};
+  float acc_edge = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  Raw in;
+  load((int64_t)blockIdx.x * blockDim.y + threadIdx.y, in);
   int flip = 0;
-  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < A.rows; base += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
+  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < A.rows; base += step, flip ^= 1) {
     const int64_t row = base + threadIdx.y;
-    const int cols = row < A.rows ? A.cols : 0;
+    Raw next;
+    load(row + step, next);
+    auto gain = [&](int c) { return make_float2(__ldg(A.gain + c), N == 2 ? __ldg(A.gain + c + N - 1) : 0.0f); };
+    const float he = One::unpack(in.he).x, de = One::unpack(in.de).x, ge = in.edge >= 0 ? __ldg(A.gain + in.edge) : 0.0f;
+    float2 sh = make_float2(he * he, 0.0f), sa = make_float2(de * ge * he, 0.0f);   // sums of h^2 and a h
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (i * T + t < in.n) {
+        const float2 h = Some::unpack(in.h[i]);
+        sh = fma2(h, h, sh);
+        sa = fma2(mul2(Some::unpack(in.d[i]), gain(in.head + N * (i * T + t))), h, sa);
+      }
+    const float2 sum = row_sum(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
+    const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
+    const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
+    void* dx = row_of<DT>(A.dx, row, A.ld_dx);
+    if (in.edge >= 0) {
+      float o = inv * fmaf(he, c, de * ge);
+      if constexpr (DSUM) o += One::unpack(in.se).x;
+      One::store(dx, in.edge, make_float2(o, 0.0f));
+      acc_edge = fmaf(de, he * inv, acc_edge);
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (i * T + t < in.n) {
+        const int col = in.head + N * (i * T + t);
+        const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
+        const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(col)));
+        float2 o;
+        if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
+        else o = mul2(e, inv);
+        Some::store(dx, col, o);
+        const float2 n = mul2(h, inv);
+        if (kKinds == 1 || in.head == 0) acc[0][i] = fma2(d, n, acc[0][i]);
+        else acc[kKinds - 1][i] = fma2(d, n, acc[kKinds - 1][i]);
+      }
+    in = next;
+  }
+  // the columns' sums: those of rows whose pairs start at column 0, then at column 1, then the ends'
+  float* mine = s_acc + (size_t)threadIdx.y * A.cols;
+  for (int c = t; c < A.cols; c += T) mine[c] = 0.0f;
+#pragma unroll
+  for (int kind = 0; kind < kKinds; ++kind) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int c = kind + N * (i * T + t);
+      if (c + N <= A.cols) {
+        mine[c] += acc[kind][i].x;
+        if constexpr (N == 2) mine[c + 1] += acc[kind][i].y;
+      }
+    }
+  }
+  __syncthreads();
+  if (N == 2 && t == 0) mine[0] += acc_edge;
+  __syncthreads();   // one column: both are its
+  if (N == 2 && t == T - 1) mine[A.cols - 1] += acc_edge;
+  __syncthreads();
+  for (int c = threadIdx.y * T + t; c < A.cols; c += T * blockDim.y) {
+    float v = 0.0f;
+    for (int y = 0; y < (int)blockDim.y; ++y) v += s_acc[(size_t)y * A.cols + c];
+    A.partial[(int64_t)blockIdx.x * A.cols + c] = v;
+  }
+}
+
+// Longer rows: read twice; a thread's columns of the gain's gradient lie in
+// the CTA's row of `partial`.
+template <int DT, int N>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_constant__ BwdArgs A) {
+  __shared__ float2 part[2][32];
+  const int T = blockDim.x, t = threadIdx.x;
+  float* acc = A.partial + (int64_t)blockIdx.x * A.cols;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
     const void* hp = row_of<DT>(A.h, row, A.ld_h);
     const void* dp = row_of<DT>(A.dy, row, A.ld_dy);
-    const void* sp = A.dsum ? row_of<DT>(A.dsum, row, A.ld_dsum) : nullptr;
-    void* dx = row_of<DT>(A.dx, row, A.ld_dx);
-    int head = 0;
-    const int how = row_kind<DT>(A.vec, &head, hp, dp, sp, dx);
     float2 s = make_float2(0.0f, 0.0f);   // sums of h^2 and a h
-    walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
-      constexpr int N = decltype(n)::value;
+#pragma unroll 4
+    for (int c = t * N; c < A.cols; c += T * N) {
       float h[N], d[N];
       load_n<DT, N>(hp, c, h);
       load_n<DT, N>(dp, c, d);
@@ -461,37 +588,29 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_con
         s.x = fmaf(h[j], h[j], s.x);
         s.y = fmaf(d[j] * __ldg(A.gain + c + j), h[j], s.y);
       }
-    });
-    // A column may be another thread's than in the row before: the barrier (the shuffles, within a warp) orders the two.
+    }
     s = row_sum(s, T, part[flip]);
-    if (T <= 32) __syncwarp();
     const float inv = inverse_norm(s.x, A.inv_cols, A.eps);
     const float k = s.y * A.inv_cols * inv * inv;
-    walk_row<DT>(cols, how, head, T, t, [&](int c, auto n) {
-      constexpr int N = decltype(n)::value;
+    const bool first = row == blockIdx.x;
+#pragma unroll 2
+    for (int c = t * N; c < A.cols; c += T * N) {
       float h[N], d[N], o[N];
       load_n<DT, N>(hp, c, h);
       load_n<DT, N>(dp, c, d);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         o[j] = inv * (d[j] * __ldg(A.gain + c + j) - h[j] * k);
-        acc[c + j] = fmaf(d[j], h[j] * inv, acc[c + j]);
+        acc[c + j] = fmaf(d[j], h[j] * inv, first ? 0.0f : acc[c + j]);
       }
-      if (sp) {
+      if (A.dsum) {
         float f[N];
-        load_n<DT, N>(sp, c, f);
+        load_n<DT, N>(row_of<DT>(A.dsum, row, A.ld_dsum), c, f);
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] += f[j];
       }
-      store_n<DT, N>(dx, c, o);
-    });
-  }
-  if (!in_smem) return;
-  __syncthreads();
-  for (int c = threadIdx.y * T + t; c < A.cols; c += T * blockDim.y) {
-    float v = 0.0f;
-    for (int y = 0; y < (int)blockDim.y; ++y) v += reinterpret_cast<const float*>(smem)[(size_t)y * A.cols + c];
-    out[c] = v;
+      store_n<DT, N>(row_of<DT>(A.dx, row, A.ld_dx), c, o);
+    }
   }
 }
 
@@ -543,13 +662,6 @@ Shape pick_shape(int nv, int want, int most, MaxThreads max_threads) {
   return {0, 0};
 }
 
-// Threads of a row that is walked in pieces: about four pieces per thread.
-int walk_threads(int64_t pieces) {
-  int T = 32;
-  while (T < 1024 && T * 4 < pieces) T *= 2;
-  return T;
-}
-
 int device_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -573,15 +685,40 @@ cudaError_t allow_smem(const void* kernel) {
   return e;
 }
 
+// Whether all rows of the arrays start alike within 4 bytes.
+struct Strided {
+  const void* p;
+  int64_t ld;
+};
+bool rows_alike(std::initializer_list<Strided> arrays) {
+  const Strided& a = *arrays.begin();
+  for (const Strided& b : arrays)
+    if (b.p && (((reinterpret_cast<uintptr_t>(a.p) ^ reinterpret_cast<uintptr_t>(b.p)) & 3) || ((a.ld ^ b.ld) & 1))) return false;
+  return true;
+}
+
 template <int DT, bool RES, bool MX>
 void launch_fwd(const FwdArgs& A, cudaStream_t s) {
-  const Shape S = A.vec ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 4, fwd_max_threads) : Shape{0, 0};
-  const dim3 block = S.V ? S.block() : Shape{walk_threads(A.cols / (A.vec ? Vec16<DT>::kElems : 2)), 0}.block();
+  constexpr int K = Vec16<DT>::kElems;
+  const Shape S = A.vec ? pick_shape(A.cols / K, 4, 4, fwd_max_threads) : Shape{0, 0};
+  const bool pairs = !MX && DT != QMUON_FP32 &&
+                     rows_alike({{A.x, A.ld_x}, {A.residual, A.ld_residual}, {A.sum, A.ld_sum}, {A.y, A.ld_y}});
+  // unaligned: threads for the row's pieces, whole warps
+  const int64_t T = std::max(((A.cols / (pairs ? 2 : 1) + kPieces - 1) / kPieces + 31) / 32 * 32, 32);
+  const bool pieces = !A.vec && T <= 1024;
+  const dim3 block = S.V ? S.block() : pieces ? Shape{(int)T, 0}.block() : dim3(1024);
   const unsigned grid = (unsigned)std::min<int64_t>((A.rows + block.y - 1) / block.y, ((int64_t)1 << 31) - 1);
   if (S.V == 1) rmsnorm_fwd_rows_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
   else if (S.V == 2) rmsnorm_fwd_rows_kernel<DT, 2, RES, MX><<<grid, block, 0, s>>>(A);
   else if (S.V == 4) rmsnorm_fwd_rows_kernel<DT, 4, RES, MX><<<grid, block, 0, s>>>(A);
-  else rmsnorm_fwd_walk_kernel<DT, MX><<<grid, block, 0, s>>>(A);
+  else if (A.vec) rmsnorm_fwd_walk_kernel<DT, K, MX><<<grid, block, 0, s>>>(A);
+  else if (!pieces) rmsnorm_fwd_walk_kernel<DT, 1, MX><<<grid, block, 0, s>>>(A);
+  else if constexpr (!MX && DT != QMUON_FP32) {
+    if (pairs) rmsnorm_fwd_pieces_kernel<DT, 2, RES, MX><<<grid, block, 0, s>>>(A);
+    else rmsnorm_fwd_pieces_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
+  } else {
+    rmsnorm_fwd_pieces_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
+  }
 }
 template <int DT>
 void launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
@@ -614,13 +751,30 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
   if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(), sms, grid, s);
   if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(), sms, grid, s);
   if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(), sms, grid, s);
-  const dim3 block = Shape{walk_threads(A.cols / (A.vec ? Vec16<DT>::kElems : 2)), 0}.block();
-  const int64_t bytes = (int64_t)block.y * A.cols * 4;
-  const int in_smem = bytes <= kMaxSmem ? 1 : 0;
-  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, in_smem ? (int)(kMaxSmem / bytes) : 1);
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_walk_kernel<DT>));
-  if (e == cudaSuccess) rmsnorm_bwd_walk_kernel<DT><<<*grid, block, in_smem ? (size_t)bytes : 0, s>>>(A, in_smem);
-  return e;
+  if (!A.vec) {
+    const bool pairs =
+        DT != QMUON_FP32 && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}});
+    const int64_t T = std::max(((A.cols / (pairs ? 2 : 1) + kPieces - 1) / kPieces + 31) / 32 * 32, 32);
+    if (T <= bwd_piece_threads) {
+      const dim3 block = Shape{(int)T, 0}.block();
+      const int smem = (int)block.y * A.cols * 4;
+      *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, 1024 / (block.x * block.y));
+      if constexpr (DT != QMUON_FP32) {
+        if (pairs) {
+          const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>));
+          if (e == cudaSuccess) rmsnorm_bwd_pieces_kernel<DT, 2, DSUM><<<*grid, block, smem, s>>>(A);
+          return e;
+        }
+      }
+      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 1, DSUM>));
+      if (e == cudaSuccess) rmsnorm_bwd_pieces_kernel<DT, 1, DSUM><<<*grid, block, smem, s>>>(A);
+      return e;
+    }
+  }
+  *grid = bwd_grid(A.rows, sms, 2);
+  if (A.vec) rmsnorm_bwd_walk_kernel<DT, Vec16<DT>::kElems><<<*grid, 1024, 0, s>>>(A);
+  else rmsnorm_bwd_walk_kernel<DT, 1><<<*grid, 1024, 0, s>>>(A);
+  return cudaSuccess;
 }
 template <int DT>
 cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
