@@ -11,6 +11,7 @@
 // kernels), else in pairs of 16-bit elements or single elements ("pieces").
 // Longer ones are walked twice, the second time out of the caches ("walk").
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 #include <mutex>
@@ -75,7 +76,7 @@ __device__ __forceinline__ S row_sum(S v, int T, S* part) {
 }
 
 __device__ __forceinline__ float inverse_norm(float sumsq, float inv_cols, float eps) {
-  return __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sumsq, inv_cols, eps)));
+  return rsqrtf(fmaf(sumsq, inv_cols, eps));   // 2 ulp
 }
 
 // The MXFP8 codes of N values held by a thread whose neighbours hold the rest
@@ -145,6 +146,13 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
 #pragma unroll
       for (int j = 0; j < P; ++j) ss = fma2(h[i][j], h[i][j], ss);
     }
+    // the gain early where there are registers for it: its way from memory is as long as the row's
+    constexpr bool kGainEarly = V == 1;
+    const float4* gain = reinterpret_cast<const float4*>(A.gain) + t * (P / 2);
+    float4 ge[kGainEarly ? P / 2 : 1];
+    if constexpr (kGainEarly)
+#pragma unroll
+      for (int j = 0; j < P / 2; ++j) ge[j] = t < n ? __ldg(gain + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (A.sum) {
       uint4* sum = reinterpret_cast<uint4*>(row_of<DT>(A.sum, row, A.ld_sum)) + t;
 #pragma unroll
@@ -152,7 +160,6 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
         if (i * T + t < n) sum[i * T] = X::pack(h[i]);
     }
     const float inv = inverse_norm(row_sum(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
-    const float4* gain = reinterpret_cast<const float4*>(A.gain) + t * (P / 2);
     uint4* y = reinterpret_cast<uint4*>(row_of<DT>(A.y, row, A.ld_y)) + t;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
       if (in) {
 #pragma unroll
         for (int j = 0; j < P; j += 2) {
-          const float4 g = __ldg(gain + i * T * (P / 2) + j / 2);
+          const float4 g = kGainEarly ? ge[j / 2 % (P / 2)] : __ldg(gain + i * T * (P / 2) + j / 2);
           h[i][j] = mul2(mul2(h[i][j], inv), make_float2(g.x, g.y));
           h[i][j + 1] = mul2(mul2(h[i][j + 1], inv), make_float2(g.z, g.w));
         }
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_con
 // columns, which leaves as one row of `partial`; dgain_kernel adds those rows
 // in order.  The next rows come through a ring of shared-memory slots, each
 // thread's own, `stages` rows ahead.
-constexpr int bwd_max_threads(int V) { return V == 8 ? 512 : 256; }
+constexpr int bwd_max_threads(int V) { return V >= 4 ? 512 : 256; }
 
 __device__ __forceinline__ void wait_rows(int pending) {
   if (pending >= 2) async_wait<2>();
@@ -418,6 +425,7 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
     issue(row + stages * step, slot);
     s = s + 1 == stages ? 0 : s + 1;
   }
+  asm volatile("griddepcontrol.launch_dependents;");
   float* out = A.partial + (int64_t)blockIdx.x * A.cols;
   if (T > 32) {
 #pragma unroll
@@ -539,6 +547,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       }
     in = next;
   }
+  asm volatile("griddepcontrol.launch_dependents;");
   // the columns' sums: those of rows whose pairs start at column 0, then at column 1, then the ends'
   float* mine = s_acc + (size_t)threadIdx.y * A.cols;
   for (int c = t; c < A.cols; c += T) mine[c] = 0.0f;
@@ -614,18 +623,32 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_con
   }
 }
 
-// dgain[c] = sum of n rows of partial, in an order that n alone fixes.
+// dgain[c] = sum of n rows of partial, in an order that n alone fixes.  A
+// launch's end to the next one's start is hidden: the kernel starts while the
+// one before it drains (griddepcontrol), and waits for it to complete.
+constexpr int kSlices = 32;
+
 __global__ void __launch_bounds__(1024) dgain_kernel(const float* partial, int32_t n, int32_t cols, float* dgain) {
-  __shared__ float s[32][33];
+  __shared__ float s[kSlices][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
-  if (c < cols)
-    for (int r = threadIdx.y; r < n; r += 32) v += partial[(int64_t)r * cols + c];
+  if (c < cols) {
+    const float* p = partial + c;
+    constexpr int kAhead = 10;   // loads in flight
+    for (int r = threadIdx.y; r < n; r += kAhead * kSlices) {
+      float f[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = r + i * kSlices < n ? __ldcg(p + (int64_t)(r + i * kSlices) * cols) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) v += f[i];
+    }
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = s[threadIdx.x][threadIdx.y];   // a warp per column
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) v += lane_xor(v, o);
   const int cc = blockIdx.x * 32 + threadIdx.y;
   if (threadIdx.x == 0 && cc < cols) dgain[cc] = v;
 }
@@ -636,24 +659,24 @@ __global__ void __launch_bounds__(1024) dgain_kernel(const float* partial, int32
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool is_dtype(int v) { return v == QMUON_BF16 || v == QMUON_FP16 || v == QMUON_FP32; }
 
-// Threads of a row and 16-byte vectors per thread, V being the largest allowed
-// that leaves a row at least eight threads (128 contiguous bytes per access),
-// or the smallest that fits.  V == 0: it does not fit.
+// Threads of a row and 16-byte vectors per thread: V is the largest up to
+// `want` that leaves a row `least` threads, or the smallest that fits.  V == 0:
+// none does.
 struct Shape {
   int T, V;
   dim3 block() const { return dim3(T, T > 32 ? 1 : 256 / T); }
 };
 
 template <class MaxThreads>
-Shape pick_shape(int nv, int want, int most, MaxThreads max_threads) {
+Shape pick_shape(int nv, int want, int most, int least, MaxThreads max_threads) {
   int V = want;
-  while (V > 1 && nv / V < 8) V /= 2;
+  while (V > 1 && nv / V < least) V /= 2;
   for (; V <= most; V *= 2) {
     int T = (nv + V - 1) / V;
     if (T > 32) {
       T = (T + 31) / 32 * 32;
     } else {
-      int p = 8;
+      int p = least;
       while (p < T) p *= 2;
       T = p;
     }
@@ -663,9 +686,12 @@ Shape pick_shape(int nv, int want, int most, MaxThreads max_threads) {
 }
 
 int device_sms() {
+  static std::atomic<int> cached[64] = {};
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if ((sms = cached[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  cached[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
@@ -700,7 +726,11 @@ bool rows_alike(std::initializer_list<Strided> arrays) {
 template <int DT, bool RES, bool MX>
 void launch_fwd(const FwdArgs& A, cudaStream_t s) {
   constexpr int K = Vec16<DT>::kElems;
-  const Shape S = A.vec ? pick_shape(A.cols / K, 4, 4, fwd_max_threads) : Shape{0, 0};
+  // Four vectors per thread, so that a row takes few warps (and the bytes in flight are many); where rows do not fill
+  // the SMs, one, so that a row is done sooner: one row of 4096 bf16 in FEW_US, in FEW_US4 with four.
+  const bool few = A.rows <= device_sms();
+  const int least = MX && DT == QMUON_FP32 ? 8 : 4;   // the 32 elements of a scale lie in one access of a row's threads
+  const Shape S = A.vec ? pick_shape(A.cols / K, few ? 1 : 4, 4, least, fwd_max_threads) : Shape{0, 0};
   const bool pairs = !MX && DT != QMUON_FP32 &&
                      rows_alike({{A.x, A.ld_x}, {A.residual, A.ld_residual}, {A.sum, A.ld_sum}, {A.y, A.ld_y}});
   // unaligned: threads for the row's pieces, whole warps
@@ -746,7 +776,7 @@ cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* g
 
 template <int DT, bool DSUM>
 cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
-  const Shape S = A.vec ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 8, bwd_max_threads) : Shape{0, 0};
+  const Shape S = A.vec ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 8, 4, bwd_max_threads) : Shape{0, 0};
   if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(), sms, grid, s);
   if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(), sms, grid, s);
   if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(), sms, grid, s);
@@ -853,8 +883,17 @@ extern "C" qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* n, void
                   : n->dtype == QMUON_FP16 ? launch_bwd_dt<QMUON_FP16>(A, sms, &grid, s)
                                            : launch_bwd_dt<QMUON_FP32>(A, sms, &grid, s);
   if (e == cudaSuccess) {
-    dgain_kernel<<<(unsigned)((n->cols + 31) / 32), dim3(32, 32), 0, s>>>(A.partial, grid, A.cols, n->dgain);
     e = cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((n->cols + 31) / 32));
+    cfg.blockDim = dim3(32, kSlices);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, dgain_kernel, (const float*)A.partial, (int32_t)grid, A.cols, n->dgain);
   }
   return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (launch)", e);
 }
