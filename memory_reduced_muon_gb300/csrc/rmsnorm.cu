@@ -187,21 +187,24 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
 template <int DT, int N>
 struct Piece {
   using Raw = std::conditional_t<N == 2 || DT == QMUON_FP32, uint32_t, uint16_t>;
-  __device__ __forceinline__ static Raw load(const void* row, int c) {
-    return *reinterpret_cast<const Raw*>(static_cast<const unsigned char*>(row) + c * elem_size(DT));
+  static constexpr int kStep = 32 * N;   // columns between a thread's pieces: a warp's lie side by side
+  __device__ __forceinline__ static Raw load(const unsigned char* row, int c) {
+    return *reinterpret_cast<const Raw*>(row + c * elem_size(DT));
   }
   __device__ __forceinline__ static float2 unpack(Raw w) {
     if constexpr (N == 2) return unpack2<DT>(w);
     else if constexpr (DT == QMUON_FP32) return make_float2(__uint_as_float(w), 0.0f);
     else return make_float2(unpack2<DT>(w).x, 0.0f);
   }
-  __device__ __forceinline__ static void store(void* row, int c, float2 f) {
-    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(row) + c * 2) = pack2<DT>(f.x, f.y);
+  __device__ __forceinline__ static void store(unsigned char* row, int c, float2 f) {
+    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(row + c * 2) = pack2<DT>(f.x, f.y);
     else store_elem<DT>(row, c, f.x);
   }
 };
 
 constexpr int kPieces = 8;   // per thread
+// A thread's first piece, counted along the row: warp w has pieces 256 w .. 256 w + 255, lane by lane.
+__device__ __forceinline__ int first_piece(int t) { return (t >> 5) * (32 * kPieces) + (t & 31); }
 
 template <int DT, int N, bool RES, bool MX>
 __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_constant__ FwdArgs A) {
@@ -213,8 +216,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
   for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
     const int64_t row = r0 + threadIdx.y;
     const bool live = row < A.rows;
-    const void* x = row_of<DT>(A.x, row, A.ld_x);
-    const void* res = row_of<DT>(A.residual, row, A.ld_residual);
+    const unsigned char* x = row_of<DT>(A.x, row, A.ld_x);
+    const unsigned char* res = row_of<DT>(A.residual, row, A.ld_residual);
     const int head = N == 2 ? (int)(reinterpret_cast<uintptr_t>(x) >> 1) & 1 : 0;
     const int n = live ? (A.cols - head) / N : 0;   // whole pieces, from column head on
     // the single elements of the first and the last thread (one thread's, where T is 1: never, T is 32 or more)
@@ -228,11 +231,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
       ex = One::load(x, edge);
       if constexpr (RES) er = One::load(res, edge);
     }
+    const int k0 = first_piece(t), c0 = head + N * k0;
+    x += c0 * elem_size(DT);
+    res += c0 * elem_size(DT);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int k = i * T + t;
-      rx[i] = k < n ? Some::load(x, head + N * k) : 0;
-      if constexpr (RES) rr[i] = k < n ? Some::load(res, head + N * k) : 0;
+      rx[i] = k0 + 32 * i < n ? Some::load(x, i * Some::kStep) : 0;
+      if constexpr (RES) rr[i] = k0 + 32 * i < n ? Some::load(res, i * Some::kStep) : 0;
     }
     float2 h[kPieces], ss = make_float2(0.0f, 0.0f);
     float he = One::unpack(ex).x;
@@ -245,21 +250,25 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
       ss = fma2(h[i], h[i], ss);
     }
     const float inv = inverse_norm(row_sum(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
-    void* sum = row_of<DT>(A.sum, row, A.ld_sum);
-    void* y = row_of<DT>(A.y, row, A.ld_y);
+    unsigned char* sum = row_of<DT>(A.sum, row, A.ld_sum);
+    unsigned char* y = row_of<DT>(A.y, row, A.ld_y);
     if (edge >= 0) {
       if (A.sum) One::store(sum, edge, make_float2(he, 0.0f));
       One::store(y, edge, make_float2(he * inv * __ldg(A.gain + edge), 0.0f));
     }
+    sum += c0 * elem_size(DT);
+    y += c0 * elem_size(DT);
+    const float* gain = A.gain + c0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int k = i * T + t, c = head + N * k;
-      if (k < n) {
-        if (A.sum) Some::store(sum, c, h[i]);
-        h[i] = mul2(mul2(h[i], inv), make_float2(__ldg(A.gain + c), N == 2 ? __ldg(A.gain + c + N - 1) : 0.0f));
-        if (!MX || A.y) Some::store(y, c, h[i]);
+      const bool in = k0 + 32 * i < n;
+      const int d = i * Some::kStep;
+      if (in) {
+        if (A.sum) Some::store(sum, d, h[i]);
+        h[i] = mul2(mul2(h[i], inv), make_float2(__ldg(gain + d), N == 2 ? __ldg(gain + d + N - 1) : 0.0f));
+        if (!MX || A.y) Some::store(y, d, h[i]);
       }
-      if constexpr (MX) store_mxfp8<1>(&h[i].x, k < n, row * A.cols + c, A.payload, A.scale);
+      if constexpr (MX) store_mxfp8<1>(&h[i].x, in, row * A.cols + c0 + d, A.payload, A.scale);
     }
   }
 }
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   constexpr int kKinds = N;   // 1, or pairs from column 0 and pairs from column 1
   __shared__ float2 part[2][32];
   extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols]
-  const int T = blockDim.x, t = threadIdx.x;
+  const int T = blockDim.x, t = threadIdx.x, k0 = first_piece(t);
   struct Raw {
     typename Some::Raw h[kPieces], d[kPieces], s[DSUM ? kPieces : 1];
     typename One::Raw he, de, se;
@@ -474,9 +483,9 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   };
   auto load = [&](int64_t row, Raw& r) {
     const bool live = row < A.rows;
-    const void* h = row_of<DT>(A.h, row, A.ld_h);
-    const void* d = row_of<DT>(A.dy, row, A.ld_dy);
-    const void* s = row_of<DT>(A.dsum, row, A.ld_dsum);
+    const unsigned char* h = row_of<DT>(A.h, row, A.ld_h);
+    const unsigned char* d = row_of<DT>(A.dy, row, A.ld_dy);
+    const unsigned char* s = row_of<DT>(A.dsum, row, A.ld_dsum);
     r.head = N == 2 ? (int)(reinterpret_cast<uintptr_t>(h) >> 1) & 1 : 0;
     r.n = live ? (A.cols - r.head) / N : 0;
     r.edge = N == 1 || !live                        ? -1
@@ -489,16 +498,14 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       r.de = One::load(d, r.edge);
       if constexpr (DSUM) r.se = One::load(s, r.edge);
     }
+    const int c0 = (r.head + N * k0) * elem_size(DT);
+    h += c0, d += c0, s += c0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int k = i * T + t, c = r.head + N * k;
-      r.h[i] = r.d[i] = 0;
-      if constexpr (DSUM) r.s[i] = 0;
-      if (k < r.n) {
-        r.h[i] = Some::load(h, c);
-        r.d[i] = Some::load(d, c);
-        if constexpr (DSUM) r.s[i] = Some::load(s, c);
-      }
+      const bool in = k0 + 32 * i < r.n;
+      r.h[i] = in ? Some::load(h, i * Some::kStep) : 0;
+      r.d[i] = in ? Some::load(d, i * Some::kStep) : 0;
+      if constexpr (DSUM) r.s[i] = in ? Some::load(s, i * Some::kStep) : 0;
     }
   };
   float2 acc[kKinds][kPieces] = {};
@@ -511,36 +518,39 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     const int64_t row = base + threadIdx.y;
     Raw next;
     load(row + step, next);
-    auto gain = [&](int c) { return make_float2(__ldg(A.gain + c), N == 2 ? __ldg(A.gain + c + N - 1) : 0.0f); };
+    const float* g0 = A.gain + in.head + N * k0;
+    auto gain = [&](int i) {
+      return make_float2(__ldg(g0 + i * Some::kStep), N == 2 ? __ldg(g0 + i * Some::kStep + N - 1) : 0.0f);
+    };
     const float he = One::unpack(in.he).x, de = One::unpack(in.de).x, ge = in.edge >= 0 ? __ldg(A.gain + in.edge) : 0.0f;
     float2 sh = make_float2(he * he, 0.0f), sa = make_float2(de * ge * he, 0.0f);   // sums of h^2 and a h
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-      if (i * T + t < in.n) {
+      if (k0 + 32 * i < in.n) {
         const float2 h = Some::unpack(in.h[i]);
         sh = fma2(h, h, sh);
-        sa = fma2(mul2(Some::unpack(in.d[i]), gain(in.head + N * (i * T + t))), h, sa);
+        sa = fma2(mul2(Some::unpack(in.d[i]), gain(i)), h, sa);
       }
     const float2 sum = row_sum(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
     const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
     const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
-    void* dx = row_of<DT>(A.dx, row, A.ld_dx);
+    unsigned char* dx = row_of<DT>(A.dx, row, A.ld_dx);
     if (in.edge >= 0) {
       float o = inv * fmaf(he, c, de * ge);
       if constexpr (DSUM) o += One::unpack(in.se).x;
       One::store(dx, in.edge, make_float2(o, 0.0f));
       acc_edge = fmaf(de, he * inv, acc_edge);
     }
+    dx += (in.head + N * k0) * elem_size(DT);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-      if (i * T + t < in.n) {
-        const int col = in.head + N * (i * T + t);
+      if (k0 + 32 * i < in.n) {
         const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
-        const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(col)));
+        const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
         float2 o;
         if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
         else o = mul2(e, inv);
-        Some::store(dx, col, o);
+        Some::store(dx, i * Some::kStep, o);
         const float2 n = mul2(h, inv);
         if (kKinds == 1 || in.head == 0) acc[0][i] = fma2(d, n, acc[0][i]);
         else acc[kKinds - 1][i] = fma2(d, n, acc[kKinds - 1][i]);
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int c = kind + N * (i * T + t);
+      const int c = kind + N * (k0 + 32 * i);
       if (c + N <= A.cols) {
         mine[c] += acc[kind][i].x;
         if constexpr (N == 2) mine[c + 1] += acc[kind][i].y;
