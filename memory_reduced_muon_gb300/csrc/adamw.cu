@@ -1,8 +1,8 @@
 // Global gradient clipping and the AdamW step over many tensors.
 //
-// Both walk a list of tensors of any sizes cut into chunks: a plan's device
-// table says which tensor each chunk belongs to, and one CTA takes one chunk
-// (or, in the norm, every gridDim.x-th one).  There is no work per tensor, so
+// Both walk a list of tensors of any sizes cut into chunks, of which a plan
+// keeps a device table; one CTA takes one chunk (or, in the norm, every
+// gridDim.x-th one).  There is no work per tensor, so
 // hundreds of short vectors cost what one tensor of their total size costs.
 #include <algorithm>
 #include <cfloat>
@@ -19,24 +19,23 @@ namespace qm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kMaxElems = (int64_t)1 << 40;   // elements of one tensor
+constexpr int64_t kMaxElems = (int64_t)1 << 40;         // elements of one tensor
+constexpr int64_t kMaxChunks = ((int64_t)1 << 31) - 1;   // of a plan: a grid's CTAs
 
 // ---------------------------------------------------------------------------
 // global norm and clipping
 // ---------------------------------------------------------------------------
 constexpr int kClipChunk = 8192;   // elements
 
-struct ClipTensor {
+struct ClipChunk {
   void* grad;
-  int64_t numel;
-  int32_t first_chunk;
+  int32_t n;           // elements, up to kClipChunk
   int16_t dtype;
   int16_t vec;         // 16-byte aligned
 };
 
 struct ClipLaunch {
-  const ClipTensor* tensors;
-  const int32_t* chunk_tensor;
+  const ClipChunk* chunks;
   int32_t n_chunks;
   unsigned int* ticket;   // the plan's: 0 between calls
   double* partials;       // workspace, one per CTA
@@ -45,13 +44,14 @@ struct ClipLaunch {
 };
 
 template <int DT>
-__device__ __forceinline__ float chunk_sumsq(const ClipTensor& T, int64_t e0, int n, int tid) {
+__device__ __forceinline__ float chunk_sumsq(const ClipChunk& T, int tid) {
+  const int n = T.n;
   constexpr int K = Vec16<DT>::kElems;
   float2 s[2] = {};
   int done = 0;
-  const unsigned char* base = static_cast<const unsigned char*>(T.grad) + e0 * elem_size(DT);
+  const void* base = T.grad;
   if (T.vec) {
-    const uint4* p = reinterpret_cast<const uint4*>(base);
+    const uint4* p = static_cast<const uint4*>(base);
     const int nv = n / K;
 #pragma unroll 4
     for (int i = tid; i < nv; i += kThreads) {
@@ -74,13 +74,12 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const ClipLaunch L)
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   double acc = 0.0;
+  depends_wait();
   for (int c = blockIdx.x; c < L.n_chunks; c += gridDim.x) {
-    const ClipTensor T = L.tensors[__ldg(L.chunk_tensor + c)];
-    const int64_t e0 = (int64_t)(c - T.first_chunk) * kClipChunk;
-    const int n = (int)min(T.numel - e0, (int64_t)kClipChunk);
-    const float s = T.dtype == QMUON_BF16   ? chunk_sumsq<QMUON_BF16>(T, e0, n, tid)
-                    : T.dtype == QMUON_FP16 ? chunk_sumsq<QMUON_FP16>(T, e0, n, tid)
-                                            : chunk_sumsq<QMUON_FP32>(T, e0, n, tid);
+    const ClipChunk T = L.chunks[c];
+    const float s = T.dtype == QMUON_BF16   ? chunk_sumsq<QMUON_BF16>(T, tid)
+                    : T.dtype == QMUON_FP16 ? chunk_sumsq<QMUON_FP16>(T, tid)
+                                            : chunk_sumsq<QMUON_FP32>(T, tid);
     acc += (double)s;
   }
   auto block_sum = [&](double v) {
@@ -116,12 +115,13 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const ClipLaunch L)
 }
 
 template <int DT>
-__device__ __forceinline__ void chunk_scale(const ClipTensor& T, int64_t e0, int n, int tid, float c) {
+__device__ __forceinline__ void chunk_scale(const ClipChunk& T, int tid, float c) {
+  const int n = T.n;
   constexpr int K = Vec16<DT>::kElems;
   int done = 0;
-  unsigned char* base = static_cast<unsigned char*>(T.grad) + e0 * elem_size(DT);
+  void* base = T.grad;
   if (T.vec) {
-    uint4* p = reinterpret_cast<uint4*>(base);
+    uint4* p = static_cast<uint4*>(base);
     const int nv = n / K;
 #pragma unroll 4
     for (int i = tid; i < nv; i += kThreads) {
@@ -137,15 +137,14 @@ __device__ __forceinline__ void chunk_scale(const ClipTensor& T, int64_t e0, int
 }
 
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const ClipLaunch L) {
-  const float c = __ldg(L.norm + 1);
+  // the last chunks first: L2 still holds them from the norm
+  const ClipChunk T = L.chunks[gridDim.x - 1 - blockIdx.x];
+  depends_wait();
+  const float c = __ldcg(L.norm + 1);
   if (!(c < 1.0f)) return;   // within the bound, or not finite
-  const int k = blockIdx.x;
-  const ClipTensor T = L.tensors[__ldg(L.chunk_tensor + k)];
-  const int64_t e0 = (int64_t)(k - T.first_chunk) * kClipChunk;
-  const int n = (int)min(T.numel - e0, (int64_t)kClipChunk);
-  if (T.dtype == QMUON_BF16) chunk_scale<QMUON_BF16>(T, e0, n, threadIdx.x, c);
-  else if (T.dtype == QMUON_FP16) chunk_scale<QMUON_FP16>(T, e0, n, threadIdx.x, c);
-  else chunk_scale<QMUON_FP32>(T, e0, n, threadIdx.x, c);
+  if (T.dtype == QMUON_BF16) chunk_scale<QMUON_BF16>(T, threadIdx.x, c);
+  else if (T.dtype == QMUON_FP16) chunk_scale<QMUON_FP16>(T, threadIdx.x, c);
+  else chunk_scale<QMUON_FP32>(T, threadIdx.x, c);
 }
 
 // ---------------------------------------------------------------------------
@@ -299,12 +298,14 @@ __device__ __forceinline__ void with_types(const AdamTensor& T, F&& f) {
   else copy(std::integral_constant<int, QMUON_FP16>{});
 }
 
-// Calls f(T, C, c) for this CTA's chunk: chunk c of tensor T.
+// Calls f(T, C, c) for this CTA's chunk: chunk c of tensor T, by reference into
+// the plan's table.
 template <class F>
 __device__ __forceinline__ void for_chunk(const AdamLaunch& L, F&& f) {
-  const AdamTensor T = L.tensors[__ldg(L.chunk_tensor + blockIdx.x)];
-  const float scale = L.grad_scale ? __ldg(L.grad_scale) : 1.0f;
-  if (isfinite(scale)) f(T, adam_coef(L, T, scale), (int)blockIdx.x - T.first_chunk);
+  const AdamTensor& T = L.tensors[__ldg(L.chunk_tensor + blockIdx.x)];
+  depends_wait();
+  const float scale = L.grad_scale ? __ldcg(L.grad_scale) : 1.0f;
+  if (isfinite(scale)) f(T, scale, (int)blockIdx.x - T.first_chunk);
 }
 
 // ---- fp32 states ----
@@ -335,7 +336,9 @@ __device__ __forceinline__ void f32_fast(const AdamLaunch& L, const AdamTensor& 
   }
 }
 
-__device__ __noinline__ void f32_slow(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int c) {
+__device__ __noinline__ void f32_slow(const AdamLaunch& L, const AdamTensor& in_table, float scale, int c) {
+  const AdamTensor T = in_table;
+  const AdamCoef C = adam_coef(L, T, scale);
   const int t = threadIdx.x;
   const int64_t e0 = (int64_t)c * kAdamChunk;
   if (!T.vec) {   // neighbouring threads on neighbouring elements
@@ -368,11 +371,13 @@ __device__ __noinline__ void f32_slow(const AdamLaunch& L, const AdamTensor& T, 
 }
 
 __global__ void __launch_bounds__(kThreads, 4) adamw_f32_kernel(const __grid_constant__ AdamLaunch L) {
-  for_chunk(L, [&](const AdamTensor& T, const AdamCoef& C, int c) {
+  for_chunk(L, [&](const AdamTensor& in_table, float scale, int c) {
+    const AdamTensor T = in_table;
+    const AdamCoef C = adam_coef(L, T, scale);
     if (T.vec && (c > 0 || T.begin == 0) && (int64_t)(c + 1) * kAdamChunk <= T.end)
       with_types(T, [&](auto g, auto k) { f32_fast<decltype(g)::value, decltype(k)::value>(L, T, C, c); });
     else
-      f32_slow(L, T, C, c);
+      f32_slow(L, in_table, scale, c);
   });
 }
 
@@ -536,7 +541,9 @@ __device__ __forceinline__ void e4m3_fast(const AdamLaunch& L, const AdamTensor&
 
 // One block, whole or not, by the calling warp.
 template <bool SR>
-__device__ __noinline__ void e4m3_slow(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int64_t blk) {
+__device__ __noinline__ void e4m3_slow(const AdamLaunch& L, const AdamTensor& in_table, float scale, int64_t blk) {
+  const AdamTensor T = in_table;
+  const AdamCoef C = adam_coef(L, T, scale);
   const int lane = threadIdx.x & 31;
   const int64_t e0 = blk * kBlock + 4 * lane;
   uint8_t* mp = static_cast<uint8_t*>(T.m) + e0;
@@ -597,13 +604,15 @@ __device__ __noinline__ void e4m3_slow(const AdamLaunch& L, const AdamTensor& T,
 template <bool SR, int J>
 __global__ void __launch_bounds__(kThreads, 4) adamw_e4m3_kernel(const __grid_constant__ AdamLaunch L) {
   extern __shared__ __align__(16) unsigned char smem[];
-  for_chunk(L, [&](const AdamTensor& T, const AdamCoef& C, int c) {
+  for_chunk(L, [&](const AdamTensor& in_table, float scale, int c) {
+    const AdamTensor T = in_table;
+    const AdamCoef C = adam_coef(L, T, scale);
     constexpr int kPer = J * kWarps;
     const int64_t first = (int64_t)c * kPer, nb = (T.end + kBlock - 1) / kBlock;
     const int whole = T.vec ? (int)min((int64_t)kPer, T.end / kBlock - first) : 0, all = (int)min((int64_t)kPer, nb - first);
     if (whole > 0)
       with_types(T, [&](auto g, auto k) { e4m3_fast<decltype(g)::value, decltype(k)::value, SR, J>(L, T, C, first, whole, smem); });
-    for (int b = whole + (int)(threadIdx.x >> 5); b < all; b += kWarps) e4m3_slow<SR>(L, T, C, first + b);
+    for (int b = whole + (int)(threadIdx.x >> 5); b < all; b += kWarps) e4m3_slow<SR>(L, in_table, scale, first + b);
   });
 }
 
@@ -626,14 +635,14 @@ struct Chunks {
   std::vector<int32_t> first;   // per non-empty tensor
   bool add(int64_t numel, int64_t chunk) {
     const int64_t k = (numel + chunk - 1) / chunk;
-    if ((int64_t)tensor.size() + k > ((int64_t)1 << 31) - 1) return false;
+    if ((int64_t)tensor.size() + k > kMaxChunks) return false;
     first.push_back((int32_t)tensor.size());
     tensor.insert(tensor.end(), (size_t)k, (int32_t)first.size() - 1);
     return true;
   }
 };
 
-// One device allocation holding [head bytes, zeroed | tensors | chunk table].
+// One device allocation holding [256 zero bytes | tensors | chunk table].
 template <class Tensor>
 cudaError_t upload(const std::vector<Tensor>& ts, const std::vector<int32_t>& chunks, void** table, Tensor** d_ts,
                    int32_t** d_chunks) {
@@ -641,7 +650,7 @@ cudaError_t upload(const std::vector<Tensor>& ts, const std::vector<int32_t>& ch
   const size_t tb = (ts.size() * sizeof(Tensor) + 255) / 256 * 256;
   std::vector<unsigned char> blob(head + tb + chunks.size() * 4, 0);
   std::memcpy(blob.data() + head, ts.data(), ts.size() * sizeof(Tensor));
-  std::memcpy(blob.data() + head + tb, chunks.data(), chunks.size() * 4);
+  if (!chunks.empty()) std::memcpy(blob.data() + head + tb, chunks.data(), chunks.size() * 4);
   cudaError_t e = cudaMalloc(table, blob.size());
   if (e != cudaSuccess) return e;
   e = cudaMemcpy(*table, blob.data(), blob.size(), cudaMemcpyHostToDevice);
@@ -652,7 +661,7 @@ cudaError_t upload(const std::vector<Tensor>& ts, const std::vector<int32_t>& ch
   }
   unsigned char* b = static_cast<unsigned char*>(*table);
   *d_ts = reinterpret_cast<Tensor*>(b + head);
-  *d_chunks = reinterpret_cast<int32_t*>(b + head + tb);
+  if (d_chunks) *d_chunks = reinterpret_cast<int32_t*>(b + head + tb);
   return cudaSuccess;
 }
 
@@ -663,8 +672,7 @@ using namespace qm;
 
 struct qmuon_clip_plan {
   void* table = nullptr;   // the ticket is its first word
-  ClipTensor* tensors = nullptr;
-  int32_t* chunk_tensor = nullptr;
+  ClipChunk* chunks = nullptr;
   int32_t n_chunks = 0;
   int32_t grid = 0;
 };
@@ -685,26 +693,28 @@ extern "C" qmuon_status qmuon_clip_plan_create(const qmuon_grad* grads, int32_t 
     if (!out) return QMUON_ERR_INVALID_ARGUMENT;
     *out = nullptr;
     if (!grads || n <= 0) return QMUON_ERR_INVALID_ARGUMENT;
-    Chunks ch;
-    std::vector<ClipTensor> ts;
+    std::vector<ClipChunk> chunks;
     for (int32_t i = 0; i < n; ++i) {
       const qmuon_grad& g = grads[i];
       if (!is_dtype(g.dtype) || g.numel < 0 || g.numel > kMaxElems) return QMUON_ERR_INVALID_ARGUMENT;
       if (g.numel == 0) continue;
       if (!g.grad || !is_aligned(g.grad, elem_size(g.dtype))) return QMUON_ERR_INVALID_ARGUMENT;
-      if (!ch.add(g.numel, kClipChunk)) return QMUON_ERR_INVALID_ARGUMENT;
-      ts.push_back({g.grad, g.numel, ch.first.back(), (int16_t)g.dtype, (int16_t)is_aligned(g.grad, 16)});
+      if ((int64_t)chunks.size() + (g.numel + kClipChunk - 1) / kClipChunk > kMaxChunks) return QMUON_ERR_INVALID_ARGUMENT;
+      for (int64_t e = 0; e < g.numel; e += kClipChunk)
+        chunks.push_back({static_cast<unsigned char*>(g.grad) + e * elem_size(g.dtype),
+                          (int32_t)std::min<int64_t>(g.numel - e, kClipChunk), (int16_t)g.dtype,
+                          (int16_t)is_aligned(g.grad, 16)});
     }
-    if (ts.empty()) return QMUON_ERR_INVALID_ARGUMENT;
+    if (chunks.empty()) return QMUON_ERR_INVALID_ARGUMENT;
     std::unique_ptr<qmuon_clip_plan> P(new qmuon_clip_plan);
     int dev = 0, sms = 0, per_sm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, clip_norm_kernel, kThreads, 0);
     if (e != cudaSuccess) return set_error("qmuon_clip_plan_create (device)", e);
-    P->n_chunks = (int32_t)ch.tensor.size();
+    P->n_chunks = (int32_t)chunks.size();
     P->grid = std::min(P->n_chunks, sms * std::max(per_sm, 1));
-    e = upload(ts, ch.tensor, &P->table, &P->tensors, &P->chunk_tensor);
+    e = upload(chunks, {}, &P->table, &P->chunks, nullptr);
     if (e != cudaSuccess) return set_error("qmuon_clip_plan_create (tables)", e);
     *out = P.release();
     return QMUON_OK;
@@ -728,17 +738,15 @@ extern "C" qmuon_status qmuon_grad_clip(const qmuon_clip_plan* plan, float max_n
   if (!(max_norm > 0.0f) || (apply != 0 && apply != 1)) return QMUON_ERR_INVALID_ARGUMENT;
   if (ws_bytes < qmuon_clip_workspace_size(plan)) return QMUON_ERR_WORKSPACE_TOO_SMALL;
   ClipLaunch L{};
-  L.tensors = plan->tensors;
-  L.chunk_tensor = plan->chunk_tensor;
+  L.chunks = plan->chunks;
   L.n_chunks = plan->n_chunks;
   L.ticket = static_cast<unsigned int*>(plan->table);
   L.partials = static_cast<double*>(ws);
   L.norm = norm;
   L.max_norm = max_norm;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  clip_norm_kernel<<<plan->grid, kThreads, 0, s>>>(L);
-  if (apply) clip_scale_kernel<<<plan->n_chunks, kThreads, 0, s>>>(L);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(clip_norm_kernel, plan->grid, kThreads, 0, s, L);
+  if (e == cudaSuccess && apply) e = launch_dependent(clip_scale_kernel, plan->n_chunks, kThreads, 0, s, L);
   return e == cudaSuccess ? QMUON_OK : set_error("qmuon_grad_clip (launch)", e);
 }
 
@@ -858,8 +866,8 @@ qmuon_status adamw_step(const char* where, const qmuon_adamw_plan* plan, int64_t
   L.keys.set(seed);
   L.step = (uint32_t)t;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  adam_kernel(plan->state, sr, plan->per_warp)<<<plan->n_chunks, kThreads, plan->smem, s>>>(L);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_dependent(adam_kernel(plan->state, sr, plan->per_warp), plan->n_chunks, kThreads, plan->smem, s, L);
   return e == cudaSuccess ? QMUON_OK : set_error(where, e);
 }
 

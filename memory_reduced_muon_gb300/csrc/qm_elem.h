@@ -109,6 +109,29 @@ __device__ __forceinline__ void async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Every kernel of these operators is launched as a programmatic dependent of
+// what runs before it in its stream: it may start while that drains (and lets
+// its own successor do so), and touches nothing that others write before
+// depends_wait() has returned, which is once that has completed.  Every thread
+// calls it, so that a kernel never completes before its predecessor.
+__device__ __forceinline__ void depends_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <class... Params, class... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Two E4M3 codes (the low one first) from fp32, nearest even, |x| > 448
 // saturating, NaN to 0x7F; and back, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {

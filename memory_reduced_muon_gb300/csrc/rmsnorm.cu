@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
   __shared__ float part[2][32];
   const int T = blockDim.x, t = threadIdx.x;
   const int nv = A.cols / X::kElems;
+  depends_wait();
   int flip = 0;
   // every thread of a warp leaves the loop together: the CTA's rows of one pass are one step of it
   for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
   using Some = Piece<DT, N>;
   __shared__ float part[2][32];
   const int T = blockDim.x, t = threadIdx.x;
+  depends_wait();
   int flip = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
     const int64_t row = r0 + threadIdx.y;
@@ -292,6 +294,7 @@ template <int DT, int N, bool MX>
 __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_constant__ FwdArgs A) {
   __shared__ float part[2][32];
   const int T = blockDim.x, t = threadIdx.x;
+  depends_wait();
   int flip = 0;
   for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
     const void* x = row_of<DT>(A.x, row, A.ld_x);
@@ -354,6 +357,7 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
   __shared__ float2 part[2][32];
   extern __shared__ __align__(16) unsigned char smem[];
   const int T = blockDim.x, t = threadIdx.x, threads = T * blockDim.y, me = threadIdx.y * T + t;
+  depends_wait();
   uint4* ring = reinterpret_cast<uint4*>(smem) + me;   // [stages][kArrays][V][threads]
   const int nv = A.cols / X::kElems;
   const float4* gain = reinterpret_cast<const float4*>(A.gain) + t * (P / 2);
@@ -434,7 +438,6 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
     issue(row + stages * step, slot);
     s = s + 1 == stages ? 0 : s + 1;
   }
-  asm volatile("griddepcontrol.launch_dependents;");
   float* out = A.partial + (int64_t)blockIdx.x * A.cols;
   if (T > 32) {
 #pragma unroll
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   __shared__ float2 part[2][32];
   extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols]
   const int T = blockDim.x, t = threadIdx.x, k0 = first_piece(t);
+  depends_wait();
   struct Raw {
     typename Some::Raw h[kPieces], d[kPieces], s[DSUM ? kPieces : 1];
     typename One::Raw he, de, se;
@@ -542,22 +546,23 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       acc_edge = fmaf(de, he * inv, acc_edge);
     }
     dx += (in.head + N * k0) * elem_size(DT);
+    auto finish = [&](float2* sums) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (k0 + 32 * i < in.n) {
-        const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
-        const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
-        float2 o;
-        if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
-        else o = mul2(e, inv);
-        Some::store(dx, i * Some::kStep, o);
-        const float2 n = mul2(h, inv);
-        if (kKinds == 1 || in.head == 0) acc[0][i] = fma2(d, n, acc[0][i]);
-        else acc[kKinds - 1][i] = fma2(d, n, acc[kKinds - 1][i]);
-      }
+      for (int i = 0; i < kPieces; ++i)
+        if (k0 + 32 * i < in.n) {
+          const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
+          const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
+          float2 o;
+          if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
+          else o = mul2(e, inv);
+          Some::store(dx, i * Some::kStep, o);
+          sums[i] = fma2(d, mul2(h, inv), sums[i]);
+        }
+    };
+    if (kKinds == 1 || in.head == 0) finish(acc[0]);
+    else finish(acc[kKinds - 1]);
     in = next;
   }
-  asm volatile("griddepcontrol.launch_dependents;");
   // the columns' sums: those of rows whose pairs start at column 0, then at column 1, then the ends'
   float* mine = s_acc + (size_t)threadIdx.y * A.cols;
   for (int c = t; c < A.cols; c += T) mine[c] = 0.0f;
@@ -591,6 +596,7 @@ template <int DT, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_constant__ BwdArgs A) {
   __shared__ float2 part[2][32];
   const int T = blockDim.x, t = threadIdx.x;
+  depends_wait();
   float* acc = A.partial + (int64_t)blockIdx.x * A.cols;
   int flip = 0;
   for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
@@ -633,14 +639,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_con
   }
 }
 
-// dgain[c] = sum of n rows of partial, in an order that n alone fixes.  A
-// launch's end to the next one's start is hidden: the kernel starts while the
-// one before it drains (griddepcontrol), and waits for it to complete.
+// dgain[c] = sum of n rows of partial, in an order that n alone fixes.
 constexpr int kSlices = 32;
 
 __global__ void __launch_bounds__(1024) dgain_kernel(const float* partial, int32_t n, int32_t cols, float* dgain) {
   __shared__ float s[kSlices][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  depends_wait();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
   if (c < cols) {
@@ -734,7 +738,7 @@ bool rows_alike(std::initializer_list<Strided> arrays) {
 }
 
 template <int DT, bool RES, bool MX>
-void launch_fwd(const FwdArgs& A, cudaStream_t s) {
+cudaError_t launch_fwd(const FwdArgs& A, cudaStream_t s) {
   constexpr int K = Vec16<DT>::kElems;
   // Four vectors per thread, so that a row takes few warps (and the bytes in flight are many); where rows do not fill
   // the SMs, one, so that a row is done sooner: one row of 4096 bf16 in FEW_US, in FEW_US4 with four.
@@ -748,22 +752,19 @@ void launch_fwd(const FwdArgs& A, cudaStream_t s) {
   const bool pieces = !A.vec && T <= 1024;
   const dim3 block = S.V ? S.block() : pieces ? Shape{(int)T, 0}.block() : dim3(1024);
   const unsigned grid = (unsigned)std::min<int64_t>((A.rows + block.y - 1) / block.y, ((int64_t)1 << 31) - 1);
-  if (S.V == 1) rmsnorm_fwd_rows_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
-  else if (S.V == 2) rmsnorm_fwd_rows_kernel<DT, 2, RES, MX><<<grid, block, 0, s>>>(A);
-  else if (S.V == 4) rmsnorm_fwd_rows_kernel<DT, 4, RES, MX><<<grid, block, 0, s>>>(A);
-  else if (A.vec) rmsnorm_fwd_walk_kernel<DT, K, MX><<<grid, block, 0, s>>>(A);
-  else if (!pieces) rmsnorm_fwd_walk_kernel<DT, 1, MX><<<grid, block, 0, s>>>(A);
-  else if constexpr (!MX && DT != QMUON_FP32) {
-    if (pairs) rmsnorm_fwd_pieces_kernel<DT, 2, RES, MX><<<grid, block, 0, s>>>(A);
-    else rmsnorm_fwd_pieces_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
-  } else {
-    rmsnorm_fwd_pieces_kernel<DT, 1, RES, MX><<<grid, block, 0, s>>>(A);
-  }
+  if (S.V == 1) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 1, RES, MX>, grid, block, 0, s, A);
+  if (S.V == 2) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 2, RES, MX>, grid, block, 0, s, A);
+  if (S.V == 4) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 4, RES, MX>, grid, block, 0, s, A);
+  if (A.vec) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K, MX>, grid, block, 0, s, A);
+  if (!pieces) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 1, MX>, grid, block, 0, s, A);
+  if constexpr (!MX && DT != QMUON_FP32)
+    if (pairs) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, 2, RES, MX>, grid, block, 0, s, A);
+  return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, 1, RES, MX>, grid, block, 0, s, A);
 }
 template <int DT>
-void launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
-  if (A.payload) A.residual ? launch_fwd<DT, true, true>(A, s) : launch_fwd<DT, false, true>(A, s);
-  else A.residual ? launch_fwd<DT, true, false>(A, s) : launch_fwd<DT, false, false>(A, s);
+cudaError_t launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
+  if (A.payload) return A.residual ? launch_fwd<DT, true, true>(A, s) : launch_fwd<DT, false, true>(A, s);
+  return A.residual ? launch_fwd<DT, true, false>(A, s) : launch_fwd<DT, false, false>(A, s);
 }
 
 // CTAs of the backward pass, each with its row of `partial`: at most four per SM.
@@ -779,8 +780,8 @@ cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* g
   const int stages = std::min(3, std::max(1, kMaxSmem / row));
   const int smem = std::max(stages * row, block.y > 1 ? (int)block.y * A.cols * 4 : 0);
   *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, kMaxSmem / smem);
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_rows_kernel<DT, V, DSUM>));
-  if (e == cudaSuccess) rmsnorm_bwd_rows_kernel<DT, V, DSUM><<<*grid, block, smem, s>>>(A, stages);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_rows_kernel<DT, V, DSUM>));
+  if (e == cudaSuccess) e = launch_dependent(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, *grid, block, smem, s, A, stages);
   return e;
 }
 
@@ -801,20 +802,19 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
       *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, 1024 / (block.x * block.y));
       if constexpr (DT != QMUON_FP32) {
         if (pairs) {
-          const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>));
-          if (e == cudaSuccess) rmsnorm_bwd_pieces_kernel<DT, 2, DSUM><<<*grid, block, smem, s>>>(A);
+          cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>));
+          if (e == cudaSuccess) e = launch_dependent(rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>, *grid, block, smem, s, A);
           return e;
         }
       }
-      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 1, DSUM>));
-      if (e == cudaSuccess) rmsnorm_bwd_pieces_kernel<DT, 1, DSUM><<<*grid, block, smem, s>>>(A);
+      cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 1, DSUM>));
+      if (e == cudaSuccess) e = launch_dependent(rmsnorm_bwd_pieces_kernel<DT, 1, DSUM>, *grid, block, smem, s, A);
       return e;
     }
   }
   *grid = bwd_grid(A.rows, sms, 2);
-  if (A.vec) rmsnorm_bwd_walk_kernel<DT, Vec16<DT>::kElems><<<*grid, 1024, 0, s>>>(A);
-  else rmsnorm_bwd_walk_kernel<DT, 1><<<*grid, 1024, 0, s>>>(A);
-  return cudaSuccess;
+  if (A.vec) return launch_dependent(rmsnorm_bwd_walk_kernel<DT, Vec16<DT>::kElems>, *grid, 1024, 0, s, A);
+  return launch_dependent(rmsnorm_bwd_walk_kernel<DT, 1>, *grid, 1024, 0, s, A);
 }
 template <int DT>
 cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
@@ -855,10 +855,9 @@ extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stre
   FwdArgs A{n->x,    n->residual,    n->gain,   n->sum,  n->y,    n->payload, n->scale_inv, n->rows,
             n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n->dtype == QMUON_BF16) launch_fwd_dt<QMUON_BF16>(A, s);
-  else if (n->dtype == QMUON_FP16) launch_fwd_dt<QMUON_FP16>(A, s);
-  else launch_fwd_dt<QMUON_FP32>(A, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = n->dtype == QMUON_BF16   ? launch_fwd_dt<QMUON_BF16>(A, s)
+                        : n->dtype == QMUON_FP16 ? launch_fwd_dt<QMUON_FP16>(A, s)
+                                                 : launch_fwd_dt<QMUON_FP32>(A, s);
   return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_forward (launch)", e);
 }
 
@@ -893,17 +892,7 @@ extern "C" qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* n, void
                   : n->dtype == QMUON_FP16 ? launch_bwd_dt<QMUON_FP16>(A, sms, &grid, s)
                                            : launch_bwd_dt<QMUON_FP32>(A, sms, &grid, s);
   if (e == cudaSuccess) {
-    e = cudaGetLastError();
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((n->cols + 31) / 32));
-    cfg.blockDim = dim3(32, kSlices);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, dgain_kernel, (const float*)A.partial, (int32_t)grid, A.cols, n->dgain);
+    e = launch_dependent(dgain_kernel, (unsigned)((n->cols + 31) / 32), dim3(32, kSlices), 0, s, A.partial, grid, A.cols, n->dgain);
   }
   return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (launch)", e);
 }
