@@ -2,8 +2,8 @@
 //
 // Both walk a list of tensors of any sizes cut into chunks, of which a plan
 // keeps a device table; one CTA takes one chunk (or, in the norm, every
-// gridDim.x-th one).  There is no work per tensor, so
-// hundreds of short vectors cost what one tensor of their total size costs.
+// gridDim.x-th one).  There is no work per tensor, so hundreds of short vectors
+// cost what one tensor of their total size costs.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -69,6 +69,8 @@ __device__ __forceinline__ float chunk_sumsq(const ClipChunk& T, int tid) {
   return (s[0].x + s[0].y) + (s[1].x + s[1].y);
 }
 
+// One read: 872M bf16 elements in 258 us, 6.76 TB/s.  A few elements are bound
+// by latency: 24 vectors of 4096 take 5 us, most of it the two reductions.
 __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const ClipLaunch L) {
   __shared__ double s_warp[kThreads / 32];
   __shared__ int s_last;
@@ -136,6 +138,7 @@ __device__ __forceinline__ void chunk_scale(const ClipChunk& T, int tid, float c
   for (int i = done + tid; i < n; i += kThreads) store_elem<DT>(base, i, load_elem<DT>(base, i) * c);
 }
 
+// Another read and a write, at 7.1 TB/s.
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const ClipLaunch L) {
   // the last chunks first: L2 still holds them from the norm
   const ClipChunk T = L.chunks[gridDim.x - 1 - blockIdx.x];
@@ -223,7 +226,9 @@ __device__ __forceinline__ void adam_pair(const AdamLaunch& L, const AdamCoef& C
 // chunk and leaves keeps DRAM busier than one that stays: the same traffic
 // without any arithmetic runs at 7.06 TB/s with one CTA per 2048 elements and at
 // 6.4 with the resident CTAs looping over chunks (2^28 elements), rings of
-// asynchronous copies ahead of them or not.  Chunks that lie wholly inside a
+// asynchronous copies ahead of them or not.  What is left is DRAM: 419M elements
+// with fp32 states, bf16 gradients and a bf16 copy take 1656 us (7.09 TB/s), with
+// 8-bit states 995 us (6.77 TB/s).  Chunks that lie wholly inside a
 // tensor whose arrays are aligned (AdamTensor::vec) move in vectors; in the
 // chunks at a tensor's ends, and in all of an unaligned one, quads that are not
 // whole move element by element.
@@ -417,9 +422,8 @@ struct E4m3Quads {
   float m_max, r_max;
 };
 
-// Decodes, updates and, for the n[k] elements of each quad that exist, takes
-// part in the block's maxima; m and r leave scaled for encoding, mc and vc as
-// the new codes.
+// Decodes a block, updates it and encodes it under its new maxima, in which
+// only the n[k] elements of each quad that exist take part.
 template <bool SR, bool WHOLE>
 __device__ __forceinline__ void e4m3_update(const AdamLaunch& L, const AdamCoef& C, E4m3Quads& q, const int* n, int64_t e0,
                                             int32_t index) {
@@ -476,11 +480,15 @@ struct __align__(16) E4m3Stage {
 };
 
 // J whole blocks per warp, all of their loads in flight from the start: the
-// copies need no registers while they are (64 registers' worth of blocks in
-// flight per thread were too few for the arithmetic's length).
+// copies need no registers while they are.  With one block per warp, loaded
+// into registers, the arithmetic (48 instructions per element, 75 with random
+// numbers) left too few bytes in flight.  2^28 elements with a copy: 776 us so,
+// 680 with J = 2, 653 with 3 (6.6 TB/s), 647 with 4; rounded stochastically 743,
+// 688 and 713, where the arithmetic is the bound.
 template <int GDT, int CDT, bool SR, int J>
 __device__ __forceinline__ void e4m3_fast(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int64_t first, int n,
                                           unsigned char* smem) {
+  static_assert(J <= 3, "one wait per block in flight below");
   constexpr int kGs = elem_size(GDT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   E4m3Stage<GDT>* ring = reinterpret_cast<E4m3Stage<GDT>*>(smem) + warp;
@@ -504,10 +512,9 @@ __device__ __forceinline__ void e4m3_fast(const AdamLaunch& L, const AdamTensor&
   }
 #pragma unroll 1
   for (int j = 0; j < n; ++j, blk += kWarps) {
-    if (J == 1 || j == J - 1) async_wait<0>();
+    if (j == J - 1) async_wait<0>();
     else if (j == J - 2) async_wait<1>();
-    else if (j == J - 3) async_wait<2>();
-    else async_wait<3>();
+    else async_wait<2>();
     __syncwarp();   // the other lanes' copies
     const E4m3Stage<GDT>& S = ring[j * kWarps];
     const int64_t e = blk * kBlock + 4 * lane;   // of the first quad; the second is 128 on
