@@ -203,11 +203,14 @@ struct Piece {
   }
 };
 
-constexpr int kPieces = 8;   // per thread
-// A thread's first piece, counted along the row: warp w has pieces 256 w .. 256 w + 255, lane by lane.
-__device__ __forceinline__ int first_piece(int t) { return (t >> 5) * (32 * kPieces) + (t & 31); }
+// A thread has P pieces: piece i is 32 i on from its first one, so that a warp's
+// lie side by side.
+template <int P>
+__device__ __forceinline__ int first_piece(int t) {
+  return (t >> 5) * (32 * P) + (t & 31);
+}
 
-template <int DT, int N, bool RES, bool MX>
+template <int DT, int N, int P, bool RES, bool MX>
 __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_constant__ FwdArgs A) {
   using One = Piece<DT, 1>;
   using Some = Piece<DT, N>;
@@ -227,26 +230,26 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
                      : t == 0 && head        ? 0
                      : t == T - 1 && ((A.cols - head) & 1) ? A.cols - 1
                                              : -1;
-    typename Some::Raw rx[kPieces], rr[RES ? kPieces : 1];
+    typename Some::Raw rx[P], rr[RES ? P : 1];
     typename One::Raw ex = 0, er = 0;
     if (edge >= 0) {
       ex = One::load(x, edge);
       if constexpr (RES) er = One::load(res, edge);
     }
-    const int k0 = first_piece(t), c0 = head + N * k0;
+    const int k0 = first_piece<P>(t), c0 = head + N * k0;
     x += c0 * elem_size(DT);
     res += c0 * elem_size(DT);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       rx[i] = k0 + 32 * i < n ? Some::load(x, i * Some::kStep) : 0;
       if constexpr (RES) rr[i] = k0 + 32 * i < n ? Some::load(res, i * Some::kStep) : 0;
     }
-    float2 h[kPieces], ss = make_float2(0.0f, 0.0f);
+    float2 h[P], ss = make_float2(0.0f, 0.0f);
     float he = One::unpack(ex).x;
     if constexpr (RES) he += One::unpack(er).x;
     ss.x = he * he;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       h[i] = Some::unpack(rx[i]);
       if constexpr (RES) h[i] = add2(h[i], Some::unpack(rr[i]));
       ss = fma2(h[i], h[i], ss);
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
     y += c0 * elem_size(DT);
     const float* gain = A.gain + c0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       const bool in = k0 + 32 * i < n;
       const int d = i * Some::kStep;
       if (in) {
@@ -471,17 +474,17 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
 // columns differ between the two kinds of rows: it sums each kind's apart.
 constexpr int bwd_piece_threads = 512;
 
-template <int DT, int N, bool DSUM>
+template <int DT, int N, int P, bool DSUM>
 __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(const __grid_constant__ BwdArgs A) {
   using One = Piece<DT, 1>;
   using Some = Piece<DT, N>;
   constexpr int kKinds = N;   // 1, or pairs from column 0 and pairs from column 1
   __shared__ float2 part[2][32];
   extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols]
-  const int T = blockDim.x, t = threadIdx.x, k0 = first_piece(t);
+  const int T = blockDim.x, t = threadIdx.x, k0 = first_piece<P>(t);
   depends_wait();
   struct Raw {
-    typename Some::Raw h[kPieces], d[kPieces], s[DSUM ? kPieces : 1];
+    typename Some::Raw h[P], d[P], s[DSUM ? P : 1];
     typename One::Raw he, de, se;
     int head, n, edge;
   };
@@ -505,14 +508,14 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     const int c0 = (r.head + N * k0) * elem_size(DT);
     h += c0, d += c0, s += c0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       const bool in = k0 + 32 * i < r.n;
       r.h[i] = in ? Some::load(h, i * Some::kStep) : 0;
       r.d[i] = in ? Some::load(d, i * Some::kStep) : 0;
       if constexpr (DSUM) r.s[i] = in ? Some::load(s, i * Some::kStep) : 0;
     }
   };
-  float2 acc[kKinds][kPieces] = {};
+  float2 acc[kKinds][P] = {};
   float acc_edge = 0.0f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   Raw in;
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     const float he = One::unpack(in.he).x, de = One::unpack(in.de).x, ge = in.edge >= 0 ? __ldg(A.gain + in.edge) : 0.0f;
     float2 sh = make_float2(he * he, 0.0f), sa = make_float2(de * ge * he, 0.0f);   // sums of h^2 and a h
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < P; ++i)
       if (k0 + 32 * i < in.n) {
         const float2 h = Some::unpack(in.h[i]);
         sh = fma2(h, h, sh);
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     dx += (in.head + N * k0) * elem_size(DT);
     auto finish = [&](float2* sums) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
+      for (int i = 0; i < P; ++i)
         if (k0 + 32 * i < in.n) {
           const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
           const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   for (int kind = 0; kind < kKinds; ++kind) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       const int c = kind + N * (k0 + 32 * i);
       if (c + N <= A.cols) {
         mine[c] += acc[kind][i].x;
@@ -699,6 +702,19 @@ Shape pick_shape(int nv, int want, int most, int least, MaxThreads max_threads) 
   return {0, 0};
 }
 
+// Threads and pieces per thread of a row of n pieces: a warp with two for short
+// rows (six more would be tests without work: 300000 x 100 bf16 forward in
+// 61 us with two, 91 with eight), else `want`, or eight where those need too
+// many threads.  V == 0: too long.
+Shape piece_shape(int n, int want, int max_threads) {
+  if (n <= 64) return {32, 2};
+  for (int V = want; V <= 8; V *= 2) {
+    const int T = ((n + V - 1) / V + 31) / 32 * 32;
+    if (T <= max_threads) return {T, V};
+  }
+  return {0, 0};
+}
+
 int device_sms() {
   static std::atomic<int> cached[64] = {};
   int dev = 0, sms = 0;
@@ -748,19 +764,24 @@ cudaError_t launch_fwd(const FwdArgs& A, cudaStream_t s) {
   const Shape S = A.vec ? pick_shape(A.cols / K, few ? 1 : 4, 4, least, fwd_max_threads) : Shape{0, 0};
   const bool pairs = !MX && DT != QMUON_FP32 &&
                      rows_alike({{A.x, A.ld_x}, {A.residual, A.ld_residual}, {A.sum, A.ld_sum}, {A.y, A.ld_y}});
-  // unaligned: threads for the row's pieces, whole warps
-  const int64_t T = std::max(((A.cols / (pairs ? 2 : 1) + kPieces - 1) / kPieces + 31) / 32 * 32, 32);
-  const bool pieces = !A.vec && T <= 1024;
-  const dim3 block = S.V ? S.block() : pieces ? Shape{(int)T, 0}.block() : dim3(1024);
+  const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 4, 1024);
+  const bool pieces = !A.vec && C.V;
+  const dim3 block = S.V ? S.block() : pieces ? C.block() : dim3(1024);
   const unsigned grid = (unsigned)std::min<int64_t>((A.rows + block.y - 1) / block.y, ((int64_t)1 << 31) - 1);
   if (S.V == 1) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 1, RES, MX>, grid, block, 0, s, A);
   if (S.V == 2) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 2, RES, MX>, grid, block, 0, s, A);
   if (S.V == 4) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 4, RES, MX>, grid, block, 0, s, A);
   if (A.vec) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K, MX>, grid, block, 0, s, A);
   if (!pieces) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 1, MX>, grid, block, 0, s, A);
+  auto in_pieces = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (C.V == 2) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 2, RES, MX>, grid, block, 0, s, A);
+    if (C.V == 4) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 4, RES, MX>, grid, block, 0, s, A);
+    return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 8, RES, MX>, grid, block, 0, s, A);
+  };
   if constexpr (!MX && DT != QMUON_FP32)
-    if (pairs) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, 2, RES, MX>, grid, block, 0, s, A);
-  return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, 1, RES, MX>, grid, block, 0, s, A);
+    if (pairs) return in_pieces(std::integral_constant<int, 2>{});
+  return in_pieces(std::integral_constant<int, 1>{});
 }
 template <int DT>
 cudaError_t launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
@@ -796,21 +817,22 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
   if (!A.vec) {
     const bool pairs =
         DT != QMUON_FP32 && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}});
-    const int64_t T = std::max(((A.cols / (pairs ? 2 : 1) + kPieces - 1) / kPieces + 31) / 32 * 32, 32);
-    if (T <= bwd_piece_threads) {
-      const dim3 block = Shape{(int)T, 0}.block();
+    const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 8, bwd_piece_threads);
+    if (C.V) {
+      const dim3 block = C.block();
       const int smem = (int)block.y * A.cols * 4;
       *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, 1024 / (block.x * block.y));
-      if constexpr (DT != QMUON_FP32) {
-        if (pairs) {
-          cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>));
-          if (e == cudaSuccess) e = launch_dependent(rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>, *grid, block, smem, s, A);
-          return e;
-        }
-      }
-      cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_pieces_kernel<DT, 1, DSUM>));
-      if (e == cudaSuccess) e = launch_dependent(rmsnorm_bwd_pieces_kernel<DT, 1, DSUM>, *grid, block, smem, s, A);
-      return e;
+      auto in_pieces = [&](auto n, auto p) {
+        const auto kernel = rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>;
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
+        return e != cudaSuccess ? e : launch_dependent(kernel, *grid, block, smem, s, A);
+      };
+      const std::integral_constant<int, 1> one;
+      const std::integral_constant<int, 2> two;
+      const std::integral_constant<int, 8> eight;
+      if constexpr (DT != QMUON_FP32)
+        if (pairs) return C.V == 2 ? in_pieces(two, two) : in_pieces(two, eight);
+      return C.V == 2 ? in_pieces(one, two) : in_pieces(one, eight);
     }
   }
   *grid = bwd_grid(A.rows, sms, 2);
