@@ -29,6 +29,9 @@ What it computes, and where that is defined:
   refreshed by one warm-started power iteration plus a grid-quantised
   residual ("4-bit-Muon-GRASP", the update equations and the grid
   quantisation on that page).
+* ``oracle.training`` -- gradient clipping, AdamW with fp32 and 8-bit states,
+  and the RMS norm with its gradients (the definitions of the library's
+  header; the pages give none).
 
 Every function names the passage it follows.  Where the pages are silent the
 docstring states the reading taken.  Pins (tests that tie each function to
