@@ -33,7 +33,8 @@ struct FwdArgs {
   uint8_t* payload;       // MXFP8 output, or null
   uint8_t* scale;
   int64_t rows, ld_x, ld_residual, ld_sum, ld_y;
-  int32_t cols, vec;
+  int32_t cols;
+  int32_t align;          // bytes on which all rows start, and which divide a row: 2 (4 for fp32), 4, 8 or 16
   float eps, inv_cols;
 };
 
@@ -45,7 +46,8 @@ struct BwdArgs {
   void* dx;
   float* partial;         // [grid][cols]
   int64_t rows, ld_dy, ld_h, ld_dsum, ld_dx;
-  int32_t cols, vec;
+  int32_t cols;
+  int32_t align;          // bytes on which all rows start, and which divide a row: 2 (4 for fp32), 4, 8 or 16
   float eps, inv_cols;
 };
 
@@ -56,20 +58,24 @@ __device__ __forceinline__ auto row_of(P* base, int64_t row, int64_t ld) {
 }
 
 // Sum of v over the T threads of a row, the same bits in all of them.  T > 32:
-// `part` is one value per warp; callers alternate two of them, so that one
-// barrier per sum is enough.
+// `part` is one value per warp of the CTA; callers alternate two of them, so
+// that one barrier per sum is enough.  MANY: the CTA may have several rows of
+// more than a warp, each with a barrier of its own (a kernel that names its
+// barriers at run time reserves all sixteen, which leaves an SM few CTAs).
 __device__ __forceinline__ float plus(float a, float b) { return a + b; }
 __device__ __forceinline__ float2 plus(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ float lane_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
 __device__ __forceinline__ float2 lane_xor(float2 v, int o) { return make_float2(lane_xor(v.x, o), lane_xor(v.y, o)); }
 
-template <class S>
+template <bool MANY, class S>
 __device__ __forceinline__ S row_sum(S v, int T, S* part) {
   for (int o = min(T, 32) >> 1; o > 0; o >>= 1) v = plus(v, lane_xor(v, o));
   if (T <= 32) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = T >> 5;
+  if constexpr (MANY) part += threadIdx.y * nw;
   if (lane == 0) part[warp] = v;
-  __syncthreads();
+  if constexpr (MANY) asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(T) : "memory");
+  else __syncthreads();
   v = lane < nw ? part[lane] : S{};
   for (int o = 16; o > 0; o >>= 1) v = plus(v, lane_xor(v, o));
   return v;
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
       for (int i = 0; i < V; ++i)
         if (i * T + t < n) sum[i * T] = X::pack(h[i]);
     }
-    const float inv = inverse_norm(row_sum(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
+    const float inv = inverse_norm(row_sum<false>(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
     uint4* y = reinterpret_cast<uint4*>(row_of<DT>(A.y, row, A.ld_y)) + t;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
       if constexpr (RES) h[i] = add2(h[i], Some::unpack(rr[i]));
       ss = fma2(h[i], h[i], ss);
     }
-    const float inv = inverse_norm(row_sum(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
+    const float inv = inverse_norm(row_sum<false>(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
     unsigned char* sum = row_of<DT>(A.sum, row, A.ld_sum);
     unsigned char* y = row_of<DT>(A.y, row, A.ld_y);
     if (edge >= 0) {
@@ -278,17 +284,61 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
   }
 }
 
-// N consecutive elements of a row at column c, moved at once: one, or a
-// 16-byte vector.
+// N consecutive elements of a row at column c, moved at once: one, or 4, 8 or
+// 16 bytes of them.
 template <int DT, int N>
 __device__ __forceinline__ void load_n(const void* row, int c, float* f) {
-  if constexpr (N == 1) f[0] = load_elem<DT>(row, c);
-  else Vec16<DT>::unpack(reinterpret_cast<const uint4*>(row)[c / N], reinterpret_cast<float2*>(f));
+  constexpr int kBytes = N * elem_size(DT);
+  const void* p = static_cast<const unsigned char*>(row) + (int64_t)c * elem_size(DT);
+  if constexpr (N == 1) {
+    f[0] = load_elem<DT>(p, 0);
+  } else {
+    uint32_t w[kBytes / 4];
+    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(w) = *static_cast<const uint4*>(p);
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(w) = *static_cast<const uint2*>(p);
+    else w[0] = *static_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) {
+      if constexpr (DT == QMUON_FP32) f[i] = __uint_as_float(w[i]);
+      else reinterpret_cast<float2*>(f)[i] = unpack2<DT>(w[i]);
+    }
+  }
 }
 template <int DT, int N>
 __device__ __forceinline__ void store_n(void* row, int c, const float* f) {
-  if constexpr (N == 1) store_elem<DT>(row, c, f[0]);
-  else reinterpret_cast<uint4*>(row)[c / N] = Vec16<DT>::pack(reinterpret_cast<const float2*>(f));
+  constexpr int kBytes = N * elem_size(DT);
+  void* p = static_cast<unsigned char*>(row) + (int64_t)c * elem_size(DT);
+  if constexpr (N == 1) {
+    store_elem<DT>(p, 0, f[0]);
+  } else {
+    uint32_t w[kBytes / 4];
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) {
+      if constexpr (DT == QMUON_FP32) w[i] = __float_as_uint(f[i]);
+      else w[i] = pack2<DT>(f[2 * i], f[2 * i + 1]);
+    }
+    if constexpr (kBytes == 16) *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 8) *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *static_cast<uint32_t*>(p) = w[0];
+  }
+}
+
+// N fp32 values side by side, N of the gain or of its gradient.
+template <int N>
+__device__ __forceinline__ void load_f32(const float* p, float* f) {
+  if constexpr (N == 1) f[0] = p[0];
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(p);
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(p + i);
+}
+template <int N>
+__device__ __forceinline__ void store_f32(float* p, const float* f) {
+  if constexpr (N == 1) p[0] = f[0];
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(f);
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = *reinterpret_cast<const float4*>(f + i);
 }
 
 // Rows longer than a CTA holds: read for the sum, and again, out of the
@@ -319,7 +369,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_con
 #pragma unroll
       for (int j = 0; j < N; ++j) ss = fmaf(h[j], h[j], ss);
     }
-    const float inv = inverse_norm(row_sum(ss, T, part[flip]), A.inv_cols, A.eps);
+    const float inv = inverse_norm(row_sum<false>(ss, T, part[flip]), A.inv_cols, A.eps);
 #pragma unroll 2
     for (int c0 = 0; c0 < A.cols; c0 += T * N) {   // the same number of passes in every thread: lanes share scales
       const int c = c0 + t * N;
@@ -327,8 +377,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_con
       if (c < A.cols) {
         load(c, h);
         if (A.sum) store_n<DT, N>(row_of<DT>(A.sum, row, A.ld_sum), c, h);
+        float g[N];
+        load_f32<N>(A.gain + c, g);
 #pragma unroll
-        for (int j = 0; j < N; ++j) h[j] = h[j] * inv * __ldg(A.gain + c + j);
+        for (int j = 0; j < N; ++j) h[j] = h[j] * inv * g[j];
         if (A.y) store_n<DT, N>(row_of<DT>(A.y, row, A.ld_y), c, h);
       }
       if constexpr (MX) store_mxfp8<N>(h, c < A.cols, row * A.cols + c, A.payload, A.scale);
@@ -416,7 +468,7 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
           sa = fma2(mul2(d[j], kKeepGain ? kept[i % V][j] : g[j]), h[j], sa);
         }
       }
-    const float2 sum = row_sum(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
+    const float2 sum = row_sum<true>(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
     const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
     const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
     uint4* dx = reinterpret_cast<uint4*>(row_of<DT>(A.dx, row, A.ld_dx)) + t;
@@ -442,7 +494,7 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
     s = s + 1 == stages ? 0 : s + 1;
   }
   float* out = A.partial + (int64_t)blockIdx.x * A.cols;
-  if (T > 32) {
+  if (blockDim.y == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i * T + t < nv)
@@ -538,7 +590,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
         sh = fma2(h, h, sh);
         sa = fma2(mul2(Some::unpack(in.d[i]), gain(i)), h, sa);
       }
-    const float2 sum = row_sum(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
+    const float2 sum = row_sum<true>(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
     const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
     const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
     unsigned char* dx = row_of<DT>(A.dx, row, A.ld_dx);
@@ -593,14 +645,24 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   }
 }
 
-// Longer rows: read twice; a thread's columns of the gain's gradient lie in
-// the CTA's row of `partial`.
-template <int DT, int N>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_constant__ BwdArgs A) {
+// Longer rows: read twice.  A thread's columns are the same in every row; their
+// sums lie in shared memory, or, where a row is too long for it, in the CTA's
+// row of `partial`.  3005 x 11828 bf16 in pieces of 8 bytes: 65 us with three
+// CTAs of 512 threads per SM, 86 with one of 1024.
+constexpr int kWalkThreads = 512, kWalkPerSm = 3;
+
+template <int DT, int N, bool IN_SMEM>
+__global__ void __launch_bounds__(kWalkThreads, kWalkPerSm) rmsnorm_bwd_walk_kernel(const __grid_constant__ BwdArgs A) {
   __shared__ float2 part[2][32];
+  extern __shared__ __align__(16) float s_acc[];
   const int T = blockDim.x, t = threadIdx.x;
   depends_wait();
-  float* acc = A.partial + (int64_t)blockIdx.x * A.cols;
+  float* out = A.partial + (int64_t)blockIdx.x * A.cols;
+  float* acc = IN_SMEM ? s_acc : out;
+  for (int c = t * N; c < A.cols; c += T * N) {
+    const float zero[N] = {};
+    store_f32<N>(acc + c, zero);
+  }
   int flip = 0;
   for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
     const void* hp = row_of<DT>(A.h, row, A.ld_h);
@@ -608,29 +670,32 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_con
     float2 s = make_float2(0.0f, 0.0f);   // sums of h^2 and a h
 #pragma unroll 4
     for (int c = t * N; c < A.cols; c += T * N) {
-      float h[N], d[N];
+      float h[N], d[N], g[N];
       load_n<DT, N>(hp, c, h);
       load_n<DT, N>(dp, c, d);
+      load_f32<N>(A.gain + c, g);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         s.x = fmaf(h[j], h[j], s.x);
-        s.y = fmaf(d[j] * __ldg(A.gain + c + j), h[j], s.y);
+        s.y = fmaf(d[j] * g[j], h[j], s.y);
       }
     }
-    s = row_sum(s, T, part[flip]);
+    s = row_sum<false>(s, T, part[flip]);
     const float inv = inverse_norm(s.x, A.inv_cols, A.eps);
     const float k = s.y * A.inv_cols * inv * inv;
-    const bool first = row == blockIdx.x;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = t * N; c < A.cols; c += T * N) {
-      float h[N], d[N], o[N];
+      float h[N], d[N], g[N], o[N], sum[N];
       load_n<DT, N>(hp, c, h);
       load_n<DT, N>(dp, c, d);
+      load_f32<N>(A.gain + c, g);
+      load_f32<N>(acc + c, sum);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        o[j] = inv * (d[j] * __ldg(A.gain + c + j) - h[j] * k);
-        acc[c + j] = fmaf(d[j], h[j] * inv, first ? 0.0f : acc[c + j]);
+        o[j] = inv * (d[j] * g[j] - h[j] * k);
+        sum[j] = fmaf(d[j], h[j] * inv, sum[j]);
       }
+      store_f32<N>(acc + c, sum);
       if (A.dsum) {
         float f[N];
         load_n<DT, N>(row_of<DT>(A.dsum, row, A.ld_dsum), c, f);
@@ -638,6 +703,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_walk_kernel(const __grid_con
         for (int j = 0; j < N; ++j) o[j] += f[j];
       }
       store_n<DT, N>(row_of<DT>(A.dx, row, A.ld_dx), c, o);
+    }
+  }
+  if constexpr (IN_SMEM) {
+    for (int c = t * N; c < A.cols; c += T * N) {
+      float sum[N];
+      load_f32<N>(acc + c, sum);
+      store_f32<N>(out + c, sum);
     }
   }
 }
@@ -681,7 +753,8 @@ inline bool is_dtype(int v) { return v == QMUON_BF16 || v == QMUON_FP16 || v == 
 // none does.
 struct Shape {
   int T, V;
-  dim3 block() const { return dim3(T, T > 32 ? 1 : 256 / T); }
+  // rows of at most a warp: a CTA of 256 threads; of more: of `threads`, or one row
+  dim3 block(int threads) const { return dim3(T, T <= 32 ? 256 / T : std::max(1, threads / T)); }
 };
 
 template <class MaxThreads>
@@ -761,18 +834,25 @@ cudaError_t launch_fwd(const FwdArgs& A, cudaStream_t s) {
   // takes 3.7 us so, 4.5 with four.
   const bool few = A.rows <= device_sms();
   const int least = MX && DT == QMUON_FP32 ? 8 : 4;   // the 32 elements of a scale lie in one access of a row's threads
-  const Shape S = A.vec ? pick_shape(A.cols / K, few ? 1 : 4, 4, least, fwd_max_threads) : Shape{0, 0};
+  const Shape S = A.align == 16 ? pick_shape(A.cols / K, few ? 1 : 4, 4, least, fwd_max_threads) : Shape{0, 0};
   const bool pairs = !MX && DT != QMUON_FP32 &&
                      rows_alike({{A.x, A.ld_x}, {A.residual, A.ld_residual}, {A.sum, A.ld_sum}, {A.y, A.ld_y}});
   const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 4, 1024);
-  const bool pieces = !A.vec && C.V;
-  const dim3 block = S.V ? S.block() : pieces ? C.block() : dim3(1024);
+  const bool pieces = A.align < 16 && C.V;
+  const dim3 block = S.V ? S.block(0) : pieces ? C.block(0) : dim3(1024);
   const unsigned grid = (unsigned)std::min<int64_t>((A.rows + block.y - 1) / block.y, ((int64_t)1 << 31) - 1);
   if (S.V == 1) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 1, RES, MX>, grid, block, 0, s, A);
   if (S.V == 2) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 2, RES, MX>, grid, block, 0, s, A);
   if (S.V == 4) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 4, RES, MX>, grid, block, 0, s, A);
-  if (A.vec) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K, MX>, grid, block, 0, s, A);
-  if (!pieces) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 1, MX>, grid, block, 0, s, A);
+  if (!pieces) {
+    if (A.align == 16) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K, MX>, grid, block, 0, s, A);
+    if constexpr (!MX) {
+      if (A.align == 8) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K / 2, MX>, grid, block, 0, s, A);
+      if constexpr (K == 8)
+        if (A.align == 4) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 2, MX>, grid, block, 0, s, A);
+    }
+    return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 1, MX>, grid, block, 0, s, A);
+  }
   auto in_pieces = [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (C.V == 2) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 2, RES, MX>, grid, block, 0, s, A);
@@ -809,19 +889,19 @@ cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* g
 
 template <int DT, bool DSUM>
 cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
-  const Shape S = A.vec ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 8, 4, bwd_max_threads) : Shape{0, 0};
-  if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(), sms, grid, s);
-  if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(), sms, grid, s);
-  if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(), sms, grid, s);
-  if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(), sms, grid, s);
-  if (!A.vec) {
+  const Shape S = A.align == 16 ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 8, 4, bwd_max_threads) : Shape{0, 0};
+  if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(128), sms, grid, s);
+  if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(128), sms, grid, s);
+  if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(128), sms, grid, s);
+  if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(128), sms, grid, s);
+  if (A.align < 16) {
     const bool pairs =
         DT != QMUON_FP32 && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}});
     const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 8, bwd_piece_threads);
     if (C.V) {
-      const dim3 block = C.block();
+      const dim3 block = C.block(256);
       const int smem = (int)block.y * A.cols * 4;
-      *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, 1024 / (block.x * block.y));
+      *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, (C.V == 2 ? 1024 : 512) / (block.x * block.y));   // registers
       auto in_pieces = [&](auto n, auto p) {
         const auto kernel = rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>;
         const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
@@ -835,9 +915,20 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
       return C.V == 2 ? in_pieces(one, two) : in_pieces(one, eight);
     }
   }
-  *grid = bwd_grid(A.rows, sms, 2);
-  if (A.vec) return launch_dependent(rmsnorm_bwd_walk_kernel<DT, Vec16<DT>::kElems>, *grid, 1024, 0, s, A);
-  return launch_dependent(rmsnorm_bwd_walk_kernel<DT, 1>, *grid, 1024, 0, s, A);
+  const int64_t bytes = (int64_t)A.cols * 4;
+  const bool in_smem = bytes <= kMaxSmem;
+  *grid = bwd_grid(A.rows, sms, in_smem ? (int)std::min<int64_t>(kWalkPerSm, kMaxSmem / bytes) : kWalkPerSm);
+  auto walk = [&](auto n) {
+    const auto kernel = in_smem ? rmsnorm_bwd_walk_kernel<DT, decltype(n)::value, true> : rmsnorm_bwd_walk_kernel<DT, decltype(n)::value, false>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
+    return e != cudaSuccess ? e : launch_dependent(kernel, *grid, kWalkThreads, in_smem ? (size_t)bytes : 0, s, A);
+  };
+  constexpr int K = Vec16<DT>::kElems;
+  if (A.align == 16) return walk(std::integral_constant<int, K>{});
+  if (A.align == 8) return walk(std::integral_constant<int, K / 2>{});
+  if constexpr (K == 8)
+    if (A.align == 4) return walk(std::integral_constant<int, 2>{});
+  return walk(std::integral_constant<int, 1>{});
 }
 template <int DT>
 cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
@@ -845,12 +936,19 @@ cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) 
 }
 
 // A matrix argument: non-null, aligned to its elements, rows at least cols
-// apart; `vec` stays true if every row starts on a 16-byte boundary.
-bool check_matrix(const void* p, int64_t ld, int64_t cols, int dt, bool* vec) {
-  const size_t es = elem_size(dt);
+// apart; `align` falls to the bytes on which its rows start.
+bool check_matrix(const void* p, int64_t ld, int64_t cols, int dt, int* align) {
+  const int es = elem_size(dt);
   if (!p || ld < cols || !is_aligned(p, es)) return false;
-  if (!is_aligned(p, 16) || (ld * (int64_t)es) % 16) *vec = false;
+  while (!is_aligned(p, *align) || (ld * es) % *align) *align /= 2;
   return true;
+}
+// The bytes that a row's elements, its gain and an MXFP8 payload allow to move at once.
+int row_align(int64_t cols, int dt, const float* gain, const uint8_t* payload) {
+  const int es = elem_size(dt);
+  int align = is_aligned(payload, 8) ? 16 : 8;
+  while (align > es && ((cols * es) % align || !is_aligned(gain, std::min(16, 4 * align / es)))) align /= 2;
+  return align;
 }
 
 bool check_sizes(int64_t rows, int64_t cols, int dt, float eps) {
@@ -869,14 +967,14 @@ extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stre
   if (n->rows == 0) return QMUON_OK;
   if ((!n->y && !n->payload) || (n->payload == nullptr) != (n->scale_inv == nullptr)) return QMUON_ERR_INVALID_ARGUMENT;
   if (n->payload && n->cols % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
-  bool vec = n->cols % (16 / elem_size(n->dtype)) == 0 && is_aligned(n->gain, 16) && is_aligned(n->payload, 8);
-  if (!n->gain || !is_aligned(n->gain, 4) || !check_matrix(n->x, n->ld_x, n->cols, n->dtype, &vec))
+  int align = row_align(n->cols, n->dtype, n->gain, n->payload);
+  if (!n->gain || !is_aligned(n->gain, 4) || !check_matrix(n->x, n->ld_x, n->cols, n->dtype, &align))
     return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->residual && !check_matrix(n->residual, n->ld_residual, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->sum && !check_matrix(n->sum, n->ld_sum, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->y && !check_matrix(n->y, n->ld_y, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (n->residual && !check_matrix(n->residual, n->ld_residual, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (n->sum && !check_matrix(n->sum, n->ld_sum, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (n->y && !check_matrix(n->y, n->ld_y, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
   FwdArgs A{n->x,    n->residual,    n->gain,   n->sum,  n->y,    n->payload, n->scale_inv, n->rows,
-            n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
+            n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, align, n->eps, 1.0f / (float)n->cols};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = n->dtype == QMUON_BF16   ? launch_fwd_dt<QMUON_BF16>(A, s)
                         : n->dtype == QMUON_FP16 ? launch_fwd_dt<QMUON_FP16>(A, s)
@@ -900,17 +998,17 @@ extern "C" qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* n, void
       const cudaError_t e = cudaMemsetAsync(n->dgain, 0, (size_t)n->cols * 4, s);
       return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_backward (memset)", e);
     }
-    bool vec = n->cols % (16 / elem_size(n->dtype)) == 0 && is_aligned(n->gain, 16);
+    int align = row_align(n->cols, n->dtype, n->gain, nullptr);
     if (!n->gain || !is_aligned(n->gain, 4) || !ws || !is_aligned(ws, 256)) return QMUON_ERR_INVALID_ARGUMENT;
-    if (!check_matrix(n->dy, n->ld_dy, n->cols, n->dtype, &vec) || !check_matrix(n->h, n->ld_h, n->cols, n->dtype, &vec) ||
-        !check_matrix(n->dx, n->ld_dx, n->cols, n->dtype, &vec))
+    if (!check_matrix(n->dy, n->ld_dy, n->cols, n->dtype, &align) || !check_matrix(n->h, n->ld_h, n->cols, n->dtype, &align) ||
+        !check_matrix(n->dx, n->ld_dx, n->cols, n->dtype, &align))
       return QMUON_ERR_INVALID_ARGUMENT;
-    if (n->dsum && !check_matrix(n->dsum, n->ld_dsum, n->cols, n->dtype, &vec)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->dsum && !check_matrix(n->dsum, n->ld_dsum, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
     const int sms = device_sms();
     if (sms <= 0) return set_error_msg("qmuon_rmsnorm_backward: SM count query failed", QMUON_ERR_CUDA);
     if (ws_bytes < qmuon_rmsnorm_workspace_size(n->rows, n->cols)) return QMUON_ERR_WORKSPACE_TOO_SMALL;
     BwdArgs A{n->dy,    n->h,    n->dsum,    n->gain,  n->dx,            static_cast<float*>(ws), n->rows,
-              n->ld_dy, n->ld_h, n->ld_dsum, n->ld_dx, (int32_t)n->cols, vec, n->eps, 1.0f / (float)n->cols};
+              n->ld_dy, n->ld_h, n->ld_dsum, n->ld_dx, (int32_t)n->cols, align, n->eps, 1.0f / (float)n->cols};
     int grid = 0;
     cudaError_t e = n->dtype == QMUON_BF16   ? launch_bwd_dt<QMUON_BF16>(A, sms, &grid, s)
                     : n->dtype == QMUON_FP16 ? launch_bwd_dt<QMUON_FP16>(A, sms, &grid, s)
