@@ -93,8 +93,12 @@ __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t 
 #pragma unroll
   for (int j = 0; j < N; ++j) amax = fmaxf(amax, fabsf(y[j]));
   if (!valid) amax = 0.0f;
+  if constexpr (N == 1) {
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // not negative: ordered as integers
+  } else {
 #pragma unroll
-  for (int o = 16 / N; o > 0; o >>= 1) amax = fmaxf(amax, lane_xor(amax, o));
+    for (int o = 16 / N; o > 0; o >>= 1) amax = fmaxf(amax, lane_xor(amax, o));
+  }
   const int byte = e8m0_byte(amax);
   const float mult = e8m0_inverse(byte);
   if (!valid) return;
@@ -116,7 +120,11 @@ __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// blockDim = (T, rows per CTA); V 16-byte vectors per thread.
+// blockDim = (T, rows per CTA); V 16-byte vectors per thread, those of x and of
+// the residual all in flight before the first is unpacked (unpacking x before
+// loading the residual cost a quarter of the rate).  One CTA per row, or per
+// 256 threads of short rows: bound by DRAM, 16384 x 4096 bf16 with the residual
+// to bf16 81 us (6.65 TB/s), to MXFP8 71 us (6.7 TB/s); 131072 x 128 bf16 14.5 us.
 constexpr int fwd_max_threads(int V) { return V == 4 ? 512 : 1024; }
 
 template <int DT, int V, bool RES, bool MX>
@@ -190,7 +198,11 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
 // A row whose arrays are not aligned, in pieces of one element or, where all
 // arrays' rows start alike within 4 bytes, of a pair of 16-bit elements; these
 // start at column `head` (0 or 1) and leave one element at either end, which
-// the first and the last thread hold besides.
+// the first and the last thread hold besides, loaded with the others (loaded
+// after them they cost another trip to memory).  Bound by its instructions, 37
+// per element, three quarters of what the schedulers can issue: 6001 x 2049 fp16
+// with an odd stride 20.8 us, 0.70 of the copy rate (41.7 us by single elements
+// that were read twice).
 template <int DT, int N>
 struct Piece {
   using Raw = std::conditional_t<N == 2 || DT == QMUON_FP32, uint32_t, uint16_t>;
@@ -394,7 +406,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_con
 // A CTA walks over rows and keeps the gradient of the gain of its threads'
 // columns, which leaves as one row of `partial`; dgain_kernel adds those rows
 // in order.  The next rows come through a ring of shared-memory slots, each
-// thread's own, `stages` rows ahead.
+// thread's own, `stages` rows ahead.  A CTA has to stay for that sum to stay in
+// registers, and CTAs that stay reach 6.5 TB/s: 16384 x 4096 bf16 in 83 us and
+// 5 more for dgain_kernel, 131072 x 128 fp32 in 29 and 5.  CTAs of 8, 16 or 24
+// rows, whose partial sums are then many, take 96 to 99 us for the first.
 constexpr int bwd_max_threads(int V) { return V >= 4 ? 512 : 256; }
 
 __device__ __forceinline__ void wait_rows(int pending) {
@@ -714,7 +729,8 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkPerSm) rmsnorm_bwd_walk_ker
   }
 }
 
-// dgain[c] = sum of n rows of partial, in an order that n alone fixes.
+// dgain[c] = sum of n rows of partial, in an order that n alone fixes.  Bound by
+// latency: two batches of loads and a reduction.
 constexpr int kSlices = 32;
 
 __global__ void __launch_bounds__(1024) dgain_kernel(const float* partial, int32_t n, int32_t cols, float* dgain) {

@@ -348,3 +348,77 @@ def test_clip_coefficient_feeds_the_step():
     for a, b in zip(ts, us):
         for k in ("param", "m", "v"):
             assert torch.equal(a[k], b[k])
+
+
+@pytest.mark.parametrize("offs", [(1, 0, 2, 3, 0), (0, 1, 0, 0, 0), (2, 2, 2, 2, 1), (3, 3, 3, 3, 3), (1, 1, 1, 1, 5)])
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+def test_adamw_f32_arrays_at_offsets_of_their_own(grad, offs):
+    # param, grad, m, v and copy start at different places: no head makes all of them aligned together (or one does)
+    gen = torch.Generator("cuda").manual_seed(3)
+    descs, ref, guards, ts = [], [], [], []
+    for n in SIZES:
+        vals = [torch.randn(n, generator=gen, device="cuda") * s for s in (1.0, 1e-2, 1e-2, 1e-2, 0.0)]
+        vals[3] = vals[3].square()
+        made = [_offset(n, dt, o) for dt, o in zip((torch.float32, DT[grad], torch.float32, torch.float32, torch.bfloat16), offs)]
+        for (g, t), v in zip(made, vals):
+            t.copy_(v)
+            guards.append(g)
+        p, g, m, v, c = (t for _, t in made)
+        ts.append((p, m, v, c))
+        descs.append(q.adamw_tensor(p, g, m, v, n, grad, copy=c, weight_decay=0.1))
+        ref.append([t.clone() for t in (p, g, m, v)])
+    q.qmuon_adamw_step(q.qmuon_adamw_plan_create(descs), 2, 1e-2, 0.9, 0.99, 1e-8)
+    # the same numbers as aligned arrays give, bit for bit
+    plain = [[t.clone() for t in r] for r in ref]
+    q.qmuon_adamw_step(q.qmuon_adamw_plan_create([q.adamw_tensor(p, g, m, v, p.numel(), grad, weight_decay=0.1) for p, g, m, v in plain]),
+                       2, 1e-2, 0.9, 0.99, 1e-8)
+    for (p, m, v, c), (p1, _, m1, v1) in zip(ts, plain):
+        assert torch.equal(p, p1) and torch.equal(m, m1) and torch.equal(v, v1) and torch.equal(c, p1.bfloat16())
+    for g in guards:
+        g.check()
+
+
+def test_adamw_many_tensors_of_mixed_types():
+    # 400 tensors, some of them empty, gradients of all types in one plan: each as if alone
+    gen = torch.Generator("cuda").manual_seed(4)
+    rnd = lambda n: torch.randn(n, generator=gen, device="cuda")   # noqa: E731
+    made = []
+    for i in range(400):
+        n = (i * 37) % 3000
+        name = ("bf16", "f16", "f32")[i % 3]
+        made.append((rnd(n), (rnd(n) * 1e-2).to(DT[name]), rnd(n) * 1e-2, (rnd(n) * 1e-2).square(), name))
+    alone = [[t.clone() for t in x[:4]] for x in made]
+    desc = lambda t, name: q.adamw_tensor(*t, t[0].numel(), name, weight_decay=0.01)   # noqa: E731
+    q.qmuon_adamw_step(q.qmuon_adamw_plan_create([desc(x[:4], x[4]) for x in made]), 3, 1e-2, 0.9, 0.99, 1e-8)
+    for x, a in list(zip(made, alone))[::13]:
+        if a[0].numel():
+            q.qmuon_adamw_step(q.qmuon_adamw_plan_create([desc(a, x[4])]), 3, 1e-2, 0.9, 0.99, 1e-8)
+            for s, t in zip(x[:4], a):
+                assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("sr", [False, True])
+def test_adamw_e4m3_one_large_tensor_equals_many_launches_of_it(sr):
+    # enough blocks for several per warp, against the same blocks as tensors of their own (nearest), or the oracle's
+    # bits on a sample of them (stochastic: the counter holds the element's place)
+    n, blk = 3 * 256 * 8 * 400, 256
+    ts, guards, plan = _e4m3_case([n], "bf16", "bf16", 0, 9)
+    host = _host(ts)
+    if sr:
+        q.qmuon_adamw_step_sr(plan, 4, 1e-2, 0.9, 0.99, 1e-8, 77)
+    else:
+        q.qmuon_adamw_step(plan, 4, 1e-2, 0.9, 0.99, 1e-8)
+    torch.cuda.synchronize()
+    d, h = ts[0], host[0]
+    if sr:
+        _check_e4m3(ts, host, 4, 1e-2, 0.9, 0.99, 1e-8, 1.0, 77)
+    else:
+        for b in range(0, n // blk, 997):
+            s = slice(b * blk, (b + 1) * blk)
+            p, m, v, mm, vm = training.adamw_e4m3(h["param"][s], h["grad"][s], h["m"][s], h["v"][s], h["m_absmax"][b:b + 1],
+                                                  h["v_absmax"][b:b + 1], 4, 1e-2, 0.9, 0.99, 1e-8, d["wd"], d["ls"])
+            _same_codes(d["m"][s].cpu().numpy(), m)
+            _same_codes(d["v"][s].cpu().numpy(), v)
+            assert d["m_absmax"][b].item() == mm[0] and d["v_absmax"][b].item() == vm[0]
+    for g in guards:
+        g.check()

@@ -268,3 +268,65 @@ def test_offsets_past_32_bits():
     np.testing.assert_allclose(_np(dg), wg, rtol=160 * U)
     assert not bool(y[:-3].any())
     assert bool(y[-3:].any())
+
+
+WIDTHS = list(range(1, 70)) + [96, 100, 127, 128, 129, 255, 256, 257, 300, 511, 512, 513, 1000, 1023, 1024, 1025, 2047, 2048, 2049, 2050, 2052, 4095,
+                               4096, 4098, 4100]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows", [3, 200])
+def test_every_width(dtype, rows):
+    # forward and backward of each width: fp64 as above
+    gen = torch.Generator("cuda").manual_seed(9)
+    ut = UT[dtype]
+    for cols in WIDTHS:
+        h, dy, ds = (_rnd(gen, rows, cols).to(DT[dtype]) for _ in range(3))
+        gain = torch.randn(cols, generator=gen, device="cuda")
+        y, dx, dg = torch.empty_like(h), torch.empty_like(h), torch.empty(cols, device="cuda")
+        ws = torch.empty(q.qmuon_rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device="cuda")
+        q.qmuon_rmsnorm_forward(h, gain, rows, cols, dtype, 1e-5, y=y)
+        q.qmuon_rmsnorm_backward(dy, h, gain, rows, cols, dtype, 1e-5, dx, dg, ws, dsum=ds)
+        H, D, G, S = _np(h), _np(dy), _np(gain), _np(ds)
+        _, want = training.rmsnorm64(H, G, 1e-5)
+        assert (np.abs(_np(y) - want) <= (ut + 64 * U) * np.abs(want) + TINY[dtype]).all(), cols
+        wx, wg = training.rmsnorm_grad64(D, H, G, 1e-5, S)
+        n = np.abs(H) / np.sqrt(np.mean(H * H, 1, keepdims=True) + 1e-5)
+        inv = 1 / np.sqrt(np.mean(H * H, 1, keepdims=True) + 1e-5)
+        a = np.abs(D * G)
+        mag = inv * (a + n * np.mean(a * n, 1, keepdims=True))
+        assert (np.abs(_np(dx) - wx) <= ut * (1 + U) * np.abs(wx) + 128 * U * mag + U * (np.abs(S) + np.abs(wx)) + TINY[dtype]).all(), cols
+        assert (np.abs(_np(dg) - wg) <= 160 * U * np.sum(np.abs(D) * n, 0) + 1e-44).all(), cols
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [5, 64, 100, 2049, 4100, 9001, 20004, 70003])
+@pytest.mark.parametrize("pads,offs", [((0, 1, 2, 3), (0, 0, 0, 0)), ((1, 3, 1, 5), (0, 0, 0, 0)), ((4, 4, 12, 8), (0, 4, 0, 8)),
+                                       ((2, 2, 6, 2), (2, 0, 2, 4)), ((8, 16, 0, 8), (1, 1, 1, 1)), ((0, 0, 0, 0), (1, 0, 3, 2))])
+def test_arrays_with_strides_and_starts_of_their_own(dtype, cols, pads, offs):
+    # each array has its own stride and start, guards around and between its rows; the numbers are those of contiguous arrays
+    rows = 21 if cols < 9000 else 4
+    gen = torch.Generator("cuda").manual_seed(10)
+    dt, ut = DT[dtype], UT[dtype]
+    x, r, d = (_rnd(gen, rows, cols).to(dt) for _ in range(3))
+    gain = torch.randn(cols, generator=gen, device="cuda")
+    X, R, S, Y = (Matrix(rows, cols, p, dt, o, f) for p, o, f in zip(pads, offs, (x, r, None, None)))
+    q.qmuon_rmsnorm_forward(X.t, gain, rows, cols, dtype, 1e-5, y=Y.t, residual=R.t, sum=S.t, ld_x=X.ld, ld_residual=R.ld, ld_sum=S.ld, ld_y=Y.ld)
+    h, want = training.rmsnorm64(_np(x), _np(gain), 1e-5, _np(r))
+    assert (np.abs(_np(Y.t) - want) <= (ut + 64 * U) * np.abs(want) + TINY[dtype]).all()
+    assert (np.abs(_np(S.t) - h) <= ut * np.abs(h) * (1 + U) + U * (np.abs(_np(x)) + np.abs(_np(r))) + TINY[dtype]).all()
+    for m in (X, R, S, Y):
+        m.check()
+    D, H, T, O = (Matrix(rows, cols, p, dt, o, f) for p, o, f in zip(pads, offs, (d, x, r, None)))
+    dg, ws = torch.empty(cols, device="cuda"), torch.empty(q.qmuon_rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device="cuda")
+    q.qmuon_rmsnorm_backward(D.t, H.t, gain, rows, cols, dtype, 1e-5, O.t, dg, ws, dsum=T.t, ld_dy=D.ld, ld_h=H.ld, ld_dsum=T.ld, ld_dx=O.ld)
+    wx, wg = training.rmsnorm_grad64(_np(d), _np(x), _np(gain), 1e-5, _np(r))
+    inv = 1 / np.sqrt(np.mean(_np(x) ** 2, 1, keepdims=True) + 1e-5)
+    n, a = np.abs(_np(x)) * inv, np.abs(_np(d) * _np(gain))
+    # the longest rows add up to 256 terms in a thread: four times the bound of the others
+    k = 4 if cols > 20000 else 1
+    mag = inv * (a + n * np.mean(a * n, 1, keepdims=True))
+    assert (np.abs(_np(O.t) - wx) <= ut * (1 + U) * np.abs(wx) + 128 * k * U * mag + U * (np.abs(_np(r)) + np.abs(wx)) + TINY[dtype]).all()
+    assert (np.abs(_np(dg) - wg) <= 160 * k * U * np.sum(np.abs(_np(d)) * n, 0) + 1e-44).all()
+    for m in (D, H, T, O):
+        m.check()
