@@ -56,7 +56,7 @@ __device__ __forceinline__ float chunk_sumsq(const ClipChunk& T, int tid) {
 #pragma unroll 4
     for (int i = tid; i < nv; i += kThreads) {
       float2 f[K / 2];
-      Vec16<DT>::unpack(__ldg(p + i), f);
+      Vec16<DT>::unpack(p[i], f);
 #pragma unroll
       for (int j = 0; j < K / 2; ++j) s[j & 1] = fma2(f[j], f[j], s[j & 1]);
     }

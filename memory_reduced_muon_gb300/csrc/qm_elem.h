@@ -113,7 +113,9 @@ __device__ __forceinline__ void async_wait() {
 // what runs before it in its stream: it may start while that drains (and lets
 // its own successor do so), and touches nothing that others write before
 // depends_wait() has returned, which is once that has completed.  Every thread
-// calls it, so that a kernel never completes before its predecessor.
+// calls it, so that a kernel never completes before its predecessor.  Loads of
+// what others write are plain ones: a load that may use the read-only path
+// (__ldg) is not held back by the wait.
 __device__ __forceinline__ void depends_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

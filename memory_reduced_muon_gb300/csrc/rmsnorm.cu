@@ -161,13 +161,15 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
 #pragma unroll
       for (int j = 0; j < P; ++j) ss = fma2(h[i][j], h[i][j], ss);
     }
-    // the gain early where there are registers for it: its way from memory is as long as the row's
-    constexpr bool kGainEarly = V == 1;
+    // The gain of each vector comes before the output of the one before it is stored, and the first one's before the
+    // sum: its way from memory may be as long as the row's.
     const float4* gain = reinterpret_cast<const float4*>(A.gain) + t * (P / 2);
-    float4 ge[kGainEarly ? P / 2 : 1];
-    if constexpr (kGainEarly)
+    float4 g[P / 2];
+    auto load_gain = [&](int i) {
 #pragma unroll
-      for (int j = 0; j < P / 2; ++j) ge[j] = t < n ? __ldg(gain + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int j = 0; j < P / 2; ++j) g[j] = i * T + t < n ? gain[i * T * (P / 2) + j] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    load_gain(0);
     if (A.sum) {
       uint4* sum = reinterpret_cast<uint4*>(row_of<DT>(A.sum, row, A.ld_sum)) + t;
 #pragma unroll
@@ -181,13 +183,13 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
       const bool in = i * T + t < n;
       if (in) {
 #pragma unroll
-        for (int j = 0; j < P; j += 2) {
-          const float4 g = kGainEarly ? ge[j / 2 % (P / 2)] : __ldg(gain + i * T * (P / 2) + j / 2);
-          h[i][j] = mul2(mul2(h[i][j], inv), make_float2(g.x, g.y));
-          h[i][j + 1] = mul2(mul2(h[i][j + 1], inv), make_float2(g.z, g.w));
+        for (int j = 0; j < P / 2; ++j) {
+          h[i][2 * j] = mul2(mul2(h[i][2 * j], inv), make_float2(g[j].x, g[j].y));
+          h[i][2 * j + 1] = mul2(mul2(h[i][2 * j + 1], inv), make_float2(g[j].z, g[j].w));
         }
-        if (!MX || A.y) y[i * T] = X::pack(h[i]);
       }
+      if (i + 1 < V) load_gain(i + 1);
+      if (in && (!MX || A.y)) y[i * T] = X::pack(h[i]);
       if constexpr (MX)
         store_mxfp8<2 * P>(reinterpret_cast<const float*>(h[i]), in, row * A.cols + (int64_t)(i * T + t) * X::kElems, A.payload,
                            A.scale);
@@ -272,23 +274,29 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
       if constexpr (RES) h[i] = add2(h[i], Some::unpack(rr[i]));
       ss = fma2(h[i], h[i], ss);
     }
+    const float* gain = A.gain + c0;
+    auto gain_of = [&](int i) {
+      const int d = i * Some::kStep;
+      return make_float2(gain[d], N == 2 ? gain[d + N - 1] : 0.0f);
+    };
+    const float ge = edge >= 0 ? A.gain[edge] : 0.0f;
     const float inv = inverse_norm(row_sum<false>(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
     unsigned char* sum = row_of<DT>(A.sum, row, A.ld_sum);
     unsigned char* y = row_of<DT>(A.y, row, A.ld_y);
     if (edge >= 0) {
       if (A.sum) One::store(sum, edge, make_float2(he, 0.0f));
-      One::store(y, edge, make_float2(he * inv * __ldg(A.gain + edge), 0.0f));
+      One::store(y, edge, make_float2(he * inv * ge, 0.0f));
     }
     sum += c0 * elem_size(DT);
     y += c0 * elem_size(DT);
-    const float* gain = A.gain + c0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const bool in = k0 + 32 * i < n;
       const int d = i * Some::kStep;
       if (in) {
+        const float2 g = gain_of(i);
         if (A.sum) Some::store(sum, d, h[i]);
-        h[i] = mul2(mul2(h[i], inv), make_float2(__ldg(gain + d), N == 2 ? __ldg(gain + d + N - 1) : 0.0f));
+        h[i] = mul2(mul2(h[i], inv), g);
         if (!MX || A.y) Some::store(y, d, h[i]);
       }
       if constexpr (MX) store_mxfp8<1>(&h[i].x, in, row * A.cols + c0 + d, A.payload, A.scale);
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
   auto load_gain = [&](int i, float2* g) {
 #pragma unroll
     for (int j = 0; j < P; j += 2) {
-      const float4 q = i * T + t < nv ? __ldg(gain + i * T * (P / 2) + j / 2) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float4 q = i * T + t < nv ? gain[i * T * (P / 2) + j / 2] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       g[j] = make_float2(q.x, q.y);
       g[j + 1] = make_float2(q.z, q.w);
     }
@@ -547,9 +555,11 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   using Some = Piece<DT, N>;
   constexpr int kKinds = N;   // 1, or pairs from column 0 and pairs from column 1
   __shared__ float2 part[2][32];
-  extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols]
+  extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols] of sums, then the gain and zeros for all pieces
   const int T = blockDim.x, t = threadIdx.x, k0 = first_piece<P>(t);
   depends_wait();
+  float* s_gain = s_acc + (size_t)blockDim.y * A.cols;
+  for (int c = threadIdx.y * T + t; c < T * P * N + 2; c += T * blockDim.y) s_gain[c] = c < A.cols ? A.gain[c] : 0.0f;
   struct Raw {
     typename Some::Raw h[P], d[P], s[DSUM ? P : 1];
     typename One::Raw he, de, se;
@@ -587,24 +597,24 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   Raw in;
   load((int64_t)blockIdx.x * blockDim.y + threadIdx.y, in);
+  __syncthreads();
   int flip = 0;
   for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < A.rows; base += step, flip ^= 1) {
     const int64_t row = base + threadIdx.y;
     Raw next;
     load(row + step, next);
-    const float* g0 = A.gain + in.head + N * k0;
+    const float* g0 = s_gain + in.head + N * k0;
     auto gain = [&](int i) {
-      return make_float2(__ldg(g0 + i * Some::kStep), N == 2 ? __ldg(g0 + i * Some::kStep + N - 1) : 0.0f);
+      return make_float2(g0[i * Some::kStep], N == 2 ? g0[i * Some::kStep + N - 1] : 0.0f);
     };
-    const float he = One::unpack(in.he).x, de = One::unpack(in.de).x, ge = in.edge >= 0 ? __ldg(A.gain + in.edge) : 0.0f;
+    const float he = One::unpack(in.he).x, de = One::unpack(in.de).x, ge = in.edge >= 0 ? s_gain[in.edge] : 0.0f;
     float2 sh = make_float2(he * he, 0.0f), sa = make_float2(de * ge * he, 0.0f);   // sums of h^2 and a h
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (k0 + 32 * i < in.n) {
-        const float2 h = Some::unpack(in.h[i]);
-        sh = fma2(h, h, sh);
-        sa = fma2(mul2(Some::unpack(in.d[i]), gain(i)), h, sa);
-      }
+    for (int i = 0; i < P; ++i) {   // pieces that are not there hold zeros: no branches
+      const float2 h = Some::unpack(in.h[i]);
+      sh = fma2(h, h, sh);
+      sa = fma2(mul2(Some::unpack(in.d[i]), gain(i)), h, sa);
+    }
     const float2 sum = row_sum<true>(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
     const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
     const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
@@ -618,16 +628,15 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     dx += (in.head + N * k0) * elem_size(DT);
     auto finish = [&](float2* sums) {
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (k0 + 32 * i < in.n) {
-          const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
-          const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
-          float2 o;
-          if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
-          else o = mul2(e, inv);
-          Some::store(dx, i * Some::kStep, o);
-          sums[i] = fma2(d, mul2(h, inv), sums[i]);
-        }
+      for (int i = 0; i < P; ++i) {
+        const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
+        const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
+        float2 o;
+        if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
+        else o = mul2(e, inv);
+        if (k0 + 32 * i < in.n) Some::store(dx, i * Some::kStep, o);
+        sums[i] = fma2(d, mul2(h, inv), sums[i]);
+      }
     };
     if (kKinds == 1 || in.head == 0) finish(acc[0]);
     else finish(acc[kKinds - 1]);
@@ -791,12 +800,13 @@ Shape pick_shape(int nv, int want, int most, int least, MaxThreads max_threads) 
   return {0, 0};
 }
 
-// Threads and pieces per thread of a row of n pieces: a warp with two for short
-// rows (six more would be tests without work: 300000 x 100 bf16 forward in
+// Threads and pieces per thread of a row of n pieces: a warp with two or four for
+// short rows (more would be tests without work: 300000 x 100 bf16 forward in
 // 61 us with two, 91 with eight), else `want`, or eight where those need too
 // many threads.  V == 0: too long.
 Shape piece_shape(int n, int want, int max_threads) {
   if (n <= 64) return {32, 2};
+  if (n <= 128) return {32, 4};
   for (int V = want; V <= 8; V *= 2) {
     const int T = ((n + V - 1) / V + 31) / 32 * 32;
     if (T <= max_threads) return {T, V};
@@ -916,8 +926,8 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
     const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 8, bwd_piece_threads);
     if (C.V) {
       const dim3 block = C.block(256);
-      const int smem = (int)block.y * A.cols * 4;
-      *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, (C.V == 2 ? 1024 : 512) / (block.x * block.y));   // registers
+      const int smem = ((int)block.y * A.cols + C.T * C.V * (pairs ? 2 : 1) + 2) * 4;
+      *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, (C.V <= 4 ? 1024 : 512) / (block.x * block.y));   // registers
       auto in_pieces = [&](auto n, auto p) {
         const auto kernel = rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>;
         const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
@@ -925,10 +935,11 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
       };
       const std::integral_constant<int, 1> one;
       const std::integral_constant<int, 2> two;
+      const std::integral_constant<int, 4> four;
       const std::integral_constant<int, 8> eight;
       if constexpr (DT != QMUON_FP32)
-        if (pairs) return C.V == 2 ? in_pieces(two, two) : in_pieces(two, eight);
-      return C.V == 2 ? in_pieces(one, two) : in_pieces(one, eight);
+        if (pairs) return C.V == 2 ? in_pieces(two, two) : C.V == 4 ? in_pieces(two, four) : in_pieces(two, eight);
+      return C.V == 2 ? in_pieces(one, two) : C.V == 4 ? in_pieces(one, four) : in_pieces(one, eight);
     }
   }
   const int64_t bytes = (int64_t)A.cols * 4;
