@@ -14,8 +14,9 @@
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
+#include <map>
 #include <mutex>
-#include <set>
+#include <tuple>
 #include <type_traits>
 #include <utility>
 
@@ -824,20 +825,26 @@ int device_sms() {
   return sms;
 }
 
-// Lets a kernel have kMaxSmem bytes of dynamic shared memory on the current
-// device: once per kernel and device, so that calls can be captured.
+// CTAs of a kernel that an SM of the current device holds at once.  The first
+// call for a kernel also lets it have kMaxSmem bytes of dynamic shared memory;
+// later ones make no CUDA call but cudaGetDevice, so that they can be captured.
 constexpr int kMaxSmem = 224 * 1024;
-cudaError_t allow_smem(const void* kernel) {
+cudaError_t resident_ctas(const void* kernel, int threads, int smem, int* ctas) {
   static std::mutex mu;
-  static std::set<std::pair<const void*, int>> done;
+  static std::map<std::tuple<const void*, int, int, int>, int> known;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  if (done.count({kernel, dev})) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (e == cudaSuccess) done.insert({kernel, dev});
-  return e;
+  int& n = known[{kernel, dev, threads, smem}];
+  if (n == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    n = std::max(n, 1);
+  }
+  *ctas = n;
+  return cudaSuccess;
 }
 
 // Whether all rows of the arrays start alike within 4 bytes.
@@ -895,67 +902,72 @@ cudaError_t launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
   return A.residual ? launch_fwd<DT, true, false>(A, s) : launch_fwd<DT, false, false>(A, s);
 }
 
-// CTAs of the backward pass, each with its row of `partial`: at most four per SM.
+// CTAs of the backward pass, each with its row of `partial`: those that the SMs
+// hold at once, at most four per SM.
 constexpr int kBwdPerSm = 4;
 int bwd_grid(int64_t groups, int sms, int per_sm) {
-  return (int)std::min<int64_t>(std::max<int64_t>(groups, 1), (int64_t)sms * std::min(std::max(per_sm, 1), kBwdPerSm));
+  return (int)std::min<int64_t>(std::max<int64_t>(groups, 1), (int64_t)sms * std::min(per_sm, kBwdPerSm));
+}
+
+template <class... Extra>
+cudaError_t launch_bwd_kernel(void (*kernel)(BwdArgs, Extra...), const BwdArgs& A, dim3 block, int smem, int sms, int* grid,
+                              cudaStream_t s, Extra... extra) {
+  int per_sm = 0;
+  const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(kernel), (int)(block.x * block.y), smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, per_sm);
+  return launch_dependent(kernel, *grid, block, smem, s, A, extra...);
 }
 
 template <int DT, int V, bool DSUM>
 cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* grid, cudaStream_t s) {
-  const int threads = block.x * block.y;
-  const int row = (DSUM ? 3 : 2) * V * threads * 16;
+  const int row = (DSUM ? 3 : 2) * V * (int)(block.x * block.y) * 16;   // bytes of a stage
   const int stages = std::min(3, std::max(1, kMaxSmem / row));
   const int smem = std::max(stages * row, block.y > 1 ? (int)block.y * A.cols * 4 : 0);
-  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, kMaxSmem / smem);
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&rmsnorm_bwd_rows_kernel<DT, V, DSUM>));
-  if (e == cudaSuccess) e = launch_dependent(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, *grid, block, smem, s, A, stages);
-  return e;
+  return launch_bwd_kernel(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, A, block, smem, sms, grid, s, stages);
 }
 
 template <int DT, bool DSUM>
 cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
-  const Shape S = A.align == 16 ? pick_shape(A.cols / Vec16<DT>::kElems, 4, 8, 4, bwd_max_threads) : Shape{0, 0};
-  if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(128), sms, grid, s);
-  if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(128), sms, grid, s);
-  if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(128), sms, grid, s);
-  if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(128), sms, grid, s);
-  if (A.align < 16) {
+  constexpr int K = Vec16<DT>::kElems;
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  const std::integral_constant<int, 4> four;
+  const std::integral_constant<int, 8> eight;
+  if (A.align == 16) {
+    const Shape S = pick_shape(A.cols / K, 4, 8, 4, bwd_max_threads);
+    if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(128), sms, grid, s);
+    if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(128), sms, grid, s);
+    if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(128), sms, grid, s);
+    if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(128), sms, grid, s);
+  } else {
     const bool pairs =
         DT != QMUON_FP32 && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}});
     const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 8, bwd_piece_threads);
     if (C.V) {
       const dim3 block = C.block(256);
       const int smem = ((int)block.y * A.cols + C.T * C.V * (pairs ? 2 : 1) + 2) * 4;
-      *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, (C.V <= 4 ? 1024 : 512) / (block.x * block.y));   // registers
       auto in_pieces = [&](auto n, auto p) {
-        const auto kernel = rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>;
-        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
-        return e != cudaSuccess ? e : launch_dependent(kernel, *grid, block, smem, s, A);
+        return launch_bwd_kernel(rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>, A, block, smem,
+                                 sms, grid, s);
       };
-      const std::integral_constant<int, 1> one;
-      const std::integral_constant<int, 2> two;
-      const std::integral_constant<int, 4> four;
-      const std::integral_constant<int, 8> eight;
       if constexpr (DT != QMUON_FP32)
         if (pairs) return C.V == 2 ? in_pieces(two, two) : C.V == 4 ? in_pieces(two, four) : in_pieces(two, eight);
       return C.V == 2 ? in_pieces(one, two) : C.V == 4 ? in_pieces(one, four) : in_pieces(one, eight);
     }
   }
   const int64_t bytes = (int64_t)A.cols * 4;
-  const bool in_smem = bytes <= kMaxSmem;
-  *grid = bwd_grid(A.rows, sms, in_smem ? (int)std::min<int64_t>(kWalkPerSm, kMaxSmem / bytes) : kWalkPerSm);
   auto walk = [&](auto n) {
-    const auto kernel = in_smem ? rmsnorm_bwd_walk_kernel<DT, decltype(n)::value, true> : rmsnorm_bwd_walk_kernel<DT, decltype(n)::value, false>;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
-    return e != cudaSuccess ? e : launch_dependent(kernel, *grid, kWalkThreads, in_smem ? (size_t)bytes : 0, s, A);
+    constexpr int N = decltype(n)::value;
+    return bytes <= kMaxSmem
+               ? launch_bwd_kernel(rmsnorm_bwd_walk_kernel<DT, N, true>, A, kWalkThreads, (int)bytes, sms, grid, s)
+               : launch_bwd_kernel(rmsnorm_bwd_walk_kernel<DT, N, false>, A, kWalkThreads, 0, sms, grid, s);
   };
-  constexpr int K = Vec16<DT>::kElems;
   if (A.align == 16) return walk(std::integral_constant<int, K>{});
   if (A.align == 8) return walk(std::integral_constant<int, K / 2>{});
   if constexpr (K == 8)
-    if (A.align == 4) return walk(std::integral_constant<int, 2>{});
-  return walk(std::integral_constant<int, 1>{});
+    if (A.align == 4) return walk(two);
+  return walk(one);
 }
 template <int DT>
 cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
