@@ -125,7 +125,7 @@ __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t 
 // the residual all in flight before the first is unpacked (unpacking x first, with
 // unpaired arithmetic, took 98 us for the second figure).  One CTA per row, or per
 // 256 threads of short rows: bound by DRAM, 16384 x 4096 bf16 with the residual
-// to bf16 81 us (6.65 TB/s), to MXFP8 71 us (6.7 TB/s); 131072 x 128 bf16 14.5 us.
+// to bf16 80 us (6.7 TB/s), to MXFP8 70 us (6.8 TB/s); 131072 x 128 bf16 14 us.
 constexpr int fwd_max_threads(int V) { return V == 4 ? 512 : 1024; }
 
 template <int DT, int V, bool RES, bool MX>
