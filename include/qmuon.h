@@ -495,8 +495,9 @@ QMUON_API size_t qmuon_clip_workspace_size(const qmuon_clip_plan* plan);
  *             1: g <- norm[1] g, rounded to nearest, where norm[1] < 1
  *   norm      D  two fp32
  *   ws        D  256-byte aligned, of qmuon_clip_workspace_size(plan)
- * Squares are taken in fp32 and summed in fp64 in a fixed order, so the same
- * gradients give the same bits.  Calls with one plan must not overlap on the
+ * Squares are taken and summed in fp32 over up to 8192 elements, then in fp64 in
+ * a fixed order: the same gradients give the same bits, and magnitudes above
+ * 2e17 may count as infinite.  Calls with one plan must not overlap on the
  * GPU (enqueue them on one stream). */
 QMUON_API qmuon_status qmuon_grad_clip(const qmuon_clip_plan* plan, float max_norm, int32_t apply, float* norm, void* ws,
                                        size_t ws_bytes, void* stream);
@@ -544,8 +545,9 @@ QMUON_API void qmuon_adamw_plan_destroy(qmuon_adamw_plan* plan);
  *   p <- p (1 - lr' weight_decay) - (lr' / (1 - beta1^t)) * u
  *   u = m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * 8-bit states are then requantised to the nearest code of their block's new
- * maximum (the update above uses the unrounded ones).  A NaN or infinity in a
- * block leaves NaN codes, so that it is not lost.
+ * maximum (the update above uses the unrounded ones).  A NaN keeps a NaN code,
+ * and an infinity turns its block's state into NaN at the next step, so that
+ * neither is lost.
  *   t           >= 1, the step's index; fixed in captured launches
  *   eps         at least 2^-126 (the smallest normal fp32)
  *   grad_scale  D  one fp32 s (a clipping coefficient, an inverse loss scale),
@@ -604,8 +606,8 @@ QMUON_API qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* norm, void* st
  *              dsum itself
  *   dgain      cols fp32, overwritten
  *   ws         D  256-byte aligned, of qmuon_rmsnorm_workspace_size(rows, cols)
- * Sums over rows are taken in an order that depends on the shape and the GPU's
- * SM count alone. */
+ * Sums over rows are taken in an order that depends on the sizes, strides and
+ * alignments and on the GPU's SM count alone. */
 typedef struct {
   const void* dy;
   const void* h;

@@ -130,7 +130,7 @@ __device__ __forceinline__ void chunk_scale(const ClipChunk& T, int tid, float c
       float2 f[K / 2];
       Vec16<DT>::unpack(p[i], f);
 #pragma unroll
-      for (int j = 0; j < K / 2; ++j) f[j] = mul2(f[j], c);
+      for (int j = 0; j < K / 2; ++j) f[j] = mul2_rn(f[j], c);
       p[i] = Vec16<DT>::pack(f);
     }
     done = nv * K;
@@ -210,15 +210,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // scaled by the step size.
 __device__ __forceinline__ void adam_pair(const AdamLaunch& L, const AdamCoef& C, float2 g, float2& p, float2& m, float2& v,
                                           float2& r) {
-  g = mul2(g, C.scale);
-  const float2 mb = mul2(m, L.b1), mg = mul2(g, L.omb1);
-  const float2 vb = mul2(v, L.b2), vg = mul2(mul2(g, g), L.omb2);
+  g = mul2_rn(g, C.scale);
+  const float2 mb = mul2_rn(m, L.b1), mg = mul2_rn(g, L.omb1);
+  const float2 vb = mul2_rn(v, L.b2), vg = mul2_rn(mul2_rn(g, g), L.omb2);
   m = make_float2(__fadd_rn(mb.x, mg.x), __fadd_rn(mb.y, mg.y));
   v = make_float2(__fadd_rn(vb.x, vg.x), __fadd_rn(vb.y, vg.y));
   r = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
-  const float2 d = mul2(r, L.rbc2);
-  const float2 u = mul2(mul2(m, make_float2(rcp_approx(__fadd_rn(d.x, L.eps)), rcp_approx(__fadd_rn(d.y, L.eps)))), C.step);
-  const float2 q = mul2(p, C.decay);
+  const float2 d = mul2_rn(r, L.rbc2);
+  const float2 u = mul2_rn(mul2_rn(m, make_float2(rcp_approx(__fadd_rn(d.x, L.eps)), rcp_approx(__fadd_rn(d.y, L.eps)))), C.step);
+  const float2 q = mul2_rn(p, C.decay);
   p = make_float2(__fsub_rn(q.x, u.x), __fsub_rn(q.y, u.y));
 }
 
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_f32_kernel(const __grid_con
 template <bool SIGNED>
 __device__ __forceinline__ uint32_t encode_sr4(const Quad& x, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
   constexpr float kShift = 7.52316384526264e-37f;   // 2^-120
-  const float2 a = mul2(x.a, kShift), b = mul2(x.b, kShift);
+  const float2 a = mul2_rn(x.a, kShift), b = mul2_rn(x.b, kShift);
   auto code = [](float y, uint32_t u) { return min(__float_as_uint(fabsf(y)) + u, 0x7F00000u) << 4; };
   const uint32_t c0 = code(a.x, u0), c1 = code(a.y, u1), c2 = code(b.x, u2), c3 = code(b.y, u3);
   const uint32_t w = __byte_perm(__byte_perm(c0, c1, 0x0073u), __byte_perm(c2, c3, 0x0073u), 0x5410u);
@@ -432,10 +432,10 @@ __device__ __forceinline__ void e4m3_update(const AdamLaunch& L, const AdamCoef&
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     Quad &m = q.m[k], &r = q.r[k];
-    m.a = mul2(e4m3x2_to(q.mc[k]), m_unit);
-    m.b = mul2(e4m3x2_to(q.mc[k] >> 16), m_unit);
-    const float2 ra = mul2(e4m3x2_to(q.vc[k]), r_unit), rb = mul2(e4m3x2_to(q.vc[k] >> 16), r_unit);
-    float2 va = mul2(ra, ra), vb = mul2(rb, rb);
+    m.a = mul2_rn(e4m3x2_to(q.mc[k]), m_unit);
+    m.b = mul2_rn(e4m3x2_to(q.mc[k] >> 16), m_unit);
+    const float2 ra = mul2_rn(e4m3x2_to(q.vc[k]), r_unit), rb = mul2_rn(e4m3x2_to(q.vc[k] >> 16), r_unit);
+    float2 va = mul2_rn(ra, ra), vb = mul2_rn(rb, rb);
     adam_pair(L, C, q.g[k].a, q.p[k].a, m.a, va, r.a);
     adam_pair(L, C, q.g[k].b, q.p[k].b, m.b, vb, r.b);
     if constexpr (!WHOLE) {
@@ -453,7 +453,7 @@ __device__ __forceinline__ void e4m3_update(const AdamLaunch& L, const AdamCoef&
   const float m_sc = fminf(__fdiv_rn(448.0f, q.m_max), kMax), r_sc = fminf(__fdiv_rn(448.0f, q.r_max), kMax);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const float2 ma = mul2(q.m[k].a, m_sc), mb = mul2(q.m[k].b, m_sc), ra = mul2(q.r[k].a, r_sc), rb = mul2(q.r[k].b, r_sc);
+    const float2 ma = mul2_rn(q.m[k].a, m_sc), mb = mul2_rn(q.m[k].b, m_sc), ra = mul2_rn(q.r[k].a, r_sc), rb = mul2_rn(q.r[k].b, r_sc);
     if constexpr (SR) {
       const uint64_t j = (uint64_t)(e0 + 128 * k) >> 2;
       const uint4 w = philox(make_uint4((uint32_t)j, (uint32_t)(j >> 32), (uint32_t)index, L.step), L.keys);
@@ -463,8 +463,8 @@ __device__ __forceinline__ void e4m3_update(const AdamLaunch& L, const AdamCoef&
       q.mc[k] = encode_sr4<true>({ma, mb}, lo(w.x), lo(w.y), lo(w.z), lo(w.w));
       q.vc[k] = encode_sr4<false>({ra, rb}, hi(w.x), hi(w.y), hi(w.z), hi(w.w));
     } else {
-      q.mc[k] = e4m3x2_of(ma.x, ma.y) | (e4m3x2_of(mb.x, mb.y) << 16);
-      q.vc[k] = e4m3x2_of(ra.x, ra.y) | (e4m3x2_of(rb.x, rb.y) << 16);
+      q.mc[k] = cvt_e4m3x2(ma.x, ma.y) | (cvt_e4m3x2(mb.x, mb.y) << 16);
+      q.vc[k] = cvt_e4m3x2(ra.x, ra.y) | (cvt_e4m3x2(rb.x, rb.y) << 16);
     }
   }
 }

@@ -1,6 +1,7 @@
-// Element types of the training operators (adamw.cu, rmsnorm.cu): widening
-// and rounding between the stored types and fp32, 16-byte vectors, E4M3 codes
-// and the Philox generator.
+// Device helpers shared by update.cu, adamw.cu and rmsnorm.cu: widening and
+// rounding between the stored types and fp32, 16-byte vectors, packed fp32
+// pairs, E4M3 codes and E8M0 scales, asynchronous copies, dependent launches,
+// and the Philox generator under round keys made on the host.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -66,10 +67,14 @@ struct Vec16 {
   }
 };
 
-// Products of fp32 pairs in one instruction, each rounded to nearest as
-// __fmul_rn rounds it.  A packed product is never added packed: that sum could
-// be contracted into one rounding.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+// Packed fp32 pairs (one instruction for two lanes of arithmetic), each
+// component rounded to nearest exactly as the scalar __fmul_rn / __fsub_rn.
+// ptxas fuses a packed multiply whose only use is a packed add into a packed
+// FMA (one rounding instead of two), so a product that feeds an addition is
+// always added with the scalar __fadd_rn: those chains were checked bit for
+// bit against the scalar ones on the GPU (sub -> mul, mul -> scalar add,
+// mul -> max -> add, mul -> E4M3 conversion).
+__device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
       "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
@@ -77,7 +82,16 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float b) { return mul2(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 sub2_rn(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+      "sub.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2_rn(float2 a, float b) { return mul2_rn(a, make_float2(b, b)); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
@@ -136,28 +150,37 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 b
 
 // Two E4M3 codes (the low one first) from fp32, nearest even, |x| > 448
 // saturating, NaN to 0x7F; and back, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return (uint32_t)r;
 }
+
 __device__ __forceinline__ float2 e4m3x2_to(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// E8M0 exponent byte of a block of 32: 127 + e with e the smallest integer
-// such that amax <= 448 2^e, clamped to [0, 254]; 127 for amax == 0, 254 for
-// an infinite one.  With amax = f 2^E, f in [1, 2), e = E - 8 + [f > 1.75].
-__device__ __forceinline__ int e8m0_byte(float amax) {
-  const uint32_t b = __float_as_uint(amax);
+// E8M0 exponent byte of a 32-element block: 127 + e with e the smallest
+// integer such that amax <= 448 * 2^e (448 = 1.75 * 2^8 is the largest E4M3
+// value), clamped to [0, 254]; 127 for amax == 0, 254 for amax == inf.
+// With amax = f * 2^E (f in [1, 2), biased exponent field ef = E + 127),
+// e = E - 8 + [f > 1.75], so the byte is ef - 8 + [mantissa > 0.75].  A
+// subnormal amax (ef = 0, below 2^-126) and any amax below 2^-119 give a
+// negative byte and clamp to 0, so no subnormal case is needed: the byte is
+// a few integer operations and selects, without branches.
+__device__ __forceinline__ int e8m0_of_amax(float amax) {
+  const uint32_t b = __float_as_uint(amax);   // amax >= 0: the sign bit is clear
   const int ef = (int)(b >> 23);
   const int byte = ef - 8 + (((b & 0x7FFFFFu) > 0x600000u) ? 1 : 0);
-  return b == 0u ? 127 : (ef == 0xFF ? 254 : min(max(byte, 0), 254));
+  const int clamped = byte < 0 ? 0 : (byte > 254 ? 254 : byte);
+  return b == 0u ? 127 : (ef == 0xFF ? 254 : clamped);
 }
-// 2^(127 - byte); byte 254 gives the subnormal 2^-127.
-__device__ __forceinline__ float e8m0_inverse(int byte) {
+
+// 2^(127 - byte) as an fp32 (byte in [0, 254]: exponent in [-127, 127]); the
+// one subnormal power, 2^-127 (byte 254), is the pattern 0x00400000.
+__device__ __forceinline__ float pow2_from_e8m0(int byte) {
   return __uint_as_float(byte < 254 ? (uint32_t)(254 - byte) << 23 : 0x00400000u);
 }
 

@@ -100,17 +100,17 @@ __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t 
 #pragma unroll
     for (int o = 16 / N; o > 0; o >>= 1) amax = fmaxf(amax, lane_xor(amax, o));
   }
-  const int byte = e8m0_byte(amax);
-  const float mult = e8m0_inverse(byte);
+  const int byte = e8m0_of_amax(amax);
+  const float mult = pow2_from_e8m0(byte);
   if (!valid) return;
   if constexpr (N == 1) {
-    payload[e] = (uint8_t)e4m3x2_of(__fmul_rn(y[0], mult), 0.0f);
+    payload[e] = (uint8_t)cvt_e4m3x2(__fmul_rn(y[0], mult), 0.0f);
   } else {
     uint32_t w[N / 4];
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
-      const float2 a = mul2(make_float2(y[4 * j], y[4 * j + 1]), mult), b = mul2(make_float2(y[4 * j + 2], y[4 * j + 3]), mult);
-      w[j] = e4m3x2_of(a.x, a.y) | (e4m3x2_of(b.x, b.y) << 16);
+      const float2 a = mul2_rn(make_float2(y[4 * j], y[4 * j + 1]), mult), b = mul2_rn(make_float2(y[4 * j + 2], y[4 * j + 3]), mult);
+      w[j] = cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16);
     }
     if constexpr (N == 8) *reinterpret_cast<uint2*>(payload + e) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(payload + e) = w[0];
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
       if (in) {
 #pragma unroll
         for (int j = 0; j < P / 2; ++j) {
-          h[i][2 * j] = mul2(mul2(h[i][2 * j], inv), make_float2(g[j].x, g[j].y));
-          h[i][2 * j + 1] = mul2(mul2(h[i][2 * j + 1], inv), make_float2(g[j].z, g[j].w));
+          h[i][2 * j] = mul2_rn(mul2_rn(h[i][2 * j], inv), make_float2(g[j].x, g[j].y));
+          h[i][2 * j + 1] = mul2_rn(mul2_rn(h[i][2 * j + 1], inv), make_float2(g[j].z, g[j].w));
         }
       }
       if (i + 1 < V) load_gain(i + 1);
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
       if (in) {
         const float2 g = gain_of(i);
         if (A.sum) Some::store(sum, d, h[i]);
-        h[i] = mul2(mul2(h[i], inv), g);
+        h[i] = mul2_rn(mul2_rn(h[i], inv), g);
         if (!MX || A.y) Some::store(y, d, h[i]);
       }
       if constexpr (MX) store_mxfp8<1>(&h[i].x, in, row * A.cols + c0 + d, A.payload, A.scale);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           sh = fma2(h[j], h[j], sh);
-          sa = fma2(mul2(d[j], kKeepGain ? kept[i % V][j] : g[j]), h[j], sa);
+          sa = fma2(mul2_rn(d[j], kKeepGain ? kept[i % V][j] : g[j]), h[j], sa);
         }
       }
     const float2 sum = row_sum<true>(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
@@ -506,11 +506,11 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
         if constexpr (!kKeepGain) load_gain(i, g);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const float2 a = mul2(d[j], kKeepGain ? kept[i % V][j] : g[j]);
+          const float2 a = mul2_rn(d[j], kKeepGain ? kept[i % V][j] : g[j]);
           const float2 e = fma2(h[j], make_float2(c, c), a);
           if constexpr (DSUM) o[j] = fma2(e, make_float2(inv, inv), o[j]);
-          else o[j] = mul2(e, inv);
-          acc[i][j] = fma2(d[j], mul2(h[j], inv), acc[i][j]);
+          else o[j] = mul2_rn(e, inv);
+          acc[i][j] = fma2(d[j], mul2_rn(h[j], inv), acc[i][j]);
         }
         dx[i * T] = X::pack(o);
       }
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     for (int i = 0; i < P; ++i) {   // pieces that are not there hold zeros: no branches
       const float2 h = Some::unpack(in.h[i]);
       sh = fma2(h, h, sh);
-      sa = fma2(mul2(Some::unpack(in.d[i]), gain(i)), h, sa);
+      sa = fma2(mul2_rn(Some::unpack(in.d[i]), gain(i)), h, sa);
     }
     const float2 sum = row_sum<true>(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
     const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
@@ -631,12 +631,12 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         const float2 h = Some::unpack(in.h[i]), d = Some::unpack(in.d[i]);
-        const float2 e = fma2(h, make_float2(c, c), mul2(d, gain(i)));
+        const float2 e = fma2(h, make_float2(c, c), mul2_rn(d, gain(i)));
         float2 o;
         if constexpr (DSUM) o = fma2(e, make_float2(inv, inv), Some::unpack(in.s[i]));
-        else o = mul2(e, inv);
+        else o = mul2_rn(e, inv);
         if (k0 + 32 * i < in.n) Some::store(dx, i * Some::kStep, o);
-        sums[i] = fma2(d, mul2(h, inv), sums[i]);
+        sums[i] = fma2(d, mul2_rn(h, inv), sums[i]);
       }
     };
     if (kKinds == 1 || in.head == 0) finish(acc[0]);

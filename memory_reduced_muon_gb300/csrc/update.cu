@@ -36,7 +36,7 @@
 #include <set>
 #include <utility>
 
-#include "qm_internal.h"
+#include "qm_elem.h"
 
 namespace qm {
 namespace {
@@ -110,30 +110,6 @@ __device__ __forceinline__ float code_bits(uint32_t u, int b) {
   return __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650u | (uint32_t)b));
 }
 
-// Packed fp32 pairs (one instruction for two lanes of arithmetic), each
-// component rounded to nearest exactly as the scalar __fmul_rn / __fsub_rn.
-// ptxas fuses a packed multiply whose only use is a packed add into a packed
-// FMA (one rounding instead of two), so a product that feeds an addition is
-// always added with the scalar __fadd_rn: those chains were checked bit for
-// bit against the scalar ones on the GPU (sub -> mul, mul -> scalar add,
-// mul -> max -> add, mul -> E4M3 conversion).
-__device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
-      "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 sub2_rn(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
-      "sub.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
 // Four codes (their int32 low bytes, two's complement) into one stored word.
 template <int QK>
 __device__ __forceinline__ uint32_t pack_codes(int q0, int q1, int q2, int q3) {
@@ -141,28 +117,6 @@ __device__ __forceinline__ uint32_t pack_codes(int q0, int q1, int q2, int q3) {
   const uint32_t hi = __byte_perm((uint32_t)q2, (uint32_t)q3, 0x0040u);
   const uint32_t w = __byte_perm(lo, hi, 0x5410u);
   return (QK == QMUON_Q8_INT8) ? w : (w ^ 0x80808080u);
-}
-
-// E8M0 exponent byte of a 32-element block: 127 + e with e the smallest
-// integer such that amax <= 448 * 2^e (448 = 1.75 * 2^8 is the largest E4M3
-// value), clamped to [0, 254]; 127 for amax == 0, 254 for amax == inf.
-// With amax = f * 2^E (f in [1, 2), biased exponent field ef = E + 127),
-// e = E - 8 + [f > 1.75], so the byte is ef - 8 + [mantissa > 0.75].  A
-// subnormal amax (ef = 0, below 2^-126) and any amax below 2^-119 give a
-// negative byte and clamp to 0, so no subnormal case is needed: the byte is
-// a few integer operations and selects, without branches.
-__device__ __forceinline__ int e8m0_of_amax(float amax) {
-  const uint32_t b = __float_as_uint(amax);   // amax >= 0: the sign bit is clear
-  const int ef = (int)(b >> 23);
-  const int byte = ef - 8 + (((b & 0x7FFFFFu) > 0x600000u) ? 1 : 0);
-  const int clamped = byte < 0 ? 0 : (byte > 254 ? 254 : byte);
-  return b == 0u ? 127 : (ef == 0xFF ? 254 : clamped);
-}
-
-// 2^(127 - byte) as an fp32 (byte in [0, 254]: exponent in [-127, 127]); the
-// one subnormal power, 2^-127 (byte 254), is the pattern 0x00400000.
-__device__ __forceinline__ float pow2_from_e8m0(int byte) {
-  return __uint_as_float(byte < 254 ? (uint32_t)(254 - byte) << 23 : 0x00400000u);
 }
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy
@@ -180,12 +134,6 @@ __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1
     k1 += 0xBB67AE85u;
   }
   return c;
-}
-
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return (uint32_t)r;
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
