@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;         // elements of one tensor
-constexpr int64_t kMaxChunks = ((int64_t)1 << 31) - 1;   // of a plan: a grid's CTAs
+constexpr int64_t kMaxChunks = (int64_t)1 << 30;        // of a plan: a grid's CTAs, and int indexes beyond them
 
 // ---------------------------------------------------------------------------
 // global norm and clipping
