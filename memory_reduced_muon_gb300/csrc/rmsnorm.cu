@@ -910,12 +910,12 @@ int bwd_grid(int64_t groups, int sms, int per_sm) {
 }
 
 template <class... Extra>
-cudaError_t launch_bwd_kernel(void (*kernel)(BwdArgs, Extra...), const BwdArgs& A, dim3 block, int smem, int sms, int* grid,
-                              cudaStream_t s, Extra... extra) {
+cudaError_t launch_bwd_kernel(void (*kernel)(BwdArgs, Extra...), const BwdArgs& A, dim3 block, int smem, int most, int sms,
+                              int* grid, cudaStream_t s, Extra... extra) {
   int per_sm = 0;
   const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(kernel), (int)(block.x * block.y), smem, &per_sm);
   if (e != cudaSuccess) return e;
-  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, per_sm);
+  *grid = bwd_grid((A.rows + block.y - 1) / block.y, sms, std::min(per_sm, most));
   return launch_dependent(kernel, *grid, block, smem, s, A, extra...);
 }
 
@@ -924,7 +924,11 @@ cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* g
   const int row = (DSUM ? 3 : 2) * V * (int)(block.x * block.y) * 16;   // bytes of a stage
   const int stages = std::min(3, std::max(1, kMaxSmem / row));
   const int smem = std::max(stages * row, block.y > 1 ? (int)block.y * A.cols * 4 : 0);
-  return launch_bwd_kernel(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, A, block, smem, sms, grid, s, stages);
+  // Rings of up to 150 KB per SM: more bytes in flight slow DRAM down.  16384 x 4096 bf16 takes 83 us with 147 KB (one
+  // CTA of two rows), 91 with 221 (three of one row), 88 with 196 (four, two stages); 32768 x 1024 fp16 37 with 98, 39
+  // with 196.
+  return launch_bwd_kernel(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, A, block, smem, std::max(1, 150 * 1024 / smem), sms, grid, s,
+                           stages);
 }
 
 template <int DT, bool DSUM>
@@ -936,10 +940,12 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
   const std::integral_constant<int, 8> eight;
   if (A.align == 16) {
     const Shape S = pick_shape(A.cols / K, 4, 8, 4, bwd_max_threads);
-    if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, S.block(128), sms, grid, s);
-    if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, S.block(128), sms, grid, s);
-    if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, S.block(128), sms, grid, s);
-    if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, S.block(128), sms, grid, s);
+    // two or more rows per CTA, where there are enough of them
+    const dim3 block = S.V ? S.block(A.rows >= 4 * (int64_t)sms ? 256 : 0) : dim3(1);
+    if (S.V == 1) return launch_bwd_rows<DT, 1, DSUM>(A, block, sms, grid, s);
+    if (S.V == 2) return launch_bwd_rows<DT, 2, DSUM>(A, block, sms, grid, s);
+    if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, block, sms, grid, s);
+    if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, block, sms, grid, s);
   } else {
     const bool pairs =
         DT != QMUON_FP32 && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}});
@@ -949,7 +955,7 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
       const int smem = ((int)block.y * A.cols + C.T * C.V * (pairs ? 2 : 1) + 2) * 4;
       auto in_pieces = [&](auto n, auto p) {
         return launch_bwd_kernel(rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>, A, block, smem,
-                                 sms, grid, s);
+                                 kBwdPerSm, sms, grid, s);
       };
       if constexpr (DT != QMUON_FP32)
         if (pairs) return C.V == 2 ? in_pieces(two, two) : C.V == 4 ? in_pieces(two, four) : in_pieces(two, eight);
@@ -960,8 +966,8 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
   auto walk = [&](auto n) {
     constexpr int N = decltype(n)::value;
     return bytes <= kMaxSmem
-               ? launch_bwd_kernel(rmsnorm_bwd_walk_kernel<DT, N, true>, A, kWalkThreads, (int)bytes, sms, grid, s)
-               : launch_bwd_kernel(rmsnorm_bwd_walk_kernel<DT, N, false>, A, kWalkThreads, 0, sms, grid, s);
+               ? launch_bwd_kernel(rmsnorm_bwd_walk_kernel<DT, N, true>, A, kWalkThreads, (int)bytes, kBwdPerSm, sms, grid, s)
+               : launch_bwd_kernel(rmsnorm_bwd_walk_kernel<DT, N, false>, A, kWalkThreads, 0, kBwdPerSm, sms, grid, s);
   };
   if (A.align == 16) return walk(std::integral_constant<int, K>{});
   if (A.align == 8) return walk(std::integral_constant<int, K / 2>{});
