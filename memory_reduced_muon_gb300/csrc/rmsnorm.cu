@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_walk_kernel(const __grid_con
 // columns, which leaves as one row of `partial`; dgain_kernel adds those rows
 // in order.  The next rows come through a ring of shared-memory slots, each
 // thread's own, `stages` rows ahead.  A CTA has to stay for that sum to stay in
-// registers, and CTAs that stay reach 6.5 TB/s: 16384 x 4096 bf16 in 83 us and
-// 5 more for dgain_kernel, 131072 x 128 fp32 in 29 and 5.  CTAs of 8, 16 or 24
-// rows, whose partial sums are then many, take 96 to 99 us for the first.
+// registers.  16384 x 4096 bf16: 81 us with dgain_kernel (6.6 TB/s), 131072 x 128
+// fp32 34 us.  CTAs of 8, 16 or 24 rows, whose partial sums are then many, took
+// 96 to 99 us for the first.
 constexpr int bwd_max_threads(int V) { return V >= 4 ? 512 : 256; }
 
 __device__ __forceinline__ void wait_rows(int pending) {
