@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
         sums[i] = fma2(d, mul2_rn(h, inv), sums[i]);
       }
     };
-    if (kKinds == 1 || in.head == 0) finish(acc[0]);
-    else finish(acc[kKinds - 1]);
+    if (row < A.rows) {   // past the end inv is infinite where eps is zero
+      if (kKinds == 1 || in.head == 0) finish(acc[0]);
+      else finish(acc[kKinds - 1]);
+    }
     in = next;
   }
   // the columns' sums: those of rows whose pairs start at column 0, then at column 1, then the ends'

@@ -200,6 +200,28 @@ def test_backward_by_differences():
         assert abs(num - got) <= 1e-4 * (np.linalg.norm(_np(dx)) + np.linalg.norm(_np(dg)))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols", [1, 7, 64, 100, 101, 128, 257, 513, 4096])
+@pytest.mark.parametrize("rows", [1, 3, 801])
+def test_backward_without_eps(dtype, cols, rows):
+    # rows that a CTA has room for but that do not exist: 1 / sqrt(0) of theirs must not reach the gain's gradient.
+    # Bounds: test_backward's
+    gen = torch.Generator("cuda").manual_seed(12)
+    h, dy = _rnd(gen, rows, cols).to(DT[dtype]), _rnd(gen, rows, cols).to(DT[dtype])
+    h[h == 0] = 1.0
+    gain = torch.randn(cols, generator=gen, device="cuda")
+    dx, dg = torch.empty_like(h), torch.empty(cols, device="cuda")
+    ws = torch.empty(q.qmuon_rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device="cuda")
+    q.qmuon_rmsnorm_backward(dy, h, gain, rows, cols, dtype, 0.0, dx, dg, ws)
+    H, D, G = _np(h), _np(dy), _np(gain)
+    wx, wg = training.rmsnorm_grad64(D, H, G, 0.0)
+    inv = 1 / np.sqrt(np.mean(H * H, 1, keepdims=True))
+    n, a = np.abs(H) * inv, np.abs(D * G)
+    mag = inv * (a + n * np.mean(a * n, 1, keepdims=True))
+    assert (np.abs(_np(dx) - wx) <= UT[dtype] * (1 + U) * np.abs(wx) + 128 * U * mag + U * np.abs(wx) + TINY[dtype]).all()
+    assert (np.abs(_np(dg) - wg) <= 160 * U * np.sum(np.abs(D) * n, 0) + 1e-44).all()
+
+
 def test_no_rows():
     dg = torch.full((64,), 7.0, device="cuda")
     ws = torch.empty(q.qmuon_rmsnorm_workspace_size(0, 64), dtype=torch.uint8, device="cuda")
