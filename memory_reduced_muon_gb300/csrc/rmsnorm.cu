@@ -8,8 +8,9 @@
 // A row belongs to T threads: a power of two up to a warp (and a CTA then takes
 // several rows), or whole warps.  Rows that fit their threads' registers cross
 // HBM once: in 16-byte vectors where all arrays' rows start on 16 bytes ("rows"
-// kernels), else in pairs of 16-bit elements or single elements ("pieces").
-// Longer ones are walked twice, the second time out of the caches ("walk").
+// kernels), else in pairs of 16-bit elements or single elements ("pieces"),
+// backward also by way of shared memory ("staged").  Longer ones are walked
+// twice, the second time out of the caches ("walk").
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -545,22 +546,22 @@ __global__ void __launch_bounds__(bwd_max_threads(V)) rmsnorm_bwd_rows_kernel(co
   }
 }
 
-// Rows in pieces (see the forward pass); the next row's are loaded while one is
-// computed.  Pairs start at column 0 or 1, by the row, so that a thread's
-// columns differ between the two kinds of rows: it sums each kind's apart.
+// Unaligned rows of 16-bit elements that start alike in all arrays, in pairs
+// (see the forward pass); the next row's are loaded while one is computed.
+// Pairs start at column 0 or 1, by the row, so that a thread's columns differ
+// between the two kinds of rows: it sums each kind's apart.
 constexpr int bwd_piece_threads = 512;
 
-template <int DT, int N, int P, bool DSUM>
+template <int DT, int P, bool DSUM>
 __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(const __grid_constant__ BwdArgs A) {
   using One = Piece<DT, 1>;
-  using Some = Piece<DT, N>;
-  constexpr int kKinds = N;   // 1, or pairs from column 0 and pairs from column 1
+  using Some = Piece<DT, 2>;
   __shared__ float2 part[2][32];
   extern __shared__ __align__(16) float s_acc[];   // [rows of the CTA][cols] of sums, then the gain and zeros for all pieces
   const int T = blockDim.x, t = threadIdx.x, k0 = first_piece<P>(t);
   depends_wait();
   float* s_gain = s_acc + (size_t)blockDim.y * A.cols;
-  for (int c = threadIdx.y * T + t; c < T * P * N + 2; c += T * blockDim.y) s_gain[c] = c < A.cols ? A.gain[c] : 0.0f;
+  for (int c = threadIdx.y * T + t; c < T * P * 2 + 2; c += T * blockDim.y) s_gain[c] = c < A.cols ? A.gain[c] : 0.0f;
   struct Raw {
     typename Some::Raw h[P], d[P], s[DSUM ? P : 1];
     typename One::Raw he, de, se;
@@ -571,9 +572,9 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     const unsigned char* h = row_of<DT>(A.h, row, A.ld_h);
     const unsigned char* d = row_of<DT>(A.dy, row, A.ld_dy);
     const unsigned char* s = row_of<DT>(A.dsum, row, A.ld_dsum);
-    r.head = N == 2 ? (int)(reinterpret_cast<uintptr_t>(h) >> 1) & 1 : 0;
-    r.n = live ? (A.cols - r.head) / N : 0;
-    r.edge = N == 1 || !live                        ? -1
+    r.head = (int)(reinterpret_cast<uintptr_t>(h) >> 1) & 1;
+    r.n = live ? (A.cols - r.head) / 2 : 0;
+    r.edge = !live                                  ? -1
              : t == 0 && r.head                     ? 0
              : t == T - 1 && ((A.cols - r.head) & 1) ? A.cols - 1
                                                     : -1;
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       r.de = One::load(d, r.edge);
       if constexpr (DSUM) r.se = One::load(s, r.edge);
     }
-    const int c0 = (r.head + N * k0) * elem_size(DT);
+    const int c0 = (r.head + 2 * k0) * 2;
     h += c0, d += c0, s += c0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       if constexpr (DSUM) r.s[i] = in ? Some::load(s, i * Some::kStep) : 0;
     }
   };
-  float2 acc[kKinds][P] = {};
+  float2 acc[2][P] = {};   // of pairs from column 0, from column 1
   float acc_edge = 0.0f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   Raw in;
@@ -604,9 +605,9 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
     const int64_t row = base + threadIdx.y;
     Raw next;
     load(row + step, next);
-    const float* g0 = s_gain + in.head + N * k0;
+    const float* g0 = s_gain + in.head + 2 * k0;
     auto gain = [&](int i) {
-      return make_float2(g0[i * Some::kStep], N == 2 ? g0[i * Some::kStep + N - 1] : 0.0f);
+      return make_float2(g0[i * Some::kStep], g0[i * Some::kStep + 1]);
     };
     const float he = One::unpack(in.he).x, de = One::unpack(in.de).x, ge = in.edge >= 0 ? s_gain[in.edge] : 0.0f;
     float2 sh = make_float2(he * he, 0.0f), sa = make_float2(de * ge * he, 0.0f);   // sums of h^2 and a h
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       One::store(dx, in.edge, make_float2(o, 0.0f));
       acc_edge = fmaf(de, he * inv, acc_edge);
     }
-    dx += (in.head + N * k0) * elem_size(DT);
+    dx += (in.head + 2 * k0) * 2;
     auto finish = [&](float2* sums) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -640,8 +641,8 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
       }
     };
     if (row < A.rows) {   // past the end inv is infinite where eps is zero
-      if (kKinds == 1 || in.head == 0) finish(acc[0]);
-      else finish(acc[kKinds - 1]);
+      if (in.head == 0) finish(acc[0]);
+      else finish(acc[1]);
     }
     in = next;
   }
@@ -649,26 +650,247 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   float* mine = s_acc + (size_t)threadIdx.y * A.cols;
   for (int c = t; c < A.cols; c += T) mine[c] = 0.0f;
 #pragma unroll
-  for (int kind = 0; kind < kKinds; ++kind) {
+  for (int kind = 0; kind < 2; ++kind) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = kind + N * (k0 + 32 * i);
-      if (c + N <= A.cols) {
+      const int c = kind + 2 * (k0 + 32 * i);
+      if (c + 2 <= A.cols) {
         mine[c] += acc[kind][i].x;
-        if constexpr (N == 2) mine[c + 1] += acc[kind][i].y;
+        mine[c + 1] += acc[kind][i].y;
       }
     }
   }
   __syncthreads();
-  if (N == 2 && t == 0) mine[0] += acc_edge;
+  if (t == 0) mine[0] += acc_edge;
   __syncthreads();   // one column: both are its
-  if (N == 2 && t == T - 1) mine[A.cols - 1] += acc_edge;
+  if (t == T - 1) mine[A.cols - 1] += acc_edge;
   __syncthreads();
   for (int c = threadIdx.y * T + t; c < A.cols; c += T * blockDim.y) {
     float v = 0.0f;
     for (int y = 0; y < (int)blockDim.y; ++y) v += s_acc[(size_t)y * A.cols + c];
     A.partial[(int64_t)blockIdx.x * A.cols + c] = v;
+  }
+}
+
+// Other rows that do not start on 16 bytes.  The 16-byte words of memory that
+// hold a row come through a ring of slots (as above) as they lie there, so that
+// the row starts in its slot where it starts in its word; the words at an
+// array's two ends, of which a part is not the array's, come by elements.
+// Threads read pairs of columns from the slot, the same ones in every row
+// whatever its start, and keep their gain and its gradient in registers.  Bound
+// by its instructions, which 15 to 20 warps per SM (for their registers) issue
+// in two cycles of three.  9000 x 6001 fp32 with an odd stride: 165 us, 258 read
+// twice by single elements; 6001 x 2049 bf16 with arrays that start unlike each
+// other: 41 us, 54 by single elements in registers (in pairs in registers, where
+// the arrays allow them, 26: hence the kernel above).  Four pairs per thread
+// take 45 us, fewer registers (which spill) 49 and more.
+constexpr int bwd_staged_threads = 512;
+
+__device__ __forceinline__ void row_sync(int T) {
+  if (T <= 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(T) : "memory");
+}
+
+__host__ __device__ constexpr int slot_bytes(int cols, int es) { return (cols * es + 15) / 16 * 16 + 16; }
+
+// An array's first byte and the one after its last, between which words are read whole.
+struct Extent {
+  const unsigned char *begin, *end;
+};
+template <int DT>
+__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int cols) {
+  const unsigned char* b = static_cast<const unsigned char*>(p);
+  return {b, b + ((rows - 1) * ld + cols) * elem_size(DT)};
+}
+
+template <int DT>
+__device__ __forceinline__ void stage_row(unsigned char* slot, const Extent& E, const unsigned char* row, int cols, int t, int T) {
+  constexpr int es = elem_size(DT);
+  const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15), end = off + cols * es, last = (end - 1) >> 4;
+  const unsigned char* words = row - off;
+  const int from = words < E.begin, to = last - (words + 16 * last + 16 > E.end);
+  const unsigned char* w = words + 16 * t;
+  unsigned char* d = slot + 16 * t;
+  for (int j = t; j <= to; j += T, w += 16 * T, d += 16 * T)
+    if (j >= from) async16(d, w);
+  if (from + last > to) {   // a word at the array's start or end
+    for (int b = t * es; b < end; b += T * es)
+      if (b >= off && (b < 16 * from || b >= 16 * to + 16)) {
+        if constexpr (es == 2) *reinterpret_cast<uint16_t*>(slot + b) = *reinterpret_cast<const uint16_t*>(words + b);
+        else *reinterpret_cast<uint32_t*>(slot + b) = *reinterpret_cast<const uint32_t*>(words + b);
+      }
+  }
+}
+
+// V pairs of columns of a staged row: 16-bit ones side by side, T pairs apart;
+// fp32 ones T columns apart.
+template <int DT, int V>
+struct Pairs {
+  using Raw = std::conditional_t<DT == QMUON_FP32, float2, uint32_t>;
+  __device__ __forceinline__ static int col(int i, int half, int t, int T) {
+    return DT == QMUON_FP32 ? t + (2 * i + half) * T : 2 * (t + i * T) + half;
+  }
+  // `row`: the low bits of where the row starts in memory
+  __device__ __forceinline__ static void load(const unsigned char* slot, uint32_t row, int cols, int t, int T, Raw* r) {
+    const int off = (int)(row & 15);
+    if constexpr (DT == QMUON_FP32) {
+      const float* p = reinterpret_cast<const float*>(slot + off);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int a = col(i, 0, t, T), b = col(i, 1, t, T);
+        r[i] = make_float2(a < cols ? p[a] : 0.0f, b < cols ? p[b] : 0.0f);
+      }
+    } else {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(slot + (off & ~3)) + t;
+      const int n = (cols + 1) >> 1;
+      if (off & 2) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = t + i * T < n ? __byte_perm(p[i * T], p[i * T + 1], 0x5432u) : 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = t + i * T < n ? p[i * T] : 0u;
+      }
+      if (cols & 1) {   // an odd row's last
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T == cols >> 1) r[i] &= 0xFFFFu;
+      }
+    }
+  }
+  __device__ __forceinline__ static float2 unpack(Raw r) {
+    if constexpr (DT == QMUON_FP32) return r;
+    else return unpack2<DT>(r);
+  }
+  __device__ __forceinline__ static void store(unsigned char* row, int cols, int t, int T, const float2* f) {
+    if constexpr (DT == QMUON_FP32) {
+      float* p = reinterpret_cast<float*>(row);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int a = col(i, 0, t, T), b = col(i, 1, t, T);
+        if (a < cols) p[a] = f[i].x;
+        if (b < cols) p[b] = f[i].y;
+      }
+    } else {
+      const int n = cols >> 1;
+      uint16_t* p = reinterpret_cast<uint16_t*>(row) + 2 * t;
+      uint32_t w[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = pack2<DT>(f[i].x, f[i].y);
+      if ((reinterpret_cast<uintptr_t>(row) & 2) == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < n) *reinterpret_cast<uint32_t*>(p + 2 * i * T) = w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < n) p[2 * i * T] = (uint16_t)w[i], p[2 * i * T + 1] = (uint16_t)(w[i] >> 16);
+      }
+      if (cols & 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T == n) p[2 * i * T] = (uint16_t)w[i];
+      }
+    }
+  }
+};
+
+template <int DT, int V, bool DSUM>
+__global__ void __launch_bounds__(bwd_staged_threads) rmsnorm_bwd_staged_kernel(const __grid_constant__ BwdArgs A, int stages) {
+  using X = Pairs<DT, V>;
+  constexpr int kArrays = DSUM ? 3 : 2;
+  __shared__ float2 part[2][32];
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int T = blockDim.x, t = threadIdx.x, bytes = slot_bytes(A.cols, elem_size(DT));
+  depends_wait();
+  unsigned char* ring = smem + (size_t)threadIdx.y * stages * kArrays * bytes;   // [stages][kArrays][bytes]
+  float2 acc[V], gain[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int a = X::col(i, 0, t, T), b = X::col(i, 1, t, T);
+    acc[i] = make_float2(0.0f, 0.0f);
+    gain[i] = make_float2(a < A.cols ? A.gain[a] : 0.0f, b < A.cols ? A.gain[b] : 0.0f);
+  }
+  const Extent eh = extent_of<DT>(A.h, A.rows, A.ld_h, A.cols), ed = extent_of<DT>(A.dy, A.rows, A.ld_dy, A.cols),
+               es = DSUM ? extent_of<DT>(A.dsum, A.rows, A.ld_dsum, A.cols) : eh;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t r0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const unsigned char *fh = row_of<DT>(A.h, r0, A.ld_h), *fd = row_of<DT>(A.dy, r0, A.ld_dy), *fs = row_of<DT>(A.dsum, r0, A.ld_dsum);
+  const int64_t step_h = step * A.ld_h * elem_size(DT), step_d = step * A.ld_dy * elem_size(DT),
+                step_s = step * A.ld_dsum * elem_size(DT), step_x = step * A.ld_dx * elem_size(DT);
+  uint32_t oh = (uint32_t)(uintptr_t)fh, od = (uint32_t)(uintptr_t)fd, os = (uint32_t)(uintptr_t)fs;   // low bits of the computed row's
+  int64_t ahead = r0;   // row that is fetched next
+  auto issue = [&](unsigned char* slot) {
+    if (ahead < A.rows) {
+      stage_row<DT>(slot, eh, fh, A.cols, t, T);
+      stage_row<DT>(slot + bytes, ed, fd, A.cols, t, T);
+      if constexpr (DSUM) stage_row<DT>(slot + 2 * bytes, es, fs, A.cols, t, T);
+    }
+    async_commit();   // one group per row, empty past the end
+    ahead += step;
+    fh += step_h, fd += step_d, fs += step_s;
+  };
+  for (int s = 0; s < stages; ++s) issue(ring + s * kArrays * bytes);
+  unsigned char* dx = row_of<DT>(A.dx, r0, A.ld_dx);
+  int flip = 0, s = 0;
+  // the same number of passes in every thread of the CTA
+  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < A.rows; base += step, flip ^= 1) {
+    const bool live = base + threadIdx.y < A.rows;
+    const int cols = live ? A.cols : 0;
+    unsigned char* slot = ring + s * kArrays * bytes;
+    wait_rows(stages - 1);
+    row_sync(T);   // the other threads' copies
+    typename X::Raw rh[V], rd[V], rs[DSUM ? V : 1];
+    X::load(slot, oh, cols, t, T, rh);
+    X::load(slot + bytes, od, cols, t, T, rd);
+    if constexpr (DSUM) X::load(slot + 2 * bytes, os, cols, t, T, rs);
+    oh += (uint32_t)step_h, od += (uint32_t)step_d, os += (uint32_t)step_s;
+    float2 sh = make_float2(0.0f, 0.0f), sa = sh;   // sums of h^2 and a h
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 h = X::unpack(rh[i]);
+      sh = fma2(h, h, sh);
+      sa = fma2(mul2_rn(X::unpack(rd[i]), gain[i]), h, sa);
+    }
+    const float2 sum = row_sum<true>(make_float2(sh.x + sh.y, sa.x + sa.y), T, part[flip]);
+    if (T <= 32) __syncwarp();   // else row_sum's barrier: all threads of the row have read the slot
+    issue(slot);
+    const float inv = inverse_norm(sum.x, A.inv_cols, A.eps);
+    const float c = -(sum.y * A.inv_cols * inv * inv);   // -mean(a h) inv^2
+    if (live) {   // past the end inv is infinite where eps is zero
+      float2 o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 h = X::unpack(rh[i]), d = X::unpack(rd[i]);
+        const float2 e = fma2(h, make_float2(c, c), mul2_rn(d, gain[i]));
+        if constexpr (DSUM) o[i] = fma2(e, make_float2(inv, inv), X::unpack(rs[i]));
+        else o[i] = mul2_rn(e, inv);
+        acc[i] = fma2(d, mul2_rn(h, inv), acc[i]);
+      }
+      X::store(dx, cols, t, T, o);
+    }
+    dx += step_x;
+    s = s + 1 == stages ? 0 : s + 1;
+  }
+  float* out = A.partial + (int64_t)blockIdx.x * A.cols;
+  float* mine = out;
+  if (blockDim.y > 1) {
+    async_wait<0>();
+    __syncthreads();   // the ring is free
+    mine = reinterpret_cast<float*>(smem) + (size_t)threadIdx.y * A.cols;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int a = X::col(i, 0, t, T), b = X::col(i, 1, t, T);
+    if (a < A.cols) mine[a] = acc[i].x;
+    if (b < A.cols) mine[b] = acc[i].y;
+  }
+  if (blockDim.y == 1) return;
+  __syncthreads();
+  for (int k = threadIdx.y * T + t; k < A.cols; k += T * blockDim.y) {
+    float v = 0.0f;
+    for (int y = 0; y < (int)blockDim.y; ++y) v += reinterpret_cast<const float*>(smem)[(size_t)y * A.cols + k];
+    out[k] = v;
   }
 }
 
@@ -921,25 +1143,25 @@ cudaError_t launch_bwd_kernel(void (*kernel)(BwdArgs, Extra...), const BwdArgs& 
   return launch_dependent(kernel, *grid, block, smem, s, A, extra...);
 }
 
-template <int DT, int V, bool DSUM>
-cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* grid, cudaStream_t s) {
-  const int row = (DSUM ? 3 : 2) * V * (int)(block.x * block.y) * 16;   // bytes of a stage
+// `row`: bytes of a stage of the CTA's rings.
+inline cudaError_t launch_bwd_ring(void (*kernel)(BwdArgs, int), const BwdArgs& A, const dim3& block, int row, int sms, int* grid,
+                                   cudaStream_t s) {
   const int stages = std::min(3, std::max(1, kMaxSmem / row));
   const int smem = std::max(stages * row, block.y > 1 ? (int)block.y * A.cols * 4 : 0);
   // Rings of up to 150 KB per SM: more bytes in flight slow DRAM down.  16384 x 4096 bf16 takes 83 us with 147 KB (one
   // CTA of two rows), 91 with 221 (three of one row), 88 with 196 (four, two stages); 32768 x 1024 fp16 37 with 98, 39
   // with 196.
-  return launch_bwd_kernel(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, A, block, smem, std::max(1, 150 * 1024 / smem), sms, grid, s,
-                           stages);
+  return launch_bwd_kernel(kernel, A, block, smem, std::max(1, 150 * 1024 / smem), sms, grid, s, stages);
+}
+template <int DT, int V, bool DSUM>
+cudaError_t launch_bwd_rows(const BwdArgs& A, const dim3& block, int sms, int* grid, cudaStream_t s) {
+  return launch_bwd_ring(rmsnorm_bwd_rows_kernel<DT, V, DSUM>, A, block, (DSUM ? 3 : 2) * V * (int)(block.x * block.y) * 16, sms, grid,
+                         s);
 }
 
 template <int DT, bool DSUM>
 cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
   constexpr int K = Vec16<DT>::kElems;
-  const std::integral_constant<int, 1> one;
-  const std::integral_constant<int, 2> two;
-  const std::integral_constant<int, 4> four;
-  const std::integral_constant<int, 8> eight;
   if (A.align == 16) {
     const Shape S = pick_shape(A.cols / K, 4, 8, 4, bwd_max_threads);
     // two or more rows per CTA, where there are enough of them
@@ -949,19 +1171,26 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
     if (S.V == 4) return launch_bwd_rows<DT, 4, DSUM>(A, block, sms, grid, s);
     if (S.V == 8) return launch_bwd_rows<DT, 8, DSUM>(A, block, sms, grid, s);
   } else {
-    const bool pairs =
-        DT != QMUON_FP32 && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}});
-    const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), 8, bwd_piece_threads);
+    if constexpr (DT != QMUON_FP32) {
+      const Shape C = piece_shape(A.cols / 2, 8, bwd_piece_threads);
+      if (C.V && rows_alike({{A.h, A.ld_h}, {A.dy, A.ld_dy}, {A.dsum, A.ld_dsum}, {A.dx, A.ld_dx}})) {
+        const dim3 block = C.block(256);
+        const int smem = ((int)block.y * A.cols + C.T * C.V * 2 + 2) * 4;
+        auto launch = [&](auto kernel) { return launch_bwd_kernel(kernel, A, block, smem, kBwdPerSm, sms, grid, s); };
+        if (C.V == 2) return launch(rmsnorm_bwd_pieces_kernel<DT, 2, DSUM>);
+        if (C.V == 4) return launch(rmsnorm_bwd_pieces_kernel<DT, 4, DSUM>);
+        return launch(rmsnorm_bwd_pieces_kernel<DT, 8, DSUM>);
+      }
+    }
+    const Shape C = pick_shape((A.cols + 1) / 2, 8, 8, 8, [](int) { return bwd_staged_threads; });
     if (C.V) {
       const dim3 block = C.block(256);
-      const int smem = ((int)block.y * A.cols + C.T * C.V * (pairs ? 2 : 1) + 2) * 4;
-      auto in_pieces = [&](auto n, auto p) {
-        return launch_bwd_kernel(rmsnorm_bwd_pieces_kernel<DT, decltype(n)::value, decltype(p)::value, DSUM>, A, block, smem,
-                                 kBwdPerSm, sms, grid, s);
-      };
-      if constexpr (DT != QMUON_FP32)
-        if (pairs) return C.V == 2 ? in_pieces(two, two) : C.V == 4 ? in_pieces(two, four) : in_pieces(two, eight);
-      return C.V == 2 ? in_pieces(one, two) : C.V == 4 ? in_pieces(one, four) : in_pieces(one, eight);
+      const int row = (DSUM ? 3 : 2) * (int)block.y * slot_bytes(A.cols, elem_size(DT));
+      auto launch = [&](auto kernel) { return launch_bwd_ring(kernel, A, block, row, sms, grid, s); };
+      if (C.V == 1) return launch(rmsnorm_bwd_staged_kernel<DT, 1, DSUM>);
+      if (C.V == 2) return launch(rmsnorm_bwd_staged_kernel<DT, 2, DSUM>);
+      if (C.V == 4) return launch(rmsnorm_bwd_staged_kernel<DT, 4, DSUM>);
+      return launch(rmsnorm_bwd_staged_kernel<DT, 8, DSUM>);
     }
   }
   const int64_t bytes = (int64_t)A.cols * 4;
@@ -974,8 +1203,8 @@ cudaError_t launch_bwd(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
   if (A.align == 16) return walk(std::integral_constant<int, K>{});
   if (A.align == 8) return walk(std::integral_constant<int, K / 2>{});
   if constexpr (K == 8)
-    if (A.align == 4) return walk(two);
-  return walk(one);
+    if (A.align == 4) return walk(std::integral_constant<int, 2>{});
+  return walk(std::integral_constant<int, 1>{});
 }
 template <int DT>
 cudaError_t launch_bwd_dt(const BwdArgs& A, int sms, int* grid, cudaStream_t s) {
