@@ -111,6 +111,10 @@ __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t 
   if (!valid) return;
   if constexpr (N == 1) {
     payload[e] = (uint8_t)cvt_e4m3x2(__fmul_rn(y[0], mult), 0.0f);
+  } else if constexpr (N == 2) {
+    const uint32_t w = cvt_e4m3x2(__fmul_rn(y[0], mult), __fmul_rn(y[1], mult));
+    if ((reinterpret_cast<uintptr_t>(payload) & 1) == 0) *reinterpret_cast<uint16_t*>(payload + e) = (uint16_t)w;
+    else payload[e] = (uint8_t)w, payload[e + 1] = (uint8_t)(w >> 8);
   } else {
     uint32_t w[N / 4];
 #pragma unroll
@@ -123,6 +127,124 @@ __device__ __forceinline__ void store_mxfp8(const float* y, bool valid, int64_t 
   }
   if ((e & 31) == 0) scale[e >> 5] = (uint8_t)byte;
 }
+
+// ---------------------------------------------------------------------------
+// rows that start anywhere, in shared memory
+// ---------------------------------------------------------------------------
+// The 16-byte words of memory that hold a row are copied to a slot as they lie
+// there, so that the row starts in its slot where it starts in its word; the
+// words at an array's two ends, of which a part is not the array's, come by
+// elements.  Threads then read pairs of columns, the same ones in every row
+// whatever its start.
+template <bool MANY>   // see row_sum
+__device__ __forceinline__ void row_sync(int T) {
+  if (T <= 32) __syncwarp();
+  else if constexpr (MANY) asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(T) : "memory");
+  else __syncthreads();
+}
+
+__host__ __device__ constexpr int slot_bytes(int cols, int es) { return (cols * es + 15) / 16 * 16 + 16; }
+
+// An array's first byte and the one after its last, between which words are read whole.
+struct Extent {
+  const unsigned char *begin, *end;
+};
+template <int DT>
+__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int cols) {
+  const unsigned char* b = static_cast<const unsigned char*>(p);
+  return {b, b + ((rows - 1) * ld + cols) * elem_size(DT)};
+}
+
+template <int DT>
+__device__ __forceinline__ void stage_row(unsigned char* slot, const Extent& E, const unsigned char* row, int cols, int t, int T) {
+  constexpr int es = elem_size(DT);
+  const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15), end = off + cols * es, last = (end - 1) >> 4;
+  const unsigned char* words = row - off;
+  const int from = words < E.begin, to = last - (words + 16 * last + 16 > E.end);
+  const unsigned char* w = words + 16 * t;
+  unsigned char* d = slot + 16 * t;
+  for (int j = t; j <= to; j += T, w += 16 * T, d += 16 * T)
+    if (j >= from) async16(d, w);
+  if (from + last > to) {   // a word at the array's start or end
+    for (int b = t * es; b < end; b += T * es)
+      if (b >= off && (b < 16 * from || b >= 16 * to + 16)) {
+        if constexpr (es == 2) *reinterpret_cast<uint16_t*>(slot + b) = *reinterpret_cast<const uint16_t*>(words + b);
+        else *reinterpret_cast<uint32_t*>(slot + b) = *reinterpret_cast<const uint32_t*>(words + b);
+      }
+  }
+}
+
+// V pairs of columns of a staged row: 16-bit ones side by side, T pairs apart;
+// fp32 ones T columns apart.
+template <int DT, int V>
+struct Pairs {
+  using Raw = std::conditional_t<DT == QMUON_FP32, float2, uint32_t>;
+  __device__ __forceinline__ static int col(int i, int half, int t, int T) {
+    return DT == QMUON_FP32 ? t + (2 * i + half) * T : 2 * (t + i * T) + half;
+  }
+  // `row`: the low bits of where the row starts in memory
+  __device__ __forceinline__ static void load(const unsigned char* slot, uint32_t row, int cols, int t, int T, Raw* r) {
+    const int off = (int)(row & 15);
+    if constexpr (DT == QMUON_FP32) {
+      const float* p = reinterpret_cast<const float*>(slot + off);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int a = col(i, 0, t, T), b = col(i, 1, t, T);
+        r[i] = make_float2(a < cols ? p[a] : 0.0f, b < cols ? p[b] : 0.0f);
+      }
+    } else {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(slot + (off & ~3)) + t;
+      const int n = (cols + 1) >> 1;
+      if (off & 2) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = t + i * T < n ? __byte_perm(p[i * T], p[i * T + 1], 0x5432u) : 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = t + i * T < n ? p[i * T] : 0u;
+      }
+      if (cols & 1) {   // an odd row's last
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T == cols >> 1) r[i] &= 0xFFFFu;
+      }
+    }
+  }
+  __device__ __forceinline__ static float2 unpack(Raw r) {
+    if constexpr (DT == QMUON_FP32) return r;
+    else return unpack2<DT>(r);
+  }
+  __device__ __forceinline__ static void store(unsigned char* row, int cols, int t, int T, const float2* f) {
+    if constexpr (DT == QMUON_FP32) {
+      float* p = reinterpret_cast<float*>(row);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int a = col(i, 0, t, T), b = col(i, 1, t, T);
+        if (a < cols) p[a] = f[i].x;
+        if (b < cols) p[b] = f[i].y;
+      }
+    } else {
+      const int n = cols >> 1;
+      uint16_t* p = reinterpret_cast<uint16_t*>(row) + 2 * t;
+      uint32_t w[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = pack2<DT>(f[i].x, f[i].y);
+      if ((reinterpret_cast<uintptr_t>(row) & 2) == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < n) *reinterpret_cast<uint32_t*>(p + 2 * i * T) = w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < n) p[2 * i * T] = (uint16_t)w[i], p[2 * i * T + 1] = (uint16_t)(w[i] >> 16);
+      }
+      if (cols & 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T == n) p[2 * i * T] = (uint16_t)w[i];
+      }
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // forward
@@ -215,7 +337,7 @@ __global__ void __launch_bounds__(fwd_max_threads(V)) rmsnorm_fwd_rows_kernel(co
 template <int DT, int N>
 struct Piece {
   using Raw = std::conditional_t<N == 2 || DT == QMUON_FP32, uint32_t, uint16_t>;
-  static constexpr int kStep = 32 * N;   // columns between a thread's pieces: a warp's lie side by side
+  [[maybe_unused]] static constexpr int kStep = 32 * N;   // columns between a thread's pieces: a warp's lie side by side
   __device__ __forceinline__ static Raw load(const unsigned char* row, int c) {
     return *reinterpret_cast<const Raw*>(row + c * elem_size(DT));
   }
@@ -237,7 +359,7 @@ __device__ __forceinline__ int first_piece(int t) {
   return (t >> 5) * (32 * P) + (t & 31);
 }
 
-template <int DT, int N, int P, bool RES, bool MX>
+template <int DT, int N, int P, bool RES>
 __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_constant__ FwdArgs A) {
   using One = Piece<DT, 1>;
   using Some = Piece<DT, N>;
@@ -304,9 +426,72 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
         const float2 g = gain_of(i);
         if (A.sum) Some::store(sum, d, h[i]);
         h[i] = mul2_rn(mul2_rn(h[i], inv), g);
-        if (!MX || A.y) Some::store(y, d, h[i]);
+        Some::store(y, d, h[i]);
       }
-      if constexpr (MX) store_mxfp8<1>(&h[i].x, in, row * A.cols + c0 + d, A.payload, A.scale);
+    }
+  }
+}
+
+// Rows in a slot each (see above): where 16-bit arrays start unlike each other,
+// and to MXFP8, whose blocks of 32 start where pairs of a row with a head do not.
+// Bound by its instructions: 8000 x 4096 bf16 with a residual and odd strides to
+// MXFP8 72 us (97 by single elements in registers; 94 with four pairs per
+// thread), 9000 x 7001 bf16 with arrays that start unlike each other 145 us (207).
+template <int DT, int V, bool RES, bool MX>
+__global__ void __launch_bounds__(1024) rmsnorm_fwd_staged_kernel(const __grid_constant__ FwdArgs A) {
+  using X = Pairs<DT, V>;
+  __shared__ float part[2][32];
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int T = blockDim.x, t = threadIdx.x, bytes = slot_bytes(A.cols, elem_size(DT));
+  unsigned char* slot = smem + threadIdx.y * (RES ? 2 : 1) * bytes;
+  depends_wait();
+  const Extent ex = extent_of<DT>(A.x, A.rows, A.ld_x, A.cols), er = extent_of<DT>(A.residual, A.rows, A.ld_residual, A.cols);
+  int flip = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < A.rows; r0 += (int64_t)gridDim.x * blockDim.y, flip ^= 1) {
+    const int64_t row = r0 + threadIdx.y;
+    const int cols = row < A.rows ? A.cols : 0;
+    const unsigned char *x = row_of<DT>(A.x, row, A.ld_x), *res = row_of<DT>(A.residual, row, A.ld_residual);
+    if (cols) {
+      stage_row<DT>(slot, ex, x, cols, t, T);
+      if constexpr (RES) stage_row<DT>(slot + bytes, er, res, cols, t, T);
+    }
+    async_commit();
+    float2 gain[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int a = X::col(i, 0, t, T), b = X::col(i, 1, t, T);
+      gain[i] = make_float2(a < cols ? A.gain[a] : 0.0f, b < cols ? A.gain[b] : 0.0f);
+    }
+    async_wait<0>();
+    row_sync<false>(T);
+    typename X::Raw rx[V], rr[RES ? V : 1];
+    X::load(slot, (uint32_t)(uintptr_t)x, cols, t, T, rx);
+    if constexpr (RES) X::load(slot + bytes, (uint32_t)(uintptr_t)res, cols, t, T, rr);
+    float2 h[V], ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      h[i] = X::unpack(rx[i]);
+      if constexpr (RES) h[i] = add2(h[i], X::unpack(rr[i]));
+      ss = fma2(h[i], h[i], ss);
+    }
+    const float inv = inverse_norm(row_sum<false>(ss.x + ss.y, T, part[flip]), A.inv_cols, A.eps);
+    if (T <= 32) __syncwarp();   // else row_sum's barrier: all threads of the row have read the slots
+    if (A.sum) X::store(row_of<DT>(A.sum, row, A.ld_sum), cols, t, T, h);
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = mul2_rn(mul2_rn(h[i], inv), gain[i]);
+    if (!MX || A.y) X::store(row_of<DT>(A.y, row, A.ld_y), cols, t, T, h);
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int a = X::col(i, 0, t, T), b = X::col(i, 1, t, T);
+        const int64_t e = row * A.cols;
+        if constexpr (DT == QMUON_FP32) {
+          store_mxfp8<1>(&h[i].x, a < cols, e + a, A.payload, A.scale);
+          store_mxfp8<1>(&h[i].y, b < cols, e + b, A.payload, A.scale);
+        } else {
+          store_mxfp8<2>(&h[i].x, a < cols, e + a, A.payload, A.scale);
+        }
+      }
     }
   }
 }
@@ -678,127 +863,15 @@ __global__ void __launch_bounds__(bwd_piece_threads) rmsnorm_bwd_pieces_kernel(c
   }
 }
 
-// Other rows that do not start on 16 bytes.  The 16-byte words of memory that
-// hold a row come through a ring of slots (as above) as they lie there, so that
-// the row starts in its slot where it starts in its word; the words at an
-// array's two ends, of which a part is not the array's, come by elements.
-// Threads read pairs of columns from the slot, the same ones in every row
-// whatever its start, and keep their gain and its gradient in registers.  Bound
-// by its instructions, which 15 to 20 warps per SM (for their registers) issue
-// in two cycles of three.  9000 x 6001 fp32 with an odd stride: 165 us, 258 read
+// Other rows that do not start on 16 bytes, through a ring of slots (as above).
+// The gain of a thread's columns and its gradient stay in registers.  Bound by
+// its instructions, which 15 to 20 warps per SM (for their registers) issue in
+// two cycles of three.  9000 x 6001 fp32 with an odd stride: 165 us, 258 read
 // twice by single elements; 6001 x 2049 bf16 with arrays that start unlike each
 // other: 41 us, 54 by single elements in registers (in pairs in registers, where
 // the arrays allow them, 26: hence the kernel above).  Four pairs per thread
 // take 45 us, fewer registers (which spill) 49 and more.
 constexpr int bwd_staged_threads = 512;
-
-__device__ __forceinline__ void row_sync(int T) {
-  if (T <= 32) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(T) : "memory");
-}
-
-__host__ __device__ constexpr int slot_bytes(int cols, int es) { return (cols * es + 15) / 16 * 16 + 16; }
-
-// An array's first byte and the one after its last, between which words are read whole.
-struct Extent {
-  const unsigned char *begin, *end;
-};
-template <int DT>
-__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int cols) {
-  const unsigned char* b = static_cast<const unsigned char*>(p);
-  return {b, b + ((rows - 1) * ld + cols) * elem_size(DT)};
-}
-
-template <int DT>
-__device__ __forceinline__ void stage_row(unsigned char* slot, const Extent& E, const unsigned char* row, int cols, int t, int T) {
-  constexpr int es = elem_size(DT);
-  const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15), end = off + cols * es, last = (end - 1) >> 4;
-  const unsigned char* words = row - off;
-  const int from = words < E.begin, to = last - (words + 16 * last + 16 > E.end);
-  const unsigned char* w = words + 16 * t;
-  unsigned char* d = slot + 16 * t;
-  for (int j = t; j <= to; j += T, w += 16 * T, d += 16 * T)
-    if (j >= from) async16(d, w);
-  if (from + last > to) {   // a word at the array's start or end
-    for (int b = t * es; b < end; b += T * es)
-      if (b >= off && (b < 16 * from || b >= 16 * to + 16)) {
-        if constexpr (es == 2) *reinterpret_cast<uint16_t*>(slot + b) = *reinterpret_cast<const uint16_t*>(words + b);
-        else *reinterpret_cast<uint32_t*>(slot + b) = *reinterpret_cast<const uint32_t*>(words + b);
-      }
-  }
-}
-
-// V pairs of columns of a staged row: 16-bit ones side by side, T pairs apart;
-// fp32 ones T columns apart.
-template <int DT, int V>
-struct Pairs {
-  using Raw = std::conditional_t<DT == QMUON_FP32, float2, uint32_t>;
-  __device__ __forceinline__ static int col(int i, int half, int t, int T) {
-    return DT == QMUON_FP32 ? t + (2 * i + half) * T : 2 * (t + i * T) + half;
-  }
-  // `row`: the low bits of where the row starts in memory
-  __device__ __forceinline__ static void load(const unsigned char* slot, uint32_t row, int cols, int t, int T, Raw* r) {
-    const int off = (int)(row & 15);
-    if constexpr (DT == QMUON_FP32) {
-      const float* p = reinterpret_cast<const float*>(slot + off);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int a = col(i, 0, t, T), b = col(i, 1, t, T);
-        r[i] = make_float2(a < cols ? p[a] : 0.0f, b < cols ? p[b] : 0.0f);
-      }
-    } else {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(slot + (off & ~3)) + t;
-      const int n = (cols + 1) >> 1;
-      if (off & 2) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) r[i] = t + i * T < n ? __byte_perm(p[i * T], p[i * T + 1], 0x5432u) : 0u;
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) r[i] = t + i * T < n ? p[i * T] : 0u;
-      }
-      if (cols & 1) {   // an odd row's last
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (t + i * T == cols >> 1) r[i] &= 0xFFFFu;
-      }
-    }
-  }
-  __device__ __forceinline__ static float2 unpack(Raw r) {
-    if constexpr (DT == QMUON_FP32) return r;
-    else return unpack2<DT>(r);
-  }
-  __device__ __forceinline__ static void store(unsigned char* row, int cols, int t, int T, const float2* f) {
-    if constexpr (DT == QMUON_FP32) {
-      float* p = reinterpret_cast<float*>(row);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int a = col(i, 0, t, T), b = col(i, 1, t, T);
-        if (a < cols) p[a] = f[i].x;
-        if (b < cols) p[b] = f[i].y;
-      }
-    } else {
-      const int n = cols >> 1;
-      uint16_t* p = reinterpret_cast<uint16_t*>(row) + 2 * t;
-      uint32_t w[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) w[i] = pack2<DT>(f[i].x, f[i].y);
-      if ((reinterpret_cast<uintptr_t>(row) & 2) == 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (t + i * T < n) *reinterpret_cast<uint32_t*>(p + 2 * i * T) = w[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (t + i * T < n) p[2 * i * T] = (uint16_t)w[i], p[2 * i * T + 1] = (uint16_t)(w[i] >> 16);
-      }
-      if (cols & 1) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (t + i * T == n) p[2 * i * T] = (uint16_t)w[i];
-      }
-    }
-  }
-};
 
 template <int DT, int V, bool DSUM>
 __global__ void __launch_bounds__(bwd_staged_threads) rmsnorm_bwd_staged_kernel(const __grid_constant__ BwdArgs A, int stages) {
@@ -844,7 +917,7 @@ __global__ void __launch_bounds__(bwd_staged_threads) rmsnorm_bwd_staged_kernel(
     const int cols = live ? A.cols : 0;
     unsigned char* slot = ring + s * kArrays * bytes;
     wait_rows(stages - 1);
-    row_sync(T);   // the other threads' copies
+    row_sync<true>(T);   // the other threads' copies
     typename X::Raw rh[V], rd[V], rs[DSUM ? V : 1];
     X::load(slot, oh, cols, t, T, rh);
     X::load(slot + bytes, od, cols, t, T, rd);
@@ -1092,40 +1165,64 @@ template <int DT, bool RES, bool MX>
 cudaError_t launch_fwd(const FwdArgs& A, cudaStream_t s) {
   constexpr int K = Vec16<DT>::kElems;
   // Four vectors per thread, so that a row takes few warps (and the bytes in flight are many); where rows do not fill
-  // the SMs, one, so that a row is done sooner: one row of 4096 bf16
-  // takes 3.7 us so, 4.5 with four.
+  // the SMs, one, so that a row is done sooner: one row of 4096 bf16 takes 3.7 us so,
+  // 4.5 with four.
   const bool few = A.rows <= device_sms();
   const int least = MX && DT == QMUON_FP32 ? 8 : 4;   // the 32 elements of a scale lie in one access of a row's threads
   const Shape S = A.align == 16 ? pick_shape(A.cols / K, few ? 1 : 4, 4, least, fwd_max_threads) : Shape{0, 0};
-  const bool pairs = !MX && DT != QMUON_FP32 &&
-                     rows_alike({{A.x, A.ld_x}, {A.residual, A.ld_residual}, {A.sum, A.ld_sum}, {A.y, A.ld_y}});
-  // Pairs: four per thread (8 take 22.2 us for 6001 x 2049 fp16, four 20.6); single elements: eight (8000 x 4096 bf16 to
-  // MXFP8 97 us, 110 with four).
-  const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), pairs ? 4 : 8, 1024);
-  const bool pieces = A.align < 16 && C.V;
-  const dim3 block = S.V ? S.block(0) : pieces ? C.block(0) : dim3(1024);
-  const unsigned grid = (unsigned)std::min<int64_t>((A.rows + block.y - 1) / block.y, ((int64_t)1 << 31) - 1);
-  if (S.V == 1) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 1, RES, MX>, grid, block, 0, s, A);
-  if (S.V == 2) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 2, RES, MX>, grid, block, 0, s, A);
-  if (S.V == 4) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 4, RES, MX>, grid, block, 0, s, A);
-  if (!pieces) {
-    if (A.align == 16) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K, MX>, grid, block, 0, s, A);
-    if constexpr (!MX) {
-      if (A.align == 8) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K / 2, MX>, grid, block, 0, s, A);
-      if constexpr (K == 8)
-        if (A.align == 4) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 2, MX>, grid, block, 0, s, A);
-    }
-    return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 1, MX>, grid, block, 0, s, A);
+  auto grid = [&](const dim3& b) { return (unsigned)std::min<int64_t>((A.rows + b.y - 1) / b.y, ((int64_t)1 << 31) - 1); };
+  if (A.align == 16) {
+    const dim3 block = S.V ? S.block(0) : dim3(1024);
+    if (S.V == 1) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 1, RES, MX>, grid(block), block, 0, s, A);
+    if (S.V == 2) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 2, RES, MX>, grid(block), block, 0, s, A);
+    if (S.V == 4) return launch_dependent(rmsnorm_fwd_rows_kernel<DT, 4, RES, MX>, grid(block), block, 0, s, A);
+    return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K, MX>, grid(block), block, 0, s, A);
   }
-  auto in_pieces = [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    if (C.V == 2) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 2, RES, MX>, grid, block, 0, s, A);
-    if (C.V == 4) return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 4, RES, MX>, grid, block, 0, s, A);
-    return launch_dependent(rmsnorm_fwd_pieces_kernel<DT, N, 8, RES, MX>, grid, block, 0, s, A);
-  };
-  if constexpr (!MX && DT != QMUON_FP32)
-    if (pairs) return in_pieces(std::integral_constant<int, 2>{});
-  return in_pieces(std::integral_constant<int, 1>{});
+  if constexpr (!MX) {
+    // Pairs: four per thread (eight take 22.2 us for 6001 x 2049 fp16, four 20.6).  Single elements: eight; those of 16 bits
+    // in rows of up to 128 columns only (300000 x 101 bf16 62 us, 84 by way of shared memory; 100000 x 257 57 and 49).
+    const bool pairs = DT != QMUON_FP32 &&
+                       rows_alike({{A.x, A.ld_x}, {A.residual, A.ld_residual}, {A.sum, A.ld_sum}, {A.y, A.ld_y}});
+    const Shape C = piece_shape(A.cols / (pairs ? 2 : 1), pairs ? 4 : 8, 1024);
+    const dim3 block = C.V ? C.block(0) : dim3(1);
+    auto launch = [&](auto kernel) { return launch_dependent(kernel, grid(block), block, 0, s, A); };
+    if constexpr (DT != QMUON_FP32) {
+      if (pairs && C.V == 2) return launch(rmsnorm_fwd_pieces_kernel<DT, 2, 2, RES>);
+      if (pairs && C.V == 4) return launch(rmsnorm_fwd_pieces_kernel<DT, 2, 4, RES>);
+      if (pairs && C.V == 8) return launch(rmsnorm_fwd_pieces_kernel<DT, 2, 8, RES>);
+    }
+    if (!pairs && C.V == 2) return launch(rmsnorm_fwd_pieces_kernel<DT, 1, 2, RES>);
+    if (!pairs && C.V == 4) return launch(rmsnorm_fwd_pieces_kernel<DT, 1, 4, RES>);
+    if constexpr (DT == QMUON_FP32)
+      if (C.V == 8) return launch(rmsnorm_fwd_pieces_kernel<DT, 1, 8, RES>);
+  }
+  if constexpr (MX || DT != QMUON_FP32) {
+    // The 32 elements of a scale lie in one access of a row's threads.  Without a scale, rows that take more than 512
+    // threads are as fast read twice (4000 x 12001 bf16 128 us, 136 so); with one, not (12032 columns 174 and 142).
+    const Shape C = pick_shape((A.cols + 1) / 2, 8, 8, !MX ? 8 : DT == QMUON_FP32 ? 32 : 16, [](int) { return MX ? 1024 : 512; });
+    if (C.V) {
+      const dim3 block = C.block(0);
+      const int smem = (RES ? 2 : 1) * (int)block.y * slot_bytes(A.cols, elem_size(DT));
+      auto launch = [&](auto kernel) {
+        int per_sm = 0;   // the query lets the kernel have its shared memory
+        const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(kernel), (int)(block.x * block.y), smem, &per_sm);
+        return e != cudaSuccess ? e : launch_dependent(kernel, grid(block), block, smem, s, A);
+      };
+      if constexpr (MX) {   // the others have more than 128 columns: eight pairs
+        if (C.V == 1) return launch(rmsnorm_fwd_staged_kernel<DT, 1, RES, MX>);
+        if (C.V == 2) return launch(rmsnorm_fwd_staged_kernel<DT, 2, RES, MX>);
+        if (C.V == 4) return launch(rmsnorm_fwd_staged_kernel<DT, 4, RES, MX>);
+      }
+      return launch(rmsnorm_fwd_staged_kernel<DT, 8, RES, MX>);
+    }
+  }
+  const dim3 block(1024);
+  if constexpr (!MX) {
+    if (A.align == 8) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, K / 2, MX>, grid(block), block, 0, s, A);
+    if constexpr (K == 8)
+      if (A.align == 4) return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 2, MX>, grid(block), block, 0, s, A);
+  }
+  return launch_dependent(rmsnorm_fwd_walk_kernel<DT, 1, MX>, grid(block), block, 0, s, A);
 }
 template <int DT>
 cudaError_t launch_fwd_dt(const FwdArgs& A, cudaStream_t s) {
@@ -1246,23 +1343,25 @@ using namespace qm;
 
 extern "C" qmuon_status qmuon_rmsnorm_forward(const qmuon_rmsnorm* n, void* stream) {
   NvtxRange nvtx_range("qmuon_rmsnorm_forward");
-  if (!n || !check_sizes(n->rows, n->cols, n->dtype, n->eps)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->rows == 0) return QMUON_OK;
-  if ((!n->y && !n->payload) || (n->payload == nullptr) != (n->scale_inv == nullptr)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->payload && n->cols % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
-  int align = row_align(n->cols, n->dtype, n->gain, n->payload);
-  if (!n->gain || !is_aligned(n->gain, 4) || !check_matrix(n->x, n->ld_x, n->cols, n->dtype, &align))
-    return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->residual && !check_matrix(n->residual, n->ld_residual, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->sum && !check_matrix(n->sum, n->ld_sum, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (n->y && !check_matrix(n->y, n->ld_y, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
-  FwdArgs A{n->x,    n->residual,    n->gain,   n->sum,  n->y,    n->payload, n->scale_inv, n->rows,
-            n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, align, n->eps, 1.0f / (float)n->cols};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = n->dtype == QMUON_BF16   ? launch_fwd_dt<QMUON_BF16>(A, s)
-                        : n->dtype == QMUON_FP16 ? launch_fwd_dt<QMUON_FP16>(A, s)
-                                                 : launch_fwd_dt<QMUON_FP32>(A, s);
-  return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_forward (launch)", e);
+  return no_throw("qmuon_rmsnorm_forward", [&]() -> qmuon_status {
+    if (!n || !check_sizes(n->rows, n->cols, n->dtype, n->eps)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->rows == 0) return QMUON_OK;
+    if ((!n->y && !n->payload) || (n->payload == nullptr) != (n->scale_inv == nullptr)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->payload && n->cols % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
+    int align = row_align(n->cols, n->dtype, n->gain, n->payload);
+    if (!n->gain || !is_aligned(n->gain, 4) || !check_matrix(n->x, n->ld_x, n->cols, n->dtype, &align))
+      return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->residual && !check_matrix(n->residual, n->ld_residual, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->sum && !check_matrix(n->sum, n->ld_sum, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (n->y && !check_matrix(n->y, n->ld_y, n->cols, n->dtype, &align)) return QMUON_ERR_INVALID_ARGUMENT;
+    FwdArgs A{n->x,    n->residual,    n->gain,   n->sum,  n->y,    n->payload, n->scale_inv, n->rows,
+              n->ld_x, n->ld_residual, n->ld_sum, n->ld_y, (int32_t)n->cols, align, n->eps, 1.0f / (float)n->cols};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = n->dtype == QMUON_BF16   ? launch_fwd_dt<QMUON_BF16>(A, s)
+                          : n->dtype == QMUON_FP16 ? launch_fwd_dt<QMUON_FP16>(A, s)
+                                                   : launch_fwd_dt<QMUON_FP32>(A, s);
+    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_rmsnorm_forward (launch)", e);
+  });
 }
 
 extern "C" size_t qmuon_rmsnorm_workspace_size(int64_t rows, int64_t cols) {

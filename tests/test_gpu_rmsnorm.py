@@ -118,6 +118,37 @@ def test_forward_mxfp8(shape, dtype, both):
     assert (np.abs(got) <= 448 * np.repeat(scale, 32, 1)).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols", [32, 64, 96, 160, 512, 1056, 4096, 9984, 16384])
+@pytest.mark.parametrize("pay_off,offs", [(1, (0, 0, 0)), (2, (1, 2, 3)), (8, (3, 0, 1)), (0, (0, 1, 0))])
+def test_forward_mxfp8_from_anywhere(dtype, cols, pay_off, offs):
+    # payloads at any address, inputs that start unlike each other.  Bounds: test_forward_mxfp8's, with h's rounding in both terms
+    rows, pads = 19 if cols < 4096 else 5, (1, 4, 3)
+    gen = torch.Generator("cuda").manual_seed(13)
+    x, r = _rnd(gen, rows, cols).to(DT[dtype]), _rnd(gen, rows, cols).to(DT[dtype])
+    gain = torch.randn(cols, generator=gen, device="cuda")
+    X, R, S = (Matrix(rows, cols, p, DT[dtype], o, f) for p, o, f in zip(pads, offs, (x, r, None)))
+    pay, sc = Guarded((rows * cols + pay_off,), torch.uint8), Guarded((rows, cols // 32), torch.uint8)
+    pay.t[:pay_off] = 7
+    q.qmuon_rmsnorm_forward(X.t, gain, rows, cols, dtype, 1e-5, residual=R.t, sum=S.t, payload=pay.t[pay_off:], scale_inv=sc.t, ld_x=X.ld,
+                            ld_residual=R.ld, ld_sum=S.ld)
+    torch.cuda.synchronize()
+    for m in (X, R, S, pay, sc):
+        m.check()
+    assert bool((pay.t[:pay_off] == 7).all())
+    h, want = training.rmsnorm64(_np(x), _np(gain), 1e-5, _np(r))
+    mag = (np.abs(_np(x)) + np.abs(_np(r))) / np.sqrt(np.mean(h * h, 1, keepdims=True)) * np.abs(_np(gain))
+    assert (np.abs(_np(S.t) - h) <= UT[dtype] * np.abs(h) * (1 + U) + U * (np.abs(_np(x)) + np.abs(_np(r))) + TINY[dtype]).all()
+    top = np.abs(want.reshape(rows, -1, 32)).max(2)
+    err = 64 * U * top + (U * mag).reshape(rows, -1, 32).max(2)
+    scale = 2.0 ** (sc.t.cpu().numpy().astype(np.int64) - 127)
+    assert (top <= 448 * scale + err).all() and (top > 224 * scale - err).all()
+    scale = np.repeat(scale, 32, 1)
+    got = carrier.e4m3_decode(pay.t[pay_off:].cpu().numpy()).reshape(rows, cols) * scale
+    assert (np.abs(got - want) <= np.abs(want) * (2.0 ** -4 + 64 * U) + 2 * U * mag + 2.0 ** -10 * scale).all()
+    assert (np.abs(got) <= 448 * scale).all()
+
+
 def test_forward_mxfp8_equals_the_carrier_of_y():
     # in fp32, the payload and scales are the carrier of the y that the same call stores
     rows, cols = 130, 1056
