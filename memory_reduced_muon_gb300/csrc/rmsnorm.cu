@@ -8,9 +8,9 @@
 // A row belongs to T threads: a power of two up to a warp (and a CTA then takes
 // several rows), or whole warps.  Rows that fit their threads' registers cross
 // HBM once: in 16-byte vectors where all arrays' rows start on 16 bytes ("rows"
-// kernels), else in pairs of 16-bit elements or single elements ("pieces"),
-// backward also by way of shared memory ("staged").  Longer ones are walked
-// twice, the second time out of the caches ("walk").
+// kernels), else in pairs of 16-bit elements or single elements ("pieces") or
+// by way of shared memory ("staged").  Longer ones are walked twice, the second
+// time out of the caches ("walk").
 #include <algorithm>
 #include <atomic>
 #include <cmath>
