@@ -434,9 +434,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_pieces_kernel(const __grid_c
 
 // Rows in a slot each (see above): where 16-bit arrays start unlike each other,
 // and to MXFP8, whose blocks of 32 start where pairs of a row with a head do not.
-// Bound by its instructions: 8000 x 4096 bf16 with a residual and odd strides to
-// MXFP8 72 us (97 by single elements in registers; 94 with four pairs per
-// thread), 9000 x 7001 bf16 with arrays that start unlike each other 145 us (207).
+// Bound by its instructions (64 per element, 0.78 issued per cycle and
+// scheduler): 8000 x 4096 bf16 with a residual and odd strides to MXFP8 72 us,
+// 97 by single elements in registers and 94 with four pairs per thread;
+// 9000 x 7001 bf16 with arrays that start unlike each other 145 us, 207.
 template <int DT, int V, bool RES, bool MX>
 __global__ void __launch_bounds__(1024) rmsnorm_fwd_staged_kernel(const __grid_constant__ FwdArgs A) {
   using X = Pairs<DT, V>;
