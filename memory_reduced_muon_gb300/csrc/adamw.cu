@@ -399,13 +399,15 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_f32_kernel(const __grid_con
 // E4M3 of four scaled values with 16 random bits each: rounded up in magnitude
 // with probability (remainder / step) to 2^-16.  2^-120 |x| has its exponent
 // field where the code's is, subnormals included, so the bits above the lowest
-// 20 are the code.  The largest value's code, 0x7E with all lower bits zero (up
+// 20 are the code; it is cut, not rounded, to the 20 that a subnormal code's
+// remainder keeps, as a remainder that misses a whole step with its random bits
+// must not be rounded up to one.  The largest value's code, 0x7E with all lower bits zero (up
 // to an ulp), cannot be carried to 0x7F by random bits of which the lowest four
 // are zero: 0x7F remains for NaN alone.
 template <bool SIGNED>
 __device__ __forceinline__ uint32_t encode_sr4(const Quad& x, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
   constexpr float kShift = 7.52316384526264e-37f;   // 2^-120
-  const float2 a = mul2_rn(x.a, kShift), b = mul2_rn(x.b, kShift);
+  const float2 a = mul2_rz(x.a, kShift), b = mul2_rz(x.b, kShift);
   auto code = [](float y, uint32_t u) { return min(__float_as_uint(fabsf(y)) + u, 0x7F00000u) << 4; };
   const uint32_t c0 = code(a.x, u0), c1 = code(a.y, u1), c2 = code(b.x, u2), c3 = code(b.y, u3);
   const uint32_t w = __byte_perm(__byte_perm(c0, c1, 0x0073u), __byte_perm(c2, c3, 0x0073u), 0x5410u);

@@ -92,6 +92,15 @@ __device__ __forceinline__ float2 sub2_rn(float2 a, float2 b) {
 }
 
 __device__ __forceinline__ float2 mul2_rn(float2 a, float b) { return mul2_rn(a, make_float2(b, b)); }
+// Rounded towards zero.
+__device__ __forceinline__ float2 mul2_rz(float2 a, float b) {
+  float2 r;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %4};\n\t"
+      "mul.rz.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
