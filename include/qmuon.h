@@ -545,9 +545,10 @@ QMUON_API void qmuon_adamw_plan_destroy(qmuon_adamw_plan* plan);
  *   p <- p (1 - lr' weight_decay) - (lr' / (1 - beta1^t)) * u
  *   u = m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * 8-bit states are then requantised to the nearest code of their block's new
- * maximum (the update above uses the unrounded ones).  A NaN keeps a NaN code,
- * and an infinity turns its block's state into NaN at the next step, so that
- * neither is lost.
+ * maximum (the update above uses the unrounded ones); a root above zero takes
+ * at least code 1, so that no later step divides its momentum by eps alone.
+ * A NaN keeps a NaN code, and an infinity turns its block's state into NaN at
+ * the next step, so that neither is lost.
  *   t           >= 1, the step's index; fixed in captured launches
  *   eps         at least 2^-126 (the smallest normal fp32)
  *   grad_scale  D  one fp32 s (a clipping coefficient, an inverse loss scale),
@@ -564,7 +565,8 @@ QMUON_API qmuon_status qmuon_adamw_step(const qmuon_adamw_plan* plan, int64_t t,
  * Element e of tensor i takes word w = word (e mod 4) of Philox4x32-10 with
  * key (seed mod 2^32, seed >> 32) and counter (e/4 mod 2^32, e/2^34, i, t mod
  * 2^32); m is rounded up in magnitude where its remainder's fraction of a step
- * plus (w mod 2^16) 2^-16 reaches 1, the root of v likewise with w >> 16. */
+ * plus (w mod 2^16) 2^-16 reaches 1, the root of v likewise with w >> 16 (above
+ * zero to code 1 at least). */
 QMUON_API qmuon_status qmuon_adamw_step_sr(const qmuon_adamw_plan* plan, int64_t t, double lr, double beta1, double beta2,
                                            double eps, uint64_t seed, const float* grad_scale, void* stream);
 

@@ -8,7 +8,8 @@ that 8-bit states can be compared bit for bit:
 
 * 8-bit AdamW states: E4M3 codes of the first moment ``m`` and of the square
   root ``r`` of the second, one fp32 maximum per 256 elements;
-  ``x = code * (max / 448)``; new codes from ``x * min(448 / max, FLT_MAX)``;
+  ``x = code * (max / 448)``; new codes from ``x * min(448 / max, FLT_MAX)``,
+  at least 1 for a root above zero;
 * stochastic requantisation: magnitudes are cut to the 3-bit grid after 16
   random bits are added below it (``oracle.rng`` words: the low half for m, the
   high half for r);
@@ -79,6 +80,11 @@ def e4m3_stochastic(x: np.ndarray, u16: np.ndarray) -> np.ndarray:
     return np.where(np.isnan(x), 0x7F, code).astype(np.uint8)
 
 
+def root_codes(codes: np.ndarray, scaled: np.ndarray) -> np.ndarray:
+    """Codes of the scaled roots: 1 instead of 0 where the root is above zero (and its block's maximum finite)."""
+    return np.where((scaled > 0) & (codes == 0), np.uint8(1), codes)
+
+
 def adamw_e4m3(p, g, m, v, m_max, v_max, t, lr, beta1, beta2, eps, weight_decay=0.0, lr_scale=1.0, scale=1.0,
                seed=None, tensor_index=0):
     """New (p, m codes, v codes, m_max, v_max) in the header's fp32 order; ``seed``: stochastic requantisation."""
@@ -97,12 +103,12 @@ def adamw_e4m3(p, g, m, v, m_max, v_max, t, lr, beta1, beta2, eps, weight_decay=
         mx = m1 * spread(np.minimum(F32(448) / mm, FLT_MAX), n)
         vx = r1 * spread(np.minimum(F32(448) / vm, FLT_MAX), n)
         if seed is None:
-            return p1, carrier.e4m3_encode(mx), carrier.e4m3_encode(vx), mm, vm
+            return p1, carrier.e4m3_encode(mx), root_codes(carrier.e4m3_encode(vx), vx), mm, vm
         j = np.arange((n + 3) // 4, dtype=np.uint64)
         ctr = np.stack([j & np.uint64(0xFFFFFFFF), j >> np.uint64(32), np.full_like(j, tensor_index),
                         np.full_like(j, t & 0xFFFFFFFF)], 1)
         w = rng.philox4x32_10(ctr, (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF)).reshape(-1)[:n]
-        return p1, e4m3_stochastic(mx, w & 0xFFFF), e4m3_stochastic(vx, w >> 16), mm, vm
+        return p1, e4m3_stochastic(mx, w & 0xFFFF), root_codes(e4m3_stochastic(vx, w >> 16), vx), mm, vm
 
 
 # --------------------------------------------------------------------------
