@@ -686,7 +686,7 @@ cudaError_t upload(const std::vector<Tensor>& ts, const std::vector<int32_t>& ch
   if (!chunks.empty()) std::memcpy(blob.data() + head + tb, chunks.data(), chunks.size() * 4);
   cudaError_t e = cudaMalloc(table, blob.size());
   if (e != cudaSuccess) return e;
-  e = cudaMemcpy(*table, blob.data(), blob.size(), cudaMemcpyHostToDevice);
+  e = upload_and_wait(*table, blob.data(), blob.size());
   if (e != cudaSuccess) {
     cudaFree(*table);
     *table = nullptr;

@@ -355,7 +355,7 @@ extern "C" qmuon_status qmuon_plan_create(const qmuon_tensor* tensors, int32_t n
     }
     ce = cudaMalloc(&P->d_table, blob.size());
     if (ce != cudaSuccess) return set_error("qmuon_plan_create (cudaMalloc tables)", ce);
-    ce = cudaMemcpy(P->d_table, blob.data(), blob.size(), cudaMemcpyHostToDevice);
+    ce = upload_and_wait(P->d_table, blob.data(), blob.size());
     if (ce != cudaSuccess) {
       cudaFree(P->d_table);
       return set_error("qmuon_plan_create (upload tables)", ce);
@@ -864,7 +864,7 @@ extern "C" qmuon_status qmuon_sync_status(void* ws, void* stream) {
   if (e != cudaSuccess) return set_error("qmuon_sync_status (read header)", e);
   if (err[0] != 0) {
     const unsigned int zero[2] = {0u, 0u};
-    cudaMemcpy(ws, zero, sizeof(zero), cudaMemcpyHostToDevice);
+    upload_and_wait(ws, zero, sizeof(zero));
     char msg[128];
     std::snprintf(msg, sizeof(msg), "kernel reported status %u at site 0x%x", err[0], err[1]);
     return set_error_msg(msg, (qmuon_status)err[0]);

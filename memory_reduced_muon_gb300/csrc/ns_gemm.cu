@@ -1363,7 +1363,7 @@ cudaError_t upload_table(const Launchable& L, const std::vector<NsProb>& hp, con
   auto copy = [&](void* dst, const void* src, size_t bytes) {
     if (bytes == 0) return cudaSuccess;
     return async ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyHostToDevice, s)
-                 : cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice);
+                 : upload_and_wait(dst, src, bytes);
   };
   cudaError_t e = copy(L.d_probs, hp.data(), hp.size() * sizeof(NsProb));
   for (int k = 0; k < 3 && e == cudaSuccess; ++k) {

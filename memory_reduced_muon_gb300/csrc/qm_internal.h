@@ -144,6 +144,14 @@ void tally(Tally t, uint64_t v = 1);
 // One tensor read as a gradient of `dt` and one 8-bit state of `q8` updated.
 void tally_grad_state(qmuon_dtype dt, qmuon_q8_kind q8, uint64_t tensors);
 
+// A copy from host memory that is on the device when this returns.  cudaMemcpy
+// alone may return once pageable memory is staged, and orders the rest with the
+// legacy stream only: a kernel on a non-blocking stream could read the old bytes.
+inline cudaError_t upload_and_wait(void* dst, const void* src, size_t bytes) {
+  const cudaError_t e = cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice);
+  return e == cudaSuccess ? cudaStreamSynchronize(cudaStreamLegacy) : e;
+}
+
 // Host-side launchers (update.cu).  Return a cudaError_t from the launch.
 cudaError_t launch_update(const UpdLaunch& L, qmuon_q8_kind q8, qmuon_dtype dt, bool carrier,
                           cudaStream_t stream);

@@ -798,6 +798,13 @@ cudaError_t static_scratch(int dev, void** out) {
   return cudaSuccess;
 }
 
+// Host bytes into the current device's array, `offset` bytes in.
+cudaError_t upload_to_scratch(int dev, size_t offset, const void* src, size_t bytes) {
+  void* p = nullptr;
+  const cudaError_t e = static_scratch(dev, &p);
+  return e == cudaSuccess ? qm::upload_and_wait(static_cast<unsigned char*>(p) + offset, src, bytes) : e;
+}
+
 // Carries a status recorded by the previous call into the pending words and
 // clears what the update kernel needs at zero: the error word and the ticket.
 __global__ void noalloc_carry_status_kernel(qm::WsHeader* h) {
@@ -897,7 +904,7 @@ extern "C" qmuon_status qmuon_noalloc_sync_status(void* stream) {
   if (st != QMUON_OK) return st;
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error("qmuon_noalloc_sync_status (stream synchronize)", e);
-  // the symbol copies read and write the array on the current device and
+  // the copies read and write the array on the current device and
   // allocate nothing
   WsHeader h{};
   e = cudaMemcpyFromSymbol(&h, g_static_scratch, sizeof(h), 0, cudaMemcpyDeviceToHost);
@@ -906,10 +913,8 @@ extern "C" qmuon_status qmuon_noalloc_sync_status(void* stream) {
   const unsigned site = h.pad[kPendingStatus] ? h.pad[kPendingSite] : h.error_info;
   if (status == 0u) return QMUON_OK;
   const unsigned zero[2] = {0u, 0u};
-  e = cudaMemcpyToSymbol(g_static_scratch, zero, sizeof(zero), offsetof(WsHeader, error), cudaMemcpyHostToDevice);
-  if (e == cudaSuccess)
-    e = cudaMemcpyToSymbol(g_static_scratch, zero, sizeof(zero), offsetof(WsHeader, pad) + kPendingStatus * 4,
-                           cudaMemcpyHostToDevice);
+  e = upload_to_scratch(dev, offsetof(WsHeader, error), zero, sizeof(zero));
+  if (e == cudaSuccess) e = upload_to_scratch(dev, offsetof(WsHeader, pad) + kPendingStatus * 4, zero, sizeof(zero));
   if (e != cudaSuccess) return set_error("qmuon_noalloc_sync_status (clear header)", e);
   char msg[128];
   std::snprintf(msg, sizeof(msg), "qmuon_update_normalize_noalloc: kernel reported status %u at site 0x%x", status,
@@ -925,8 +930,7 @@ extern "C" qmuon_status qmuon_noalloc_inject_status(qmuon_status status, uint32_
   qmuon_status st = current_device("qmuon_noalloc_inject_status (device)", &dev);
   if (st != QMUON_OK) return st;
   const unsigned words[2] = {(unsigned)status, site};
-  const cudaError_t e = cudaMemcpyToSymbol(g_static_scratch, words, sizeof(words),
-                                           offsetof(WsHeader, pad) + kPendingStatus * 4, cudaMemcpyHostToDevice);
+  const cudaError_t e = upload_to_scratch(dev, offsetof(WsHeader, pad) + kPendingStatus * 4, words, sizeof(words));
   if (e != cudaSuccess) return set_error("qmuon_noalloc_inject_status (write header)", e);
   return QMUON_OK;
 }
