@@ -112,18 +112,19 @@ class Block:
         return F.cross_entropy((y.view(rows, cols).bfloat16() @ self.head16.T).float(), targets)
 
     def step(self, tokens, targets, lr=3e-3, eta=0.02, max_norm=1.0):
-        """One training step; the loss, on the device."""
-        self.t += 1
+        """One training step; the loss, on the device.  A step whose gradients are not finite changes nothing."""
         for p in self.leaves:
             p.grad.zero_()        # autograd adds into the plans' buffers
         loss = self.loss(tokens, targets)
         loss.backward()
         q.qmuon_grad_clip(self.clip, max_norm, True, self.norm, self.clip_ws)
-        # a norm that is not finite leaves a coefficient that is not: AdamW then changes nothing (the Muon step has no
-        # such guard).  The gradients are scaled already, so a finite coefficient counts as 1.
-        ok = torch.where(torch.isfinite(self.norm[1:]), 1.0, self.norm[1:])
-        q.qmuon_adamw_step(self.adam, self.t, lr, 0.9, 0.95, 1e-8, ok)
-        q.qmuon_adamw_step_sr(self.adam8, self.t, lr, 0.9, 0.95, 1e-8, 17, ok)
+        # AdamW alone could take the coefficient on the device, and changes nothing where that is not finite; the Muon
+        # step takes none, so the host looks at the norm.  The gradients are scaled already.
+        if not math.isfinite(self.norm[0].item()):
+            return loss.detach()
+        self.t += 1
+        q.qmuon_adamw_step(self.adam, self.t, lr, 0.9, 0.95, 1e-8)
+        q.qmuon_adamw_step_sr(self.adam8, self.t, lr, 0.9, 0.95, 1e-8, 17)
         q.qmuon_step(self.muon, self.t, 1, 0.95, eta, eta, self.mats, COEFFS, 5, None, self.muon_ws)
         with torch.no_grad():
             for p, w in zip(self.mats16, self.mats):
