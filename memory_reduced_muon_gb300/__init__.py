@@ -7,7 +7,8 @@ the library's CUDA kernels; there is no Python or CPU fallback, and calling
 any entry point without the built library raises.
 
 Device buffers are passed as torch tensors (their ``data_ptr()``) or as raw
-integer addresses; ``stream`` is a ``torch.cuda.Stream``, a raw
+integer addresses; the clipping, AdamW and RMS norm entries, which take a
+model's own tensors, check the former.  ``stream`` is a ``torch.cuda.Stream``, a raw
 ``cudaStream_t`` integer, or ``None`` for torch's current stream.
 """
 
@@ -15,6 +16,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Iterable, Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,13 +43,14 @@ STATE_KINDS = {"f32": QMUON_STATE_F32, "e4m3": QMUON_STATE_E4M3}
 
 
 class QmuonError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, detail: Optional[str] = None):
         self.status = int(status)
-        detail = ""
-        try:
-            detail = lib().qmuon_last_error().decode()
-        except Exception:
-            pass
+        if detail is None:
+            detail = ""
+            try:
+                detail = lib().qmuon_last_error().decode()
+            except Exception:
+                pass
         super().__init__(f"{where}: {status_string(status)} (status {status})" + (f" -- {detail}" if detail else ""))
 
 
@@ -493,6 +496,67 @@ def qmuon_grasp_step(matrices: Sequence, mu: float, ws, ws_bytes: Optional[int] 
 # --------------------------------------------------------------------------
 # beside the Muon step: gradient clipping, AdamW, RMS norm
 # --------------------------------------------------------------------------
+# These entries take a model's own tensors.  Torch tensors are checked: their type,
+# that they are on the GPU, and that they hold what the call reads and writes there;
+# a mismatch is QMUON_ERR_INVALID_ARGUMENT.  Raw addresses are taken as they are.
+
+_types: dict = {}   # torch dtype of a qmuon_dtype
+
+
+def _type_of(code):
+    """The torch dtype of a qmuon_dtype; None for a code that the library refuses."""
+    if not _types:
+        import torch
+        _types.update({QMUON_BF16: torch.bfloat16, QMUON_FP16: torch.float16, QMUON_FP32: torch.float32})
+    return _types.get(code)
+
+
+def _refuse(x, where: str, what: str, need: str):
+    raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where,
+                     f"{what} has to be {need}; it is {tuple(x.shape)}, strides {x.stride()}, of {x.dtype} on {x.device}")
+
+
+def _array(x, dtype, n: int, where: str, what: str) -> int:
+    """The address of n elements side by side (a torch dtype; None: any)."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    if (x.dtype is dtype or dtype is None) and x.is_cuda and x.is_contiguous() and x.numel() >= n:
+        return x.data_ptr()
+    _refuse(x, where, what, f"a contiguous GPU tensor of {n} or more elements" + (f" of {dtype}" if dtype else ""))
+
+
+def _bytes(x, n: int, where: str, what: str) -> int:
+    """The address of n elements of any type of one byte."""
+    if x is not None and not isinstance(x, int) and x.element_size() != 1:
+        _refuse(x, where, what, "of one byte per element")
+    return _array(x, None, n, where, what)
+
+
+def _matrix(x, dtype, rows: int, cols: int, ld: int, where: str, what: str) -> int:
+    """The address of `rows` rows of `cols` elements, `ld` apart (a tensor or an address)."""
+    try:
+        if (x.dtype is dtype or dtype is None) and x.is_cuda:
+            if x.is_contiguous():
+                n = x.numel()
+                if n >= rows * ld or n >= (rows - 1) * ld + cols:
+                    return x.data_ptr()
+            elif (x.dim() == 2 and x.shape[0] >= rows and x.shape[1] >= cols and (x.stride(1) == 1 or cols == 1) and
+                  (x.stride(0) == ld or rows == 1)):
+                return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x or 0
+        raise
+    _refuse(x, where, what, f"a GPU tensor of {rows} x {cols} elements of {dtype}, rows {ld} elements apart")
+
+
+def _on_gpu(x, where: str, what: str) -> Optional[int]:
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        _refuse(x, where, what, "on the GPU")
+    return x.data_ptr()
+
 
 class ClipPlan:
     """An owned ``qmuon_clip_plan*`` (destroyed with the object)."""
@@ -506,9 +570,16 @@ class ClipPlan:
 
 
 def qmuon_clip_plan_create(grads: Sequence) -> ClipPlan:
-    """``grads``: ``qmuon_grad`` or ``(gradient tensor, dtype name)`` tuples."""
-    descs = [g if isinstance(g, qmuon_grad) else
-             qmuon_grad(_ptr(g[0]), int(g[0].numel()), DTYPES.get(g[1], g[1]), 0) for g in grads]
+    """``grads``: ``qmuon_grad`` or ``(gradient tensor, dtype name)`` tuples.
+
+    The plan holds the gradients' addresses: zero them in place, do not let them go (``set_to_none=False``).
+    """
+    def desc(g):
+        if isinstance(g, qmuon_grad):
+            return g
+        n, dtype = int(g[0].numel()), DTYPES.get(g[1], g[1])
+        return qmuon_grad(_array(g[0], _type_of(dtype), n, "qmuon_clip_plan_create", "a gradient"), n, dtype, 0)
+    descs = [desc(g) for g in grads]
     arr = (qmuon_grad * max(1, len(descs)))(*descs)
     out = C.c_void_p()
     _check(lib().qmuon_clip_plan_create(arr, len(descs), C.byref(out)), "qmuon_clip_plan_create")
@@ -527,8 +598,9 @@ def qmuon_clip_workspace_size(plan: ClipPlan) -> int:
 
 def qmuon_grad_clip(plan: ClipPlan, max_norm: float, apply: bool, norm, ws, ws_bytes: Optional[int] = None, stream=None):
     """``norm``: a device fp32 tensor of two: the norm and the coefficient."""
-    st = lib().qmuon_grad_clip(plan.handle, float(max_norm), int(apply), _ptr(norm), _ptr(ws),
-                               _nbytes(ws) if ws_bytes is None else int(ws_bytes), _stream(stream))
+    where = "qmuon_grad_clip"
+    st = lib().qmuon_grad_clip(plan.handle, float(max_norm), int(apply), _array(norm, _type_of(QMUON_FP32), 2, where, "norm"),
+                               _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes), _stream(stream))
     _check(st, "qmuon_grad_clip")
 
 
@@ -545,18 +617,31 @@ class AdamwPlan:
 
 def adamw_tensor(param, grad, m, v, numel: int, grad_dtype="bf16", m_absmax=None, v_absmax=None, copy=None,
                  copy_dtype="bf16", weight_decay: float = 0.0, lr_scale: float = 1.0) -> qmuon_adamw_tensor:
-    t = qmuon_adamw_tensor(_ptr(param), _ptr(grad), _ptr(copy), _ptr(m), _ptr(v), _ptr(m_absmax), _ptr(v_absmax),
-                           int(numel), float(lr_scale), float(weight_decay), DTYPES.get(grad_dtype, grad_dtype),
-                           DTYPES.get(copy_dtype, copy_dtype))
+    """The plan made of it holds these addresses; m and v are checked there, against the kind of state."""
+    n, where = int(numel), "adamw_tensor"
+    grad_dtype, copy_dtype = DTYPES.get(grad_dtype, grad_dtype), DTYPES.get(copy_dtype, copy_dtype)
+    f32 = _type_of(QMUON_FP32)
+    t = qmuon_adamw_tensor(_array(param, f32, n, where, "param"), _array(grad, _type_of(grad_dtype), n, where, "grad"),
+                           _array(copy, _type_of(copy_dtype), n, where, "copy"), _ptr(m), _ptr(v),
+                           _array(m_absmax, f32, -(-n // 256), where, "m_absmax"),
+                           _array(v_absmax, f32, -(-n // 256), where, "v_absmax"), n, float(lr_scale),
+                           float(weight_decay), grad_dtype, copy_dtype)
     t._keep = (param, grad, copy, m, v, m_absmax, v_absmax)
     return t
 
 
 def qmuon_adamw_plan_create(tensors: Sequence, state="f32") -> AdamwPlan:
     """``tensors``: ``adamw_tensor(...)``; ``state``: "f32" or "e4m3"."""
+    kind = STATE_KINDS.get(state, state)
+    for t in tensors:
+        for x, what in zip(getattr(t, "_keep", ())[3:5], "mv"):
+            if kind == QMUON_STATE_E4M3:
+                _bytes(x, t.numel, "qmuon_adamw_plan_create", what)
+            else:
+                _array(x, _type_of(QMUON_FP32), t.numel, "qmuon_adamw_plan_create", what)
     arr = (qmuon_adamw_tensor * max(1, len(tensors)))(*tensors)
     out = C.c_void_p()
-    st = lib().qmuon_adamw_plan_create(arr, len(tensors), STATE_KINDS.get(state, state), C.byref(out))
+    st = lib().qmuon_adamw_plan_create(arr, len(tensors), kind, C.byref(out))
     _check(st, "qmuon_adamw_plan_create")
     return AdamwPlan(out.value, tensors)
 
@@ -570,25 +655,63 @@ def qmuon_adamw_plan_destroy(plan: AdamwPlan):
 def qmuon_adamw_step(plan: AdamwPlan, t: int, lr: float, beta1: float, beta2: float, eps: float, grad_scale=None,
                      stream=None):
     """``grad_scale``: a device fp32 tensor of one (a clipping coefficient), or None."""
-    _check(lib().qmuon_adamw_step(plan.handle, int(t), lr, beta1, beta2, eps, _ptr(grad_scale), _stream(stream)),
-           "qmuon_adamw_step")
+    where = "qmuon_adamw_step"
+    scale = None if grad_scale is None else _array(grad_scale, _types.get(QMUON_FP32) or _type_of(QMUON_FP32), 1, where, "grad_scale")
+    st = (_lib_handle or lib()).qmuon_adamw_step(plan.handle, int(t), lr, beta1, beta2, eps, scale,
+                                                 _raw_stream() if stream is None and _raw_stream else _stream(stream))
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
 
 
 def qmuon_adamw_step_sr(plan: AdamwPlan, t: int, lr: float, beta1: float, beta2: float, eps: float, seed: int,
                         grad_scale=None, stream=None):
+    where = "qmuon_adamw_step_sr"
     _check(lib().qmuon_adamw_step_sr(plan.handle, int(t), lr, beta1, beta2, eps, int(seed) & 0xFFFFFFFFFFFFFFFF,
-                                     _ptr(grad_scale), _stream(stream)), "qmuon_adamw_step_sr")
+                                     _array(grad_scale, _type_of(QMUON_FP32), 1, where, "grad_scale"), _stream(stream)), where)
+
+
+# The structures as bytes, which take a sixth of a ctypes object's time, and the entries that take them so: what the
+# checks of the tensors cost a small call comes back here.
+_RMSNORM, _RMSNORM_GRAD = struct.Struct("@7Q6qfi").pack, struct.Struct("@6Q6qfi").pack
+_bytes_entries: dict = {}
+
+
+def _by_bytes(name: str):
+    fn = lib()[name]    # a function object of its own
+    fn.restype, fn.argtypes = C.c_int32, [C.c_char_p, *getattr(lib(), name).argtypes[1:]]
+    _bytes_entries[name] = fn
+    return fn
 
 
 def qmuon_rmsnorm_forward(x, gain, rows: int, cols: int, dtype, eps: float, y=None, residual=None, sum=None,
                           payload=None, scale_inv=None, ld_x: Optional[int] = None, ld_residual: Optional[int] = None,
                           ld_sum: Optional[int] = None, ld_y: Optional[int] = None, stream=None):
     """The ``ld_*`` default to ``cols`` (rows next to one another)."""
-    n = qmuon_rmsnorm(_ptr(x), _ptr(residual), _ptr(gain), _ptr(sum), _ptr(y), _ptr(payload), _ptr(scale_inv),
-                           rows, cols, cols if ld_x is None else ld_x, cols if ld_residual is None else ld_residual,
-                           cols if ld_sum is None else ld_sum, cols if ld_y is None else ld_y, eps,
-                           DTYPES.get(dtype, dtype))
-    _check(lib().qmuon_rmsnorm_forward(C.byref(n), _stream(stream)), "qmuon_rmsnorm_forward")
+    where = "qmuon_rmsnorm_forward"
+    dtype = DTYPES.get(dtype, dtype)
+    t = _types.get(dtype) or _type_of(dtype)
+    if ld_x is None:
+        ld_x = cols
+    if ld_residual is None:
+        ld_residual = cols
+    if ld_sum is None:
+        ld_sum = cols
+    if ld_y is None:
+        ld_y = cols
+    try:
+        n = _RMSNORM(_matrix(x, t, rows, cols, ld_x, where, "x"),
+                     0 if residual is None else _matrix(residual, t, rows, cols, ld_residual, where, "residual"),
+                     _array(gain, _types[QMUON_FP32], cols, where, "gain"),
+                     0 if sum is None else _matrix(sum, t, rows, cols, ld_sum, where, "sum"),
+                     0 if y is None else _matrix(y, t, rows, cols, ld_y, where, "y"),
+                     0 if payload is None else _bytes(payload, rows * cols, where, "payload"),
+                     0 if scale_inv is None else _bytes(scale_inv, rows * (cols // 32), where, "scale_inv"), rows, cols, ld_x,
+                     ld_residual, ld_sum, ld_y, eps, dtype)
+    except (struct.error, OverflowError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    st = (_bytes_entries.get(where) or _by_bytes(where))(n, _raw_stream() if stream is None and _raw_stream else _stream(stream))
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
 
 
 def qmuon_rmsnorm_workspace_size(rows: int, cols: int) -> int:
@@ -598,9 +721,27 @@ def qmuon_rmsnorm_workspace_size(rows: int, cols: int) -> int:
 def qmuon_rmsnorm_backward(dy, h, gain, rows: int, cols: int, dtype, eps: float, dx, dgain, ws, dsum=None,
                            ld_dy: Optional[int] = None, ld_h: Optional[int] = None, ld_dsum: Optional[int] = None,
                            ld_dx: Optional[int] = None, ws_bytes: Optional[int] = None, stream=None):
-    n = qmuon_rmsnorm_grad(_ptr(dy), _ptr(h), _ptr(dsum), _ptr(gain), _ptr(dx), _ptr(dgain), rows, cols,
-                           cols if ld_dy is None else ld_dy, cols if ld_h is None else ld_h,
-                           cols if ld_dsum is None else ld_dsum, cols if ld_dx is None else ld_dx, eps,
-                           DTYPES.get(dtype, dtype))
-    _check(lib().qmuon_rmsnorm_backward(C.byref(n), _ptr(ws), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
-                                        _stream(stream)), "qmuon_rmsnorm_backward")
+    where = "qmuon_rmsnorm_backward"
+    dtype = DTYPES.get(dtype, dtype)
+    t = _types.get(dtype) or _type_of(dtype)
+    if ld_dy is None:
+        ld_dy = cols
+    if ld_h is None:
+        ld_h = cols
+    if ld_dsum is None:
+        ld_dsum = cols
+    if ld_dx is None:
+        ld_dx = cols
+    try:
+        n = _RMSNORM_GRAD(_matrix(dy, t, rows, cols, ld_dy, where, "dy"), _matrix(h, t, rows, cols, ld_h, where, "h"),
+                          0 if dsum is None else _matrix(dsum, t, rows, cols, ld_dsum, where, "dsum"),
+                          _array(gain, _types[QMUON_FP32], cols, where, "gain"), _matrix(dx, t, rows, cols, ld_dx, where, "dx"),
+                          _array(dgain, _types[QMUON_FP32], cols, where, "dgain"), rows, cols, ld_dy, ld_h, ld_dsum, ld_dx, eps,
+                          dtype)
+    except (struct.error, OverflowError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    st = (_bytes_entries.get(where) or _by_bytes(where))(
+        n, _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
+        _raw_stream() if stream is None and _raw_stream else _stream(stream))
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
