@@ -495,10 +495,10 @@ QMUON_API size_t qmuon_clip_workspace_size(const qmuon_clip_plan* plan);
  *             1: g <- norm[1] g, rounded to nearest, where norm[1] < 1
  *   norm      D  two fp32
  *   ws        D  256-byte aligned, of qmuon_clip_workspace_size(plan)
- * Squares are taken and summed in fp32 over up to 8192 elements, then in fp64 in
- * a fixed order: the same gradients give the same bits, and magnitudes above
- * 2e17 may count as infinite.  Calls with one plan must not overlap on the
- * GPU (enqueue them on one stream). */
+ * Squares are taken and summed in fp32 over up to 32 elements, then in fp64 in a
+ * fixed order: the same gradients give the same bits; magnitudes above 3e18 may
+ * count as infinite, those below 1e-19 lose bits and below 2e-23 count as zero.
+ * Calls with one plan must not overlap on the GPU (enqueue them on one stream). */
 QMUON_API qmuon_status qmuon_grad_clip(const qmuon_clip_plan* plan, float max_norm, int32_t apply, float* norm, void* ws,
                                        size_t ws_bytes, void* stream);
 

@@ -43,6 +43,8 @@ struct ClipLaunch {
   float max_norm;
 };
 
+// A thread's share of a chunk, up to 32 squares, in four running sums: a sum's
+// error grows with its additions, of which the norm then sees 12 at most.
 template <int DT>
 __device__ __forceinline__ float chunk_sumsq(const ClipChunk& T, int tid) {
   const int n = T.n;
@@ -62,7 +64,16 @@ __device__ __forceinline__ float chunk_sumsq(const ClipChunk& T, int tid) {
     }
     done = nv * K;
   }
-  for (int i = done + tid; i < n; i += kThreads) {
+  int i = done + tid;
+  for (; i + 3 * kThreads < n; i += 4 * kThreads) {
+    float2 f[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      f[j] = make_float2(load_elem<DT>(base, i + 2 * j * kThreads), load_elem<DT>(base, i + (2 * j + 1) * kThreads));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s[j] = fma2(f[j], f[j], s[j]);
+  }
+  for (; i < n; i += kThreads) {
     const float f = load_elem<DT>(base, i);
     s[0].x = fmaf(f, f, s[0].x);
   }
