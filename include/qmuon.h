@@ -550,7 +550,7 @@ QMUON_API void qmuon_adamw_plan_destroy(qmuon_adamw_plan* plan);
  * A NaN keeps a NaN code, and an infinity turns its block's state into NaN at
  * the next step, so that neither is lost.
  *   t           >= 1, the step's index; fixed in captured launches
- *   eps         at least 2^-126 (the smallest normal fp32)
+ *   lr, eps     within fp32's range; eps at least 2^-126 (its smallest normal)
  *   grad_scale  D  one fp32 s (a clipping coefficient, an inverse loss scale),
  *                  or NULL for 1.  Where s is not finite the step changes
  *                  nothing.

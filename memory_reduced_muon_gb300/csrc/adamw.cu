@@ -891,9 +891,10 @@ namespace {
 qmuon_status adamw_step(const char* where, const qmuon_adamw_plan* plan, int64_t t, double lr, double beta1, double beta2,
                         double eps, bool sr, uint64_t seed, const float* grad_scale, void* stream) {
   if (!plan || t < 1 || !is_aligned(grad_scale, 4)) return QMUON_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+  // as the kernels take them, in fp32
+  if (!(std::fabs(lr) <= FLT_MAX) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
     return QMUON_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(eps) || !((float)eps >= FLT_MIN)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (!(eps <= FLT_MAX) || !((float)eps >= FLT_MIN)) return QMUON_ERR_INVALID_ARGUMENT;
   if (sr && plan->state != QMUON_STATE_E4M3) return QMUON_ERR_UNSUPPORTED;
   AdamLaunch L{};
   L.tensors = plan->tensors;
