@@ -479,7 +479,10 @@ typedef struct qmuon_clip_plan qmuon_clip_plan;
 
 /* A reusable plan over n gradients (H array, copied) of at most 2^40 elements
  * each.  Empty ones are skipped, but there must be at least one element.
- * Allocates a small device table on the current device, and uploads it. */
+ * Allocates a small device table on the current device, and uploads it.  The
+ * table holds the arrays' addresses: they stay where they are as long as the
+ * plan is used (a training loop zeroes its gradients in place rather than
+ * allocating them anew, or makes its plans anew with them). */
 QMUON_API qmuon_status qmuon_clip_plan_create(const qmuon_grad* grads, int32_t n, qmuon_clip_plan** out);
 QMUON_API void qmuon_clip_plan_destroy(qmuon_clip_plan* plan);
 /* Workspace bytes of qmuon_grad_clip (0 for a NULL plan). */
@@ -533,14 +536,15 @@ typedef struct {
 
 typedef struct qmuon_adamw_plan qmuon_adamw_plan;
 
-/* A reusable plan over n tensors (H array, copied); limits as in
- * qmuon_clip_plan_create. */
+/* A reusable plan over n tensors (H array, copied); limits, and what it holds,
+ * as in qmuon_clip_plan_create. */
 QMUON_API qmuon_status qmuon_adamw_plan_create(const qmuon_adamw_tensor* tensors, int32_t n, qmuon_state_kind state,
                                                qmuon_adamw_plan** out);
 QMUON_API void qmuon_adamw_plan_destroy(qmuon_adamw_plan* plan);
 
 /* One AdamW step of every tensor of the plan in one launch.  With g' = s g,
- * lr' = lr * lr_scale, fp32, one rounding per operation:
+ * lr' = lr * lr_scale, fp32, one rounding per operation but in u, whose quotient
+ * is within 2 ulp (and 0 where its denominator is above 2^126):
  *   m <- beta1 m + (1 - beta1) g'       v <- beta2 v + (1 - beta2) g'^2
  *   p <- p (1 - lr' weight_decay) - (lr' / (1 - beta1^t)) * u
  *   u = m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
@@ -582,6 +586,9 @@ QMUON_API qmuon_status qmuon_adamw_step_sr(const qmuon_adamw_plan* plan, int64_t
  *                qmuon_update_mxfp8_carrier writes them), or both NULL;
  *                cols % 32 != 0 is QMUON_ERR_UNSUPPORTED
  * One of y and payload at least.  The MXFP8 codes are taken from the fp32 y.
+ * Squares are summed in fp32: a row whose sum is beyond its range (elements of
+ * 1.8e19 / sqrt(cols) and more) gives y = 0, and squares below 2^-126 lose bits,
+ * which shows where eps does not outweigh them.
  * rows may be 0; cols at most 2^30, rows * cols at most 2^40. */
 typedef struct {
   const void* x;
