@@ -517,11 +517,14 @@ def _refuse(x, where: str, what: str, need: str):
 
 
 def _array(x, dtype, n: int, where: str, what: str) -> int:
-    """The address of n elements side by side (a torch dtype; None: any)."""
-    if x is None or isinstance(x, int):
-        return x or 0
-    if (x.dtype is dtype or dtype is None) and x.is_cuda and x.is_contiguous() and x.numel() >= n:
-        return x.data_ptr()
+    """The address of n elements side by side (of a torch dtype; None: any), a tensor or an address."""
+    try:
+        if (x.dtype is dtype or dtype is None) and x.is_cuda and x.is_contiguous() and x.numel() >= n:
+            return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x or 0
+        raise
     _refuse(x, where, what, f"a contiguous GPU tensor of {n} or more elements" + (f" of {dtype}" if dtype else ""))
 
 
@@ -599,9 +602,12 @@ def qmuon_clip_workspace_size(plan: ClipPlan) -> int:
 def qmuon_grad_clip(plan: ClipPlan, max_norm: float, apply: bool, norm, ws, ws_bytes: Optional[int] = None, stream=None):
     """``norm``: a device fp32 tensor of two: the norm and the coefficient."""
     where = "qmuon_grad_clip"
-    st = lib().qmuon_grad_clip(plan.handle, float(max_norm), int(apply), _array(norm, _type_of(QMUON_FP32), 2, where, "norm"),
-                               _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes), _stream(stream))
-    _check(st, "qmuon_grad_clip")
+    st = (_lib_handle or lib()).qmuon_grad_clip(
+        plan.handle, float(max_norm), int(apply), _array(norm, _types.get(QMUON_FP32) or _type_of(QMUON_FP32), 2, where, "norm"),
+        _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
+        _raw_stream() if stream is None and _raw_stream else _stream(stream))
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
 
 
 class AdamwPlan:
@@ -617,14 +623,15 @@ class AdamwPlan:
 
 def adamw_tensor(param, grad, m, v, numel: int, grad_dtype="bf16", m_absmax=None, v_absmax=None, copy=None,
                  copy_dtype="bf16", weight_decay: float = 0.0, lr_scale: float = 1.0) -> qmuon_adamw_tensor:
-    """The plan made of it holds these addresses; m and v are checked there, against the kind of state."""
+    """The plan made of it holds these addresses, and is where the types of m and v are checked."""
     n, where = int(numel), "adamw_tensor"
     grad_dtype, copy_dtype = DTYPES.get(grad_dtype, grad_dtype), DTYPES.get(copy_dtype, copy_dtype)
     f32 = _type_of(QMUON_FP32)
-    t = qmuon_adamw_tensor(_array(param, f32, n, where, "param"), _array(grad, _type_of(grad_dtype), n, where, "grad"),
-                           _array(copy, _type_of(copy_dtype), n, where, "copy"), _ptr(m), _ptr(v),
-                           _array(m_absmax, f32, -(-n // 256), where, "m_absmax"),
-                           _array(v_absmax, f32, -(-n // 256), where, "v_absmax"), n, float(lr_scale),
+    t = qmuon_adamw_tensor(_array(param, f32, n, where, "param"), _array(grad, _types.get(grad_dtype), n, where, "grad"),
+                           None if copy is None else _array(copy, _types.get(copy_dtype), n, where, "copy"),
+                           _array(m, None, n, where, "m"), _array(v, None, n, where, "v"),
+                           None if m_absmax is None else _array(m_absmax, f32, -(-n // 256), where, "m_absmax"),
+                           None if v_absmax is None else _array(v_absmax, f32, -(-n // 256), where, "v_absmax"), n, float(lr_scale),
                            float(weight_decay), grad_dtype, copy_dtype)
     t._keep = (param, grad, copy, m, v, m_absmax, v_absmax)
     return t
@@ -633,12 +640,11 @@ def adamw_tensor(param, grad, m, v, numel: int, grad_dtype="bf16", m_absmax=None
 def qmuon_adamw_plan_create(tensors: Sequence, state="f32") -> AdamwPlan:
     """``tensors``: ``adamw_tensor(...)``; ``state``: "f32" or "e4m3"."""
     kind = STATE_KINDS.get(state, state)
+    held = _type_of(QMUON_FP32) if kind == QMUON_STATE_F32 else None    # None: one byte
     for t in tensors:
-        for x, what in zip(getattr(t, "_keep", ())[3:5], "mv"):
-            if kind == QMUON_STATE_E4M3:
-                _bytes(x, t.numel, "qmuon_adamw_plan_create", what)
-            else:
-                _array(x, _type_of(QMUON_FP32), t.numel, "qmuon_adamw_plan_create", what)
+        for x in getattr(t, "_keep", ())[3:5]:
+            if x is not None and not isinstance(x, int) and (x.dtype is not held if held else x.element_size() != 1):
+                _refuse(x, "qmuon_adamw_plan_create", "m" if x is t._keep[3] else "v", f"of {held or 'one byte per element'}")
     arr = (qmuon_adamw_tensor * max(1, len(tensors)))(*tensors)
     out = C.c_void_p()
     st = lib().qmuon_adamw_plan_create(arr, len(tensors), kind, C.byref(out))
