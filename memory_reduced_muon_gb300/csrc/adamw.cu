@@ -518,10 +518,11 @@ struct __align__(16) E4m3Stage {
 
 // J whole blocks per warp, all of their loads in flight from the start: the
 // copies need no registers while they are.  With one block per warp, loaded
-// into registers, the arithmetic (48 instructions per element, 75 with random
-// numbers) left too few bytes in flight.  2^28 elements with a copy: 776 us so,
-// 680 with J = 2, 653 with 3 (6.6 TB/s), 647 with 4; rounded stochastically 743,
-// 688 and 713, where the arithmetic is the bound.
+// into registers, the arithmetic (54 instructions per element, 77 with random
+// numbers) left too few bytes in flight.  2^28 elements with a copy took 776 us
+// so, 680 with J = 2, 653 with 3, 647 with 4; rounded stochastically 743, 688 and
+// 713, where the arithmetic is the bound.  With the tensor's record in registers
+// 638 (6.75 TB/s) and 667.
 template <int GDT, int CDT, bool SR, int J>
 __device__ __forceinline__ void e4m3_fast(const AdamLaunch& L, const AdamTensor& T, const AdamCoef& C, int64_t first, int n,
                                           unsigned char* smem) {
