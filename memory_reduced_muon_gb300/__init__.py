@@ -516,16 +516,46 @@ def _refuse(x, where: str, what: str, need: str):
                      f"{what} has to be {need}; it is {tuple(x.shape)}, strides {x.stride()}, of {x.dtype} on {x.device}")
 
 
-def _array(x, dtype, n: int, where: str, what: str) -> int:
-    """The address of n elements side by side (of a torch dtype; None: any), a tensor or an address."""
+def _rows_apart(x, rows: int, cols: int, ld: int) -> bool:
+    """Whether a tensor that is not contiguous is rows `ld` apart in all of its leading dimensions together."""
+    *lead, width = zip(x.shape, x.stride())
+    if width[0] < cols or (width[1] != 1 and cols != 1):
+        return False
+    n = 1
+    for size, stride in reversed(lead):
+        if size != 1 and stride != ld * n:
+            return False
+        n *= size
+    return bool(lead) and n >= rows
+
+
+def _dense(x) -> bool:
+    """Whether a tensor's elements lie side by side in some order."""
+    n = 1
+    for stride, size in sorted(zip(x.stride(), x.shape)):
+        if size != 1:
+            if stride != n:
+                return False
+            n *= size
+    return True
+
+
+def _array(x, dtype, n: int, where: str, what: str, beside=None) -> int:
+    """The address of n elements side by side (of a torch dtype; None: any), a tensor or an address.  `beside`: the
+    arrays that are gone through together with this one: it may then be in any order that is theirs too."""
     try:
-        if (x.dtype is dtype or dtype is None) and x.is_cuda and x.is_contiguous() and x.numel() >= n:
-            return x.data_ptr()
+        if (x.dtype is dtype or dtype is None) and x.is_cuda and x.numel() >= n:
+            if x.is_contiguous():
+                return x.data_ptr()
+            if beside is not None and _dense(x) and all(
+                    b is None or isinstance(b, int) or b.shape != x.shape or b.stride() == x.stride() for b in beside):
+                return x.data_ptr()
     except AttributeError:
         if x is None or isinstance(x, int):
             return x or 0
         raise
-    _refuse(x, where, what, f"a contiguous GPU tensor of {n} or more elements" + (f" of {dtype}" if dtype else ""))
+    _refuse(x, where, what, f"a contiguous GPU tensor of {n} or more elements" + (f" of {dtype}" if dtype else "") +
+            ("" if beside is None else ", or one in the same order as the others"))
 
 
 def _bytes(x, n: int, where: str, what: str) -> int:
@@ -543,8 +573,7 @@ def _matrix(x, dtype, rows: int, cols: int, ld: int, where: str, what: str) -> i
                 n = x.numel()
                 if n >= rows * ld or n >= (rows - 1) * ld + cols:
                     return x.data_ptr()
-            elif (x.dim() == 2 and x.shape[0] >= rows and x.shape[1] >= cols and (x.stride(1) == 1 or cols == 1) and
-                  (x.stride(0) == ld or rows == 1)):
+            elif _rows_apart(x, rows, cols, ld):
                 return x.data_ptr()
     except AttributeError:
         if x is None or isinstance(x, int):
@@ -581,7 +610,7 @@ def qmuon_clip_plan_create(grads: Sequence) -> ClipPlan:
         if isinstance(g, qmuon_grad):
             return g
         n, dtype = int(g[0].numel()), DTYPES.get(g[1], g[1])
-        return qmuon_grad(_array(g[0], _type_of(dtype), n, "qmuon_clip_plan_create", "a gradient"), n, dtype, 0)
+        return qmuon_grad(_array(g[0], _type_of(dtype), n, "qmuon_clip_plan_create", "a gradient", ()), n, dtype, 0)
     descs = [desc(g) for g in grads]
     arr = (qmuon_grad * max(1, len(descs)))(*descs)
     out = C.c_void_p()
@@ -627,9 +656,11 @@ def adamw_tensor(param, grad, m, v, numel: int, grad_dtype="bf16", m_absmax=None
     n, where = int(numel), "adamw_tensor"
     grad_dtype, copy_dtype = DTYPES.get(grad_dtype, grad_dtype), DTYPES.get(copy_dtype, copy_dtype)
     f32 = _type_of(QMUON_FP32)
-    t = qmuon_adamw_tensor(_array(param, f32, n, where, "param"), _array(grad, _types.get(grad_dtype), n, where, "grad"),
-                           None if copy is None else _array(copy, _types.get(copy_dtype), n, where, "copy"),
-                           _array(m, None, n, where, "m"), _array(v, None, n, where, "v"),
+    these = (param, grad, copy, m, v)
+    t = qmuon_adamw_tensor(_array(param, f32, n, where, "param", these),
+                           _array(grad, _types.get(grad_dtype), n, where, "grad", these),
+                           None if copy is None else _array(copy, _types.get(copy_dtype), n, where, "copy", these),
+                           _array(m, None, n, where, "m", these), _array(v, None, n, where, "v", these),
                            None if m_absmax is None else _array(m_absmax, f32, -(-n // 256), where, "m_absmax"),
                            None if v_absmax is None else _array(v_absmax, f32, -(-n // 256), where, "v_absmax"), n, float(lr_scale),
                            float(weight_decay), grad_dtype, copy_dtype)
@@ -676,8 +707,8 @@ def qmuon_adamw_step_sr(plan: AdamwPlan, t: int, lr: float, beta1: float, beta2:
                                      _array(grad_scale, _type_of(QMUON_FP32), 1, where, "grad_scale"), _stream(stream)), where)
 
 
-# The structures as bytes, which take a sixth of a ctypes object's time, and the entries that take them so: what the
-# checks of the tensors cost a small call comes back here.
+# The structures as bytes, which take a sixth of a ctypes object's time, and the entries that take them so: most of what
+# the checks of the tensors cost a small call comes back here.
 _RMSNORM, _RMSNORM_GRAD = struct.Struct("@7Q6qfi").pack, struct.Struct("@6Q6qfi").pack
 _bytes_entries: dict = {}
 

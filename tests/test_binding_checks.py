@@ -107,7 +107,7 @@ def test_backward_refuses():
 def test_plans_and_scalars_refuse():
     g = torch.zeros(64, 64, device="cuda")
     _refused(lambda: q.qmuon_clip_plan_create([(g, "bf16")]), "gradient")
-    _refused(lambda: q.qmuon_clip_plan_create([(g.t()[:, 1:], "f32")]), "gradient")
+    _refused(lambda: q.qmuon_clip_plan_create([(g[:, 1:], "f32")]), "gradient")
     clip = q.qmuon_clip_plan_create([(g.t().t(), "f32"), (g[3], "f32")])
     ws = torch.empty(q.qmuon_clip_workspace_size(clip), dtype=U8, device="cuda")
     for norm in (torch.zeros(2, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda"), torch.zeros(2)):
@@ -131,4 +131,40 @@ def test_plans_and_scalars_refuse():
     for bad in (z(1, BF16), torch.ones(1), z(1, torch.float64)):
         _refused(lambda: q.qmuon_adamw_step(plan, 1, 1e-3, 0.9, 0.99, 1e-8, bad), "grad_scale")
     q.qmuon_adamw_step(plan, 1, 1e-3, 0.9, 0.99, 1e-8, z(2)[1:])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_orders_and_slices_that_are_right_are_taken():
+    # rows of a slice of (batch, time, width): uniformly apart; of a slice of (time, batch): not
+    wide = torch.randn(3, 5, 2 * COLS, device="cuda")
+    gain = torch.ones(COLS, device="cuda")
+    y = torch.zeros(15, COLS, device="cuda")
+    want = torch.zeros(15, COLS, device="cuda")
+    part = wide[:, :, :COLS]
+    q.qmuon_rmsnorm_forward(part.contiguous(), gain, 15, COLS, "f32", 1e-5, y=want)
+    q.qmuon_rmsnorm_forward(part, gain, 15, COLS, "f32", 1e-5, y=y, ld_x=2 * COLS)
+    assert torch.equal(y, want)
+    q.qmuon_rmsnorm_forward(part[1], gain, 5, COLS, "f32", 1e-5, y=y, ld_x=2 * COLS)
+    assert torch.equal(y[:5], want[5:10])
+    q.qmuon_rmsnorm_forward(part[1:2, 2:3], gain, 1, COLS, "f32", 1e-5, y=y, ld_x=2 * COLS)
+    assert torch.equal(y[:1], want[7:8])
+    for bad in (part[:, :4], part.transpose(0, 1), part[:, ::2], part[..., 0], wide[0, 0, ::2]):
+        _refused(lambda: q.qmuon_rmsnorm_forward(bad, gain, bad.numel() // COLS or 2, COLS, "f32", 1e-5, y=y, ld_x=2 * COLS), "x has")
+    # transposed weights: the elements' order in memory is one and the same in what the step goes through together
+    z = lambda *s: torch.zeros(*s, device="cuda")   # noqa: E731
+    p, g, c = z(8, 40).t(), z(8, 40).t(), torch.zeros(8, 40, dtype=BF16, device="cuda").t()
+    g.copy_(torch.arange(320.0, device="cuda").view(40, 8) + 1)
+    plan = q.qmuon_adamw_plan_create([q.adamw_tensor(p, g, z(320), z(320), 320, "f32", copy=c)])
+    q.qmuon_adamw_step(plan, 1, 0.5, 0.9, 0.99, 1e-8)
+    assert bool(((p + 0.5).abs() < 1e-5).all()) and torch.equal(c, p.to(BF16))
+    clip = q.qmuon_clip_plan_create([(g, "f32")])
+    norm = torch.zeros(2, device="cuda")
+    q.qmuon_grad_clip(clip, 1.0, False, norm, torch.empty(q.qmuon_clip_workspace_size(clip), dtype=U8, device="cuda"))
+    assert abs(norm[0].item() - g.norm().item()) <= 1e-6 * norm[0].item()
+    _refused(lambda: q.adamw_tensor(p, g.contiguous(), z(320), z(320), 320, "f32"), "param")
+    _refused(lambda: q.adamw_tensor(p.contiguous(), g, z(320), z(320), 320, "f32"), "grad")
+    _refused(lambda: q.adamw_tensor(p, g, z(40, 8), z(320), 320, "f32"), "param")
+    _refused(lambda: q.adamw_tensor(p, g, z(320), z(320), 320, "f32", copy=c.contiguous()), "param")
+    _refused(lambda: q.adamw_tensor(z(80, 8)[::2], z(320), z(320), z(320), 320, "f32"), "param")
     torch.cuda.synchronize()
