@@ -636,6 +636,182 @@ QMUON_API size_t qmuon_rmsnorm_workspace_size(int64_t rows, int64_t cols);
 QMUON_API qmuon_status qmuon_rmsnorm_backward(const qmuon_rmsnorm_grad* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A model's activations: the token embedding, the gated feed-forward block and
+ * 8-bit activation checkpoints, with their gradients.  The pages have no
+ * counterpart.  Conventions as in the section above: matrices are row-major,
+ * rows ld_* >= cols elements apart, 16-byte aligned rows are faster; an array
+ * that is written overlaps no other array of the call.
+ * ------------------------------------------------------------------------- */
+
+/* Lookup of n_tokens rows of a table of vocab x cols, all of `dtype`:
+ *   out[t] = scale * table[tokens[t]]
+ * rounded once; zeros for a token outside [0, vocab).
+ *   tokens   D  int32 or int64 (token_bits 32 or 64)
+ * n_tokens may be 0 and is at most 2^28; cols at most 2^22, vocab at most
+ * 2^31 - 2, vocab * cols at most 2^40. */
+typedef struct {
+  const void* table;
+  const void* tokens;
+  void* out;
+  int64_t n_tokens, vocab, cols;
+  int64_t ld_table, ld_out;
+  float scale;
+  int32_t dtype;               /* qmuon_dtype */
+  int32_t token_bits;
+  int32_t reserved;
+} qmuon_embedding;
+
+QMUON_API qmuon_status qmuon_embedding_forward(const qmuon_embedding* embedding, void* stream);
+
+/* Its gradient, from tokens sorted on the GPU:
+ *   dtable[v] = scale * sum over t with tokens[t] = v of dout[t]
+ * summed in fp32 in an order that depends on the tokens alone (the same inputs
+ * give the same bits), rounded once.  Tokens outside [0, vocab) add nothing.
+ *   dout        of `dtype`
+ *   dtable      of `grad_dtype`: dtype, or QMUON_FP32
+ *   accumulate  0: rows without a token become zero
+ *               1: dtable += the sums; rows without a token are left alone
+ *   ws          D  256-byte aligned, of qmuon_embedding_workspace_size */
+typedef struct {
+  const void* dout;
+  const void* tokens;
+  void* dtable;
+  int64_t n_tokens, vocab, cols;
+  int64_t ld_dout, ld_dtable;
+  float scale;
+  int32_t dtype, grad_dtype;
+  int32_t token_bits;
+  int32_t accumulate;
+  int32_t reserved;
+} qmuon_embedding_grad;
+
+/* Workspace bytes of qmuon_embedding_backward (0 for sizes it rejects). */
+QMUON_API size_t qmuon_embedding_workspace_size(int64_t n_tokens, int64_t vocab, int64_t cols);
+QMUON_API qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* embedding, void* ws, size_t ws_bytes, void* stream);
+
+/* An activation as an MXFP8 carrier (qmuon_rmsnorm's and
+ * qmuon_update_mxfp8_carrier's format), and back.
+ *   x          rows x cols of `dtype`
+ *   payload    rows x cols E4M3 codes, contiguous, 16-byte aligned
+ *   scale_inv  rows x (cols/32) E8M0 exponents, contiguous
+ * cols % 32 != 0 is QMUON_ERR_UNSUPPORTED.  Codes are to the nearest under the
+ * smallest power of two that leaves a block's largest magnitude within 448; a
+ * NaN keeps a NaN code.  Decoding is exact in bf16 and fp32 but for products
+ * beyond their ranges; in fp16 it rounds below the normal range, and a finite
+ * value beyond 65504 becomes 65504.  rows may be 0; cols at most 2^30,
+ * rows * cols at most 2^40. */
+typedef struct {
+  void* x;                     /* read by the encoder, written by the decoder */
+  uint8_t* payload;
+  uint8_t* scale_inv;
+  int64_t rows, cols, ld_x;
+  int32_t dtype;
+  int32_t reserved;
+} qmuon_mxfp8;
+
+QMUON_API qmuon_status qmuon_mxfp8_encode(const qmuon_mxfp8* carrier, void* stream);
+QMUON_API qmuon_status qmuon_mxfp8_decode(const qmuon_mxfp8* carrier, void* stream);
+
+typedef enum {
+  QMUON_ACT_SILU = 0,          /* g / (1 + exp(-g))                                */
+  QMUON_ACT_GELU = 1,          /* g (1 + erf(g / sqrt 2)) / 2                       */
+  QMUON_ACT_GELU_TANH = 2      /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+} qmuon_act;
+
+/* What a forward pass keeps of gate and up for the backward pass. */
+typedef enum {
+  QMUON_SAVE_NONE = 0,         /* nothing: the backward pass computes them again from x */
+  QMUON_SAVE_SAME = 1,         /* rounded to dtype                                      */
+  QMUON_SAVE_MXFP8 = 2         /* as MXFP8 carriers, from their fp32 values             */
+} qmuon_saved;
+
+/* Gated feed-forward block on tensor cores, fp32 accumulation:
+ *   gate = x Wg^T    up = x Wu^T    h = act(gate) * up
+ *   x             rows x width          w_gate, w_up   inner x width
+ *   h             rows x inner, from the unrounded gate and up, rounded once
+ *   gate, up      QMUON_SAVE_SAME: rows x inner of dtype;  QMUON_SAVE_MXFP8:
+ *                 rows x inner codes, contiguous, 16-byte aligned (inner % 32
+ *                 != 0 is QMUON_ERR_UNSUPPORTED);  QMUON_SAVE_NONE: not looked at
+ *   gate_scale,   QMUON_SAVE_MXFP8: rows x (inner/32) exponents
+ *     up_scale
+ *   dtype         QMUON_BF16 or QMUON_FP16 (else QMUON_ERR_UNSUPPORTED)
+ *   ws            D  256-byte aligned, of qmuon_gated_ffn_workspace_size(ffn);
+ *                 qmuon_sync_status reports a wait in the kernel that expired
+ * Rows of x and of the weights that do not all start on 16 bytes are copied to
+ * the workspace first.  rows may be 0; rows, width and inner at most 2^28,
+ * inner * width at most 2^36, rows * inner and rows * width at most 2^38.
+ * Sums are taken in an order that depends on the sizes and on the GPU's SM
+ * count alone. */
+typedef struct {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  void* h;
+  void* gate;
+  void* up;
+  uint8_t* gate_scale;
+  uint8_t* up_scale;
+  int64_t rows, width, inner;
+  int64_t ld_x, ld_w_gate, ld_w_up, ld_h, ld_gate, ld_up;
+  int32_t act;                 /* qmuon_act */
+  int32_t dtype;
+  int32_t saved;               /* qmuon_saved */
+  int32_t reserved;
+} qmuon_gated_ffn;
+
+/* Workspace bytes of a call (0 where the call would be refused). */
+QMUON_API size_t qmuon_gated_ffn_workspace_size(const qmuon_gated_ffn* ffn);
+QMUON_API qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* ffn, void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward pass:
+ *   dgate = dh * up * act'(gate)    dup = dh * act(gate)
+ *   dx = dgate Wg + dup Wu          dWg = dgate^T x       dWu = dup^T x
+ * dgate and dup are rounded to dtype before the products; dx, dWg and dWu once
+ * more at the end.
+ *   x, x_scale   x_scale NULL: x as in the forward pass;  else x is an MXFP8
+ *                carrier (codes, 16-byte aligned, and exponents; width % 32 != 0
+ *                is QMUON_ERR_UNSUPPORTED), decoded as qmuon_mxfp8_decode does;
+ *                not looked at where neither dw_gate is given nor gate and up
+ *                have to be computed again
+ *   w_gate, w_up  likewise where neither dx is given nor gate and up are needed
+ *   gate, up, gate_scale, up_scale   what `saved` says, as the forward pass left
+ *                them
+ *   dx           or NULL
+ *   dw_gate,     inner x width of `grad_dtype` (dtype, or QMUON_FP32), or both
+ *     dw_up      NULL; accumulate 1: added to what is there
+ *   h            the block's output again, for the gradient of the product that
+ *                follows it, or NULL
+ *   ws           D  256-byte aligned, of qmuon_gated_ffn_backward_workspace_size
+ * One of dx, dw_gate and h at least.  With no rows the weights' gradients are
+ * zero, or left alone where they accumulate. */
+typedef struct {
+  const void* dh;
+  const void* x;
+  const uint8_t* x_scale;
+  const void* w_gate;
+  const void* w_up;
+  const void* gate;
+  const void* up;
+  const uint8_t* gate_scale;
+  const uint8_t* up_scale;
+  void* dx;
+  void* dw_gate;
+  void* dw_up;
+  void* h;
+  int64_t rows, width, inner;
+  int64_t ld_dh, ld_x, ld_w_gate, ld_w_up, ld_gate, ld_up, ld_dx, ld_dw_gate, ld_dw_up, ld_h;
+  int32_t act;
+  int32_t dtype;
+  int32_t saved;
+  int32_t grad_dtype;
+  int32_t accumulate;
+  int32_t reserved;
+} qmuon_gated_ffn_grad;
+
+QMUON_API size_t qmuon_gated_ffn_backward_workspace_size(const qmuon_gated_ffn_grad* ffn);
+QMUON_API qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* ffn, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Path and dtype audit.  "Quantized Muon Momentum", §Wave18B MXFP8 Carrier
  * Probe, checks a run with counters: calls of the carrier update and the
  * dtypes of the tensors it read and wrote (uint8 payload and scales, fp32

@@ -7,8 +7,8 @@ the library's CUDA kernels; there is no Python or CPU fallback, and calling
 any entry point without the built library raises.
 
 Device buffers are passed as torch tensors (their ``data_ptr()``) or as raw
-integer addresses; the clipping, AdamW and RMS norm entries, which take a
-model's own tensors, check the former.  ``stream`` is a ``torch.cuda.Stream``, a raw
+integer addresses; the clipping, AdamW, RMS norm, embedding, checkpoint and
+feed-forward entries, which take a model's own tensors, check the former.  ``stream`` is a ``torch.cuda.Stream``, a raw
 ``cudaStream_t`` integer, or ``None`` for torch's current stream.
 """
 
@@ -40,6 +40,10 @@ QMUON_STATE_F32, QMUON_STATE_E4M3 = 0, 1
 Q8_KINDS = {"int8": QMUON_Q8_INT8, "uint8": QMUON_Q8_UINT8}
 DTYPES = {"bf16": QMUON_BF16, "f16": QMUON_FP16, "f32": QMUON_FP32}
 STATE_KINDS = {"f32": QMUON_STATE_F32, "e4m3": QMUON_STATE_E4M3}
+QMUON_ACT_SILU, QMUON_ACT_GELU, QMUON_ACT_GELU_TANH = 0, 1, 2
+QMUON_SAVE_NONE, QMUON_SAVE_SAME, QMUON_SAVE_MXFP8 = 0, 1, 2
+ACTS = {"silu": QMUON_ACT_SILU, "gelu": QMUON_ACT_GELU, "gelu_tanh": QMUON_ACT_GELU_TANH}
+SAVED = {"none": QMUON_SAVE_NONE, "same": QMUON_SAVE_SAME, "mxfp8": QMUON_SAVE_MXFP8}
 
 
 class QmuonError(RuntimeError):
@@ -99,6 +103,37 @@ class qmuon_rmsnorm_grad(C.Structure):
                 ("dx", C.c_void_p), ("dgain", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
                 ("ld_dy", C.c_int64), ("ld_h", C.c_int64), ("ld_dsum", C.c_int64), ("ld_dx", C.c_int64),
                 ("eps", C.c_float), ("dtype", C.c_int32)]
+
+
+class qmuon_embedding(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("tokens", C.c_void_p), ("out", C.c_void_p), ("n_tokens", C.c_int64), ("vocab", C.c_int64),
+                ("cols", C.c_int64), ("ld_table", C.c_int64), ("ld_out", C.c_int64), ("scale", C.c_float), ("dtype", C.c_int32),
+                ("token_bits", C.c_int32), ("reserved", C.c_int32)]
+
+
+class qmuon_embedding_grad(C.Structure):
+    _fields_ = [("dout", C.c_void_p), ("tokens", C.c_void_p), ("dtable", C.c_void_p), ("n_tokens", C.c_int64), ("vocab", C.c_int64),
+                ("cols", C.c_int64), ("ld_dout", C.c_int64), ("ld_dtable", C.c_int64), ("scale", C.c_float), ("dtype", C.c_int32),
+                ("grad_dtype", C.c_int32), ("token_bits", C.c_int32), ("accumulate", C.c_int32), ("reserved", C.c_int32)]
+
+
+class qmuon_mxfp8(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("payload", C.c_void_p), ("scale_inv", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("ld_x", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class qmuon_gated_ffn(C.Structure):
+    _fields_ = [(f, C.c_void_p) for f in ("x", "w_gate", "w_up", "h", "gate", "up", "gate_scale", "up_scale")] + \
+               [(f, C.c_int64) for f in ("rows", "width", "inner", "ld_x", "ld_w_gate", "ld_w_up", "ld_h", "ld_gate", "ld_up")] + \
+               [(f, C.c_int32) for f in ("act", "dtype", "saved", "reserved")]
+
+
+class qmuon_gated_ffn_grad(C.Structure):
+    _fields_ = [(f, C.c_void_p) for f in ("dh", "x", "x_scale", "w_gate", "w_up", "gate", "up", "gate_scale", "up_scale", "dx",
+                                          "dw_gate", "dw_up", "h")] + \
+               [(f, C.c_int64) for f in ("rows", "width", "inner", "ld_dh", "ld_x", "ld_w_gate", "ld_w_up", "ld_gate", "ld_up",
+                                         "ld_dx", "ld_dw_gate", "ld_dw_up", "ld_h")] + \
+               [(f, C.c_int32) for f in ("act", "dtype", "saved", "grad_dtype", "accumulate", "reserved")]
 
 
 GRASP_RANK, GRASP_BLOCK = 8, 64
@@ -168,6 +203,15 @@ def lib() -> C.CDLL:
         "qmuon_rmsnorm_forward": (i32, [C.POINTER(qmuon_rmsnorm), vp]),
         "qmuon_rmsnorm_workspace_size": (sz, [i64, i64]),
         "qmuon_rmsnorm_backward": (i32, [C.POINTER(qmuon_rmsnorm_grad), vp, sz, vp]),
+        "qmuon_embedding_forward": (i32, [C.POINTER(qmuon_embedding), vp]),
+        "qmuon_embedding_workspace_size": (sz, [i64, i64, i64]),
+        "qmuon_embedding_backward": (i32, [C.POINTER(qmuon_embedding_grad), vp, sz, vp]),
+        "qmuon_mxfp8_encode": (i32, [C.POINTER(qmuon_mxfp8), vp]),
+        "qmuon_mxfp8_decode": (i32, [C.POINTER(qmuon_mxfp8), vp]),
+        "qmuon_gated_ffn_workspace_size": (sz, [C.POINTER(qmuon_gated_ffn)]),
+        "qmuon_gated_ffn_forward": (i32, [C.POINTER(qmuon_gated_ffn), vp, sz, vp]),
+        "qmuon_gated_ffn_backward_workspace_size": (sz, [C.POINTER(qmuon_gated_ffn_grad)]),
+        "qmuon_gated_ffn_backward": (i32, [C.POINTER(qmuon_gated_ffn_grad), vp, sz, vp]),
         "qmuon_get_counters": (i32, [C.POINTER(qmuon_counters), sz]),
         "qmuon_reset_counters": (None, []),
     }
@@ -191,7 +235,10 @@ def exported_symbols() -> list:
             "qmuon_get_counters", "qmuon_reset_counters", "qmuon_plan_set_host_ingest",
             "qmuon_clip_plan_create", "qmuon_clip_plan_destroy", "qmuon_clip_workspace_size", "qmuon_grad_clip",
             "qmuon_adamw_plan_create", "qmuon_adamw_plan_destroy", "qmuon_adamw_step", "qmuon_adamw_step_sr",
-            "qmuon_rmsnorm_forward", "qmuon_rmsnorm_workspace_size", "qmuon_rmsnorm_backward"]
+            "qmuon_rmsnorm_forward", "qmuon_rmsnorm_workspace_size", "qmuon_rmsnorm_backward",
+            "qmuon_embedding_forward", "qmuon_embedding_workspace_size", "qmuon_embedding_backward", "qmuon_mxfp8_encode",
+            "qmuon_mxfp8_decode", "qmuon_gated_ffn_workspace_size", "qmuon_gated_ffn_forward",
+            "qmuon_gated_ffn_backward_workspace_size", "qmuon_gated_ffn_backward"]
 
 
 # --------------------------------------------------------------------------
@@ -780,5 +827,190 @@ def qmuon_rmsnorm_backward(dy, h, gain, rows: int, cols: int, dtype, eps: float,
     st = (_bytes_entries.get(where) or _by_bytes(where))(
         n, _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
         _raw_stream() if stream is None and _raw_stream else _stream(stream))
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
+
+
+# --------------------------------------------------------------------------
+# a model's activations: embedding, 8-bit checkpoints, gated feed-forward block
+# --------------------------------------------------------------------------
+
+_EMBEDDING, _EMBEDDING_GRAD, _MXFP8 = struct.Struct("@3Q5qf3i").pack, struct.Struct("@3Q5qf5i").pack, struct.Struct("@3Q3q2i").pack
+_FFN, _FFN_GRAD = struct.Struct("@8Q9q4i").pack, struct.Struct("@13Q13q6i").pack
+
+
+def _tokens(x, n: int, bits: int, where: str):
+    """The address of n tokens and the bits of one (`bits` for an address)."""
+    if x is None or isinstance(x, int):
+        return x or 0, bits
+    import torch
+    if x.dtype is torch.int64:
+        bits = 64
+    elif x.dtype is torch.int32:
+        bits = 32
+    else:
+        _refuse(x, where, "tokens", "of int32 or int64")
+    return _array(x, None, n, where, "tokens"), bits
+
+
+def _call(where: str, packed, *args):
+    st = (_bytes_entries.get(where) or _by_bytes(where))(packed, *args)
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
+
+
+def qmuon_embedding_forward(table, tokens, out, n_tokens: int, vocab: int, cols: int, dtype, scale: float = 1.0,
+                            ld_table: Optional[int] = None, ld_out: Optional[int] = None, token_bits: int = 64, stream=None):
+    """``token_bits`` is looked at where ``tokens`` is an address."""
+    where = "qmuon_embedding_forward"
+    dtype = DTYPES.get(dtype, dtype)
+    t = _types.get(dtype) or _type_of(dtype)
+    ld_table, ld_out = cols if ld_table is None else ld_table, cols if ld_out is None else ld_out
+    try:
+        at, bits = _tokens(tokens, n_tokens, token_bits, where)
+        packed = _EMBEDDING(_matrix(table, t, vocab, cols, ld_table, where, "table"), at,
+                            _matrix(out, t, n_tokens, cols, ld_out, where, "out"), n_tokens, vocab, cols, ld_table, ld_out, scale,
+                            dtype, bits, 0)
+    except (struct.error, OverflowError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    _call(where, packed, _raw_stream() if stream is None and _raw_stream else _stream(stream))
+
+
+def qmuon_embedding_workspace_size(n_tokens: int, vocab: int, cols: int) -> int:
+    return int(lib().qmuon_embedding_workspace_size(int(n_tokens), int(vocab), int(cols)))
+
+
+def qmuon_embedding_backward(dout, tokens, dtable, n_tokens: int, vocab: int, cols: int, dtype, ws, scale: float = 1.0,
+                             grad_dtype=None, accumulate: bool = False, ld_dout: Optional[int] = None,
+                             ld_dtable: Optional[int] = None, token_bits: int = 64, ws_bytes: Optional[int] = None, stream=None):
+    """``grad_dtype``: that of ``dtable``, ``dtype`` by default."""
+    where = "qmuon_embedding_backward"
+    dtype = DTYPES.get(dtype, dtype)
+    grad_dtype = dtype if grad_dtype is None else DTYPES.get(grad_dtype, grad_dtype)
+    ld_dout, ld_dtable = cols if ld_dout is None else ld_dout, cols if ld_dtable is None else ld_dtable
+    try:
+        at, bits = _tokens(tokens, n_tokens, token_bits, where)
+        packed = _EMBEDDING_GRAD(_matrix(dout, _type_of(dtype), n_tokens, cols, ld_dout, where, "dout"), at,
+                                 _matrix(dtable, _type_of(grad_dtype), vocab, cols, ld_dtable, where, "dtable"), n_tokens, vocab, cols,
+                                 ld_dout, ld_dtable, scale, dtype, grad_dtype, bits, 1 if accumulate else 0, 0)
+    except (struct.error, OverflowError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    _call(where, packed, _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
+          _raw_stream() if stream is None and _raw_stream else _stream(stream))
+
+
+def _mxfp8(where: str, x, payload, scale_inv, rows: int, cols: int, dtype, ld_x: Optional[int], stream):
+    dtype = DTYPES.get(dtype, dtype)
+    t = _types.get(dtype) or _type_of(dtype)
+    ld_x = cols if ld_x is None else ld_x
+    try:
+        packed = _MXFP8(_matrix(x, t, rows, cols, ld_x, where, "x"), _bytes(payload, rows * cols, where, "payload"),
+                        _bytes(scale_inv, rows * (cols // 32), where, "scale_inv"), rows, cols, ld_x, dtype, 0)
+    except (struct.error, OverflowError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    _call(where, packed, _raw_stream() if stream is None and _raw_stream else _stream(stream))
+
+
+def qmuon_mxfp8_encode(x, payload, scale_inv, rows: int, cols: int, dtype, ld_x: Optional[int] = None, stream=None):
+    _mxfp8("qmuon_mxfp8_encode", x, payload, scale_inv, rows, cols, dtype, ld_x, stream)
+
+
+def qmuon_mxfp8_decode(payload, scale_inv, x, rows: int, cols: int, dtype, ld_x: Optional[int] = None, stream=None):
+    _mxfp8("qmuon_mxfp8_decode", x, payload, scale_inv, rows, cols, dtype, ld_x, stream)
+
+
+def _saved_arrays(where, saved, t, rows, inner, gate, up, gate_scale, up_scale, ld_gate, ld_up):
+    """The addresses of gate, up and their scales as `saved` reads them."""
+    if saved == QMUON_SAVE_SAME:
+        return _matrix(gate, t, rows, inner, ld_gate, where, "gate"), _matrix(up, t, rows, inner, ld_up, where, "up"), 0, 0
+    if saved == QMUON_SAVE_MXFP8:
+        n, groups = rows * inner, rows * (inner // 32)
+        return (_bytes(gate, n, where, "gate"), _bytes(up, n, where, "up"), _bytes(gate_scale, groups, where, "gate_scale"),
+                _bytes(up_scale, groups, where, "up_scale"))
+    return 0, 0, 0, 0
+
+
+def gated_ffn(x, w_gate, w_up, h, rows: int, width: int, inner: int, dtype, act="silu", saved="none", gate=None, up=None,
+              gate_scale=None, up_scale=None, ld_x: Optional[int] = None, ld_w_gate: Optional[int] = None,
+              ld_w_up: Optional[int] = None, ld_h: Optional[int] = None, ld_gate: Optional[int] = None,
+              ld_up: Optional[int] = None) -> qmuon_gated_ffn:
+    """One forward call over these arrays, which it holds: checked here, and made any number of times.  ``act``: "silu",
+    "gelu" or "gelu_tanh"; ``saved``: "none", "same" or "mxfp8"; the ``ld_*`` default to rows next to one another."""
+    where = "gated_ffn"
+    dtype, act, saved = DTYPES.get(dtype, dtype), ACTS.get(act, act), SAVED.get(saved, saved)
+    t = _type_of(dtype)
+    ld_x, ld_w_gate, ld_w_up = (width if v is None else v for v in (ld_x, ld_w_gate, ld_w_up))
+    ld_h, ld_gate, ld_up = (inner if v is None else v for v in (ld_h, ld_gate, ld_up))
+    try:
+        c = qmuon_gated_ffn.from_buffer_copy(_FFN(
+            _matrix(x, t, rows, width, ld_x, where, "x"), _matrix(w_gate, t, inner, width, ld_w_gate, where, "w_gate"),
+            _matrix(w_up, t, inner, width, ld_w_up, where, "w_up"), _matrix(h, t, rows, inner, ld_h, where, "h"),
+            *_saved_arrays(where, saved, t, rows, inner, gate, up, gate_scale, up_scale, ld_gate, ld_up), rows, width, inner, ld_x,
+            ld_w_gate, ld_w_up, ld_h, ld_gate, ld_up, act, dtype, saved, 0))
+    except (struct.error, OverflowError, TypeError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    c._keep = (x, w_gate, w_up, h, gate, up, gate_scale, up_scale)
+    return c
+
+
+def qmuon_gated_ffn_workspace_size(ffn: qmuon_gated_ffn) -> int:
+    return int(lib().qmuon_gated_ffn_workspace_size(C.byref(ffn)))
+
+
+def qmuon_gated_ffn_forward(ffn: qmuon_gated_ffn, ws, ws_bytes: Optional[int] = None, stream=None):
+    where = "qmuon_gated_ffn_forward"
+    st = (_lib_handle or lib()).qmuon_gated_ffn_forward(C.byref(ffn), _on_gpu(ws, where, "ws"),
+                                                        _nbytes(ws) if ws_bytes is None else int(ws_bytes),
+                                                        _raw_stream() if stream is None and _raw_stream else _stream(stream))
+    if st != QMUON_OK:
+        raise QmuonError(st, where)
+
+
+def gated_ffn_grad(dh, x, w_gate, w_up, dx, dw_gate, dw_up, rows: int, width: int, inner: int, dtype, act="silu", saved="none",
+                   gate=None, up=None, gate_scale=None, up_scale=None, x_scale=None, h=None, grad_dtype=None, accumulate: bool = False,
+                   ld_dh: Optional[int] = None, ld_x: Optional[int] = None, ld_w_gate: Optional[int] = None,
+                   ld_w_up: Optional[int] = None, ld_gate: Optional[int] = None, ld_up: Optional[int] = None,
+                   ld_dx: Optional[int] = None, ld_dw_gate: Optional[int] = None, ld_dw_up: Optional[int] = None,
+                   ld_h: Optional[int] = None) -> qmuon_gated_ffn_grad:
+    """One backward call over these arrays, which it holds.  ``x_scale``: the exponents of an ``x`` that is an MXFP8
+    carrier; ``grad_dtype``: that of the weights' gradients, ``dtype`` by default."""
+    where = "gated_ffn_grad"
+    dtype, act, saved = DTYPES.get(dtype, dtype), ACTS.get(act, act), SAVED.get(saved, saved)
+    grad_dtype = dtype if grad_dtype is None else DTYPES.get(grad_dtype, grad_dtype)
+    t, gt = _type_of(dtype), _type_of(grad_dtype)
+    ld_x, ld_w_gate, ld_w_up, ld_dx, ld_dw_gate, ld_dw_up = (width if v is None else v for v in (ld_x, ld_w_gate, ld_w_up, ld_dx,
+                                                                                                 ld_dw_gate, ld_dw_up))
+    ld_dh, ld_gate, ld_up, ld_h = (inner if v is None else v for v in (ld_dh, ld_gate, ld_up, ld_h))
+
+    def optional(a, ty, n, cols, ld, what):
+        return 0 if a is None else _matrix(a, ty, n, cols, ld, where, what)
+    try:
+        if x_scale is None:
+            px, ps = _matrix(x, t, rows, width, ld_x, where, "x"), 0
+        else:
+            px, ps = _bytes(x, rows * width, where, "x"), _bytes(x_scale, rows * (width // 32), where, "x_scale")
+        g, u, gs, us = _saved_arrays(where, saved, t, rows, inner, gate, up, gate_scale, up_scale, ld_gate, ld_up)
+        c = qmuon_gated_ffn_grad.from_buffer_copy(_FFN_GRAD(
+            _matrix(dh, t, rows, inner, ld_dh, where, "dh"), px, ps,
+            optional(w_gate, t, inner, width, ld_w_gate, "w_gate"), optional(w_up, t, inner, width, ld_w_up, "w_up"), g, u, gs, us,
+            optional(dx, t, rows, width, ld_dx, "dx"), optional(dw_gate, gt, inner, width, ld_dw_gate, "dw_gate"),
+            optional(dw_up, gt, inner, width, ld_dw_up, "dw_up"), optional(h, t, rows, inner, ld_h, "h"), rows, width, inner, ld_dh,
+            ld_x, ld_w_gate, ld_w_up, ld_gate, ld_up, ld_dx, ld_dw_gate, ld_dw_up, ld_h, act, dtype, saved, grad_dtype,
+            1 if accumulate else 0, 0))
+    except (struct.error, OverflowError, TypeError) as e:
+        raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    c._keep = (dh, x, x_scale, w_gate, w_up, gate, up, gate_scale, up_scale, dx, dw_gate, dw_up, h)
+    return c
+
+
+def qmuon_gated_ffn_backward_workspace_size(ffn: qmuon_gated_ffn_grad) -> int:
+    return int(lib().qmuon_gated_ffn_backward_workspace_size(C.byref(ffn)))
+
+
+def qmuon_gated_ffn_backward(ffn: qmuon_gated_ffn_grad, ws, ws_bytes: Optional[int] = None, stream=None):
+    where = "qmuon_gated_ffn_backward"
+    st = (_lib_handle or lib()).qmuon_gated_ffn_backward(C.byref(ffn), _on_gpu(ws, where, "ws"),
+                                                         _nbytes(ws) if ws_bytes is None else int(ws_bytes),
+                                                         _raw_stream() if stream is None and _raw_stream else _stream(stream))
     if st != QMUON_OK:
         raise QmuonError(st, where)

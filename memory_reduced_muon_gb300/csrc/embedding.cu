@@ -1,0 +1,527 @@
+// Token embedding: lookup with scaling, and its gradient by sorted tokens.
+//
+//   out[t] = scale table[tokens[t]]            (zeros for a token outside [0, vocab))
+//   dtable[v] = scale sum over t with tokens[t] = v of dout[t]
+//
+// The lookup moves each row once; the gradient reads dout once and writes every
+// row of dtable once.  Both are bound by DRAM.
+//
+// The gradient's order is fixed: tokens are sorted stably (radix passes of up
+// to 9 bits), so that each row's terms lie one after another in ascending t,
+// and are added in fp32 in that order, kPiece positions at a time.  A piece
+// whose run of a token neither begins before it nor goes on behind it writes
+// its row itself; runs that cross pieces leave fp32 partial sums, which a second
+// kernel adds in the pieces' order.  No atomics touch a result.
+#include <algorithm>
+
+#include "qm_lm.h"
+
+namespace qm {
+namespace lm {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <class Tok>
+__device__ __forceinline__ int64_t token_at(const void* tokens, int64_t t) {
+  return (int64_t) static_cast<const Tok*>(tokens)[t];
+}
+
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
+struct LookupArgs {
+  const void* table;
+  const void* tokens;
+  void* out;
+  int64_t n, vocab, ld_table, ld_out;
+  int32_t cols, bits64;
+  float scale;
+};
+
+// VEC: rows of 16-byte vectors, else single elements.  A row belongs to blockDim.x threads, blockDim.y rows to a CTA.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads) lookup_kernel(LookupArgs A) {
+  constexpr int es = elem_size(DT), K = VEC ? 16 / es : 1;
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  depends_wait();
+  if (t >= A.n) return;
+  const int64_t v = A.bits64 ? token_at<int64_t>(A.tokens, t) : token_at<int32_t>(A.tokens, t);
+  const bool there = v >= 0 && v < A.vocab;
+  const unsigned char* src = static_cast<const unsigned char*>(A.table) + (there ? v : 0) * A.ld_table * es;
+  unsigned char* dst = static_cast<unsigned char*>(A.out) + t * A.ld_out * es;
+  const int n = A.cols / K, step = blockDim.x * gridDim.y;
+  constexpr int U = VEC ? 4 : 8;
+  for (int i0 = blockIdx.y * blockDim.x + threadIdx.x; i0 < n; i0 += U * step) {
+    if constexpr (VEC) {
+      uint4 w[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * step;
+        w[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < n && there) w[j] = *reinterpret_cast<const uint4*>(src + 16 * (int64_t)i);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * step;
+        if (i >= n) break;
+        float2 f[Vec16<DT>::kPairs];
+        Vec16<DT>::unpack(w[j], f);
+#pragma unroll
+        for (int k = 0; k < Vec16<DT>::kPairs; ++k) f[k] = there ? mul2_rn(f[k], A.scale) : make_float2(0.0f, 0.0f);
+        *reinterpret_cast<uint4*>(dst + 16 * (int64_t)i) = Vec16<DT>::pack(f);
+      }
+    } else {
+      float f[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * step;
+        f[j] = i < n && there ? load_elem<DT>(src, i) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * step;
+        if (i < n) store_elem<DT>(dst, i, there ? __fmul_rn(f[j], A.scale) : 0.0f);
+      }
+    }
+  }
+}
+
+// Threads of a row, in x, and rows of a CTA, in y: up to `each` items per thread.
+dim3 row_block(int64_t items, int each) {
+  int x = 32;
+  while (x < kThreads && (int64_t)x * each < items) x *= 2;
+  return dim3(x, kThreads / x);
+}
+
+template <int DT>
+cudaError_t launch_lookup(const LookupArgs& A, int sms, cudaStream_t s) {
+  const bool vec = vec_class(A.table, A.ld_table, elem_size(DT)) && vec_class(A.out, A.ld_out, elem_size(DT)) &&
+                   A.cols * elem_size(DT) % 16 == 0;
+  const int64_t items = vec ? A.cols * elem_size(DT) / 16 : A.cols;
+  const dim3 block = row_block(items, vec ? 4 : 8);
+  const int64_t rows = ceil_div(A.n, block.y);
+  // few rows: several CTAs to each, so that one token's row is not one SM's work
+  const int64_t most = ceil_div(items, block.x);
+  const unsigned parts = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, sms / rows));
+  const dim3 grid((unsigned)rows, parts);
+  return vec ? launch_dependent(lookup_kernel<DT, true>, grid, block, 0, s, A)
+             : launch_dependent(lookup_kernel<DT, false>, grid, block, 0, s, A);
+}
+
+// ---------------------------------------------------------------------------
+// sorting
+// ---------------------------------------------------------------------------
+// Keys are tokens, `vocab` standing for every token outside; a key's bits are
+// sorted from the low ones up, up to 9 a pass.  A CTA takes kSortKeys keys, its
+// warps 256 each in eight rounds of 32, so that a warp's keys are ranked in
+// order: lanes of equal digits find one another by match, the lowest of them
+// adds their number to the warp's count.
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRounds = 8, kSortKeys = kSortThreads * kRounds;
+
+struct SortArgs {
+  const void* tokens;    // first pass, or null
+  const uint2* in;       // (key, position) pairs of the pass before, or null
+  uint2* out;
+  uint32_t* counts;      // [kDigits][CTAs]: the CTAs' digits
+  uint8_t* present;      // [vocab] or null: first pass marks the tokens that occur
+  int64_t n, vocab;
+  int32_t bits64, shift, n_cta;
+};
+
+__device__ __forceinline__ uint2 key_of(const SortArgs& A, int64_t i) {
+  if (A.in) return A.in[i];
+  const int64_t v = A.bits64 ? token_at<int64_t>(A.tokens, i) : token_at<int32_t>(A.tokens, i);
+  return make_uint2(v >= 0 && v < A.vocab ? (uint32_t)v : (uint32_t)A.vocab, (uint32_t)i);
+}
+
+__global__ void __launch_bounds__(kSortThreads) count_kernel(SortArgs A) {
+  __shared__ uint32_t count[kDigits];
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
+  __syncthreads();
+  depends_wait();
+  const int64_t base = (int64_t)blockIdx.x * kSortKeys;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = base + r * kSortThreads + threadIdx.x;
+    if (i < A.n) {
+      const uint32_t key = key_of(A, i).x;
+      atomicAdd(&count[(key >> A.shift) & (kDigits - 1)], 1u);
+      if (A.present && key < (uint32_t)A.vocab) A.present[key] = 1;
+    }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) A.counts[(int64_t)d * A.n_cta + blockIdx.x] = count[d];
+}
+
+// Where each CTA's keys of each digit go: an exclusive sum over digits, then CTAs.  One CTA; a thread per digit.
+__global__ void __launch_bounds__(kDigits) offsets_kernel(uint32_t* counts, int n_cta) {
+  __shared__ uint32_t warp_sum[kDigits / 32];
+  depends_wait();
+  uint32_t* mine = counts + (int64_t)threadIdx.x * n_cta;
+  uint32_t total = 0;
+  for (int c = 0; c < n_cta; ++c) {
+    const uint32_t k = mine[c];
+    mine[c] = total;
+    total += k;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = total;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  uint32_t before = incl - total;
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  for (int c = 0; c < n_cta; ++c) mine[c] += before;
+}
+
+__global__ void __launch_bounds__(kSortThreads) scatter_kernel(SortArgs A) {
+  __shared__ uint16_t count[kSortWarps][kDigits];   // each warp's digits, then where its first key of the digit goes in the CTA's
+  __shared__ uint32_t base[kDigits];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int d = threadIdx.x; d < kDigits * kSortWarps; d += kSortThreads) (&count[0][0])[d] = 0;
+  __syncthreads();
+  depends_wait();
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) base[d] = A.counts[(int64_t)d * A.n_cta + blockIdx.x];
+  const int64_t first = (int64_t)blockIdx.x * kSortKeys + warp * (32 * kRounds);
+  uint2 kv[kRounds];
+  uint32_t rank[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = first + r * 32 + lane;
+    kv[r] = i < A.n ? key_of(A, i) : make_uint2(0u, 0u);
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const bool valid = first + r * 32 + lane < A.n;
+    const uint32_t digit = valid ? (kv[r].x >> A.shift) & (kDigits - 1) : (uint32_t)kDigits;
+    const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+    const uint32_t below = __popc(peers & ((1u << lane) - 1u));
+    uint32_t old = 0;
+    if (valid) old = count[warp][digit];
+    __syncwarp();
+    if (valid && below == 0) count[warp][digit] = (uint16_t)(old + __popc(peers));
+    __syncwarp();
+    rank[r] = old + below;
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) {
+    uint32_t sum = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t k = count[w][d];
+      count[w][d] = (uint16_t)sum;
+      sum += k;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    if (first + r * 32 + lane < A.n) {
+      const uint32_t digit = (kv[r].x >> A.shift) & (kDigits - 1);
+      A.out[base[digit] + count[warp][digit] + rank[r]] = kv[r];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// sums
+// ---------------------------------------------------------------------------
+constexpr int kPiece = 32;   // sorted positions of a piece
+
+struct SumArgs {
+  const uint2* sorted;
+  const void* dout;
+  void* dtable;
+  float* partial;        // [pieces][2][ldp]: a run that began before the piece, and one that goes on behind it
+  const uint8_t* present;
+  int64_t n, vocab, ld_dout, ld_dtable, ldp;
+  int32_t cols, pieces, accumulate;
+  float scale;
+};
+
+// N columns of a row as fp32, and back: 16-byte vectors (of the 16-bit type, or of fp32) or single elements.
+template <int DT, int N>
+__device__ __forceinline__ void load_cols(const void* base, int64_t e, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = load_elem<DT>(base, e);
+  } else {
+#pragma unroll
+    for (int h = 0; h < N * elem_size(DT) / 16; ++h) {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + e * elem_size(DT) + 16 * h);
+      float2 f[Vec16<DT>::kPairs];
+      Vec16<DT>::unpack(w, f);
+#pragma unroll
+      for (int k = 0; k < Vec16<DT>::kPairs; ++k) {
+        v[h * Vec16<DT>::kElems + 2 * k] = f[k].x;
+        v[h * Vec16<DT>::kElems + 2 * k + 1] = f[k].y;
+      }
+    }
+  }
+}
+template <int DT, int N>
+__device__ __forceinline__ void store_cols(void* base, int64_t e, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    store_elem<DT>(base, e, v[0]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < N * elem_size(DT) / 16; ++h) {
+      float2 f[Vec16<DT>::kPairs];
+#pragma unroll
+      for (int k = 0; k < Vec16<DT>::kPairs; ++k)
+        f[k] = make_float2(v[h * Vec16<DT>::kElems + 2 * k], v[h * Vec16<DT>::kElems + 2 * k + 1]);
+      *reinterpret_cast<uint4*>(static_cast<unsigned char*>(base) + e * elem_size(DT) + 16 * h) = Vec16<DT>::pack(f);
+    }
+  }
+}
+
+template <int GT, int N>
+__device__ __forceinline__ void write_row(const SumArgs& A, int64_t row, int64_t col, const float (&sum)[N]) {
+  const int64_t e = row * A.ld_dtable + col;
+  float v[N];
+  if (A.accumulate) {
+    load_cols<GT, N>(A.dtable, e, v);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = fmaf(A.scale, sum[k], v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __fmul_rn(A.scale, sum[k]);
+  }
+  store_cols<GT, N>(A.dtable, e, v);
+}
+
+// CTA (piece, slab of columns): a thread's N columns over the piece's positions; behind the pieces, CTAs that write the
+// zeros of the rows without a token.
+template <int DT, int GT, int N>
+__global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs A) {
+  const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
+  depends_wait();
+  if ((int64_t)blockIdx.x >= A.pieces) {
+    if (col >= A.cols) return;
+    float zero[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) zero[k] = 0.0f;
+    const int64_t r0 = ((int64_t)blockIdx.x - A.pieces) * kPiece;
+    for (int64_t r = r0; r < r0 + kPiece && r < A.vocab; ++r)
+      if (!A.present[r]) store_cols<GT, N>(A.dtable, r * A.ld_dtable + col, zero);
+    return;
+  }
+  __shared__ uint2 mine[kPiece + 2];   // the neighbours' keys at both ends
+  const int64_t i0 = (int64_t)blockIdx.x * kPiece;
+  const int n = (int)(A.n - i0 < kPiece ? A.n - i0 : kPiece);
+  if (threadIdx.x < n + 2) {
+    const int64_t i = i0 - 1 + threadIdx.x;
+    mine[threadIdx.x] = i >= 0 && i < A.n ? A.sorted[i] : make_uint2(0xFFFFFFFFu, 0u);
+  }
+  __syncthreads();
+  if (col >= A.cols) return;
+  float sum[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+  bool before = mine[0].x == mine[1].x;   // the run began in an earlier piece
+  constexpr int U = 8;                    // rows in flight
+  for (int j0 = 0; j0 < n; j0 += U) {
+    float v[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j0 + u < n && mine[j0 + u + 1].x < (uint32_t)A.vocab) {
+        load_cols<DT, N>(A.dout, (int64_t)mine[j0 + u + 1].y * A.ld_dout + col, v[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[u][k] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u;
+      if (j >= n) break;
+      const uint32_t key = mine[j + 1].x;
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum[k] += v[u][k];
+      const bool ends = mine[j + 2].x != key;
+      if (!ends && j + 1 < n) continue;
+      if (key < (uint32_t)A.vocab) {
+        if (!before && ends) {
+          write_row<GT, N>(A, key, col, sum);
+        } else {
+          // slot 0: the run began before this piece (and may go on); slot 1: it begins here and goes on
+          float* p = A.partial + ((int64_t)blockIdx.x * 2 + (before ? 0 : 1)) * A.ldp + col;
+          store_cols<QMUON_FP32, N>(p, 0, sum);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+      before = false;
+    }
+  }
+}
+
+// The runs that cross pieces: CTA (piece, slab) adds up the run that begins in its piece and goes on behind it.  The
+// pieces' sums are added in four interleaved chains (piece j in chain j mod 4), then the chains in order.
+template <int GT, int N>
+__global__ void __launch_bounds__(kThreads) join_kernel(SumArgs A) {
+  const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
+  depends_wait();
+  const int64_t p = blockIdx.x, last = (p + 1) * kPiece - 1;
+  if (last + 1 >= A.n || col >= A.cols) return;
+  const uint32_t key = A.sorted[last].x;
+  if (key >= (uint32_t)A.vocab || A.sorted[last + 1].x != key) return;
+  if (A.sorted[p * kPiece].x == key && p > 0 && A.sorted[p * kPiece - 1].x == key) return;   // it began before
+  // the last piece that the run reaches: it holds whole pieces up to there
+  int64_t lo = p + 1, hi = A.pieces;   // first piece in [lo, hi) whose first key differs
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (A.sorted[mid * kPiece].x == key) lo = mid + 1;
+    else hi = mid;
+  }
+  float chain[4][N];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int k = 0; k < N; ++k) chain[c][k] = 0.0f;
+  load_cols<QMUON_FP32, N>(A.partial, (p * 2 + 1) * A.ldp + col, chain[0]);
+  for (int64_t j = p + 1; j < lo; j += 4) {
+    float v[4][N];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (j + c < lo) {
+        load_cols<QMUON_FP32, N>(A.partial, (j + c) * 2 * A.ldp + col, v[c]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[c][k] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int k = 0; k < N; ++k) chain[c][k] += v[c][k];
+  }
+  float sum[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum[k] = (chain[0][k] + chain[1][k]) + (chain[2][k] + chain[3][k]);
+  write_row<GT, N>(A, key, col, sum);
+}
+
+struct Layout {
+  int passes, n_cta, pieces;
+  size_t pairs[2], counts, present, partial, total;
+  int64_t ldp;
+};
+
+Layout layout_of(int64_t n, int64_t vocab, int64_t cols) {
+  Layout L{};
+  L.passes = 1;
+  while (L.passes * kDigitBits < 32 && (vocab >> (L.passes * kDigitBits)) != 0) ++L.passes;   // keys 0 .. vocab
+  L.n_cta = (int)ceil_div(n, kSortKeys);
+  L.pieces = (int)ceil_div(n, kPiece);
+  L.ldp = (int64_t)round_up((size_t)cols, 8);
+  size_t at = 0;
+  for (size_t& p : L.pairs) p = at, at += round_up((size_t)n * 8, 256);
+  L.counts = at, at += round_up((size_t)kDigits * L.n_cta * 4, 256);
+  L.present = at, at += round_up((size_t)vocab, 256);
+  L.partial = at, at += round_up((size_t)L.pieces * 2 * L.ldp * 4, 256);
+  L.total = at;
+  return L;
+}
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 28, kMaxVocab = ((int64_t)1 << 31) - 2, kMaxCols = (int64_t)1 << 22;
+
+bool sizes_ok(int64_t n, int64_t vocab, int64_t cols) {
+  return n >= 0 && n <= kMaxTokens && vocab >= 1 && vocab <= kMaxVocab && cols >= 1 && cols <= kMaxCols &&
+         vocab <= ((int64_t)1 << 40) / cols;
+}
+bool rows_ok(const void* p, int64_t ld, int64_t cols, int es) {
+  return p && is_aligned(p, es) && ld >= cols && ld <= ((int64_t)1 << 40);
+}
+bool is_type(int dt) { return dt == QMUON_BF16 || dt == QMUON_FP16 || dt == QMUON_FP32; }
+bool tokens_ok(const void* p, int bits) { return p && (bits == 32 || bits == 64) && is_aligned(p, bits / 8); }
+
+template <int DT, int GT, int N>
+cudaError_t launch_sums(const SumArgs& A, cudaStream_t s) {
+  const unsigned slabs = (unsigned)ceil_div(A.cols, (int64_t)kThreads * N);
+  const int64_t zeros = A.accumulate ? 0 : ceil_div(A.vocab, kPiece);
+  const int threads = (int)std::min<int64_t>(kThreads, round_up((size_t)ceil_div(A.cols, N), 32));
+  cudaError_t e = launch_dependent(sum_kernel<DT, GT, N>, dim3((unsigned)(A.pieces + zeros), slabs), dim3(std::max(threads, 64)), 0, s, A);
+  if (e == cudaSuccess && A.pieces > 1) e = launch_dependent(join_kernel<GT, N>, dim3(A.pieces - 1, slabs), dim3(std::max(threads, 64)), 0, s, A);
+  return e;
+}
+template <int DT>
+cudaError_t launch_sums_of(const SumArgs& A, int gt, cudaStream_t s) {
+  const int gs = elem_size(gt);
+  constexpr int K = 16 / elem_size(DT);
+  const bool vec = A.cols % K == 0 && vec_class(A.dout, A.ld_dout, elem_size(DT)) && vec_class(A.dtable, A.ld_dtable, gs);
+  if (gt == QMUON_FP32)
+    return vec ? launch_sums<DT, QMUON_FP32, K>(A, s) : launch_sums<DT, QMUON_FP32, 1>(A, s);
+  return vec ? launch_sums<DT, DT, K>(A, s) : launch_sums<DT, DT, 1>(A, s);
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace qm
+
+using namespace qm;
+using namespace qm::lm;
+
+extern "C" qmuon_status qmuon_embedding_forward(const qmuon_embedding* c, void* stream) {
+  NvtxRange nvtx_range("qmuon_embedding_forward");
+  return no_throw("qmuon_embedding_forward", [&]() -> qmuon_status {
+    if (!c || !sizes_ok(c->n_tokens, c->vocab, c->cols) || !is_type(c->dtype)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (c->n_tokens == 0) return QMUON_OK;
+    const int es = elem_size(c->dtype);
+    if (!tokens_ok(c->tokens, c->token_bits) || !rows_ok(c->table, c->ld_table, c->cols, es) || !rows_ok(c->out, c->ld_out, c->cols, es))
+      return QMUON_ERR_INVALID_ARGUMENT;
+    const int sms = num_sms();
+    if (sms <= 0) return set_error_msg("qmuon_embedding_forward: SM count query failed", QMUON_ERR_CUDA);
+    const LookupArgs A{c->table,  c->tokens,        c->out,                  c->n_tokens, c->vocab, c->ld_table,
+                       c->ld_out, (int32_t)c->cols, c->token_bits == 64, c->scale};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = c->dtype == QMUON_BF16   ? launch_lookup<QMUON_BF16>(A, sms, s)
+                          : c->dtype == QMUON_FP16 ? launch_lookup<QMUON_FP16>(A, sms, s)
+                                                   : launch_lookup<QMUON_FP32>(A, sms, s);
+    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_embedding_forward (launch)", e);
+  });
+}
+
+extern "C" size_t qmuon_embedding_workspace_size(int64_t n_tokens, int64_t vocab, int64_t cols) {
+  return sizes_ok(n_tokens, vocab, cols) ? layout_of(n_tokens, vocab, cols).total : 0;
+}
+
+extern "C" qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* c, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qmuon_embedding_backward");
+  return no_throw("qmuon_embedding_backward", [&]() -> qmuon_status {
+    if (!c || !sizes_ok(c->n_tokens, c->vocab, c->cols) || !is_type(c->dtype)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (c->grad_dtype != c->dtype && c->grad_dtype != QMUON_FP32) return QMUON_ERR_INVALID_ARGUMENT;
+    const int es = elem_size(c->dtype), gs = elem_size(c->grad_dtype);
+    if (!rows_ok(c->dtable, c->ld_dtable, c->cols, gs) || !ws || !is_aligned(ws, 256)) return QMUON_ERR_INVALID_ARGUMENT;
+    if (c->n_tokens > 0 && (!tokens_ok(c->tokens, c->token_bits) || !rows_ok(c->dout, c->ld_dout, c->cols, es)))
+      return QMUON_ERR_INVALID_ARGUMENT;
+    const Layout L = layout_of(c->n_tokens, c->vocab, c->cols);
+    if (ws_bytes < L.total) return QMUON_ERR_WORKSPACE_TOO_SMALL;
+    if (c->n_tokens == 0 && c->accumulate) return QMUON_OK;
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* present = w + L.present;
+    cudaError_t e = cudaSuccess;
+    if (!c->accumulate) e = cudaMemsetAsync(present, 0, (size_t)c->vocab, s);
+    const uint2* sorted = nullptr;
+    for (int p = 0; c->n_tokens > 0 && p < L.passes && e == cudaSuccess; ++p) {
+      SortArgs A{c->tokens, sorted, reinterpret_cast<uint2*>(w + L.pairs[p & 1]), reinterpret_cast<uint32_t*>(w + L.counts),
+                 p == 0 && !c->accumulate ? present : nullptr, c->n_tokens, c->vocab, c->token_bits == 64, p * kDigitBits, L.n_cta};
+      e = launch_dependent(count_kernel, dim3(L.n_cta), dim3(kSortThreads), 0, s, A);
+      if (e == cudaSuccess) e = launch_dependent(offsets_kernel, dim3(1), dim3(kDigits), 0, s, A.counts, L.n_cta);
+      if (e == cudaSuccess) e = launch_dependent(scatter_kernel, dim3(L.n_cta), dim3(kSortThreads), 0, s, A);
+      sorted = A.out;
+    }
+    if (e != cudaSuccess) return set_error("qmuon_embedding_backward (sort)", e);
+    const SumArgs A{sorted, c->dout, c->dtable, reinterpret_cast<float*>(w + L.partial), present, c->n_tokens, c->vocab, c->ld_dout,
+                    c->ld_dtable, L.ldp, (int32_t)c->cols, L.pieces, c->accumulate != 0, c->scale};
+    e = c->dtype == QMUON_BF16   ? launch_sums_of<QMUON_BF16>(A, c->grad_dtype, s)
+        : c->dtype == QMUON_FP16 ? launch_sums_of<QMUON_FP16>(A, c->grad_dtype, s)
+                                 : launch_sums_of<QMUON_FP32>(A, c->grad_dtype, s);
+    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_embedding_backward (launch)", e);
+  });
+}

@@ -1,0 +1,975 @@
+// Gated feed-forward block, forward and backward, on tcgen05 tensor cores.
+//
+//   gate = x Wg^T   up = x Wu^T   h = act(gate) up
+//   dgate = dh up act'(gate)   dup = dh act(gate)
+//   dx = dgate Wg + dup Wu   dWg = dgate^T x   dWu = dup^T x
+//
+// One kernel makes all the products.  A persistent CTA pair (cta_group::2) runs
+// units of work, each a 256 x 256 accumulator over a range of K: in the forward
+// product 256 rows by 128 columns of gate and the same 128 of up (one CTA of the
+// pair brings the rows of Wg, the other those of Wu), so that a thread of the
+// epilogue holds both and the activation, the product and the 8-bit codes need
+// nothing from memory; in the gradients 256 x 256 of dx, dWg or dWu.  The
+// operands are read where they lie: K-major for x W^T, MN-major for the weights
+// in dx and for both operands in dW, as the instruction descriptor says.
+//
+// The gradients dgate and dup are rounded to the type of the activations before
+// the products that read them (tensor cores take 16-bit operands of one type);
+// each rounding is 2^-9 (bf16) or 2^-12 (fp16) of a term on average, which the
+// sums over many terms bring below that of the result's own rounding.
+//
+// Few tiles: the K range is split over units, whose fp32 partial sums go
+// through the workspace and a second kernel that adds them in order.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+
+#include "qm_lm.h"
+#include "qm_tc.h"
+
+namespace qm {
+namespace lm {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 256, kBK = 64;
+constexpr int kInnerTile = 128;                    // columns of gate, and of up, in a forward tile
+constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter
+constexpr int kThreads = 64 + 32 * kEpiWarps;      // warp 0 TMA, warp 1 MMA, warps 2.. epilogue
+constexpr int kStages = 7;
+constexpr uint32_t kStageBytes = 4 * kBox;         // per CTA: 128 x 64 of A, 128 x 64 of B
+constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
+static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
+constexpr int kGroupM = 8;                         // tile rows that run side by side
+
+enum { K_FWD = 0, K_BWD = 1, K_GRAD = 2 };
+
+// ---------------------------------------------------------------------------
+// activations
+// ---------------------------------------------------------------------------
+// The logistic function; 0 and 1 at the ends, NaN for NaN.
+__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float g) {
+  if constexpr (ACT == QMUON_ACT_SILU) {
+    return g * logistic(g);
+  } else if constexpr (ACT == QMUON_ACT_GELU) {
+    return g * (0.5f * erfcf(g * -0.70710678f));
+  } else {   // 0.5 (1 + tanh z) = logistic(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3)
+    return g * logistic(1.5957691f * g * fmaf(0.044715f * g, g, 1.0f));
+  }
+}
+// The activation and its derivative.
+template <int ACT>
+__device__ __forceinline__ float2 act_and_slope(float g) {
+  if constexpr (ACT == QMUON_ACT_SILU) {
+    const float s = logistic(g);
+    return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
+  } else if constexpr (ACT == QMUON_ACT_GELU) {
+    const float cdf = 0.5f * erfcf(g * -0.70710678f);
+    return make_float2(g * cdf, fmaf(g, 0.39894228f * __expf(-0.5f * g * g), cdf));
+  } else {
+    const float s = logistic(1.5957691f * g * fmaf(0.044715f * g, g, 1.0f));
+    // beyond +-16 the slope is 0 or 1 in fp32; there the polynomial may overflow where s (1 - s) is zero
+    const float c = g > 16.0f ? 16.0f : g < -16.0f ? -16.0f : g;
+    return make_float2(g * s, fmaf(c * (s * (1.0f - s)), 1.5957691f * fmaf(0.134145f * c, c, 1.0f), s));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel's arguments and units of work
+// ---------------------------------------------------------------------------
+struct GemmArgs {
+  CUtensorMap a[2];          // forward: x; gradients: dgate, dup
+  CUtensorMap b[3];          // Wg, Wu, x (gradients)
+  int64_t rows, width, inner;
+  // forward: `tiles` x `splits` units.  Gradients: units of dx (first), then of dWg and dWu
+  int32_t tiles_m, tiles_n, splits;            // forward, or dx
+  int32_t tiles_wm, tiles_wn, splits_w;        // dW: tile rows of one weight, tile columns, splits
+  int32_t units, units_w;                      // of the first kind, of dW
+  int32_t rounds_w, few_w;                     // dW units: rounds over all pairs, then those for pairs with one dx unit less
+  // forward
+  void *h, *gate, *up;
+  uint8_t *gate_scale, *up_scale;
+  int64_t ld_h, ld_gate, ld_up;
+  const void* dh;            // backward
+  int64_t ld_dh;
+  void *dgate, *dup;
+  int64_t ld_d;
+  // gradients
+  void *dx, *dw[2];
+  int64_t ld_dx, ld_dw[2];
+  float* part;               // partial sums of the forward or of dx, or null; ld_part apart
+  float* part_w;             // of dW
+  int64_t ld_part;
+  int32_t vec_h, vec_gate, vec_up, vec_dh, vec_dx, vec_dw[2];
+  int32_t act, saved, dw_f32, accumulate;
+  WsHeader* hdr;
+};
+
+struct Unit {
+  int32_t kind;          // 0: the forward or dx, 1: dWg, 2: dWu
+  int32_t m0, n0;        // tile's first row and column
+  int32_t kb0, kb1;      // K blocks
+  int32_t split;
+};
+
+__device__ __forceinline__ void raster(int tile, int tiles_m, int tiles_n, int* tm, int* tn) {
+  const int per = kGroupM * tiles_n, g = tile / per, r = tile - g * per;
+  const int gm = tiles_m - g * kGroupM < kGroupM ? tiles_m - g * kGroupM : kGroupM;
+  *tn = r / gm;
+  *tm = g * kGroupM + (r - *tn * gm);
+}
+
+__device__ __forceinline__ int blocks_of(int64_t k) { return (int)((k + kBK - 1) / kBK); }
+
+// The i-th unit of CTA pair `pair` out of `pairs`; false behind its last one.
+template <int KIND>
+__device__ __forceinline__ bool unit_at(const GemmArgs& A, int pair, int pairs, int i, Unit* u) {
+  const int64_t first = (int64_t)i * pairs + pair;
+  int tm, tn;
+  if (KIND != K_GRAD || first < A.units) {
+    if (first >= A.units) return false;
+    const int tile = (int)first / A.splits;
+    u->split = (int)first - tile * A.splits;
+    raster(tile, A.tiles_m, A.tiles_n, &tm, &tn);
+    u->kind = 0;
+    u->m0 = tm * kTile;
+    u->n0 = tn * (KIND == K_GRAD ? kTile : kInnerTile);
+    const int kb = KIND == K_GRAD ? 2 * blocks_of(A.inner) : blocks_of(A.width);
+    u->kb0 = (int)((int64_t)kb * u->split / A.splits);
+    u->kb1 = (int)((int64_t)kb * (u->split + 1) / A.splits);
+    return true;
+  }
+  if (KIND == K_GRAD) {
+    // dW units: whole rounds, then the share of the pairs that have one unit of dx less, then one more at most
+    const int extra = A.units % pairs;                       // pairs [0, extra) have one unit of dx more
+    const int done = A.units / pairs + (pair < extra ? 1 : 0);
+    int j = i - done;
+    int64_t w;
+    if (j < A.rounds_w) {
+      w = (int64_t)j * pairs + pair;
+    } else {
+      j -= A.rounds_w;
+      const int few = pairs - extra;
+      const int64_t base = (int64_t)A.rounds_w * pairs;
+      if (pair >= extra && j < A.few_w) {
+        w = base + (int64_t)j * few + (pair - extra);
+      } else {
+        if (pair >= extra) j -= A.few_w;
+        w = base + (int64_t)A.few_w * few + (int64_t)j * pairs + pair;
+      }
+    }
+    if (w >= A.units_w) return false;
+    const int tile = (int)w / A.splits_w;
+    u->split = (int)w - tile * A.splits_w;
+    raster(tile, 2 * A.tiles_wm, A.tiles_wn, &tm, &tn);
+    const int second = tm >= A.tiles_wm;
+    u->kind = 1 + second;
+    u->m0 = (tm - (second ? A.tiles_wm : 0)) * kTile;
+    u->n0 = tn * kTile;
+    const int kb = blocks_of(A.rows);
+    u->kb0 = (int)((int64_t)kb * u->split / A.splits_w);
+    u->kb1 = (int)((int64_t)kb * (u->split + 1) / A.splits_w);
+    return true;
+  }
+  return false;
+}
+
+// kind::f16: fp32 accumulator, A and B bf16 or fp16, M = 256, N = 256.
+template <int DT>
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn) {
+  constexpr uint32_t type = DT == QMUON_BF16 ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+// A thread's 32 columns of gate and up: what the forward stores.
+template <int DT, int ACT>
+__device__ __forceinline__ void finish_forward(const GemmArgs& A, int64_t r, int64_t c, const float (&g)[32], const float (&u)[32]) {
+  constexpr int es = elem_size(DT);
+  const int n = (int)(A.inner - c < 32 ? A.inner - c : 32);
+  float h[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) h[i] = act_of<ACT>(g[i]) * u[i];
+  store_row32<DT>(static_cast<unsigned char*>(A.h) + (r * A.ld_h + c) * es, n, A.vec_h, h);
+  if (A.saved == QMUON_SAVE_SAME) {
+    store_row32<DT>(static_cast<unsigned char*>(A.gate) + (r * A.ld_gate + c) * es, n, A.vec_gate, g);
+    store_row32<DT>(static_cast<unsigned char*>(A.up) + (r * A.ld_up + c) * es, n, A.vec_up, u);
+  } else if (A.saved == QMUON_SAVE_MXFP8) {
+    const int64_t b = (r * A.inner + c) >> 5;
+    A.gate_scale[b] = (uint8_t)encode_row32(static_cast<uint8_t*>(A.gate) + 32 * b, A.vec_gate, g);
+    A.up_scale[b] = (uint8_t)encode_row32(static_cast<uint8_t*>(A.up) + 32 * b, A.vec_up, u);
+  }
+}
+// The same of the backward pass: dgate and dup for the products, and h again.
+template <int DT, int ACT>
+__device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, int64_t c, const float (&g)[32], const float (&u)[32],
+                                                const uint32_t (&dh)[16]) {
+  constexpr int es = elem_size(DT);
+  const int n = (int)(A.inner - c < 32 ? A.inner - c : 32);
+  float h[32], dg[32], du[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float2 a = act_and_slope<ACT>(g[i]), d = unpack2<DT>(dh[i >> 1]);
+    const float x = i & 1 ? d.y : d.x;
+    h[i] = a.x * u[i];
+    dg[i] = x * u[i] * a.y;
+    du[i] = x * a.x;
+  }
+  // the workspace's rows are padded to 32 bytes: vectors wherever all 32 columns exist
+  store_row32<DT>(static_cast<unsigned char*>(A.dgate) + (r * A.ld_d + c) * es, n, 2, dg);
+  store_row32<DT>(static_cast<unsigned char*>(A.dup) + (r * A.ld_d + c) * es, n, 2, du);
+  if (A.h) store_row32<DT>(static_cast<unsigned char*>(A.h) + (r * A.ld_h + c) * es, n, A.vec_h, h);
+}
+
+template <int KIND, int DT, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ GemmArgs A) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
+  const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);   // one arrival per epilogue warp of the pair
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_cg<2>(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_cg<2>();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();   // the peer's barriers exist before anyone signals them
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  depends_wait();
+  const uint32_t tmem = *tmem_slot;
+  const int inner_blocks = KIND == K_GRAD ? blocks_of(A.inner) : 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- TMA producer: every CTA loads its own halves of the operands ----
+      const uint32_t full_l = cluster_map(full0, 0);   // the leader's barriers
+      int it = 0;
+      bool ok = true;
+      Unit u;
+      for (int i = 0; ok && unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+        const bool dx = KIND == K_GRAD && u.kind == 0, dw = KIND == K_GRAD && u.kind > 0;
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          const int s = it % kStages, round = it / kStages;
+          if (round > 0 && !mbar_wait(empty0 + 8 * s, (round - 1) & 1, A.hdr, 0x2100u | KIND)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_expect_tx(full0 + 8 * s, 2 * kStageBytes);
+          const uint32_t bar = full_l + 8 * s;
+          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + 2 * kBox;
+          // dx runs over the columns of dgate, then over those of dup
+          const int seg = dx && kb >= inner_blocks ? 1 : 0;
+          const int k0 = (kb - seg * inner_blocks) * kBK;
+          const CUtensorMap* ma = &A.a[dw ? u.kind - 1 : seg];
+          const CUtensorMap* mb = &A.b[KIND != K_GRAD ? rank : dw ? 2 : seg];
+          const int am = u.m0 + 128 * rank, bn = KIND != K_GRAD ? u.n0 : u.n0 + 128 * rank;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (dw) tma_load_2d_pair(sa + j * kBox, ma, bar, am + 64 * j, k0);
+            else tma_load_2d_pair(sa + j * kBox, ma, bar, k0, am + 64 * j);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (KIND == K_GRAD) tma_load_2d_pair(sb + j * kBox, mb, bar, bn + 64 * j, k0);
+            else tma_load_2d_pair(sb + j * kBox, mb, bar, k0, bn + 64 * j);
+          }
+        }
+      }
+      // every load issued has landed before the CTA may exit (the leader's
+      // full barriers also count the peer's loads)
+      if (leader)
+        for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
+          mbar_wait(full0 + 8 * (k % kStages), (k / kStages) & 1, A.hdr, 0x2200u | KIND);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---- MMA issuer ----
+      int it = 0;
+      bool ok = true;
+      Unit u;
+      for (int i = 0; ok && unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+        const int acc = i & 1, use = i >> 1;
+        if (use > 0 && !mbar_wait(tempty0 + 8 * acc, (use - 1) & 1, A.hdr, 0x2500u | KIND)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * kTile);
+        const bool amn = KIND == K_GRAD && u.kind > 0, bmn = KIND == K_GRAD;
+        const uint32_t idesc = instr_desc<DT>(amn, bmn);
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          const int s = it % kStages, round = it / kStages;
+          if (!mbar_wait(full0 + 8 * s, round & 1, A.hdr, 0x2300u | KIND)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + 2 * kBox;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            const uint64_t ad = amn ? desc_mnmajor(sa, kk) : desc_kmajor(sa, kk);
+            const uint64_t bd = bmn ? desc_mnmajor(sb, kk) : desc_kmajor(sb, kk);
+            mma_bf16_cg<2>(d, ad, bd, idesc, (kb > u.kb0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit_cg<2>(empty0 + 8 * s);
+        }
+        mma_commit_cg<2>(tfull0 + 8 * acc);   // accumulator ready (also on the error path)
+      }
+    }
+  } else {
+    // ---- epilogue: warps 2..9; TMEM lane quarter = warp % 4 ----
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty_l = cluster_map(tempty0, 0);
+    Unit u;
+    for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+      const int64_t r = u.m0 + 128 * rank + quarter * 32 + lane;
+      const int acc = i & 1, use = i >> 1;
+      const int64_t c0 = KIND != K_GRAD ? u.n0 + 64 * half : u.n0 + 128 * half;   // this warp's first column
+      uint32_t dh[KIND == K_BWD ? 2 : 1][16];
+      if (KIND == K_BWD && !A.part) {   // while the tensor cores work
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int64_t c = c0 + 32 * j;
+          const int n = r < A.rows && c < A.inner ? (int)(A.inner - c < 32 ? A.inner - c : 32) : 0;
+          load_words32(static_cast<const unsigned char*>(A.dh) + (n ? (r * A.ld_dh + c) * elem_size(DT) : 0), n, A.vec_dh, dh[j]);
+        }
+      }
+      bool ok = mbar_wait(tfull0 + 8 * acc, use & 1, A.hdr, 0x2400u | KIND);
+      tc_fence_after();
+      ok = ok && *reinterpret_cast<volatile unsigned*>(&A.hdr->error) == 0u;
+      if (!__all_sync(0xffffffffu, ok)) break;   // tcgen05.ld is warp-collective
+      const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
+      auto release = [&] {   // every TMEM read of this accumulator by this warp is done
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_l + 8 * acc);
+      };
+      if (KIND != K_GRAD) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t gv[32], uv[32];
+          __syncwarp();   // lanes without a row rejoin: tcgen05.ld is warp-collective
+          tmem_ld32_async(t + (uint32_t)(64 * half + 32 * j), gv);
+          tmem_ld32_async(t + (uint32_t)(kInnerTile + 64 * half + 32 * j), uv);
+          tmem_wait_ld();
+          tmem_hold(gv);
+          tmem_hold(uv);
+          if (j == 1) release();
+          float g[32], v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) g[k] = __uint_as_float(gv[k]), v[k] = __uint_as_float(uv[k]);
+          const int64_t c = c0 + 32 * j;
+          if (r >= A.rows || c >= A.inner) continue;
+          if (A.part) {   // [split][gate, up][rows][ld_part]
+            const int n = (int)(A.ld_part - c < 32 ? A.ld_part - c : 32);
+            float* p = A.part + (((int64_t)u.split * 2) * A.rows + r) * A.ld_part + c;
+            store_row32<QMUON_FP32>(p, n, 2, g);
+            store_row32<QMUON_FP32>(p + A.rows * A.ld_part, n, 2, v);
+          } else if constexpr (KIND == K_FWD) {
+            finish_forward<DT, ACT>(A, r, c, g, v);
+          } else if constexpr (KIND == K_BWD) {
+            finish_backward<DT, ACT>(A, r, c, g, v, dh[j]);
+          }
+        }
+      } else {
+        const int64_t rows = u.kind == 0 ? A.rows : A.inner;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t av[32];
+          __syncwarp();
+          tmem_ld32(t + (uint32_t)(128 * half + 32 * j), av);
+          if (j == 3) release();
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(av[k]);
+          const int64_t c = c0 + 32 * j;
+          if (r >= rows || c >= A.width) continue;
+          const int n = (int)(A.width - c < 32 ? A.width - c : 32);
+          float* part = u.kind == 0 ? A.part : A.part_w;
+          if (part) {   // dx: [split][rows][ld_part]; dW: [weight][split][inner][ld_part]
+            const int64_t slice = u.kind == 0 ? u.split : (int64_t)(u.kind - 1) * A.splits_w + u.split;
+            const int np = (int)(A.ld_part - c < 32 ? A.ld_part - c : 32);
+            store_row32<QMUON_FP32>(part + (slice * rows + r) * A.ld_part + c, np, 2, v);
+          } else if (u.kind == 0) {
+            store_row32<DT>(static_cast<unsigned char*>(A.dx) + (r * A.ld_dx + c) * elem_size(DT), n, A.vec_dx, v);
+          } else {
+            const int w = u.kind - 1;
+            unsigned char* p = static_cast<unsigned char*>(A.dw[w]) + (r * A.ld_dw[w] + c) * (A.dw_f32 ? 4 : elem_size(DT));
+            if (A.accumulate) {
+              float old[32];
+              if (A.dw_f32) load_row32<QMUON_FP32>(p, n, A.vec_dw[w], old);
+              else load_row32<DT>(p, n, A.vec_dw[w], old);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] += old[k];
+            }
+            if (A.dw_f32) store_row32<QMUON_FP32>(p, n, A.vec_dw[w], v);
+            else store_row32<DT>(p, n, A.vec_dw[w], v);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown: every accumulator read is done and the peer no longer
+  // touches this CTA's barriers or shared memory ----
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<2>(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// element by element: gate and up from partial sums, from their 16-bit copies
+// or from their carriers
+// ---------------------------------------------------------------------------
+constexpr int kElemThreads = 256;
+enum { FROM_PART = 0, FROM_SAME = 1, FROM_MXFP8 = 2 };
+
+struct ElemArgs {
+  GemmArgs A;            // outputs, dh, sizes
+  const float* part;     // [splits][gate, up][rows][ld_part]
+  int32_t splits;
+  const void *gate, *up; // FROM_SAME and FROM_MXFP8
+  const uint8_t *gate_scale, *up_scale;
+  int64_t ld_gate, ld_up;
+  int32_t vec_in;        // rows of gate and up
+};
+
+// A thread takes 32 columns of a row, as a thread of the product's epilogue does.
+template <int DT, int ACT, int FROM, bool BWD>
+__global__ void __launch_bounds__(kElemThreads) elem_kernel(const __grid_constant__ ElemArgs E) {
+  const GemmArgs& A = E.A;
+  constexpr int es = elem_size(DT);
+  const int64_t per = (A.inner + 31) >> 5, i = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
+  depends_wait();
+  if (i >= A.rows * per) return;
+  const int64_t r = i / per, c = (i - r * per) * 32;
+  const int n = (int)(A.inner - c < 32 ? A.inner - c : 32);
+  float g[32], u[32];
+  if constexpr (FROM == FROM_PART) {
+    const int np = (int)(A.ld_part - c < 32 ? A.ld_part - c : 32);
+    const float* p = E.part + r * A.ld_part + c;
+    load_row32<QMUON_FP32>(p, np, 2, g);
+    load_row32<QMUON_FP32>(p + A.rows * A.ld_part, np, 2, u);
+    for (int s = 1; s < E.splits; ++s) {
+      p += 2 * A.rows * A.ld_part;
+      float a[32], b[32];
+      load_row32<QMUON_FP32>(p, np, 2, a);
+      load_row32<QMUON_FP32>(p + A.rows * A.ld_part, np, 2, b);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) g[k] += a[k], u[k] += b[k];
+    }
+  } else if constexpr (FROM == FROM_SAME) {
+    load_row32<DT>(static_cast<const unsigned char*>(E.gate) + (r * E.ld_gate + c) * es, n, E.vec_in, g);
+    load_row32<DT>(static_cast<const unsigned char*>(E.up) + (r * E.ld_up + c) * es, n, E.vec_in, u);
+  } else {
+    const int64_t b = (r * A.inner + c) >> 5;
+    auto decode = [&](const void* codes, const uint8_t* scale, float (&v)[32]) {
+      const uint8_t* p = static_cast<const uint8_t*>(codes) + 32 * b;
+      uint32_t w[8];
+      if (E.vec_in == 2) {
+        load32b(p, w);
+      } else {
+        const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 16);
+        w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+      }
+      const float s = scale_of_e8m0(scale[b]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 x = mul2_rn(e4m3x2_to(w[k] & 0xFFFFu), s), y = mul2_rn(e4m3x2_to(w[k] >> 16), s);
+        v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = y.x, v[4 * k + 3] = y.y;
+      }
+    };
+    decode(E.gate, E.gate_scale, g);
+    decode(E.up, E.up_scale, u);
+  }
+  if constexpr (BWD) {
+    uint32_t dh[16];
+    load_words32(static_cast<const unsigned char*>(A.dh) + (r * A.ld_dh + c) * es, n, A.vec_dh, dh);
+    finish_backward<DT, ACT>(A, r, c, g, u, dh);
+  } else {
+    finish_forward<DT, ACT>(A, r, c, g, u);
+  }
+}
+
+// Sums of split products: rows x cols of [splits][rows][ld_part] to the type of the result.
+template <int DT>
+__global__ void __launch_bounds__(kElemThreads) join_kernel(const float* part, int splits, int64_t rows, int64_t cols, int64_t ld_part,
+                                                            void* out, int64_t ld, int vec, int accumulate) {
+  const int64_t per = (cols + 31) >> 5, i = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
+  depends_wait();
+  if (i >= rows * per) return;
+  const int64_t r = i / per, c = (i - r * per) * 32;
+  const int n = (int)(cols - c < 32 ? cols - c : 32), np = (int)(ld_part - c < 32 ? ld_part - c : 32);
+  const float* p = part + r * ld_part + c;
+  float v[32];
+  load_row32<QMUON_FP32>(p, np, 2, v);
+  for (int s = 1; s < splits; ++s) {
+    p += rows * ld_part;
+    float a[32];
+    load_row32<QMUON_FP32>(p, np, 2, a);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] += a[k];
+  }
+  unsigned char* o = static_cast<unsigned char*>(out) + (r * ld + c) * elem_size(DT);
+  if (accumulate) {
+    float old[32];
+    load_row32<DT>(o, n, vec, old);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] += old[k];
+  }
+  store_row32<DT>(o, n, vec, v);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// rows x cols of 16-bit elements, boxes of 64 x 64, 128-byte swizzle.
+bool encode_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int dt) {
+  EncodeTiledFn fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, 64};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r =
+      fn(m, dt == QMUON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims,
+         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r == CUDA_SUCCESS) return true;
+  char msg[256];
+  std::snprintf(msg, sizeof(msg), "cuTensorMapEncodeTiled returned %d for a %lld x %lld matrix (row stride %lld) at %p", (int)r,
+                (long long)rows, (long long)cols, (long long)ld, base);
+  set_error_msg(msg, QMUON_ERR_CUDA);
+  return false;
+}
+
+// A tensor map reads rows that start on 16 bytes; others are copied to the workspace first.
+bool tma_ready(const void* p, int64_t ld) { return is_aligned(p, 16) && ld % 8 == 0; }
+
+// Splits of a product of `tiles` tiles of `kb` K blocks: the least estimated time, in K blocks of a pair.  A unit's start
+// and epilogue cost about as much as 6 blocks, partial sums another 4 and their second kernel 8.
+int pick_splits(int64_t tiles, int kb, int pairs) {
+  if (tiles >= pairs) return 1;
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= 32 && s <= std::max(1, kb / 4); ++s) {
+    const int64_t cost = ceil_div(tiles * s, pairs) * (ceil_div(kb, s) + 6 + (s > 1 ? 4 : 0)) + (s > 1 ? 8 : 0);
+    if (cost < best_cost) best_cost = cost, best = s;
+  }
+  return best;
+}
+
+struct Geometry {
+  int pairs = 0;
+  int32_t tiles_m = 0, tiles_n = 0, splits = 1;         // forward (or the projections again)
+  int32_t dx_m = 0, dx_n = 0, dx_splits = 1;
+  int32_t dw_m = 0, dw_n = 0, dw_splits = 1;
+  int64_t ld_fwd = 0, ld_w = 0, ld_d = 0;               // of partial gate/up, of partial dx/dW, of dgate/dup
+  size_t dgate = 0, dup = 0, x = 0, w[2] = {0, 0}, part = 0, part_w = 0, total = 0;
+  int64_t ld_x = 0, ld_wp = 0;
+  bool copy_x = false, copy_w[2] = {false, false};
+};
+
+// What a call lays out in its workspace, behind the header.
+void lay(Geometry& G, size_t* at, size_t bytes) { *at = G.total, G.total += round_up(bytes, 256); }
+
+void lay_operands(Geometry& G, int64_t rows, int64_t width, int64_t inner, bool x, bool wg, bool wu) {
+  G.copy_x = x;
+  G.copy_w[0] = wg;
+  G.copy_w[1] = wu;
+  G.ld_x = G.ld_wp = (int64_t)round_up((size_t)width, 8);
+  if (x) lay(G, &G.x, (size_t)rows * G.ld_x * 2);
+  for (int i = 0; i < 2; ++i)
+    if (G.copy_w[i]) lay(G, &G.w[i], (size_t)inner * G.ld_wp * 2);
+}
+
+void lay_projections(Geometry& G, int64_t rows, int64_t width, int64_t inner) {
+  G.tiles_m = (int32_t)ceil_div(rows, kTile);
+  G.tiles_n = (int32_t)ceil_div(inner, kInnerTile);
+  G.splits = pick_splits((int64_t)G.tiles_m * G.tiles_n, (int)ceil_div(width, kBK), G.pairs);
+  G.ld_fwd = (int64_t)round_up((size_t)inner, 8);
+  if (G.splits > 1) lay(G, &G.part, (size_t)G.splits * 2 * rows * G.ld_fwd * 4);
+}
+
+Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
+  Geometry G;
+  G.pairs = pairs;
+  G.total = kWsHeader;
+  lay_operands(G, c.rows, c.width, c.inner, !tma_ready(c.x, c.ld_x), !tma_ready(c.w_gate, c.ld_w_gate), !tma_ready(c.w_up, c.ld_w_up));
+  lay_projections(G, c.rows, c.width, c.inner);
+  return G;
+}
+
+// What the backward pass reads besides dh and what was saved.
+bool needs_x(const qmuon_gated_ffn_grad& c) { return c.dw_gate || c.saved == QMUON_SAVE_NONE; }
+bool needs_weights(const qmuon_gated_ffn_grad& c) { return c.dx || c.saved == QMUON_SAVE_NONE; }
+
+Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
+  Geometry G;
+  G.pairs = pairs;
+  G.total = kWsHeader;
+  const bool w = needs_weights(c);
+  lay_operands(G, c.rows, c.width, c.inner, needs_x(c) && (c.x_scale || !tma_ready(c.x, c.ld_x)), w && !tma_ready(c.w_gate, c.ld_w_gate),
+               w && !tma_ready(c.w_up, c.ld_w_up));
+  G.ld_d = (int64_t)round_up((size_t)c.inner, 16);
+  lay(G, &G.dgate, (size_t)c.rows * G.ld_d * 2);
+  lay(G, &G.dup, (size_t)c.rows * G.ld_d * 2);
+  G.ld_w = (int64_t)round_up((size_t)c.width, 8);
+  const size_t behind = G.total;
+  if (c.saved == QMUON_SAVE_NONE) lay_projections(G, c.rows, c.width, c.inner);
+  const size_t most = G.total;
+  G.total = behind;   // the projections' partial sums are done with when the gradients' begin
+  const int kbx = 2 * (int)ceil_div(c.inner, kBK), kbw = (int)ceil_div(c.rows, kBK);
+  if (c.dx) {
+    G.dx_m = (int32_t)ceil_div(c.rows, kTile);
+    G.dx_n = (int32_t)ceil_div(c.width, kTile);
+  }
+  if (c.dw_gate) {
+    G.dw_m = (int32_t)ceil_div(c.inner, kTile);
+    G.dw_n = (int32_t)ceil_div(c.width, kTile);
+  }
+  const int64_t tx = (int64_t)G.dx_m * G.dx_n, tw = 2 * (int64_t)G.dw_m * G.dw_n;
+  if (tx + tw < 2 * (int64_t)G.pairs) {
+    // few tiles: units of about one pair's share of all K blocks, and of 8 at least
+    const int64_t share = std::max<int64_t>(8, ceil_div(tx * kbx + tw * kbw, G.pairs));
+    G.dx_splits = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(kbx, share)));
+    G.dw_splits = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(kbw, share)));
+  }
+  if (c.dx && G.dx_splits > 1) lay(G, &G.part, (size_t)G.dx_splits * c.rows * G.ld_w * 4);
+  if (c.dw_gate && G.dw_splits > 1) lay(G, &G.part_w, (size_t)2 * G.dw_splits * c.inner * G.ld_w * 4);
+  G.total = std::max(G.total, most);
+  return G;
+}
+
+template <class K>
+cudaError_t launch_pairs(K kernel, const GemmArgs& A, int64_t units, int pairs, cudaStream_t s) {
+  // the shared-memory limit is per device; setting it again costs a few hundred nanoseconds
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(units, pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, A);
+}
+
+template <int KIND, int DT>
+cudaError_t launch_act(const GemmArgs& A, int64_t units, int pairs, cudaStream_t s) {
+  if constexpr (KIND == K_GRAD) {
+    return launch_pairs(ffn_kernel<K_GRAD, DT, 0>, A, units, pairs, s);
+  } else {
+    if (A.act == QMUON_ACT_SILU) return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_SILU>, A, units, pairs, s);
+    if (A.act == QMUON_ACT_GELU) return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_GELU>, A, units, pairs, s);
+    return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_GELU_TANH>, A, units, pairs, s);
+  }
+}
+template <int KIND>
+cudaError_t launch_gemm(const GemmArgs& A, int64_t units, int pairs, int dt, cudaStream_t s) {
+  return dt == QMUON_BF16 ? launch_act<KIND, QMUON_BF16>(A, units, pairs, s) : launch_act<KIND, QMUON_FP16>(A, units, pairs, s);
+}
+
+template <int DT, int FROM, bool BWD>
+cudaError_t launch_elem_of(const ElemArgs& E, cudaStream_t s) {
+  const int64_t grid = ceil_div(E.A.rows * ceil_div(E.A.inner, 32), kElemThreads);
+  auto go = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid), dim3(kElemThreads), 0, s, E); };
+  if (E.A.act == QMUON_ACT_SILU) return go(elem_kernel<DT, QMUON_ACT_SILU, FROM, BWD>);
+  if (E.A.act == QMUON_ACT_GELU) return go(elem_kernel<DT, QMUON_ACT_GELU, FROM, BWD>);
+  return go(elem_kernel<DT, QMUON_ACT_GELU_TANH, FROM, BWD>);
+}
+template <int FROM, bool BWD>
+cudaError_t launch_elem(const ElemArgs& E, int dt, cudaStream_t s) {
+  return dt == QMUON_BF16 ? launch_elem_of<QMUON_BF16, FROM, BWD>(E, s) : launch_elem_of<QMUON_FP16, FROM, BWD>(E, s);
+}
+
+cudaError_t launch_join(const float* part, int splits, int64_t rows, int64_t cols, int64_t ld_part, void* out, int64_t ld, int dt,
+                        int accumulate, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div(rows * ceil_div(cols, 32), kElemThreads));
+  const int vec = vec_class(out, ld, elem_size(dt));
+  auto go = [&](auto kernel) {
+    return launch_dependent(kernel, grid, dim3(kElemThreads), 0, s, part, splits, rows, cols, ld_part, out, ld, vec, accumulate);
+  };
+  return dt == QMUON_BF16 ? go(join_kernel<QMUON_BF16>) : dt == QMUON_FP16 ? go(join_kernel<QMUON_FP16>) : go(join_kernel<QMUON_FP32>);
+}
+
+// The operands as the tensor maps read them: the caller's arrays, or aligned copies in the workspace.
+cudaError_t bring_operands(const Geometry& G, unsigned char* ws, const void** x, int64_t* ld_x, const uint8_t* x_scale,
+                           const void* (&w)[2], int64_t (&ld_w)[2], int64_t rows, int64_t width, int64_t inner, int dt, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (G.copy_x) {
+    void* to = ws + G.x;
+    e = x_scale ? launch_decode(static_cast<const uint8_t*>(*x), x_scale, to, rows, width, G.ld_x, dt, s)
+                : launch_repack(*x, *ld_x, to, G.ld_x, rows, width, s);
+    *x = to;
+    *ld_x = G.ld_x;
+  }
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    if (G.copy_w[i]) {
+      e = launch_repack(w[i], ld_w[i], ws + G.w[i], G.ld_wp, inner, width, s);
+      w[i] = ws + G.w[i];
+      ld_w[i] = G.ld_wp;
+    }
+  return e;
+}
+
+constexpr int64_t kMaxDim = (int64_t)1 << 28;
+
+bool sizes_ok(int64_t rows, int64_t width, int64_t inner) {
+  // products of sizes stay within what the grids and the 32-bit unit counts hold
+  return rows >= 0 && rows <= kMaxDim && width >= 1 && width <= kMaxDim && inner >= 1 && inner <= kMaxDim &&
+         inner <= ((int64_t)1 << 36) / width && (rows == 0 || inner <= ((int64_t)1 << 38) / rows) &&
+         (rows == 0 || width <= ((int64_t)1 << 38) / rows);
+}
+bool matrix_ok(const void* p, int64_t ld, int64_t cols, int es) {
+  return p && is_aligned(p, es) && ld >= cols && ld <= ((int64_t)1 << 36);
+}
+bool enums_ok(int act, int dtype, int saved) {
+  return act >= QMUON_ACT_SILU && act <= QMUON_ACT_GELU_TANH && dtype >= QMUON_BF16 && dtype <= QMUON_FP32 && saved >= QMUON_SAVE_NONE &&
+         saved <= QMUON_SAVE_MXFP8;
+}
+
+qmuon_status check_forward(const qmuon_gated_ffn* c) {
+  if (!c || !sizes_ok(c->rows, c->width, c->inner) || !enums_ok(c->act, c->dtype, c->saved)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->dtype == QMUON_FP32) return QMUON_ERR_UNSUPPORTED;
+  if (c->saved == QMUON_SAVE_MXFP8 && c->inner % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
+  if (c->rows == 0) return QMUON_OK;
+  if (!matrix_ok(c->x, c->ld_x, c->width, 2) || !matrix_ok(c->w_gate, c->ld_w_gate, c->width, 2) ||
+      !matrix_ok(c->w_up, c->ld_w_up, c->width, 2) || !matrix_ok(c->h, c->ld_h, c->inner, 2))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->saved == QMUON_SAVE_SAME && (!matrix_ok(c->gate, c->ld_gate, c->inner, 2) || !matrix_ok(c->up, c->ld_up, c->inner, 2)))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->saved == QMUON_SAVE_MXFP8 &&
+      (!c->gate || !c->up || !is_aligned(c->gate, 16) || !is_aligned(c->up, 16) || !c->gate_scale || !c->up_scale))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  return QMUON_OK;
+}
+
+qmuon_status check_backward(const qmuon_gated_ffn_grad* c) {
+  if (!c || !sizes_ok(c->rows, c->width, c->inner) || !enums_ok(c->act, c->dtype, c->saved)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->dtype == QMUON_FP32) return QMUON_ERR_UNSUPPORTED;
+  if (c->grad_dtype != c->dtype && c->grad_dtype != QMUON_FP32) return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->saved == QMUON_SAVE_MXFP8 && c->inner % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
+  if (c->x_scale && c->width % QMUON_SCALE_BLOCK) return QMUON_ERR_UNSUPPORTED;
+  if ((c->dw_gate == nullptr) != (c->dw_up == nullptr)) return QMUON_ERR_INVALID_ARGUMENT;
+  const int gs = elem_size(c->grad_dtype);
+  if (c->dw_gate && (!matrix_ok(c->dw_gate, c->ld_dw_gate, c->width, gs) || !matrix_ok(c->dw_up, c->ld_dw_up, c->width, gs)))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (!c->dx && !c->dw_gate && !c->h) return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->rows == 0) return QMUON_OK;
+  if (!matrix_ok(c->dh, c->ld_dh, c->inner, 2)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (needs_weights(*c) && (!matrix_ok(c->w_gate, c->ld_w_gate, c->width, 2) || !matrix_ok(c->w_up, c->ld_w_up, c->width, 2)))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (needs_x(*c) && (c->x_scale ? !c->x || !is_aligned(c->x, 16) : !matrix_ok(c->x, c->ld_x, c->width, 2)))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->saved == QMUON_SAVE_SAME && (!matrix_ok(c->gate, c->ld_gate, c->inner, 2) || !matrix_ok(c->up, c->ld_up, c->inner, 2)))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->saved == QMUON_SAVE_MXFP8 &&
+      (!c->gate || !c->up || !is_aligned(c->gate, 16) || !is_aligned(c->up, 16) || !c->gate_scale || !c->up_scale))
+    return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->dx && !matrix_ok(c->dx, c->ld_dx, c->width, 2)) return QMUON_ERR_INVALID_ARGUMENT;
+  if (c->h && !matrix_ok(c->h, c->ld_h, c->inner, 2)) return QMUON_ERR_INVALID_ARGUMENT;
+  return QMUON_OK;
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace qm
+
+using namespace qm;
+using namespace qm::lm;
+
+extern "C" size_t qmuon_gated_ffn_workspace_size(const qmuon_gated_ffn* c) {
+  if (check_forward(c) != QMUON_OK) return 0;
+  if (c->rows == 0) return kWsHeader;
+  const int sms = num_sms();
+  return forward_geometry(*c, std::max(1, (sms > 0 ? sms : 152) / 2)).total;
+}
+
+extern "C" qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* c, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qmuon_gated_ffn_forward");
+  return no_throw("qmuon_gated_ffn_forward", [&]() -> qmuon_status {
+    const qmuon_status st = check_forward(c);
+    if (st != QMUON_OK) return st;
+    if (c->rows == 0) return QMUON_OK;
+    if (!ws || !is_aligned(ws, 256)) return QMUON_ERR_INVALID_ARGUMENT;
+    const int sms = num_sms();
+    if (sms <= 0) return set_error_msg("qmuon_gated_ffn_forward: SM count query failed", QMUON_ERR_CUDA);
+    const Geometry G = forward_geometry(*c, std::max(1, sms / 2));
+    if (ws_bytes < G.total) return QMUON_ERR_WORKSPACE_TOO_SMALL;
+    unsigned char* b = static_cast<unsigned char*>(ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    GemmArgs A{};
+    const void *x = c->x, *w[2] = {c->w_gate, c->w_up};
+    int64_t ld_x = c->ld_x, ld_w[2] = {c->ld_w_gate, c->ld_w_up};
+    cudaError_t e = cudaMemsetAsync(b, 0, kWsHeader, s);
+    if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, nullptr, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
+    if (e != cudaSuccess) return set_error("qmuon_gated_ffn_forward (operands)", e);
+    if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) || !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
+        !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
+      return QMUON_ERR_CUDA;
+    A.rows = c->rows, A.width = c->width, A.inner = c->inner;
+    A.tiles_m = G.tiles_m, A.tiles_n = G.tiles_n, A.splits = G.splits;
+    A.units = G.tiles_m * G.tiles_n * G.splits;
+    A.h = c->h, A.ld_h = c->ld_h, A.vec_h = vec_class(c->h, c->ld_h, 2);
+    A.gate = c->gate, A.up = c->up, A.ld_gate = c->ld_gate, A.ld_up = c->ld_up;
+    A.gate_scale = c->gate_scale, A.up_scale = c->up_scale;
+    A.vec_gate = c->saved == QMUON_SAVE_MXFP8 ? vec_class(c->gate, 32, 1) : vec_class(c->gate, c->ld_gate, 2);
+    A.vec_up = c->saved == QMUON_SAVE_MXFP8 ? vec_class(c->up, 32, 1) : vec_class(c->up, c->ld_up, 2);
+    A.act = c->act, A.saved = c->saved;
+    A.hdr = reinterpret_cast<WsHeader*>(b);
+    A.ld_part = G.ld_fwd;
+    A.part = G.splits > 1 ? reinterpret_cast<float*>(b + G.part) : nullptr;
+    e = launch_gemm<K_FWD>(A, A.units, G.pairs, c->dtype, s);
+    if (e == cudaSuccess && A.part) {
+      ElemArgs E{};
+      E.A = A;
+      E.part = A.part;
+      E.splits = G.splits;
+      e = launch_elem<FROM_PART, false>(E, c->dtype, s);
+    }
+    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_gated_ffn_forward (launch)", e);
+  });
+}
+
+extern "C" size_t qmuon_gated_ffn_backward_workspace_size(const qmuon_gated_ffn_grad* c) {
+  if (check_backward(c) != QMUON_OK) return 0;
+  if (c->rows == 0) return kWsHeader;
+  const int sms = num_sms();
+  return backward_geometry(*c, std::max(1, (sms > 0 ? sms : 152) / 2)).total;
+}
+
+extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qmuon_gated_ffn_backward");
+  return no_throw("qmuon_gated_ffn_backward", [&]() -> qmuon_status {
+    const qmuon_status st = check_backward(c);
+    if (st != QMUON_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (c->rows == 0) {   // no rows: the weights' gradients are zero
+      if (c->dw_gate && !c->accumulate) {
+        const size_t gs = elem_size(c->grad_dtype);
+        e = cudaMemset2DAsync(c->dw_gate, c->ld_dw_gate * gs, 0, c->width * gs, c->inner, s);
+        if (e == cudaSuccess) e = cudaMemset2DAsync(c->dw_up, c->ld_dw_up * gs, 0, c->width * gs, c->inner, s);
+      }
+      return e == cudaSuccess ? QMUON_OK : set_error("qmuon_gated_ffn_backward (memset)", e);
+    }
+    if (!ws || !is_aligned(ws, 256)) return QMUON_ERR_INVALID_ARGUMENT;
+    const int sms = num_sms();
+    if (sms <= 0) return set_error_msg("qmuon_gated_ffn_backward: SM count query failed", QMUON_ERR_CUDA);
+    const Geometry G = backward_geometry(*c, std::max(1, sms / 2));
+    if (ws_bytes < G.total) return QMUON_ERR_WORKSPACE_TOO_SMALL;
+    unsigned char* b = static_cast<unsigned char*>(ws);
+    const void *x = c->x, *w[2] = {c->w_gate, c->w_up};
+    int64_t ld_x = c->ld_x, ld_w[2] = {c->ld_w_gate, c->ld_w_up};
+    e = cudaMemsetAsync(b, 0, kWsHeader, s);
+    if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, c->x_scale, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
+    if (e != cudaSuccess) return set_error("qmuon_gated_ffn_backward (operands)", e);
+
+    GemmArgs A{};
+    A.rows = c->rows, A.width = c->width, A.inner = c->inner;
+    A.dh = c->dh, A.ld_dh = c->ld_dh, A.vec_dh = vec_class(c->dh, c->ld_dh, 2);
+    A.h = c->h, A.ld_h = c->ld_h, A.vec_h = c->h ? vec_class(c->h, c->ld_h, 2) : 0;
+    A.dgate = b + G.dgate, A.dup = b + G.dup, A.ld_d = G.ld_d;
+    A.act = c->act, A.saved = c->saved;
+    A.hdr = reinterpret_cast<WsHeader*>(b);
+    ElemArgs E{};
+    if (c->saved == QMUON_SAVE_NONE) {   // gate and up again
+      A.tiles_m = G.tiles_m, A.tiles_n = G.tiles_n, A.splits = G.splits;
+      A.units = G.tiles_m * G.tiles_n * G.splits;
+      A.ld_part = G.ld_fwd;
+      A.part = G.splits > 1 ? reinterpret_cast<float*>(b + G.part) : nullptr;
+      if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) ||
+          !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
+          !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
+        return QMUON_ERR_CUDA;
+      e = launch_gemm<K_BWD>(A, A.units, G.pairs, c->dtype, s);
+      if (e == cudaSuccess && A.part) {
+        E.A = A;
+        E.part = A.part;
+        E.splits = G.splits;
+        e = launch_elem<FROM_PART, true>(E, c->dtype, s);
+      }
+    } else {
+      const bool mx = c->saved == QMUON_SAVE_MXFP8;
+      E.A = A;
+      E.gate = c->gate, E.up = c->up, E.gate_scale = c->gate_scale, E.up_scale = c->up_scale;
+      E.ld_gate = c->ld_gate, E.ld_up = c->ld_up;
+      E.vec_in = mx ? std::min(vec_class(c->gate, 32, 1), vec_class(c->up, 32, 1))
+                    : std::min(vec_class(c->gate, c->ld_gate, 2), vec_class(c->up, c->ld_up, 2));
+      e = mx ? launch_elem<FROM_MXFP8, true>(E, c->dtype, s) : launch_elem<FROM_SAME, true>(E, c->dtype, s);
+    }
+    if (e != cudaSuccess) return set_error("qmuon_gated_ffn_backward (launch)", e);
+    if (!c->dx && !c->dw_gate) return QMUON_OK;
+
+    const int64_t units_x = (int64_t)G.dx_m * G.dx_n * G.dx_splits, units_w = 2 * (int64_t)G.dw_m * G.dw_n * G.dw_splits;
+    const int pairs = (int)std::min<int64_t>(units_x + units_w, G.pairs);
+    A.tiles_m = G.dx_m, A.tiles_n = G.dx_n, A.splits = G.dx_splits;
+    A.tiles_wm = G.dw_m, A.tiles_wn = G.dw_n, A.splits_w = G.dw_splits;
+    A.units = (int32_t)units_x, A.units_w = (int32_t)units_w;
+    // dW units: the pairs without a last unit of dx take as many as its K blocks are worth; the rest goes round
+    {
+      const int extra = (int)(units_x % pairs), few = pairs - extra;
+      const int64_t cost_x = 2 * ceil_div(c->inner, kBK) / G.dx_splits, cost_w = std::max<int64_t>(1, ceil_div(c->rows, kBK) / G.dw_splits);
+      const int64_t worth = extra ? std::min((cost_x + cost_w / 2) / cost_w, units_w / few) : 0;
+      A.few_w = (int32_t)worth;
+      A.rounds_w = (int32_t)((units_w - worth * few) / pairs);
+    }
+    A.dx = c->dx, A.ld_dx = c->ld_dx, A.vec_dx = vec_class(c->dx, c->ld_dx, 2);
+    const int gs = elem_size(c->grad_dtype);
+    A.dw[0] = c->dw_gate, A.dw[1] = c->dw_up, A.ld_dw[0] = c->ld_dw_gate, A.ld_dw[1] = c->ld_dw_up;
+    A.vec_dw[0] = vec_class(c->dw_gate, c->ld_dw_gate, gs), A.vec_dw[1] = vec_class(c->dw_up, c->ld_dw_up, gs);
+    A.dw_f32 = c->grad_dtype == QMUON_FP32, A.accumulate = c->accumulate != 0;
+    A.ld_part = G.ld_w;
+    A.part = c->dx && G.dx_splits > 1 ? reinterpret_cast<float*>(b + G.part) : nullptr;
+    A.part_w = c->dw_gate && G.dw_splits > 1 ? reinterpret_cast<float*>(b + G.part_w) : nullptr;
+    if (!encode_map(&A.a[0], A.dgate, c->rows, c->inner, G.ld_d, c->dtype) ||
+        !encode_map(&A.a[1], A.dup, c->rows, c->inner, G.ld_d, c->dtype))
+      return QMUON_ERR_CUDA;
+    if (c->dx && (!encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
+                  !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype)))
+      return QMUON_ERR_CUDA;
+    if (c->dw_gate && !encode_map(&A.b[2], x, c->rows, c->width, ld_x, c->dtype)) return QMUON_ERR_CUDA;
+    e = launch_gemm<K_GRAD>(A, units_x + units_w, pairs, c->dtype, s);
+    if (e == cudaSuccess && A.part)
+      e = launch_join(A.part, G.dx_splits, c->rows, c->width, G.ld_w, c->dx, c->ld_dx, c->dtype, 0, s);
+    for (int i = 0; i < 2 && e == cudaSuccess && A.part_w; ++i)
+      e = launch_join(A.part_w + (size_t)i * G.dw_splits * c->inner * G.ld_w, G.dw_splits, c->inner, c->width, G.ld_w, A.dw[i], A.ld_dw[i],
+                      c->grad_dtype, A.accumulate, s);
+    return e == cudaSuccess ? QMUON_OK : set_error("qmuon_gated_ffn_backward (launch)", e);
+  });
+}
