@@ -24,6 +24,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "qm_lm.h"
 #include "qm_tc.h"
@@ -110,6 +111,9 @@ struct GemmArgs {
   int32_t act, saved, dw_f32, accumulate;
   WsHeader* hdr;
 };
+
+using Yes = std::true_type;
+using No = std::false_type;
 
 struct Unit {
   int32_t kind;          // 0: the forward or dx, 1: dWg, 2: dWu
@@ -264,78 +268,108 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
   const uint32_t tmem = *tmem_slot;
   const int inner_blocks = KIND == K_GRAD ? blocks_of(A.inner) : 0;
 
+  // Warps 0 and 1 run a K block of 64 in the tensor cores' 512 cycles or hold
+  // them up.  All lanes go through their loops, so that addresses, descriptors
+  // and parities stay in uniform registers, where the TMA and MMA instructions
+  // want them; one lane issues.  Stages are counted, not divided out, and a
+  // barrier is tried in line before the bounded wait is called.
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- TMA producer: every CTA loads its own halves of the operands ----
-      const uint32_t full_l = cluster_map(full0, 0);   // the leader's barriers
-      int it = 0;
-      bool ok = true;
-      Unit u;
-      for (int i = 0; ok && unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
-        const bool dx = KIND == K_GRAD && u.kind == 0, dw = KIND == K_GRAD && u.kind > 0;
-        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-          const int s = it % kStages, round = it / kStages;
-          if (round > 0 && !mbar_wait(empty0 + 8 * s, (round - 1) & 1, A.hdr, 0x2100u | KIND)) {
-            ok = false;
-            break;
-          }
+    // ---- TMA producer: every CTA loads its own halves of the operands ----
+    const uint32_t full_l = cluster_map(full0, 0);   // the leader's barriers
+    const uint32_t smem0 = smem_u32(smem);
+    int s = 0, it = 0;
+    uint32_t parity = 1;   // of the round before: a new barrier's wait on it returns at once
+    Unit u;
+    // one unit's loads: A at (x, y) + (64 of its rows or columns), likewise B
+    auto load = [&](auto a_mn, auto b_mn, const CUtensorMap* ma, const CUtensorMap* mb, int am, int bn, int k0, int n) -> bool {
+      for (; n > 0; --n, ++it, k0 += kBK) {
+        const uint32_t empty = empty0 + 8 * s, bar = full_l + 8 * s;
+        if (!mbar_try_wait(empty, parity) && !__all_sync(0xffffffffu, mbar_wait(empty, parity, A.hdr, 0x2100u | KIND))) return false;
+        const uint32_t sa = smem0 + s * kStageBytes;
+        if (elect_one()) {
           if (leader) mbar_expect_tx(full0 + 8 * s, 2 * kStageBytes);
-          const uint32_t bar = full_l + 8 * s;
-          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + 2 * kBox;
-          // dx runs over the columns of dgate, then over those of dup
-          const int seg = dx && kb >= inner_blocks ? 1 : 0;
-          const int k0 = (kb - seg * inner_blocks) * kBK;
-          const CUtensorMap* ma = &A.a[dw ? u.kind - 1 : seg];
-          const CUtensorMap* mb = &A.b[KIND != K_GRAD ? rank : dw ? 2 : seg];
-          const int am = u.m0 + 128 * rank, bn = KIND != K_GRAD ? u.n0 : u.n0 + 128 * rank;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (dw) tma_load_2d_pair(sa + j * kBox, ma, bar, am + 64 * j, k0);
-            else tma_load_2d_pair(sa + j * kBox, ma, bar, k0, am + 64 * j);
+          if constexpr (decltype(a_mn)::value) {
+            tma_load_2d_pair(sa, ma, bar, am, k0);
+            tma_load_2d_pair(sa + kBox, ma, bar, am + 64, k0);
+          } else {
+            tma_load_2d_pair(sa, ma, bar, k0, am);
+            tma_load_2d_pair(sa + kBox, ma, bar, k0, am + 64);
           }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (KIND == K_GRAD) tma_load_2d_pair(sb + j * kBox, mb, bar, bn + 64 * j, k0);
-            else tma_load_2d_pair(sb + j * kBox, mb, bar, k0, bn + 64 * j);
+          if constexpr (decltype(b_mn)::value) {
+            tma_load_2d_pair(sa + 2 * kBox, mb, bar, bn, k0);
+            tma_load_2d_pair(sa + 3 * kBox, mb, bar, bn + 64, k0);
+          } else {
+            tma_load_2d_pair(sa + 2 * kBox, mb, bar, k0, bn);
+            tma_load_2d_pair(sa + 3 * kBox, mb, bar, k0, bn + 64);
           }
         }
+        __syncwarp();
+        if (++s == kStages) s = 0, parity ^= 1;
       }
-      // every load issued has landed before the CTA may exit (the leader's
-      // full barriers also count the peer's loads)
-      if (leader)
-        for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
-          mbar_wait(full0 + 8 * (k % kStages), (k / kStages) & 1, A.hdr, 0x2200u | KIND);
+      return true;
+    };
+    for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+      const int am = u.m0 + 128 * rank;
+      bool ok;
+      if constexpr (KIND != K_GRAD) {
+        ok = load(No{}, No{}, &A.a[0], &A.b[rank], am, u.n0, u.kb0 * kBK, u.kb1 - u.kb0);
+      } else if (u.kind > 0) {
+        ok = load(Yes{}, Yes{}, &A.a[u.kind - 1], &A.b[2], am, u.n0 + 128 * rank, u.kb0 * kBK, u.kb1 - u.kb0);
+      } else {
+        // dx runs over the columns of dgate, then over those of dup
+        const int turn = inner_blocks < u.kb0 ? u.kb0 : inner_blocks > u.kb1 ? u.kb1 : inner_blocks;
+        ok = load(No{}, Yes{}, &A.a[0], &A.b[0], am, u.n0 + 128 * rank, u.kb0 * kBK, turn - u.kb0) &&
+             load(No{}, Yes{}, &A.a[1], &A.b[1], am, u.n0 + 128 * rank, (turn - inner_blocks) * kBK, u.kb1 - turn);
+      }
+      if (!ok) break;
     }
+    // every load issued has landed before the CTA may exit (the leader's
+    // full barriers also count the peer's loads)
+    if (leader)
+      for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
+        mbar_wait(full0 + 8 * (k % kStages), (k / kStages) & 1, A.hdr, 0x2200u | KIND);
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ---- MMA issuer ----
-      int it = 0;
-      bool ok = true;
+      // descriptors of the first stage: the low words hold the address, to which
+      // 2 KB (MN-major) or 32 bytes (K-major) per 16 of K and a stage's 32 KB are added
+      const uint32_t smem0 = smem_u32(smem);
+      int s = 0;
+      uint32_t parity = 0;
+      auto multiply = [&](auto a_mn, auto b_mn, uint32_t d, int n) -> bool {
+        constexpr bool amn = decltype(a_mn)::value, bmn = decltype(b_mn)::value;
+        constexpr uint32_t step_a = (amn ? 2048 : 32) >> 4, step_b = (bmn ? 2048 : 32) >> 4;
+        const uint64_t first_a = amn ? desc_mnmajor(smem0, 0) : desc_kmajor(smem0, 0);
+        const uint64_t first_b = bmn ? desc_mnmajor(smem0 + 2 * kBox, 0) : desc_kmajor(smem0 + 2 * kBox, 0);
+        const uint32_t idesc = instr_desc<DT>(amn, bmn);
+        for (uint32_t add = 0; n > 0; --n, add = 1) {
+          const uint32_t full = full0 + 8 * s;
+          if (!mbar_try_wait(full, parity) && !__all_sync(0xffffffffu, mbar_wait(full, parity, A.hdr, 0x2300u | KIND))) return false;
+          tc_fence_after();
+          const uint64_t ad = first_a + (uint32_t)(s * (kStageBytes >> 4)), bd = first_b + (uint32_t)(s * (kStageBytes >> 4));
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) mma_bf16_cg<2>(d, ad + kk * step_a, bd + kk * step_b, idesc, kk > 0 ? 1u : add);
+            mma_commit_cg<2>(empty0 + 8 * s);
+          }
+          __syncwarp();
+          if (++s == kStages) s = 0, parity ^= 1;
+        }
+        return true;
+      };
       Unit u;
-      for (int i = 0; ok && unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+      for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
         const int acc = i & 1, use = i >> 1;
-        if (use > 0 && !mbar_wait(tempty0 + 8 * acc, (use - 1) & 1, A.hdr, 0x2500u | KIND)) break;
+        if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * acc, (use - 1) & 1, A.hdr, 0x2500u | KIND))) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * kTile);
-        const bool amn = KIND == K_GRAD && u.kind > 0, bmn = KIND == K_GRAD;
-        const uint32_t idesc = instr_desc<DT>(amn, bmn);
-        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-          const int s = it % kStages, round = it / kStages;
-          if (!mbar_wait(full0 + 8 * s, round & 1, A.hdr, 0x2300u | KIND)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + 2 * kBox;
-#pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            const uint64_t ad = amn ? desc_mnmajor(sa, kk) : desc_kmajor(sa, kk);
-            const uint64_t bd = bmn ? desc_mnmajor(sb, kk) : desc_kmajor(sb, kk);
-            mma_bf16_cg<2>(d, ad, bd, idesc, (kb > u.kb0 || kk > 0) ? 1u : 0u);
-          }
-          mma_commit_cg<2>(empty0 + 8 * s);
-        }
-        mma_commit_cg<2>(tfull0 + 8 * acc);   // accumulator ready (also on the error path)
+        bool ok;
+        if constexpr (KIND != K_GRAD) ok = multiply(No{}, No{}, d, u.kb1 - u.kb0);
+        else if (u.kind > 0) ok = multiply(Yes{}, Yes{}, d, u.kb1 - u.kb0);
+        else ok = multiply(No{}, Yes{}, d, u.kb1 - u.kb0);
+        if (elect_one()) mma_commit_cg<2>(tfull0 + 8 * acc);   // accumulator ready (also on the error path)
+        __syncwarp();
+        if (!ok) break;
       }
     }
   } else {
