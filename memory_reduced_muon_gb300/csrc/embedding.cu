@@ -44,7 +44,7 @@ template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(LookupArgs A) {
   constexpr int es = elem_size(DT), K = VEC ? 16 / es : 1;
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  depends_wait();
+  depends_begin();
   if (t >= A.n) return;
   const int64_t v = A.bits64 ? token_at<int64_t>(A.tokens, t) : token_at<int32_t>(A.tokens, t);
   const bool there = v >= 0 && v < A.vocab;
@@ -113,132 +113,194 @@ cudaError_t launch_lookup(const LookupArgs& A, int sms, cudaStream_t s) {
 // sorting
 // ---------------------------------------------------------------------------
 // Keys are tokens, `vocab` standing for every token outside; a key's bits are
-// sorted from the low ones up, up to 9 a pass.  A CTA takes kSortKeys keys, its
-// warps 256 each in eight rounds of 32, so that a warp's keys are ranked in
-// order: lanes of equal digits find one another by match, the lowest of them
+// sorted from the low ones up, up to 9 a pass.  A CTA takes kSortKeys keys at
+// most, its warps equal shares in rounds of 32, so that a warp's keys are ranked
+// in order: lanes of equal digits find one another by match, the lowest of them
 // adds their number to the warp's count.
+//
+// Up to 8 such CTAs are one cluster, whose barriers part the passes: one launch
+// sorts 65536 tokens.  More tokens take three kernels a pass (the CTAs' counts,
+// their sums, the moves).
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRounds = 8, kSortKeys = kSortThreads * kRounds;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRounds = 16, kSortKeys = kSortThreads * kRounds;
+constexpr int kSortCluster = 8;
+static_assert(kSortThreads == kDigits, "a thread per digit");
 
 struct SortArgs {
   const void* tokens;    // first pass, or null
   const uint2* in;       // (key, position) pairs of the pass before, or null
   uint2* out;
   uint32_t* counts;      // [kDigits][CTAs]: the CTAs' digits
-  uint8_t* present;      // [vocab] or null: first pass marks the tokens that occur
   int64_t n, vocab;
   int32_t bits64, shift, n_cta;
+  int32_t share;         // keys of a warp, a multiple of 32
+  int32_t passes;        // cluster_sort_kernel
+  uint2* pairs[2];       // cluster_sort_kernel: where odd and even passes leave the pairs
 };
 
 __device__ __forceinline__ uint2 key_of(const SortArgs& A, int64_t i) {
-  if (A.in) return A.in[i];
+  if (A.in) return __ldcg(A.in + i);   // another SM's, moments ago
   const int64_t v = A.bits64 ? token_at<int64_t>(A.tokens, i) : token_at<int32_t>(A.tokens, i);
   return make_uint2(v >= 0 && v < A.vocab ? (uint32_t)v : (uint32_t)A.vocab, (uint32_t)i);
 }
 
-__global__ void __launch_bounds__(kSortThreads) count_kernel(SortArgs A) {
-  __shared__ uint32_t count[kDigits];
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
-  __syncthreads();
-  depends_wait();
-  const int64_t base = (int64_t)blockIdx.x * kSortKeys;
+// The keys of a warp, and the rank of each among the warp's keys of its digit; `count` is the warp's number of each digit.
+struct WarpKeys {
+  uint2 kv[kRounds];
+  uint32_t rank[kRounds];
+};
+__device__ __forceinline__ void rank_keys(const SortArgs& A, int64_t first, int lane, WarpKeys& K, uint16_t* count) {
+  const int64_t end = first + A.share < A.n ? first + A.share : A.n;
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = base + r * kSortThreads + threadIdx.x;
-    if (i < A.n) {
-      const uint32_t key = key_of(A, i).x;
-      atomicAdd(&count[(key >> A.shift) & (kDigits - 1)], 1u);
-      if (A.present && key < (uint32_t)A.vocab) A.present[key] = 1;
+    const int64_t i = first + r * 32 + lane;
+    K.kv[r] = i < end ? key_of(A, i) : make_uint2(0u, 0u);
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    if (first + r * 32 >= end) break;   // the same for all lanes
+    const bool valid = first + r * 32 + lane < end;
+    const uint32_t digit = valid ? (K.kv[r].x >> A.shift) & (kDigits - 1) : (uint32_t)kDigits;
+    const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+    const uint32_t below = __popc(peers & ((1u << lane) - 1u));
+    uint32_t old = 0;
+    if (valid) old = count[digit];
+    __syncwarp();
+    if (valid && below == 0) count[digit] = (uint16_t)(old + __popc(peers));
+    __syncwarp();
+    K.rank[r] = old + below;
+  }
+}
+__device__ __forceinline__ void move_keys(const SortArgs& A, int64_t first, int lane, const WarpKeys& K, const uint16_t* before,
+                                          const uint32_t* base, uint2* out) {
+  const int64_t end = first + A.share < A.n ? first + A.share : A.n;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    if (first + r * 32 + lane < end) {
+      const uint32_t digit = (K.kv[r].x >> A.shift) & (kDigits - 1);
+      out[base[digit] + before[digit] + K.rank[r]] = K.kv[r];
     }
   }
-  __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) A.counts[(int64_t)d * A.n_cta + blockIdx.x] = count[d];
 }
-
-// Where each CTA's keys of each digit go: an exclusive sum over digits, then CTAs.  One CTA; a thread per digit.
-__global__ void __launch_bounds__(kDigits) offsets_kernel(uint32_t* counts, int n_cta) {
-  __shared__ uint32_t warp_sum[kDigits / 32];
-  depends_wait();
-  uint32_t* mine = counts + (int64_t)threadIdx.x * n_cta;
-  uint32_t total = 0;
-  for (int c = 0; c < n_cta; ++c) {
-    const uint32_t k = mine[c];
-    mine[c] = total;
-    total += k;
+// Thread d: the CTA's number of digit d; count[w][d] becomes the number in the warps before w.
+__device__ __forceinline__ uint32_t warps_before(uint16_t (*count)[kDigits]) {
+  uint32_t sum = 0;
+  for (int w = 0; w < kSortWarps; ++w) {
+    const uint32_t k = count[w][threadIdx.x];
+    count[w][threadIdx.x] = (uint16_t)sum;
+    sum += k;
   }
+  return sum;
+}
+// Exclusive sum of v over the CTA's 512 threads.
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* warp_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t incl = total;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
+  __syncthreads();
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  uint32_t before = incl - total;
+  uint32_t before = incl - v;
   for (int w = 0; w < warp; ++w) before += warp_sum[w];
-  for (int c = 0; c < n_cta; ++c) mine[c] += before;
+  return before;
+}
+// Every write of the cluster's CTAs before it is seen by all of them behind it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(SortArgs A) {
+  __shared__ uint16_t count[kSortWarps][kDigits];
+  __shared__ uint32_t base[kDigits], warp_sum[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = threadIdx.x;
+  const int64_t first = ((int64_t)blockIdx.x * kSortWarps + warp) * A.share;
+  depends_begin();
+  for (int pass = 0; pass < A.passes; ++pass) {
+    for (int w = 0; w < kSortWarps; ++w) count[w][d] = 0;
+    __syncthreads();
+    WarpKeys K;
+    rank_keys(A, first, lane, K, count[warp]);
+    __syncthreads();
+    A.counts[(int64_t)d * A.n_cta + blockIdx.x] = warps_before(count);
+    cluster_barrier();
+    uint32_t total = 0, mine = 0;
+    for (int c = 0; c < A.n_cta; ++c) {
+      if (c == (int)blockIdx.x) mine = total;
+      total += __ldcg(A.counts + (int64_t)d * A.n_cta + c);
+    }
+    base[d] = sum_before(total, warp_sum) + mine;
+    __syncthreads();
+    move_keys(A, first, lane, K, count[warp], base, A.pairs[pass & 1]);
+    cluster_barrier();
+    A.in = A.pairs[pass & 1];
+    A.shift += kDigitBits;
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) count_kernel(SortArgs A) {
+  __shared__ uint32_t count[kDigits];
+  count[threadIdx.x] = 0;
+  __syncthreads();
+  depends_begin();
+  const int64_t base = (int64_t)blockIdx.x * kSortKeys;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = base + r * kSortThreads + threadIdx.x;
+    if (i < A.n) atomicAdd(&count[(key_of(A, i).x >> A.shift) & (kDigits - 1)], 1u);
+  }
+  __syncthreads();
+  A.counts[(int64_t)threadIdx.x * A.n_cta + blockIdx.x] = count[threadIdx.x];
+}
+
+// Where each CTA's keys of each digit go: an exclusive sum over digits, then CTAs.  One CTA; a thread per digit.
+__global__ void __launch_bounds__(kDigits) offsets_kernel(uint32_t* counts, int n_cta) {
+  __shared__ uint32_t warp_sum[kDigits / 32];
+  depends_begin();
+  uint32_t* mine = counts + (int64_t)threadIdx.x * n_cta;
+  uint32_t total = 0;
+#pragma unroll 8
+  for (int c = 0; c < n_cta; ++c) total += mine[c];
+  uint32_t at = sum_before(total, warp_sum);
+#pragma unroll 8
+  for (int c = 0; c < n_cta; ++c) {
+    const uint32_t k = mine[c];
+    mine[c] = at;
+    at += k;
+  }
 }
 
 __global__ void __launch_bounds__(kSortThreads) scatter_kernel(SortArgs A) {
-  __shared__ uint16_t count[kSortWarps][kDigits];   // each warp's digits, then where its first key of the digit goes in the CTA's
+  __shared__ uint16_t count[kSortWarps][kDigits];
   __shared__ uint32_t base[kDigits];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int d = threadIdx.x; d < kDigits * kSortWarps; d += kSortThreads) (&count[0][0])[d] = 0;
+  for (int w = 0; w < kSortWarps; ++w) count[w][threadIdx.x] = 0;
   __syncthreads();
-  depends_wait();
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) base[d] = A.counts[(int64_t)d * A.n_cta + blockIdx.x];
-  const int64_t first = (int64_t)blockIdx.x * kSortKeys + warp * (32 * kRounds);
-  uint2 kv[kRounds];
-  uint32_t rank[kRounds];
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = first + r * 32 + lane;
-    kv[r] = i < A.n ? key_of(A, i) : make_uint2(0u, 0u);
-  }
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const bool valid = first + r * 32 + lane < A.n;
-    const uint32_t digit = valid ? (kv[r].x >> A.shift) & (kDigits - 1) : (uint32_t)kDigits;
-    const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-    const uint32_t below = __popc(peers & ((1u << lane) - 1u));
-    uint32_t old = 0;
-    if (valid) old = count[warp][digit];
-    __syncwarp();
-    if (valid && below == 0) count[warp][digit] = (uint16_t)(old + __popc(peers));
-    __syncwarp();
-    rank[r] = old + below;
-  }
+  depends_begin();
+  base[threadIdx.x] = A.counts[(int64_t)threadIdx.x * A.n_cta + blockIdx.x];
+  const int64_t first = ((int64_t)blockIdx.x * kSortWarps + warp) * A.share;
+  WarpKeys K;
+  rank_keys(A, first, lane, K, count[warp]);
   __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t k = count[w][d];
-      count[w][d] = (uint16_t)sum;
-      sum += k;
-    }
-  }
+  warps_before(count);
   __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    if (first + r * 32 + lane < A.n) {
-      const uint32_t digit = (kv[r].x >> A.shift) & (kDigits - 1);
-      A.out[base[digit] + count[warp][digit] + rank[r]] = kv[r];
-    }
-  }
+  move_keys(A, first, lane, K, count[warp], base, A.out);
 }
 
 // ---------------------------------------------------------------------------
 // sums
 // ---------------------------------------------------------------------------
-constexpr int kPiece = 32;   // sorted positions of a piece
+constexpr int kPiece = 32;    // sorted positions of a piece
+constexpr int kZeros = 64;    // rows of a CTA that looks for rows without a token
 
 struct SumArgs {
   const uint2* sorted;
   const void* dout;
   void* dtable;
   float* partial;        // [pieces][2][ldp]: a run that began before the piece, and one that goes on behind it
-  const uint8_t* present;
   int64_t n, vocab, ld_dout, ld_dtable, ldp;
   int32_t cols, pieces, accumulate;
   float scale;
@@ -294,20 +356,47 @@ __device__ __forceinline__ void write_row(const SumArgs& A, int64_t row, int64_t
   store_cols<GT, N>(A.dtable, e, v);
 }
 
+// The first sorted position whose key is not below `key`, by a whole warp.
+__device__ __forceinline__ int64_t first_at_least(const uint2* sorted, int64_t n, uint32_t key, int lane) {
+  int64_t lo = 0, hi = n;   // lies in [lo, hi]
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step - 1;
+    const uint32_t less = __ballot_sync(0xffffffffu, i < hi && sorted[i].x < key);   // ascending: a run of low lanes
+    const int k = __popc(less);
+    const int64_t next = lo + (k + 1) * step - 1;
+    lo += k * step;
+    if (next < hi) hi = next;
+  }
+  return lo;
+}
+
 // CTA (piece, slab of columns): a thread's N columns over the piece's positions; behind the pieces, CTAs that write the
 // zeros of the rows without a token.
 template <int DT, int GT, int N>
 __global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs A) {
   const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
-  depends_wait();
+  depends_begin();
+  __shared__ int64_t range[2];
+  __shared__ uint8_t there[kZeros];
   if ((int64_t)blockIdx.x >= A.pieces) {
-    if (col >= A.cols) return;
     float zero[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) zero[k] = 0.0f;
-    const int64_t r0 = ((int64_t)blockIdx.x - A.pieces) * kPiece;
-    for (int64_t r = r0; r < r0 + kPiece && r < A.vocab; ++r)
-      if (!A.present[r]) store_cols<GT, N>(A.dtable, r * A.ld_dtable + col, zero);
+    const int64_t r0 = ((int64_t)blockIdx.x - A.pieces) * kZeros;
+    const int rows = (int)(A.vocab - r0 < kZeros ? A.vocab - r0 : kZeros);
+    if (threadIdx.x < 64) {   // the positions of these rows' tokens
+      const int warp = threadIdx.x >> 5;
+      const int64_t at = first_at_least(A.sorted, A.n, (uint32_t)(r0 + (warp ? rows : 0)), threadIdx.x & 31);
+      if ((threadIdx.x & 31) == 0) range[warp] = at;
+      there[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) there[A.sorted[i].x - (uint32_t)r0] = 1;
+    __syncthreads();
+    if (col >= A.cols) return;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      if (!there[r]) store_cols<GT, N>(A.dtable, (r0 + r) * A.ld_dtable + col, zero);
     return;
   }
   __shared__ uint2 mine[kPiece + 2];   // the neighbours' keys at both ends
@@ -365,14 +454,16 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs A) {
 template <int GT, int N>
 __global__ void __launch_bounds__(kThreads) join_kernel(SumArgs A) {
   const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
-  depends_wait();
+  depends_begin();
   const int64_t p = blockIdx.x, last = (p + 1) * kPiece - 1;
   if (last + 1 >= A.n || col >= A.cols) return;
   const uint32_t key = A.sorted[last].x;
   if (key >= (uint32_t)A.vocab || A.sorted[last + 1].x != key) return;
   if (A.sorted[p * kPiece].x == key && p > 0 && A.sorted[p * kPiece - 1].x == key) return;   // it began before
-  // the last piece that the run reaches: it holds whole pieces up to there
-  int64_t lo = p + 1, hi = A.pieces;   // first piece in [lo, hi) whose first key differs
+  // the first piece behind it that begins with another key: most runs end in the next one, so the search starts there
+  int64_t lo = p + 2, hi = p + 3, step = 1;
+  while (hi < A.pieces && A.sorted[(hi - 1) * kPiece].x == key) lo = hi, step *= 2, hi += step;
+  if (hi > A.pieces) hi = A.pieces;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
     if (A.sorted[mid * kPiece].x == key) lo = mid + 1;
@@ -408,7 +499,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SumArgs A) {
 
 struct Layout {
   int passes, n_cta, pieces;
-  size_t pairs[2], counts, present, partial, total;
+  size_t pairs[2], counts, partial, total;
   int64_t ldp;
 };
 
@@ -422,9 +513,8 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t cols) {
   size_t at = 0;
   for (size_t& p : L.pairs) p = at, at += round_up((size_t)n * 8, 256);
   L.counts = at, at += round_up((size_t)kDigits * L.n_cta * 4, 256);
-  L.present = at, at += round_up((size_t)vocab, 256);
   L.partial = at, at += round_up((size_t)L.pieces * 2 * L.ldp * 4, 256);
-  L.total = at;
+  L.total = std::max<size_t>(at, 256);   // no tokens: 0 would be a refusal
   return L;
 }
 
@@ -440,10 +530,26 @@ bool rows_ok(const void* p, int64_t ld, int64_t cols, int es) {
 bool is_type(int dt) { return dt == QMUON_BF16 || dt == QMUON_FP16 || dt == QMUON_FP32; }
 bool tokens_ok(const void* p, int bits) { return p && (bits == 32 || bits == 64) && is_aligned(p, bits / 8); }
 
+cudaError_t launch_cluster(const SortArgs& A, cudaStream_t s) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = A.n_cta;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(A.n_cta);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, cluster_sort_kernel, A);
+}
+
 template <int DT, int GT, int N>
 cudaError_t launch_sums(const SumArgs& A, cudaStream_t s) {
   const unsigned slabs = (unsigned)ceil_div(A.cols, (int64_t)kThreads * N);
-  const int64_t zeros = A.accumulate ? 0 : ceil_div(A.vocab, kPiece);
+  const int64_t zeros = A.accumulate ? 0 : ceil_div(A.vocab, kZeros);
   const int threads = (int)std::min<int64_t>(kThreads, round_up((size_t)ceil_div(A.cols, N), 32));
   cudaError_t e = launch_dependent(sum_kernel<DT, GT, N>, dim3((unsigned)(A.pieces + zeros), slabs), dim3(std::max(threads, 64)), 0, s, A);
   if (e == cudaSuccess && A.pieces > 1) e = launch_dependent(join_kernel<GT, N>, dim3(A.pieces - 1, slabs), dim3(std::max(threads, 64)), 0, s, A);
@@ -504,20 +610,32 @@ extern "C" qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* c, 
     if (c->n_tokens == 0 && c->accumulate) return QMUON_OK;
     unsigned char* w = static_cast<unsigned char*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint8_t* present = w + L.present;
     cudaError_t e = cudaSuccess;
-    if (!c->accumulate) e = cudaMemsetAsync(present, 0, (size_t)c->vocab, s);
-    const uint2* sorted = nullptr;
-    for (int p = 0; c->n_tokens > 0 && p < L.passes && e == cudaSuccess; ++p) {
-      SortArgs A{c->tokens, sorted, reinterpret_cast<uint2*>(w + L.pairs[p & 1]), reinterpret_cast<uint32_t*>(w + L.counts),
-                 p == 0 && !c->accumulate ? present : nullptr, c->n_tokens, c->vocab, c->token_bits == 64, p * kDigitBits, L.n_cta};
-      e = launch_dependent(count_kernel, dim3(L.n_cta), dim3(kSortThreads), 0, s, A);
-      if (e == cudaSuccess) e = launch_dependent(offsets_kernel, dim3(1), dim3(kDigits), 0, s, A.counts, L.n_cta);
-      if (e == cudaSuccess) e = launch_dependent(scatter_kernel, dim3(L.n_cta), dim3(kSortThreads), 0, s, A);
-      sorted = A.out;
+    const uint2* sorted = reinterpret_cast<uint2*>(w + L.pairs[(L.passes - 1) & 1]);
+    if (c->n_tokens > 0) {
+      SortArgs A{};
+      A.tokens = c->tokens;
+      A.counts = reinterpret_cast<uint32_t*>(w + L.counts);
+      A.n = c->n_tokens, A.vocab = c->vocab, A.bits64 = c->token_bits == 64;
+      A.n_cta = L.n_cta, A.passes = L.passes;
+      // equal shares: the warps of the last CTA are not idle where there are few tokens
+      A.share = (int32_t)round_up((size_t)ceil_div(c->n_tokens, (int64_t)L.n_cta * kSortWarps), 32);
+      for (int i = 0; i < 2; ++i) A.pairs[i] = reinterpret_cast<uint2*>(w + L.pairs[i]);
+      if (L.n_cta <= kSortCluster) {
+        e = launch_cluster(A, s);
+      } else {
+        A.share = kSortKeys / kSortWarps;   // as count_kernel takes them
+        for (int p = 0; p < L.passes && e == cudaSuccess; ++p, A.shift += kDigitBits) {
+          A.out = A.pairs[p & 1];
+          e = launch_dependent(count_kernel, dim3(L.n_cta), dim3(kSortThreads), 0, s, A);
+          if (e == cudaSuccess) e = launch_dependent(offsets_kernel, dim3(1), dim3(kDigits), 0, s, A.counts, L.n_cta);
+          if (e == cudaSuccess) e = launch_dependent(scatter_kernel, dim3(L.n_cta), dim3(kSortThreads), 0, s, A);
+          A.in = A.out;
+        }
+      }
     }
     if (e != cudaSuccess) return set_error("qmuon_embedding_backward (sort)", e);
-    const SumArgs A{sorted, c->dout, c->dtable, reinterpret_cast<float*>(w + L.partial), present, c->n_tokens, c->vocab, c->ld_dout,
+    const SumArgs A{sorted, c->dout, c->dtable, reinterpret_cast<float*>(w + L.partial), c->n_tokens, c->vocab, c->ld_dout,
                     c->ld_dtable, L.ldp, (int32_t)c->cols, L.pieces, c->accumulate != 0, c->scale};
     e = c->dtype == QMUON_BF16   ? launch_sums_of<QMUON_BF16>(A, c->grad_dtype, s)
         : c->dtype == QMUON_FP16 ? launch_sums_of<QMUON_FP16>(A, c->grad_dtype, s)

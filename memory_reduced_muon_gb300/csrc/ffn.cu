@@ -39,10 +39,11 @@ constexpr int kTile = 256, kBK = 64;
 constexpr int kInnerTile = 128;                    // columns of gate, and of up, in a forward tile
 constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter
 constexpr int kThreads = 64 + 32 * kEpiWarps;      // warp 0 TMA, warp 1 MMA, warps 2.. epilogue
-constexpr int kStages = 7;
+constexpr int kStages = 6;
 constexpr uint32_t kStageBytes = 4 * kBox;         // per CTA: 128 x 64 of A, 128 x 64 of B
+constexpr uint32_t kRowBytes = 32 * 32 * 4;        // of each epilogue warp: 32 rows x 32 columns that are not accessed in vectors
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
-constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + kEpiWarps * kRowBytes + 1024 + 256;
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
 constexpr int kGroupM = 8;                         // tile rows that run side by side
 
@@ -192,50 +193,77 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn) {
          ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
-// A thread's 32 columns of gate and up: what the forward stores.
-template <int DT, int ACT>
-__device__ __forceinline__ void finish_forward(const GemmArgs& A, int64_t r, int64_t c, const float (&g)[32], const float (&u)[32]) {
+// W columns of gate and up from column c of row r, n of them valid (0: none): what the forward pass stores.  Every lane
+// of the warp calls this.
+template <int DT, int ACT, int W>
+__device__ __forceinline__ void finish_forward(const GemmArgs& A, int64_t r, int64_t c, int n, const float (&g)[W], const float (&u)[W],
+                                               float* stage) {
   constexpr int es = elem_size(DT);
-  const int n = (int)(A.inner - c < 32 ? A.inner - c : 32);
-  float h[32];
+  auto at = [&](void* base, int64_t ld) { return static_cast<unsigned char*>(base) + (n ? (r * ld + c) * es : 0); };
+  float h[W];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) h[i] = act_of<ACT>(g[i]) * u[i];
-  store_row32<DT>(static_cast<unsigned char*>(A.h) + (r * A.ld_h + c) * es, n, A.vec_h, h);
+  for (int i = 0; i < W; ++i) h[i] = act_of<ACT>(g[i]) * u[i];
+  store_rows<DT, W>(at(A.h, A.ld_h), n, A.vec_h, h, stage);
   if (A.saved == QMUON_SAVE_SAME) {
-    store_row32<DT>(static_cast<unsigned char*>(A.gate) + (r * A.ld_gate + c) * es, n, A.vec_gate, g);
-    store_row32<DT>(static_cast<unsigned char*>(A.up) + (r * A.ld_up + c) * es, n, A.vec_up, u);
+    store_rows<DT, W>(at(A.gate, A.ld_gate), n, A.vec_gate, g, stage);
+    store_rows<DT, W>(at(A.up, A.ld_up), n, A.vec_up, u, stage);
   } else if (A.saved == QMUON_SAVE_MXFP8) {
-    const int64_t b = (r * A.inner + c) >> 5;
-    A.gate_scale[b] = (uint8_t)encode_row32(static_cast<uint8_t*>(A.gate) + 32 * b, A.vec_gate, g);
-    A.up_scale[b] = (uint8_t)encode_row32(static_cast<uint8_t*>(A.up) + 32 * b, A.vec_up, u);
+    const int64_t e = n ? r * A.inner + c : 0;
+    const int gs = encode_row<W>(static_cast<uint8_t*>(A.gate) + e, n > 0, A.vec_gate, g);
+    const int us = encode_row<W>(static_cast<uint8_t*>(A.up) + e, n > 0, A.vec_up, u);
+    if (n && (e & 31) == 0) A.gate_scale[e >> 5] = (uint8_t)gs, A.up_scale[e >> 5] = (uint8_t)us;
   }
 }
-// The same of the backward pass: dgate and dup for the products, and h again.
-template <int DT, int ACT>
-__device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, int64_t c, const float (&g)[32], const float (&u)[32],
-                                                const uint32_t (&dh)[16]) {
+// The same of the backward pass, from dh's words: dgate and dup for the products, and h again.
+template <int DT, int ACT, int W>
+__device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, int64_t c, int n, const float (&g)[W], const float (&u)[W],
+                                                const uint32_t (&dh)[W / 2], float* stage) {
   constexpr int es = elem_size(DT);
-  const int n = (int)(A.inner - c < 32 ? A.inner - c : 32);
-  float h[32], dg[32], du[32];
+  float h[W], dg[W], du[W];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < W; ++i) {
     const float2 a = act_and_slope<ACT>(g[i]), d = unpack2<DT>(dh[i >> 1]);
     const float x = i & 1 ? d.y : d.x;
     h[i] = a.x * u[i];
     dg[i] = x * u[i] * a.y;
     du[i] = x * a.x;
   }
-  // the workspace's rows are padded to 32 bytes: vectors wherever all 32 columns exist
-  store_row32<DT>(static_cast<unsigned char*>(A.dgate) + (r * A.ld_d + c) * es, n, 2, dg);
-  store_row32<DT>(static_cast<unsigned char*>(A.dup) + (r * A.ld_d + c) * es, n, 2, du);
-  if (A.h) store_row32<DT>(static_cast<unsigned char*>(A.h) + (r * A.ld_h + c) * es, n, A.vec_h, h);
+  // the workspace's rows are padded to 32 bytes
+  const int64_t e = n ? (r * A.ld_d + c) * es : 0;
+  store_row<DT, W>(static_cast<unsigned char*>(A.dgate) + e, n, 2, dg);
+  store_row<DT, W>(static_cast<unsigned char*>(A.dup) + e, n, 2, du);
+  if (A.h) store_rows<DT, W>(static_cast<unsigned char*>(A.h) + (n ? (r * A.ld_h + c) * es : 0), n, A.vec_h, h, stage);
 }
+// W columns of dh as words.
+template <int DT, int W>
+__device__ __forceinline__ void load_dh(const GemmArgs& A, int64_t r, int64_t c, int n, uint32_t (&w)[W / 2], float* stage) {
+  const unsigned char* p = static_cast<const unsigned char*>(A.dh) + (n ? (r * A.ld_dh + c) * elem_size(DT) : 0);
+  if (A.vec_dh && n == W) {
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) {
+      const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+  } else {
+    float v[W];
+    load_rows<DT, W>(p, n, A.vec_dh, v, stage);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+  }
+}
+// The q-th N elements of an array.
+template <int N, class T, int M>
+__device__ __forceinline__ const T (&part_of(const T (&v)[M], int q))[N] {
+  return *reinterpret_cast<const T(*)[N]>(v + N * q);
+}
+__device__ __forceinline__ int valid_columns(int64_t left, int most) { return left >= most ? most : left > 0 ? (int)left : 0; }
 
 template <int KIND, int DT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ GemmArgs A) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  float* rows_of_warp = reinterpret_cast<float*>(smem + kStages * kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + kEpiWarps * kRowBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
   const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
@@ -255,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     }
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 5) prefetch_map(lane < 2 ? &A.a[lane] : &A.b[lane - 2]);
   if (warp == 1) {
     tmem_alloc_cg<2>(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_cg<2>();
@@ -263,8 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
   __syncwarp();
   cluster_sync_all();   // the peer's barriers exist before anyone signals them
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  depends_wait();
+  depends_begin();
   const uint32_t tmem = *tmem_slot;
   const int inner_blocks = KIND == K_GRAD ? blocks_of(A.inner) : 0;
 
@@ -376,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     // ---- epilogue: warps 2..9; TMEM lane quarter = warp % 4 ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_l = cluster_map(tempty0, 0);
+    float* stage = rows_of_warp + (warp - 2) * (kRowBytes / 4);
     Unit u;
     for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
       const int64_t r = u.m0 + 128 * rank + quarter * 32 + lane;
@@ -386,8 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int64_t c = c0 + 32 * j;
-          const int n = r < A.rows && c < A.inner ? (int)(A.inner - c < 32 ? A.inner - c : 32) : 0;
-          load_words32(static_cast<const unsigned char*>(A.dh) + (n ? (r * A.ld_dh + c) * elem_size(DT) : 0), n, A.vec_dh, dh[j]);
+          load_dh<DT, 32>(A, r, c, r < A.rows ? valid_columns(A.inner - c, 32) : 0, dh[j], stage);
         }
       }
       bool ok = mbar_wait(tfull0 + 8 * acc, use & 1, A.hdr, 0x2400u | KIND);
@@ -415,16 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 32; ++k) g[k] = __uint_as_float(gv[k]), v[k] = __uint_as_float(uv[k]);
           const int64_t c = c0 + 32 * j;
-          if (r >= A.rows || c >= A.inner) continue;
+          const int n = r < A.rows ? valid_columns(A.inner - c, 32) : 0;
           if (A.part) {   // [split][gate, up][rows][ld_part]
-            const int n = (int)(A.ld_part - c < 32 ? A.ld_part - c : 32);
-            float* p = A.part + (((int64_t)u.split * 2) * A.rows + r) * A.ld_part + c;
-            store_row32<QMUON_FP32>(p, n, 2, g);
-            store_row32<QMUON_FP32>(p + A.rows * A.ld_part, n, 2, v);
+            const int np = n ? valid_columns(A.ld_part - c, 32) : 0;
+            float* p = A.part + (n ? (((int64_t)u.split * 2) * A.rows + r) * A.ld_part + c : 0);
+            store_row<QMUON_FP32, 32>(p, np, 2, g);
+            store_row<QMUON_FP32, 32>(p + A.rows * A.ld_part, np, 2, v);
           } else if constexpr (KIND == K_FWD) {
-            finish_forward<DT, ACT>(A, r, c, g, v);
+            finish_forward<DT, ACT, 32>(A, r, c, n, g, v, stage);
           } else if constexpr (KIND == K_BWD) {
-            finish_backward<DT, ACT>(A, r, c, g, v, dh[j]);
+            // in halves: the registers do not hold 32 columns of everything
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              finish_backward<DT, ACT, 16>(A, r, c + 16 * q, valid_columns(n - 16 * q, 16), part_of<16>(g, q), part_of<16>(v, q),
+                                           part_of<8>(dh[j], q), stage);
           }
         }
       } else {
@@ -439,27 +471,25 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(av[k]);
           const int64_t c = c0 + 32 * j;
-          if (r >= rows || c >= A.width) continue;
-          const int n = (int)(A.width - c < 32 ? A.width - c : 32);
+          const int n = r < rows ? valid_columns(A.width - c, 32) : 0;
           float* part = u.kind == 0 ? A.part : A.part_w;
           if (part) {   // dx: [split][rows][ld_part]; dW: [weight][split][inner][ld_part]
             const int64_t slice = u.kind == 0 ? u.split : (int64_t)(u.kind - 1) * A.splits_w + u.split;
-            const int np = (int)(A.ld_part - c < 32 ? A.ld_part - c : 32);
-            store_row32<QMUON_FP32>(part + (slice * rows + r) * A.ld_part + c, np, 2, v);
+            store_row<QMUON_FP32, 32>(part + (n ? (slice * rows + r) * A.ld_part + c : 0), n ? valid_columns(A.ld_part - c, 32) : 0, 2, v);
           } else if (u.kind == 0) {
-            store_row32<DT>(static_cast<unsigned char*>(A.dx) + (r * A.ld_dx + c) * elem_size(DT), n, A.vec_dx, v);
+            store_rows<DT, 32>(static_cast<unsigned char*>(A.dx) + (n ? (r * A.ld_dx + c) * elem_size(DT) : 0), n, A.vec_dx, v, stage);
           } else {
             const int w = u.kind - 1;
-            unsigned char* p = static_cast<unsigned char*>(A.dw[w]) + (r * A.ld_dw[w] + c) * (A.dw_f32 ? 4 : elem_size(DT));
+            unsigned char* p = static_cast<unsigned char*>(A.dw[w]) + (n ? (r * A.ld_dw[w] + c) * (A.dw_f32 ? 4 : elem_size(DT)) : 0);
             if (A.accumulate) {
               float old[32];
-              if (A.dw_f32) load_row32<QMUON_FP32>(p, n, A.vec_dw[w], old);
-              else load_row32<DT>(p, n, A.vec_dw[w], old);
+              if (A.dw_f32) load_rows<QMUON_FP32, 32>(p, n, A.vec_dw[w], old, stage);
+              else load_rows<DT, 32>(p, n, A.vec_dw[w], old, stage);
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] += old[k];
             }
-            if (A.dw_f32) store_row32<QMUON_FP32>(p, n, A.vec_dw[w], v);
-            else store_row32<DT>(p, n, A.vec_dw[w], v);
+            if (A.dw_f32) store_rows<QMUON_FP32, 32>(p, n, A.vec_dw[w], v, stage);
+            else store_rows<DT, 32>(p, n, A.vec_dw[w], v, stage);
           }
         }
       }
@@ -481,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 // element by element: gate and up from partial sums, from their 16-bit copies
 // or from their carriers
 // ---------------------------------------------------------------------------
-constexpr int kElemThreads = 256;
+constexpr int kElemThreads = 256, kElemCols = 16;
+constexpr size_t kElemRows = (size_t)kElemThreads * kElemCols * 4;   // shared memory where rows are not accessed in vectors
 enum { FROM_PART = 0, FROM_SAME = 1, FROM_MXFP8 = 2 };
 
 struct ElemArgs {
@@ -492,92 +523,233 @@ struct ElemArgs {
   const uint8_t *gate_scale, *up_scale;
   int64_t ld_gate, ld_up;
   int32_t vec_in;        // rows of gate and up
+  int32_t clear;         // the workspace's header has not been cleared
 };
 
-// A thread takes 32 columns of a row, as a thread of the product's epilogue does.
-template <int DT, int ACT, int FROM, bool BWD>
-__global__ void __launch_bounds__(kElemThreads) elem_kernel(const __grid_constant__ ElemArgs E) {
-  const GemmArgs& A = E.A;
-  constexpr int es = elem_size(DT);
-  const int64_t per = (A.inner + 31) >> 5, i = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
-  depends_wait();
-  if (i >= A.rows * per) return;
-  const int64_t r = i / per, c = (i - r * per) * 32;
-  const int n = (int)(A.inner - c < 32 ? A.inner - c : 32);
-  float g[32], u[32];
-  if constexpr (FROM == FROM_PART) {
-    const int np = (int)(A.ld_part - c < 32 ? A.ld_part - c : 32);
-    const float* p = E.part + r * A.ld_part + c;
-    load_row32<QMUON_FP32>(p, np, 2, g);
-    load_row32<QMUON_FP32>(p + A.rows * A.ld_part, np, 2, u);
-    for (int s = 1; s < E.splits; ++s) {
-      p += 2 * A.rows * A.ld_part;
-      float a[32], b[32];
-      load_row32<QMUON_FP32>(p, np, 2, a);
-      load_row32<QMUON_FP32>(p + A.rows * A.ld_part, np, 2, b);
-#pragma unroll
-      for (int k = 0; k < 32; ++k) g[k] += a[k], u[k] += b[k];
-    }
-  } else if constexpr (FROM == FROM_SAME) {
-    load_row32<DT>(static_cast<const unsigned char*>(E.gate) + (r * E.ld_gate + c) * es, n, E.vec_in, g);
-    load_row32<DT>(static_cast<const unsigned char*>(E.up) + (r * E.ld_up + c) * es, n, E.vec_in, u);
-  } else {
-    const int64_t b = (r * A.inner + c) >> 5;
-    auto decode = [&](const void* codes, const uint8_t* scale, float (&v)[32]) {
-      const uint8_t* p = static_cast<const uint8_t*>(codes) + 32 * b;
-      uint32_t w[8];
-      if (E.vec_in == 2) {
-        load32b(p, w);
-      } else {
-        const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 16);
-        w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
-      }
-      const float s = scale_of_e8m0(scale[b]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 x = mul2_rn(e4m3x2_to(w[k] & 0xFFFFu), s), y = mul2_rn(e4m3x2_to(w[k] >> 16), s);
-        v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = y.x, v[4 * k + 3] = y.y;
-      }
-    };
-    decode(E.gate, E.gate_scale, g);
-    decode(E.up, E.up_scale, u);
-  }
-  if constexpr (BWD) {
-    uint32_t dh[16];
-    load_words32(static_cast<const unsigned char*>(A.dh) + (r * A.ld_dh + c) * es, n, A.vec_dh, dh);
-    finish_backward<DT, ACT>(A, r, c, g, u, dh);
-  } else {
-    finish_forward<DT, ACT>(A, r, c, g, u);
-  }
+// The workspace's header, by the first CTA of a kernel that is complete before any kernel looks at it.
+__device__ __forceinline__ void clear_header(WsHeader* h) {
+  if (blockIdx.x == 0 && threadIdx.x < kWsHeader / 4) reinterpret_cast<uint32_t*>(h)[threadIdx.x] = 0u;
 }
 
-// Sums of split products: rows x cols of [splits][rows][ld_part] to the type of the result.
+// A thread takes 16 columns of a row.  (Of 32, as in the product's epilogue, the 160 registers left 12 warps on an SM:
+// 8192 x 14336 from carriers in 214 us.)
+template <int DT, int ACT, int FROM, bool BWD>
+__global__ void __launch_bounds__(kElemThreads) elem_kernel(const __grid_constant__ ElemArgs E) {
+  extern __shared__ float elem_rows[];
+  constexpr int W = kElemCols, es = elem_size(DT);
+  const GemmArgs& A = E.A;
+  float* stage = elem_rows + (threadIdx.x >> 5) * 32 * W;
+  const int64_t per = (A.inner + W - 1) / W, i = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
+  depends_begin();
+  if (E.clear) clear_header(A.hdr);
+  int64_t r = 0, c = 0;
+  int n = 0;
+  if (i < A.rows * per) {
+    r = i / per;
+    c = (i - r * per) * W;
+    n = valid_columns(A.inner - c, W);
+  }
+  uint32_t dh[W / 2];
+  if constexpr (BWD) load_dh<DT, W>(A, r, c, n, dh, stage);
+  float g[W], u[W];
+  if constexpr (FROM == FROM_PART) {
+    const int np = n ? valid_columns(A.ld_part - c, W) : 0;
+    const float* p = E.part + (n ? r * A.ld_part + c : 0);
+    load_row<QMUON_FP32, W>(p, np, 2, g);
+    load_row<QMUON_FP32, W>(p + A.rows * A.ld_part, np, 2, u);
+    for (int s = 1; s < E.splits; ++s) {
+      p += 2 * A.rows * A.ld_part;
+      float a[W], b[W];
+      load_row<QMUON_FP32, W>(p, np, 2, a);
+      load_row<QMUON_FP32, W>(p + A.rows * A.ld_part, np, 2, b);
+#pragma unroll
+      for (int k = 0; k < W; ++k) g[k] += a[k], u[k] += b[k];
+    }
+  } else if constexpr (FROM == FROM_SAME) {
+    load_rows<DT, W>(static_cast<const unsigned char*>(E.gate) + (n ? (r * E.ld_gate + c) * es : 0), n, E.vec_in, g, stage);
+    load_rows<DT, W>(static_cast<const unsigned char*>(E.up) + (n ? (r * E.ld_up + c) * es : 0), n, E.vec_in, u, stage);
+  } else {
+    const int64_t e = n ? r * A.inner + c : 0;
+    decode_row<W>(static_cast<const uint8_t*>(E.gate) + e, E.vec_in, scale_of_e8m0(E.gate_scale[e >> 5]), g);
+    decode_row<W>(static_cast<const uint8_t*>(E.up) + e, E.vec_in, scale_of_e8m0(E.up_scale[e >> 5]), u);
+  }
+  if constexpr (BWD) finish_backward<DT, ACT, W>(A, r, c, n, g, u, dh, stage);
+  else finish_forward<DT, ACT, W>(A, r, c, n, g, u, stage);
+}
+
+// Sums of split products, rows x cols of [splits][rows][ld_part], to the type of the result; the products of a call
+// together in one launch.
+constexpr int kJoinCols = 8;
+struct Join {
+  const float* part;
+  void* out;
+  int64_t rows, cols, ld_part, ld, first;   // first: its first CTA
+  int32_t splits, vec, accumulate, dt;
+};
+struct JoinArgs {
+  Join job[3];
+  int32_t n;
+};
 template <int DT>
-__global__ void __launch_bounds__(kElemThreads) join_kernel(const float* part, int splits, int64_t rows, int64_t cols, int64_t ld_part,
-                                                            void* out, int64_t ld, int vec, int accumulate) {
-  const int64_t per = (cols + 31) >> 5, i = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
-  depends_wait();
-  if (i >= rows * per) return;
-  const int64_t r = i / per, c = (i - r * per) * 32;
-  const int n = (int)(cols - c < 32 ? cols - c : 32), np = (int)(ld_part - c < 32 ? ld_part - c : 32);
-  const float* p = part + r * ld_part + c;
-  float v[32];
-  load_row32<QMUON_FP32>(p, np, 2, v);
-  for (int s = 1; s < splits; ++s) {
-    p += rows * ld_part;
-    float a[32];
-    load_row32<QMUON_FP32>(p, np, 2, a);
+__device__ __forceinline__ void join_rows(const Join& J, int64_t r, int64_t c, int n, float (&v)[kJoinCols], float* stage) {
+  unsigned char* o = static_cast<unsigned char*>(J.out) + (n ? (r * J.ld + c) * elem_size(DT) : 0);
+  if (J.accumulate) {
+    float old[kJoinCols];
+    load_rows<DT, kJoinCols>(o, n, J.vec, old, stage);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] += a[k];
+    for (int k = 0; k < kJoinCols; ++k) v[k] += old[k];
   }
-  unsigned char* o = static_cast<unsigned char*>(out) + (r * ld + c) * elem_size(DT);
-  if (accumulate) {
-    float old[32];
-    load_row32<DT>(o, n, vec, old);
+  store_rows<DT, kJoinCols>(o, n, J.vec, v, stage);
+}
+__global__ void __launch_bounds__(kElemThreads) join_kernel(const __grid_constant__ JoinArgs A) {
+  __shared__ float rows[kElemThreads * kJoinCols];
+  constexpr int W = kJoinCols;
+  depends_begin();
+  const Join& J = A.job[A.n > 2 && blockIdx.x >= A.job[2].first ? 2 : A.n > 1 && blockIdx.x >= A.job[1].first ? 1 : 0];
+  const int64_t per = (J.cols + W - 1) / W, i = ((int64_t)blockIdx.x - J.first) * kElemThreads + threadIdx.x;
+  int64_t r = 0, c = 0;
+  int n = 0;
+  if (i < J.rows * per) {
+    r = i / per;
+    c = (i - r * per) * W;
+    n = valid_columns(J.cols - c, W);
+  }
+  const float* p = J.part + (n ? r * J.ld_part + c : 0);   // rows are padded to W
+  float v[W];
+  load_row<QMUON_FP32, W>(p, n ? W : 0, 2, v);
+#pragma unroll 4
+  for (int s = 1; s < J.splits; ++s) {
+    float a[W];
+    load_row<QMUON_FP32, W>(p + s * J.rows * J.ld_part, n ? W : 0, 2, a);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] += old[k];
+    for (int k = 0; k < W; ++k) v[k] += a[k];
   }
-  store_row32<DT>(o, n, vec, v);
+  float* stage = rows + (threadIdx.x >> 5) * 32 * W;
+  if (J.dt == QMUON_BF16) join_rows<QMUON_BF16>(J, r, c, n, v, stage);
+  else if (J.dt == QMUON_FP16) join_rows<QMUON_FP16>(J, r, c, n, v, stage);
+  else join_rows<QMUON_FP32>(J, r, c, n, v, stage);
+}
+
+// ---------------------------------------------------------------------------
+// few rows: the weights once through the cores' registers
+// ---------------------------------------------------------------------------
+// With few rows the time is the weights' way from DRAM.  A CTA takes 8 columns
+// of gate and the same 8 of up, as the 16 rows of an m16n8k16 product whose 8
+// columns are rows of x (NT such products for 8 NT rows): gate and up of a
+// column meet in one thread.  Its 8 warps take turns over K, 32 at a time: a
+// lane loads 16 bytes of a row of Wg, of Wu and of x at the same columns, in
+// which order K is summed does not matter, so the pieces go straight into the
+// operands' registers.  The warps' sums are added through shared memory in
+// order.  (The CTA pairs above leave it to a few SMs' loads in flight: one row of
+// 4096 x 14336 took 70 us.)
+constexpr int kFewThreads = 256, kFewCols = 8, kFewRows = 16;
+
+struct FewArgs {
+  GemmArgs A;
+  const void *x, *w[2];
+  int64_t ld_x, ld_w[2];
+};
+
+template <int DT>
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (DT == QMUON_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 elements from column k of a row of `width`, zeros behind its end and where the row is not there.  ONCE: not kept in L1.
+template <bool VEC, bool ONCE>
+__device__ __forceinline__ uint4 eight_of(const uint16_t* row, bool there, int64_t k, int64_t width) {
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (VEC) {
+    if (!there || k >= width) return q;
+    if constexpr (ONCE)
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(row + k) : "memory");
+    else
+      q = *reinterpret_cast<const uint4*>(row + k);
+  } else {
+    const int n = there ? valid_columns(width - k, 8) : 0;
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? row[k + i] : 0u;
+    q = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
+  }
+  return q;
+}
+
+template <int DT, int ACT, int NT, bool VEC>
+__global__ void __launch_bounds__(kFewThreads, 3) few_kernel(const __grid_constant__ FewArgs F) {
+  const GemmArgs& A = F.A;
+  constexpr int kWarps = kFewThreads / 32, U = 2;   // U steps of K at a time
+  __shared__ float4 sums[kWarps][NT * 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t j = (int64_t)blockIdx.x * kFewCols + g;
+  const bool there = j < A.inner;
+  const uint16_t* wg = static_cast<const uint16_t*>(F.w[0]) + (there ? j : 0) * F.ld_w[0];
+  const uint16_t* wu = static_cast<const uint16_t*>(F.w[1]) + (there ? j : 0) * F.ld_w[1];
+  const int64_t steps = (A.width + 31) >> 5;
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+  depends_begin();
+  clear_header(A.hdr);
+  uint4 a[U], b[U];
+  auto load = [&](int64_t s0, uint4 (&to_a)[U], uint4 (&to_b)[U]) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t k = (s0 + i * kWarps) * 32 + 8 * t;
+      to_a[i] = eight_of<VEC, true>(wg, there, k, A.width);
+      to_b[i] = eight_of<VEC, true>(wu, there, k, A.width);
+    }
+  };
+  load(warp, a, b);
+  for (int64_t s0 = warp; s0 < steps; s0 += kWarps * U) {
+    uint4 next_a[U], next_b[U];   // on their way while these are multiplied
+    load(s0 + kWarps * U, next_a, next_b);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t k = (s0 + i * kWarps) * 32 + 8 * t;
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        const int row = 8 * m + g;
+        const uint4 x = eight_of<VEC, false>(static_cast<const uint16_t*>(F.x) + (row < A.rows ? row : 0) * F.ld_x, row < A.rows, k, A.width);
+        mma_16x8x16<DT>(acc[m], a[i].x, b[i].x, a[i].y, b[i].y, x.x, x.y);
+        mma_16x8x16<DT>(acc[m], a[i].z, b[i].z, a[i].w, b[i].w, x.z, x.w);
+      }
+      a[i] = next_a[i], b[i] = next_b[i];
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < NT; ++m) sums[warp][m * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+  __syncthreads();
+  if (threadIdx.x >= NT * 32 || !there) return;
+  float4 v = sums[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const float4 q = sums[w][threadIdx.x];
+    v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {   // gate and up of column j, rows 2 t and 2 t + 1 of this thread's product
+    const int64_t row = 8 * warp + 2 * t + i;
+    if (row >= A.rows) break;
+    const float gate = i ? v.y : v.x, up = i ? v.w : v.z;
+    if (A.part) {   // [gate, up][rows][ld_part]
+      A.part[row * A.ld_part + j] = gate;
+      A.part[(A.rows + row) * A.ld_part + j] = up;
+    } else {
+      store_elem<DT>(A.h, row * A.ld_h + j, act_of<ACT>(gate) * up);
+      if (A.saved == QMUON_SAVE_SAME) {
+        store_elem<DT>(A.gate, row * A.ld_gate + j, gate);
+        store_elem<DT>(A.up, row * A.ld_up + j, up);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -625,9 +797,10 @@ struct Geometry {
   int32_t dx_m = 0, dx_n = 0, dx_splits = 1;
   int32_t dw_m = 0, dw_n = 0, dw_splits = 1;
   int64_t ld_fwd = 0, ld_w = 0, ld_d = 0;               // of partial gate/up, of partial dx/dW, of dgate/dup
-  size_t dgate = 0, dup = 0, x = 0, w[2] = {0, 0}, part = 0, part_w = 0, total = 0;
+  size_t dgate = 0, dup = 0, x = 0, w[2] = {0, 0}, part = 0, part_x = 0, part_w = 0, total = 0;
   int64_t ld_x = 0, ld_wp = 0;
   bool copy_x = false, copy_w[2] = {false, false};
+  bool few = false;                                     // the projections by few_kernel
 };
 
 // What a call lays out in its workspace, behind the header.
@@ -643,11 +816,16 @@ void lay_operands(Geometry& G, int64_t rows, int64_t width, int64_t inner, bool 
     if (G.copy_w[i]) lay(G, &G.w[i], (size_t)inner * G.ld_wp * 2);
 }
 
-void lay_projections(Geometry& G, int64_t rows, int64_t width, int64_t inner) {
+// `direct`: few rows need no partial sums.
+void lay_projections(Geometry& G, int64_t rows, int64_t width, int64_t inner, bool direct) {
+  G.ld_fwd = (int64_t)round_up((size_t)inner, 8);
+  if (G.few) {
+    if (!direct) lay(G, &G.part, (size_t)2 * rows * G.ld_fwd * 4);
+    return;
+  }
   G.tiles_m = (int32_t)ceil_div(rows, kTile);
   G.tiles_n = (int32_t)ceil_div(inner, kInnerTile);
   G.splits = pick_splits((int64_t)G.tiles_m * G.tiles_n, (int)ceil_div(width, kBK), G.pairs);
-  G.ld_fwd = (int64_t)round_up((size_t)inner, 8);
   if (G.splits > 1) lay(G, &G.part, (size_t)G.splits * 2 * rows * G.ld_fwd * 4);
 }
 
@@ -655,8 +833,10 @@ Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
   Geometry G;
   G.pairs = pairs;
   G.total = kWsHeader;
-  lay_operands(G, c.rows, c.width, c.inner, !tma_ready(c.x, c.ld_x), !tma_ready(c.w_gate, c.ld_w_gate), !tma_ready(c.w_up, c.ld_w_up));
-  lay_projections(G, c.rows, c.width, c.inner);
+  G.few = c.rows <= kFewRows;
+  if (!G.few)
+    lay_operands(G, c.rows, c.width, c.inner, !tma_ready(c.x, c.ld_x), !tma_ready(c.w_gate, c.ld_w_gate), !tma_ready(c.w_up, c.ld_w_up));
+  lay_projections(G, c.rows, c.width, c.inner, c.saved != QMUON_SAVE_MXFP8);
   return G;
 }
 
@@ -668,15 +848,16 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
   Geometry G;
   G.pairs = pairs;
   G.total = kWsHeader;
-  const bool w = needs_weights(c);
-  lay_operands(G, c.rows, c.width, c.inner, needs_x(c) && (c.x_scale || !tma_ready(c.x, c.ld_x)), w && !tma_ready(c.w_gate, c.ld_w_gate),
-               w && !tma_ready(c.w_up, c.ld_w_up));
+  G.few = c.rows <= kFewRows;
+  const bool w = c.dx || (c.saved == QMUON_SAVE_NONE && !G.few);   // few_kernel reads them as they are
+  lay_operands(G, c.rows, c.width, c.inner, needs_x(c) && (c.x_scale || ((c.dw_gate || !G.few) && !tma_ready(c.x, c.ld_x))),
+               w && !tma_ready(c.w_gate, c.ld_w_gate), w && !tma_ready(c.w_up, c.ld_w_up));
   G.ld_d = (int64_t)round_up((size_t)c.inner, 16);
   lay(G, &G.dgate, (size_t)c.rows * G.ld_d * 2);
   lay(G, &G.dup, (size_t)c.rows * G.ld_d * 2);
   G.ld_w = (int64_t)round_up((size_t)c.width, 8);
   const size_t behind = G.total;
-  if (c.saved == QMUON_SAVE_NONE) lay_projections(G, c.rows, c.width, c.inner);
+  if (c.saved == QMUON_SAVE_NONE) lay_projections(G, c.rows, c.width, c.inner, false);
   const size_t most = G.total;
   G.total = behind;   // the projections' partial sums are done with when the gradients' begin
   const int kbx = 2 * (int)ceil_div(c.inner, kBK), kbw = (int)ceil_div(c.rows, kBK);
@@ -690,12 +871,19 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
   }
   const int64_t tx = (int64_t)G.dx_m * G.dx_n, tw = 2 * (int64_t)G.dw_m * G.dw_n;
   if (tx + tw < 2 * (int64_t)G.pairs) {
-    // few tiles: units of about one pair's share of all K blocks, and of 8 at least
-    const int64_t share = std::max<int64_t>(8, ceil_div(tx * kbx + tw * kbw, G.pairs));
-    G.dx_splits = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(kbx, share)));
-    G.dw_splits = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(kbw, share)));
+    // few tiles: units of at most `most` K blocks, of whole tiles or of a pair's share of all blocks and its multiples,
+    // whichever is estimated to end first (the longest unit, or all of them over the pairs; partial sums cost about 16
+    // blocks for their way through memory and their kernel)
+    const int64_t all = tx * kbx + tw * kbw, share = std::max<int64_t>(4, ceil_div(all, G.pairs));
+    int64_t best = INT64_MAX;
+    for (const int64_t most : {(int64_t)1 << 40, 4 * share, 2 * share, share}) {
+      const int64_t sx = tx ? std::min<int64_t>(32, ceil_div(kbx, most)) : 1, sw = tw ? std::min<int64_t>(32, ceil_div(kbw, most)) : 1;
+      const int64_t longest = std::max(tx ? ceil_div(kbx, sx) : 0, tw ? ceil_div(kbw, sw) : 0) + 6;
+      const int64_t cost = std::max(longest, ceil_div(all + 6 * (tx * sx + tw * sw), G.pairs)) + (sx > 1 || sw > 1 ? 16 : 0);
+      if (cost < best) best = cost, G.dx_splits = (int32_t)sx, G.dw_splits = (int32_t)sw;
+    }
   }
-  if (c.dx && G.dx_splits > 1) lay(G, &G.part, (size_t)G.dx_splits * c.rows * G.ld_w * 4);
+  if (c.dx && G.dx_splits > 1) lay(G, &G.part_x, (size_t)G.dx_splits * c.rows * G.ld_w * 4);
   if (c.dw_gate && G.dw_splits > 1) lay(G, &G.part_w, (size_t)2 * G.dw_splits * c.inner * G.ld_w * 4);
   G.total = std::max(G.total, most);
   return G;
@@ -740,8 +928,10 @@ cudaError_t launch_gemm(const GemmArgs& A, int64_t units, int pairs, int dt, cud
 
 template <int DT, int FROM, bool BWD>
 cudaError_t launch_elem_of(const ElemArgs& E, cudaStream_t s) {
-  const int64_t grid = ceil_div(E.A.rows * ceil_div(E.A.inner, 32), kElemThreads);
-  auto go = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid), dim3(kElemThreads), 0, s, E); };
+  const int64_t grid = ceil_div(E.A.rows * ceil_div(E.A.inner, kElemCols), kElemThreads);
+  const bool vec = (!BWD || E.A.vec_dh) && (FROM != FROM_SAME || E.vec_in) && (!E.A.h || E.A.vec_h) &&
+                   (BWD || E.A.saved != QMUON_SAVE_SAME || (E.A.vec_gate && E.A.vec_up));
+  auto go = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid), dim3(kElemThreads), vec ? 0 : kElemRows, s, E); };
   if (E.A.act == QMUON_ACT_SILU) return go(elem_kernel<DT, QMUON_ACT_SILU, FROM, BWD>);
   if (E.A.act == QMUON_ACT_GELU) return go(elem_kernel<DT, QMUON_ACT_GELU, FROM, BWD>);
   return go(elem_kernel<DT, QMUON_ACT_GELU_TANH, FROM, BWD>);
@@ -751,34 +941,52 @@ cudaError_t launch_elem(const ElemArgs& E, int dt, cudaStream_t s) {
   return dt == QMUON_BF16 ? launch_elem_of<QMUON_BF16, FROM, BWD>(E, s) : launch_elem_of<QMUON_FP16, FROM, BWD>(E, s);
 }
 
-cudaError_t launch_join(const float* part, int splits, int64_t rows, int64_t cols, int64_t ld_part, void* out, int64_t ld, int dt,
-                        int accumulate, cudaStream_t s) {
-  const dim3 grid((unsigned)ceil_div(rows * ceil_div(cols, 32), kElemThreads));
-  const int vec = vec_class(out, ld, elem_size(dt));
-  auto go = [&](auto kernel) {
-    return launch_dependent(kernel, grid, dim3(kElemThreads), 0, s, part, splits, rows, cols, ld_part, out, ld, vec, accumulate);
+void add_join(JoinArgs& A, int64_t* grid, const float* part, int splits, int64_t rows, int64_t cols, int64_t ld_part, void* out, int64_t ld,
+              int dt, int accumulate) {
+  A.job[A.n++] = Join{part, out, rows, cols, ld_part, ld, *grid, splits, vec_class(out, ld, elem_size(dt)), accumulate, dt};
+  *grid += ceil_div(rows * ceil_div(cols, kJoinCols), kElemThreads);
+}
+
+template <int DT, int ACT, int NT>
+cudaError_t launch_few_of(const FewArgs& F, bool vec, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div(F.A.inner, kFewCols));
+  return vec ? launch_dependent(few_kernel<DT, ACT, NT, true>, grid, dim3(kFewThreads), 0, s, F)
+             : launch_dependent(few_kernel<DT, ACT, NT, false>, grid, dim3(kFewThreads), 0, s, F);
+}
+template <int DT, int ACT>
+cudaError_t launch_few_act(const FewArgs& F, cudaStream_t s) {
+  const bool vec = tma_ready(F.x, F.ld_x) && tma_ready(F.w[0], F.ld_w[0]) && tma_ready(F.w[1], F.ld_w[1]) && F.A.width % 8 == 0;
+  return F.A.rows <= 8 ? launch_few_of<DT, ACT, 1>(F, vec, s) : launch_few_of<DT, ACT, 2>(F, vec, s);
+}
+cudaError_t launch_few(const FewArgs& F, int dt, cudaStream_t s) {
+  auto of = [&](auto type) {
+    constexpr int DT = decltype(type)::value;
+    if (F.A.part || F.A.act == QMUON_ACT_SILU) return launch_few_act<DT, QMUON_ACT_SILU>(F, s);
+    return F.A.act == QMUON_ACT_GELU ? launch_few_act<DT, QMUON_ACT_GELU>(F, s) : launch_few_act<DT, QMUON_ACT_GELU_TANH>(F, s);
   };
-  return dt == QMUON_BF16 ? go(join_kernel<QMUON_BF16>) : dt == QMUON_FP16 ? go(join_kernel<QMUON_FP16>) : go(join_kernel<QMUON_FP32>);
+  return dt == QMUON_BF16 ? of(std::integral_constant<int, QMUON_BF16>{}) : of(std::integral_constant<int, QMUON_FP16>{});
 }
 
 // The operands as the tensor maps read them: the caller's arrays, or aligned copies in the workspace.
 cudaError_t bring_operands(const Geometry& G, unsigned char* ws, const void** x, int64_t* ld_x, const uint8_t* x_scale,
                            const void* (&w)[2], int64_t (&ld_w)[2], int64_t rows, int64_t width, int64_t inner, int dt, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
+  Repack jobs[3];
+  int n = 0;
   if (G.copy_x) {
     void* to = ws + G.x;
-    e = x_scale ? launch_decode(static_cast<const uint8_t*>(*x), x_scale, to, rows, width, G.ld_x, dt, s)
-                : launch_repack(*x, *ld_x, to, G.ld_x, rows, width, s);
+    if (x_scale) e = launch_decode(static_cast<const uint8_t*>(*x), x_scale, to, rows, width, G.ld_x, dt, s);
+    else jobs[n++] = Repack{static_cast<const uint16_t*>(*x), static_cast<uint16_t*>(to), *ld_x, G.ld_x, rows, width};
     *x = to;
     *ld_x = G.ld_x;
   }
-  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+  for (int i = 0; i < 2; ++i)
     if (G.copy_w[i]) {
-      e = launch_repack(w[i], ld_w[i], ws + G.w[i], G.ld_wp, inner, width, s);
+      jobs[n++] = Repack{static_cast<const uint16_t*>(w[i]), reinterpret_cast<uint16_t*>(ws + G.w[i]), ld_w[i], G.ld_wp, inner, width};
       w[i] = ws + G.w[i];
       ld_w[i] = G.ld_wp;
     }
-  return e;
+  return e == cudaSuccess ? launch_repack(jobs, n, s) : e;
 }
 
 constexpr int64_t kMaxDim = (int64_t)1 << 28;
@@ -870,12 +1078,6 @@ extern "C" qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* c, void* 
     GemmArgs A{};
     const void *x = c->x, *w[2] = {c->w_gate, c->w_up};
     int64_t ld_x = c->ld_x, ld_w[2] = {c->ld_w_gate, c->ld_w_up};
-    cudaError_t e = cudaMemsetAsync(b, 0, kWsHeader, s);
-    if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, nullptr, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
-    if (e != cudaSuccess) return set_error("qmuon_gated_ffn_forward (operands)", e);
-    if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) || !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
-        !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
-      return QMUON_ERR_CUDA;
     A.rows = c->rows, A.width = c->width, A.inner = c->inner;
     A.tiles_m = G.tiles_m, A.tiles_n = G.tiles_n, A.splits = G.splits;
     A.units = G.tiles_m * G.tiles_n * G.splits;
@@ -887,8 +1089,20 @@ extern "C" qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* c, void* 
     A.act = c->act, A.saved = c->saved;
     A.hdr = reinterpret_cast<WsHeader*>(b);
     A.ld_part = G.ld_fwd;
-    A.part = G.splits > 1 ? reinterpret_cast<float*>(b + G.part) : nullptr;
-    e = launch_gemm<K_FWD>(A, A.units, G.pairs, c->dtype, s);
+    A.part = G.part ? reinterpret_cast<float*>(b + G.part) : nullptr;
+    cudaError_t e;
+    if (G.few) {
+      e = launch_few(FewArgs{A, x, {w[0], w[1]}, ld_x, {ld_w[0], ld_w[1]}}, c->dtype, s);
+    } else {
+      e = cudaMemsetAsync(b, 0, kWsHeader, s);
+      if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, nullptr, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
+      if (e != cudaSuccess) return set_error("qmuon_gated_ffn_forward (operands)", e);
+      if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) ||
+          !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
+          !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
+        return QMUON_ERR_CUDA;
+      e = launch_gemm<K_FWD>(A, A.units, G.pairs, c->dtype, s);
+    }
     if (e == cudaSuccess && A.part) {
       ElemArgs E{};
       E.A = A;
@@ -930,7 +1144,9 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
     unsigned char* b = static_cast<unsigned char*>(ws);
     const void *x = c->x, *w[2] = {c->w_gate, c->w_up};
     int64_t ld_x = c->ld_x, ld_w[2] = {c->ld_w_gate, c->ld_w_up};
-    e = cudaMemsetAsync(b, 0, kWsHeader, s);
+    // the header is cleared by the first kernel that needs no wait, where there is one
+    if (c->saved == QMUON_SAVE_NONE && !G.few) e = cudaMemsetAsync(b, 0, kWsHeader, s);
+    const void* w_given[2] = {c->w_gate, c->w_up};
     if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, c->x_scale, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
     if (e != cudaSuccess) return set_error("qmuon_gated_ffn_backward (operands)", e);
 
@@ -946,12 +1162,16 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
       A.tiles_m = G.tiles_m, A.tiles_n = G.tiles_n, A.splits = G.splits;
       A.units = G.tiles_m * G.tiles_n * G.splits;
       A.ld_part = G.ld_fwd;
-      A.part = G.splits > 1 ? reinterpret_cast<float*>(b + G.part) : nullptr;
-      if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) ||
-          !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
-          !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
-        return QMUON_ERR_CUDA;
-      e = launch_gemm<K_BWD>(A, A.units, G.pairs, c->dtype, s);
+      A.part = G.part ? reinterpret_cast<float*>(b + G.part) : nullptr;
+      if (G.few) {
+        e = launch_few(FewArgs{A, x, {w_given[0], w_given[1]}, ld_x, {c->ld_w_gate, c->ld_w_up}}, c->dtype, s);
+      } else {
+        if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) ||
+            !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
+            !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
+          return QMUON_ERR_CUDA;
+        e = launch_gemm<K_BWD>(A, A.units, G.pairs, c->dtype, s);
+      }
       if (e == cudaSuccess && A.part) {
         E.A = A;
         E.part = A.part;
@@ -963,6 +1183,7 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
       E.A = A;
       E.gate = c->gate, E.up = c->up, E.gate_scale = c->gate_scale, E.up_scale = c->up_scale;
       E.ld_gate = c->ld_gate, E.ld_up = c->ld_up;
+      E.clear = 1;
       E.vec_in = mx ? std::min(vec_class(c->gate, 32, 1), vec_class(c->up, 32, 1))
                     : std::min(vec_class(c->gate, c->ld_gate, 2), vec_class(c->up, c->ld_up, 2));
       e = mx ? launch_elem<FROM_MXFP8, true>(E, c->dtype, s) : launch_elem<FROM_SAME, true>(E, c->dtype, s);
@@ -989,7 +1210,7 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
     A.vec_dw[0] = vec_class(c->dw_gate, c->ld_dw_gate, gs), A.vec_dw[1] = vec_class(c->dw_up, c->ld_dw_up, gs);
     A.dw_f32 = c->grad_dtype == QMUON_FP32, A.accumulate = c->accumulate != 0;
     A.ld_part = G.ld_w;
-    A.part = c->dx && G.dx_splits > 1 ? reinterpret_cast<float*>(b + G.part) : nullptr;
+    A.part = c->dx && G.dx_splits > 1 ? reinterpret_cast<float*>(b + G.part_x) : nullptr;
     A.part_w = c->dw_gate && G.dw_splits > 1 ? reinterpret_cast<float*>(b + G.part_w) : nullptr;
     if (!encode_map(&A.a[0], A.dgate, c->rows, c->inner, G.ld_d, c->dtype) ||
         !encode_map(&A.a[1], A.dup, c->rows, c->inner, G.ld_d, c->dtype))
@@ -999,11 +1220,13 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
       return QMUON_ERR_CUDA;
     if (c->dw_gate && !encode_map(&A.b[2], x, c->rows, c->width, ld_x, c->dtype)) return QMUON_ERR_CUDA;
     e = launch_gemm<K_GRAD>(A, units_x + units_w, pairs, c->dtype, s);
-    if (e == cudaSuccess && A.part)
-      e = launch_join(A.part, G.dx_splits, c->rows, c->width, G.ld_w, c->dx, c->ld_dx, c->dtype, 0, s);
-    for (int i = 0; i < 2 && e == cudaSuccess && A.part_w; ++i)
-      e = launch_join(A.part_w + (size_t)i * G.dw_splits * c->inner * G.ld_w, G.dw_splits, c->inner, c->width, G.ld_w, A.dw[i], A.ld_dw[i],
-                      c->grad_dtype, A.accumulate, s);
+    JoinArgs J{};
+    int64_t grid = 0;
+    if (A.part) add_join(J, &grid, A.part, G.dx_splits, c->rows, c->width, G.ld_w, c->dx, c->ld_dx, c->dtype, 0);
+    for (int i = 0; i < 2 && A.part_w; ++i)
+      add_join(J, &grid, A.part_w + (size_t)i * G.dw_splits * c->inner * G.ld_w, G.dw_splits, c->inner, c->width, G.ld_w, A.dw[i], A.ld_dw[i],
+               c->grad_dtype, A.accumulate);
+    if (e == cudaSuccess && J.n) e = launch_dependent(join_kernel, dim3((unsigned)grid), dim3(kElemThreads), 0, s, J);
     return e == cudaSuccess ? QMUON_OK : set_error("qmuon_gated_ffn_backward (launch)", e);
   });
 }

@@ -37,13 +37,13 @@ __device__ __forceinline__ void row_and_group(const Args& A, int64_t b, int64_t*
 template <int DT>
 __global__ void __launch_bounds__(kThreads) encode_kernel(Args A) {
   const int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  depends_wait();
+  depends_begin();
   if (b >= A.rows * A.per_row) return;
   int64_t row, group;
   row_and_group(A, b, &row, &group);
   float v[32];
-  load_row32<DT>(static_cast<const unsigned char*>(A.src) + (row * A.ld + 32 * group) * elem_size(DT), 32, A.vec, v);
-  A.scale_out[b] = (uint8_t)encode_row32(static_cast<uint8_t*>(A.dst) + 32 * b, A.pvec, v);
+  load_row<DT, 32>(static_cast<const unsigned char*>(A.src) + (row * A.ld + 32 * group) * elem_size(DT), 32, A.vec, v);
+  A.scale_out[b] = (uint8_t)encode_row<32>(static_cast<uint8_t*>(A.dst) + 32 * b, true, A.pvec, v);
 }
 
 // Rows that start anywhere: a warp per group, kUnroll groups at a time.
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) encode_lanes_kernel(Args A) {
   const int64_t total = A.rows * A.per_row;
   const int64_t b0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
   const int lane = threadIdx.x & 31;
-  depends_wait();
+  depends_begin();
   float v[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
@@ -78,26 +78,15 @@ __global__ void __launch_bounds__(kThreads) encode_lanes_kernel(Args A) {
 template <int DT>
 __global__ void __launch_bounds__(kThreads) decode_kernel(Args A) {
   const int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  depends_wait();
+  depends_begin();
   if (b >= A.rows * A.per_row) return;
   int64_t row, group;
   row_and_group(A, b, &row, &group);
-  const uint8_t* p = static_cast<const uint8_t*>(A.src) + 32 * b;
-  uint32_t w[8];
-  if (A.pvec == 2) {
-    load32b(p, w);
-  } else {
-    const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 16);
-    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
-  }
-  const float s = scale_of_e8m0(A.scale_in[b]);
   float v[32];
+  decode_row<32>(static_cast<const uint8_t*>(A.src) + 32 * b, A.pvec, scale_of_e8m0(A.scale_in[b]), v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 a = mul2_rn(e4m3x2_to(w[i] & 0xFFFFu), s), c = mul2_rn(e4m3x2_to(w[i] >> 16), s);
-    v[4 * i] = decoded<DT>(a.x), v[4 * i + 1] = decoded<DT>(a.y), v[4 * i + 2] = decoded<DT>(c.x), v[4 * i + 3] = decoded<DT>(c.y);
-  }
-  store_row32<DT>(static_cast<unsigned char*>(A.dst) + (row * A.ld + 32 * group) * elem_size(DT), 32, A.vec, v);
+  for (int i = 0; i < 32; ++i) v[i] = decoded<DT>(v[i]);
+  store_row<DT, 32>(static_cast<unsigned char*>(A.dst) + (row * A.ld + 32 * group) * elem_size(DT), 32, A.vec, v);
 }
 
 template <int DT>
@@ -105,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) decode_lanes_kernel(Args A) {
   const int64_t total = A.rows * A.per_row;
   const int64_t b0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
   const int lane = threadIdx.x & 31;
-  depends_wait();
+  depends_begin();
   uint32_t code[kUnroll], byte[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
@@ -127,20 +116,26 @@ __global__ void __launch_bounds__(kThreads) decode_lanes_kernel(Args A) {
 // Rows of 16-bit elements to rows that start on 16 bytes: eight elements per
 // thread, written as one vector; the elements behind the last are left as they
 // are (the tensor maps that read the copy end at the last column).
-__global__ void __launch_bounds__(kThreads) repack_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
-                                                          int64_t rows, int64_t cols) {
-  const int64_t per = (cols + 7) >> 3, e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  depends_wait();
-  if (e >= rows * per) return;
+struct RepackArgs {
+  Repack job[3];
+  int64_t first[3];   // the jobs' first CTAs
+  int32_t n;
+};
+__global__ void __launch_bounds__(kThreads) repack_kernel(const __grid_constant__ RepackArgs A) {
+  depends_begin();
+  const int k = A.n > 2 && blockIdx.x >= A.first[2] ? 2 : A.n > 1 && blockIdx.x >= A.first[1] ? 1 : 0;
+  const Repack& J = A.job[k];
+  const int64_t per = (J.cols + 7) >> 3, e = ((int64_t)blockIdx.x - A.first[k]) * kThreads + threadIdx.x;
+  if (e >= J.rows * per) return;
   const int64_t row = e / per, c = (e - row * per) * 8;
-  const uint16_t* p = src + row * ld_src + c;
+  const uint16_t* p = J.src + row * J.ld_src + c;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t a = c + 2 * i < cols ? p[2 * i] : 0u, b = c + 2 * i + 1 < cols ? p[2 * i + 1] : 0u;
+    const uint32_t a = c + 2 * i < J.cols ? p[2 * i] : 0u, b = c + 2 * i + 1 < J.cols ? p[2 * i + 1] : 0u;
     w[i] = a | (b << 16);
   }
-  *reinterpret_cast<uint4*>(dst + row * ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(J.dst + row * J.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <class K>
@@ -175,9 +170,16 @@ cudaError_t launch_decode(const uint8_t* payload, const uint8_t* scale, void* x,
   return pick(decode_kernel<QMUON_FP32>, decode_lanes_kernel<QMUON_FP32>);
 }
 
-cudaError_t launch_repack(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols, cudaStream_t s) {
-  const int64_t grid = ceil_div(rows * ((cols + 7) / 8), kThreads);
-  return launch_dependent(repack_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, src, ld_src, dst, ld_dst, rows, cols);
+cudaError_t launch_repack(const Repack* jobs, int n, cudaStream_t s) {
+  RepackArgs A{};
+  int64_t grid = 0;
+  for (int i = 0; i < n; ++i) {
+    A.job[i] = jobs[i];
+    A.first[i] = grid;
+    grid += ceil_div(jobs[i].rows * ((jobs[i].cols + 7) / 8), kThreads);
+  }
+  A.n = n;
+  return n == 0 ? cudaSuccess : launch_dependent(repack_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, A);
 }
 
 }  // namespace lm

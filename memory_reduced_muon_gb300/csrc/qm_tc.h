@@ -93,6 +93,10 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
 __device__ __forceinline__ void fence_tensormap(const CUtensorMap* map) {
   asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
 }
+// A tensor map among a kernel's parameters, ahead of the first copy that reads it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // ---- CTA-pair (cta_group::2) forms: every tcgen05 instruction of a kernel
 // uses the same CTA group, so each wrapper is templated on it ----
 template <int CG>

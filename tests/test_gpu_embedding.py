@@ -136,6 +136,13 @@ def test_gradient_of_long_runs(n, kind, accumulate):
     _backward(n, 10, 72, 0, 0, "bf16", "f32", kind, 64, accumulate)
 
 
+@pytest.mark.parametrize("n,vocab,kind", [(8192, 600, "all"), (8193, 600, "holes"), (50001, 300000, "holes"), (65536, 500, "all"),
+                                          (65537, 500, "all"), (131073, 90000, "holes"), (140000, 7, "one")])
+def test_gradient_of_many_tokens(n, vocab, kind):
+    """One CTA that sorts, clusters of them, and sorting by several kernels."""
+    _backward(n, vocab, 8, 0, 0, "f32", "f32", kind, 64, False)
+
+
 def test_gradient_of_no_tokens():
     for accumulate in (False, True):
         _backward(0, 70, 72, 8, 0, "bf16", "bf16", "all", 64, accumulate)
