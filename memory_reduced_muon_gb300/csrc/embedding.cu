@@ -119,11 +119,13 @@ cudaError_t launch_lookup(const LookupArgs& A, int sms, cudaStream_t s) {
 // adds their number to the warp's count.
 //
 // Up to 8 such CTAs are one cluster, whose barriers part the passes: one launch
-// sorts 65536 tokens.  More tokens take three kernels a pass (the CTAs' counts,
-// their sums, the moves).
+// sorts 65536 tokens.  That takes a few SMs 10 to 20 us, in which the others
+// write zeros to the table's last rows, those of tokens too.  More tokens take
+// three kernels a pass (the CTAs' counts, their sums, the moves).
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRounds = 16, kSortKeys = kSortThreads * kRounds;
-constexpr int kSortCluster = 8;
+constexpr int kSortCluster = 8, kClusterKeys = kSortWarps * 64;   // a CTA's keys before the cluster grows
+constexpr int64_t kFillBytes = (int64_t)64 << 20;
 static_assert(kSortThreads == kDigits, "a thread per digit");
 
 struct SortArgs {
@@ -136,6 +138,10 @@ struct SortArgs {
   int32_t share;         // keys of a warp, a multiple of 32
   int32_t passes;        // cluster_sort_kernel
   uint2* pairs[2];       // cluster_sort_kernel: where odd and even passes leave the pairs
+  // cluster_sort_kernel, CTAs behind the first cluster: zeros to the last `fill` rows of the table's gradient
+  unsigned char* table;
+  int64_t fill, ld_bytes;
+  int32_t vecs;          // of 16 bytes in a row
 };
 
 __device__ __forceinline__ uint2 key_of(const SortArgs& A, int64_t i) {
@@ -219,6 +225,12 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(SortArgs A) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = threadIdx.x;
   const int64_t first = ((int64_t)blockIdx.x * kSortWarps + warp) * A.share;
   depends_begin();
+  if ((int)blockIdx.x >= A.n_cta) {
+    const int others = gridDim.x - A.n_cta;
+    for (int64_t r = A.vocab - A.fill + (blockIdx.x - A.n_cta); r < A.vocab; r += others)
+      for (int i = d; i < A.vecs; i += kSortThreads) *reinterpret_cast<uint4*>(A.table + r * A.ld_bytes + 16 * (int64_t)i) = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
   for (int pass = 0; pass < A.passes; ++pass) {
     for (int w = 0; w < kSortWarps; ++w) count[w][d] = 0;
     __syncthreads();
@@ -294,7 +306,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(SortArgs A) {
 // sums
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 32;    // sorted positions of a piece
-constexpr int kZeros = 64;    // rows of a CTA that looks for rows without a token
+constexpr int kZeros = 16;    // rows of a CTA that looks for rows without a token
 
 struct SumArgs {
   const uint2* sorted;
@@ -302,6 +314,7 @@ struct SumArgs {
   void* dtable;
   float* partial;        // [pieces][2][ldp]: a run that began before the piece, and one that goes on behind it
   int64_t n, vocab, ld_dout, ld_dtable, ldp;
+  int64_t zero_rows;     // rows [0, zero_rows) of which those without a token become zero here
   int32_t cols, pieces, accumulate;
   float scale;
 };
@@ -373,7 +386,7 @@ __device__ __forceinline__ int64_t first_at_least(const uint2* sorted, int64_t n
 // CTA (piece, slab of columns): a thread's N columns over the piece's positions; behind the pieces, CTAs that write the
 // zeros of the rows without a token.
 template <int DT, int GT, int N>
-__global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
   const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
   depends_begin();
   __shared__ int64_t range[2];
@@ -383,12 +396,12 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs A) {
 #pragma unroll
     for (int k = 0; k < N; ++k) zero[k] = 0.0f;
     const int64_t r0 = ((int64_t)blockIdx.x - A.pieces) * kZeros;
-    const int rows = (int)(A.vocab - r0 < kZeros ? A.vocab - r0 : kZeros);
+    const int rows = (int)(A.zero_rows - r0 < kZeros ? A.zero_rows - r0 : kZeros);
     if (threadIdx.x < 64) {   // the positions of these rows' tokens
       const int warp = threadIdx.x >> 5;
       const int64_t at = first_at_least(A.sorted, A.n, (uint32_t)(r0 + (warp ? rows : 0)), threadIdx.x & 31);
       if ((threadIdx.x & 31) == 0) range[warp] = at;
-      there[threadIdx.x] = 0;
+      if (threadIdx.x < kZeros) there[threadIdx.x] = 0;
     }
     __syncthreads();
     for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) there[A.sorted[i].x - (uint32_t)r0] = 1;
@@ -412,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs A) {
 #pragma unroll
   for (int k = 0; k < N; ++k) sum[k] = 0.0f;
   bool before = mine[0].x == mine[1].x;   // the run began in an earlier piece
-  constexpr int U = 8;                    // rows in flight
+  constexpr int U = 4;                    // rows in flight
   for (int j0 = 0; j0 < n; j0 += U) {
     float v[U][N];
 #pragma unroll
@@ -507,7 +520,7 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t cols) {
   Layout L{};
   L.passes = 1;
   while (L.passes * kDigitBits < 32 && (vocab >> (L.passes * kDigitBits)) != 0) ++L.passes;   // keys 0 .. vocab
-  L.n_cta = (int)ceil_div(n, kSortKeys);
+  L.n_cta = (int)std::max(std::min(ceil_div(n, kClusterKeys), (int64_t)kSortCluster), ceil_div(n, kSortKeys));
   L.pieces = (int)ceil_div(n, kPiece);
   L.ldp = (int64_t)round_up((size_t)cols, 8);
   size_t at = 0;
@@ -530,7 +543,7 @@ bool rows_ok(const void* p, int64_t ld, int64_t cols, int es) {
 bool is_type(int dt) { return dt == QMUON_BF16 || dt == QMUON_FP16 || dt == QMUON_FP32; }
 bool tokens_ok(const void* p, int bits) { return p && (bits == 32 || bits == 64) && is_aligned(p, bits / 8); }
 
-cudaError_t launch_cluster(const SortArgs& A, cudaStream_t s) {
+cudaError_t launch_cluster(const SortArgs& A, int sms, cudaStream_t s) {
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = A.n_cta;
@@ -538,7 +551,7 @@ cudaError_t launch_cluster(const SortArgs& A, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(A.n_cta);
+  cfg.gridDim = dim3(A.fill ? std::max(2, sms / A.n_cta) * A.n_cta : A.n_cta);   // whole clusters
   cfg.blockDim = dim3(kSortThreads);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -549,7 +562,7 @@ cudaError_t launch_cluster(const SortArgs& A, cudaStream_t s) {
 template <int DT, int GT, int N>
 cudaError_t launch_sums(const SumArgs& A, cudaStream_t s) {
   const unsigned slabs = (unsigned)ceil_div(A.cols, (int64_t)kThreads * N);
-  const int64_t zeros = A.accumulate ? 0 : ceil_div(A.vocab, kZeros);
+  const int64_t zeros = ceil_div(A.zero_rows, kZeros);
   const int threads = (int)std::min<int64_t>(kThreads, round_up((size_t)ceil_div(A.cols, N), 32));
   cudaError_t e = launch_dependent(sum_kernel<DT, GT, N>, dim3((unsigned)(A.pieces + zeros), slabs), dim3(std::max(threads, 64)), 0, s, A);
   if (e == cudaSuccess && A.pieces > 1) e = launch_dependent(join_kernel<GT, N>, dim3(A.pieces - 1, slabs), dim3(std::max(threads, 64)), 0, s, A);
@@ -610,7 +623,10 @@ extern "C" qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* c, 
     if (c->n_tokens == 0 && c->accumulate) return QMUON_OK;
     unsigned char* w = static_cast<unsigned char*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int sms = num_sms();
+    if (sms <= 0) return set_error_msg("qmuon_embedding_backward: SM count query failed", QMUON_ERR_CUDA);
     cudaError_t e = cudaSuccess;
+    int64_t zero_rows = c->accumulate ? 0 : c->vocab;
     const uint2* sorted = reinterpret_cast<uint2*>(w + L.pairs[(L.passes - 1) & 1]);
     if (c->n_tokens > 0) {
       SortArgs A{};
@@ -622,7 +638,15 @@ extern "C" qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* c, 
       A.share = (int32_t)round_up((size_t)ceil_div(c->n_tokens, (int64_t)L.n_cta * kSortWarps), 32);
       for (int i = 0; i < 2; ++i) A.pairs[i] = reinterpret_cast<uint2*>(w + L.pairs[i]);
       if (L.n_cta <= kSortCluster) {
-        e = launch_cluster(A, s);
+        const int64_t bytes = c->cols * gs;
+        if (!c->accumulate && bytes % 16 == 0 && vec_class(c->dtable, c->ld_dtable, gs)) {
+          A.table = static_cast<unsigned char*>(c->dtable);
+          A.fill = std::min(c->vocab, kFillBytes / bytes);
+          A.ld_bytes = c->ld_dtable * gs;
+          A.vecs = (int32_t)(bytes / 16);
+          zero_rows -= A.fill;
+        }
+        e = launch_cluster(A, sms, s);
       } else {
         A.share = kSortKeys / kSortWarps;   // as count_kernel takes them
         for (int p = 0; p < L.passes && e == cudaSuccess; ++p, A.shift += kDigitBits) {
@@ -636,7 +660,7 @@ extern "C" qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* c, 
     }
     if (e != cudaSuccess) return set_error("qmuon_embedding_backward (sort)", e);
     const SumArgs A{sorted, c->dout, c->dtable, reinterpret_cast<float*>(w + L.partial), c->n_tokens, c->vocab, c->ld_dout,
-                    c->ld_dtable, L.ldp, (int32_t)c->cols, L.pieces, c->accumulate != 0, c->scale};
+                    c->ld_dtable, L.ldp, zero_rows, (int32_t)c->cols, L.pieces, c->accumulate != 0, c->scale};
     e = c->dtype == QMUON_BF16   ? launch_sums_of<QMUON_BF16>(A, c->grad_dtype, s)
         : c->dtype == QMUON_FP16 ? launch_sums_of<QMUON_FP16>(A, c->grad_dtype, s)
                                  : launch_sums_of<QMUON_FP32>(A, c->grad_dtype, s);
