@@ -39,11 +39,10 @@ constexpr int kTile = 256, kBK = 64;
 constexpr int kInnerTile = 128;                    // columns of gate, and of up, in a forward tile
 constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter
 constexpr int kThreads = 64 + 32 * kEpiWarps;      // warp 0 TMA, warp 1 MMA, warps 2.. epilogue
-constexpr int kStages = 6;
+constexpr int kStages = 7;
 constexpr uint32_t kStageBytes = 4 * kBox;         // per CTA: 128 x 64 of A, 128 x 64 of B
-constexpr uint32_t kRowBytes = 32 * 32 * 4;        // of each epilogue warp: 32 rows x 32 columns that are not accessed in vectors
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
-constexpr size_t kSmem = (size_t)kStages * kStageBytes + kEpiWarps * kRowBytes + 1024 + 256;
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
 constexpr int kGroupM = 8;                         // tile rows that run side by side
 
@@ -193,32 +192,28 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn) {
          ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
-// W columns of gate and up from column c of row r, n of them valid (0: none): what the forward pass stores.  Every lane
-// of the warp calls this.
-template <int DT, int ACT, int W>
-__device__ __forceinline__ void finish_forward(const GemmArgs& A, int64_t r, int64_t c, int n, const float (&g)[W], const float (&u)[W],
-                                               float* stage) {
-  constexpr int es = elem_size(DT);
-  auto at = [&](void* base, int64_t ld) { return static_cast<unsigned char*>(base) + (n ? (r * ld + c) * es : 0); };
+// A thread's columns of gate and up: what the forward pass stores.  Every lane of the warp calls this.
+template <int DT, int ACT, int W, bool ANY>
+__device__ __forceinline__ void finish_forward(const GemmArgs& A, int64_t r, const Columns<W, ANY>& t, const float (&g)[W],
+                                               const float (&u)[W]) {
+  auto at = [&](void* base, int64_t ld) { return static_cast<unsigned char*>(base) + r * ld * elem_size(DT); };
   float h[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) h[i] = act_of<ACT>(g[i]) * u[i];
-  store_rows<DT, W>(at(A.h, A.ld_h), n, A.vec_h, h, stage);
+  t.template store<DT>(at(A.h, A.ld_h), A.vec_h, h);
   if (A.saved == QMUON_SAVE_SAME) {
-    store_rows<DT, W>(at(A.gate, A.ld_gate), n, A.vec_gate, g, stage);
-    store_rows<DT, W>(at(A.up, A.ld_up), n, A.vec_up, u, stage);
+    t.template store<DT>(at(A.gate, A.ld_gate), A.vec_gate, g);
+    t.template store<DT>(at(A.up, A.ld_up), A.vec_up, u);
   } else if (A.saved == QMUON_SAVE_MXFP8) {
-    const int64_t e = n ? r * A.inner + c : 0;
-    const int gs = encode_row<W>(static_cast<uint8_t*>(A.gate) + e, n > 0, A.vec_gate, g);
-    const int us = encode_row<W>(static_cast<uint8_t*>(A.up) + e, n > 0, A.vec_up, u);
-    if (n && (e & 31) == 0) A.gate_scale[e >> 5] = (uint8_t)gs, A.up_scale[e >> 5] = (uint8_t)us;
+    const int64_t e = r * A.inner;
+    encode_columns(t, static_cast<uint8_t*>(A.gate) + e, A.gate_scale + (e >> 5), A.vec_gate, g);
+    encode_columns(t, static_cast<uint8_t*>(A.up) + e, A.up_scale + (e >> 5), A.vec_up, u);
   }
 }
 // The same of the backward pass, from dh's words: dgate and dup for the products, and h again.
-template <int DT, int ACT, int W>
-__device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, int64_t c, int n, const float (&g)[W], const float (&u)[W],
-                                                const uint32_t (&dh)[W / 2], float* stage) {
-  constexpr int es = elem_size(DT);
+template <int DT, int ACT, int W, bool ANY>
+__device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, const Columns<W, ANY>& t, const float (&g)[W],
+                                                const float (&u)[W], const uint32_t (&dh)[W / 2]) {
   float h[W], dg[W], du[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -228,42 +223,41 @@ __device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, in
     dg[i] = x * u[i] * a.y;
     du[i] = x * a.x;
   }
-  // the workspace's rows are padded to 32 bytes
-  const int64_t e = n ? (r * A.ld_d + c) * es : 0;
-  store_row<DT, W>(static_cast<unsigned char*>(A.dgate) + e, n, 2, dg);
-  store_row<DT, W>(static_cast<unsigned char*>(A.dup) + e, n, 2, du);
-  if (A.h) store_rows<DT, W>(static_cast<unsigned char*>(A.h) + (n ? (r * A.ld_h + c) * es : 0), n, A.vec_h, h, stage);
+  const int64_t e = r * A.ld_d * elem_size(DT);   // the workspace's rows are padded to 32 bytes
+  t.template store<DT>(static_cast<unsigned char*>(A.dgate) + e, 2, dg);
+  t.template store<DT>(static_cast<unsigned char*>(A.dup) + e, 2, du);
+  if (A.h) t.template store<DT>(static_cast<unsigned char*>(A.h) + r * A.ld_h * elem_size(DT), A.vec_h, h);
 }
-// W columns of dh as words.
-template <int DT, int W>
-__device__ __forceinline__ void load_dh(const GemmArgs& A, int64_t r, int64_t c, int n, uint32_t (&w)[W / 2], float* stage) {
-  const unsigned char* p = static_cast<const unsigned char*>(A.dh) + (n ? (r * A.ld_dh + c) * elem_size(DT) : 0);
-  if (A.vec_dh && n == W) {
+// A thread's columns of dh as words.
+template <int DT, int W, bool ANY>
+__device__ __forceinline__ void load_dh(const GemmArgs& A, int64_t r, const Columns<W, ANY>& t, uint32_t (&w)[W / 2]) {
+  const unsigned char* row = static_cast<const unsigned char*>(A.dh) + r * A.ld_dh * elem_size(DT);
+  if (!ANY && A.vec_dh && t.n == W) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + t.c * elem_size(DT));
 #pragma unroll
     for (int i = 0; i < W / 8; ++i) {
-      const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+      const uint4 q = p[i];
       w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
   } else {
     float v[W];
-    load_rows<DT, W>(p, n, A.vec_dh, v, stage);
+    t.template load<DT>(row, A.vec_dh, v);
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
   }
 }
+
 // The q-th N elements of an array.
 template <int N, class T, int M>
 __device__ __forceinline__ const T (&part_of(const T (&v)[M], int q))[N] {
   return *reinterpret_cast<const T(*)[N]>(v + N * q);
 }
-__device__ __forceinline__ int valid_columns(int64_t left, int most) { return left >= most ? most : left > 0 ? (int)left : 0; }
 
 template <int KIND, int DT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ GemmArgs A) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* rows_of_warp = reinterpret_cast<float*>(smem + kStages * kStageBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + kEpiWarps * kRowBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
   const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
@@ -404,7 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     // ---- epilogue: warps 2..9; TMEM lane quarter = warp % 4 ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_l = cluster_map(tempty0, 0);
-    float* stage = rows_of_warp + (warp - 2) * (kRowBytes / 4);
     Unit u;
     for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
       const int64_t r = u.m0 + 128 * rank + quarter * 32 + lane;
@@ -415,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int64_t c = c0 + 32 * j;
-          load_dh<DT, 32>(A, r, c, r < A.rows ? valid_columns(A.inner - c, 32) : 0, dh[j], stage);
+          load_dh<DT, 32, false>(A, r, {c, r < A.rows ? valid_columns(A.inner - c, 32) : 0}, dh[j]);
         }
       }
       bool ok = mbar_wait(tfull0 + 8 * acc, use & 1, A.hdr, 0x2400u | KIND);
@@ -450,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
             store_row<QMUON_FP32, 32>(p, np, 2, g);
             store_row<QMUON_FP32, 32>(p + A.rows * A.ld_part, np, 2, v);
           } else if constexpr (KIND == K_FWD) {
-            finish_forward<DT, ACT, 32>(A, r, c, n, g, v, stage);
+            finish_forward<DT, ACT, 32, false>(A, r, {c, n}, g, v);
           } else if constexpr (KIND == K_BWD) {
             // in halves: the registers do not hold 32 columns of everything
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              finish_backward<DT, ACT, 16>(A, r, c + 16 * q, valid_columns(n - 16 * q, 16), part_of<16>(g, q), part_of<16>(v, q),
-                                           part_of<8>(dh[j], q), stage);
+              finish_backward<DT, ACT, 16, false>(A, r, {c + 16 * q, valid_columns(n - 16 * q, 16)}, part_of<16>(g, q),
+                                                  part_of<16>(v, q), part_of<8>(dh[j], q));
           }
         }
       } else {
@@ -477,19 +470,19 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
             const int64_t slice = u.kind == 0 ? u.split : (int64_t)(u.kind - 1) * A.splits_w + u.split;
             store_row<QMUON_FP32, 32>(part + (n ? (slice * rows + r) * A.ld_part + c : 0), n ? valid_columns(A.ld_part - c, 32) : 0, 2, v);
           } else if (u.kind == 0) {
-            store_rows<DT, 32>(static_cast<unsigned char*>(A.dx) + (n ? (r * A.ld_dx + c) * elem_size(DT) : 0), n, A.vec_dx, v, stage);
+            store_row<DT, 32>(static_cast<unsigned char*>(A.dx) + (n ? (r * A.ld_dx + c) * elem_size(DT) : 0), n, A.vec_dx, v);
           } else {
             const int w = u.kind - 1;
             unsigned char* p = static_cast<unsigned char*>(A.dw[w]) + (n ? (r * A.ld_dw[w] + c) * (A.dw_f32 ? 4 : elem_size(DT)) : 0);
             if (A.accumulate) {
               float old[32];
-              if (A.dw_f32) load_rows<QMUON_FP32, 32>(p, n, A.vec_dw[w], old, stage);
-              else load_rows<DT, 32>(p, n, A.vec_dw[w], old, stage);
+              if (A.dw_f32) load_row<QMUON_FP32, 32>(p, n, A.vec_dw[w], old);
+              else load_row<DT, 32>(p, n, A.vec_dw[w], old);
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] += old[k];
             }
-            if (A.dw_f32) store_rows<QMUON_FP32, 32>(p, n, A.vec_dw[w], v, stage);
-            else store_rows<DT, 32>(p, n, A.vec_dw[w], v, stage);
+            if (A.dw_f32) store_row<QMUON_FP32, 32>(p, n, A.vec_dw[w], v);
+            else store_row<DT, 32>(p, n, A.vec_dw[w], v);
           }
         }
       }
@@ -512,7 +505,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 // or from their carriers
 // ---------------------------------------------------------------------------
 constexpr int kElemThreads = 256, kElemCols = 16;
-constexpr size_t kElemRows = (size_t)kElemThreads * kElemCols * 4;   // shared memory where rows are not accessed in vectors
 enum { FROM_PART = 0, FROM_SAME = 1, FROM_MXFP8 = 2 };
 
 struct ElemArgs {
@@ -533,48 +525,39 @@ __device__ __forceinline__ void clear_header(WsHeader* h) {
 
 // A thread takes 16 columns of a row.  (Of 32, as in the product's epilogue, the 160 registers left 12 warps on an SM:
 // 8192 x 14336 from carriers in 214 us.)
-template <int DT, int ACT, int FROM, bool BWD>
+template <int DT, int ACT, int FROM, bool BWD, bool ANY>
 __global__ void __launch_bounds__(kElemThreads) elem_kernel(const __grid_constant__ ElemArgs E) {
-  extern __shared__ float elem_rows[];
   constexpr int W = kElemCols, es = elem_size(DT);
   const GemmArgs& A = E.A;
-  float* stage = elem_rows + (threadIdx.x >> 5) * 32 * W;
-  const int64_t per = (A.inner + W - 1) / W, i = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
   depends_begin();
   if (E.clear) clear_header(A.hdr);
-  int64_t r = 0, c = 0;
-  int n = 0;
-  if (i < A.rows * per) {
-    r = i / per;
-    c = (i - r * per) * W;
-    n = valid_columns(A.inner - c, W);
-  }
+  int64_t r;
+  const Columns<W, ANY> t = deal_columns<W, ANY>((int64_t)blockIdx.x * kElemThreads + threadIdx.x, A.rows, A.inner, &r);
   uint32_t dh[W / 2];
-  if constexpr (BWD) load_dh<DT, W>(A, r, c, n, dh, stage);
+  if constexpr (BWD) load_dh<DT, W, ANY>(A, r, t, dh);
   float g[W], u[W];
   if constexpr (FROM == FROM_PART) {
-    const int np = n ? valid_columns(A.ld_part - c, W) : 0;
-    const float* p = E.part + (n ? r * A.ld_part + c : 0);
-    load_row<QMUON_FP32, W>(p, np, 2, g);
-    load_row<QMUON_FP32, W>(p + A.rows * A.ld_part, np, 2, u);
+    const float* p = E.part + r * A.ld_part;
+    t.template load<QMUON_FP32>(p, 2, g);
+    t.template load<QMUON_FP32>(p + A.rows * A.ld_part, 2, u);
     for (int s = 1; s < E.splits; ++s) {
       p += 2 * A.rows * A.ld_part;
       float a[W], b[W];
-      load_row<QMUON_FP32, W>(p, np, 2, a);
-      load_row<QMUON_FP32, W>(p + A.rows * A.ld_part, np, 2, b);
+      t.template load<QMUON_FP32>(p, 2, a);
+      t.template load<QMUON_FP32>(p + A.rows * A.ld_part, 2, b);
 #pragma unroll
       for (int k = 0; k < W; ++k) g[k] += a[k], u[k] += b[k];
     }
   } else if constexpr (FROM == FROM_SAME) {
-    load_rows<DT, W>(static_cast<const unsigned char*>(E.gate) + (n ? (r * E.ld_gate + c) * es : 0), n, E.vec_in, g, stage);
-    load_rows<DT, W>(static_cast<const unsigned char*>(E.up) + (n ? (r * E.ld_up + c) * es : 0), n, E.vec_in, u, stage);
+    t.template load<DT>(static_cast<const unsigned char*>(E.gate) + r * E.ld_gate * es, E.vec_in, g);
+    t.template load<DT>(static_cast<const unsigned char*>(E.up) + r * E.ld_up * es, E.vec_in, u);
   } else {
-    const int64_t e = n ? r * A.inner + c : 0;
-    decode_row<W>(static_cast<const uint8_t*>(E.gate) + e, E.vec_in, scale_of_e8m0(E.gate_scale[e >> 5]), g);
-    decode_row<W>(static_cast<const uint8_t*>(E.up) + e, E.vec_in, scale_of_e8m0(E.up_scale[e >> 5]), u);
+    const int64_t e = r * A.inner;
+    decode_columns(t, static_cast<const uint8_t*>(E.gate) + e, E.gate_scale + (e >> 5), E.vec_in, g);
+    decode_columns(t, static_cast<const uint8_t*>(E.up) + e, E.up_scale + (e >> 5), E.vec_in, u);
   }
-  if constexpr (BWD) finish_backward<DT, ACT, W>(A, r, c, n, g, u, dh, stage);
-  else finish_forward<DT, ACT, W>(A, r, c, n, g, u, stage);
+  if constexpr (BWD) finish_backward<DT, ACT, W, ANY>(A, r, t, g, u, dh);
+  else finish_forward<DT, ACT, W, ANY>(A, r, t, g, u);
 }
 
 // Sums of split products, rows x cols of [splits][rows][ld_part], to the type of the result; the products of a call
@@ -590,44 +573,42 @@ struct JoinArgs {
   Join job[3];
   int32_t n;
 };
-template <int DT>
-__device__ __forceinline__ void join_rows(const Join& J, int64_t r, int64_t c, int n, float (&v)[kJoinCols], float* stage) {
-  unsigned char* o = static_cast<unsigned char*>(J.out) + (n ? (r * J.ld + c) * elem_size(DT) : 0);
-  if (J.accumulate) {
-    float old[kJoinCols];
-    load_rows<DT, kJoinCols>(o, n, J.vec, old, stage);
-#pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) v[k] += old[k];
-  }
-  store_rows<DT, kJoinCols>(o, n, J.vec, v, stage);
-}
-__global__ void __launch_bounds__(kElemThreads) join_kernel(const __grid_constant__ JoinArgs A) {
-  __shared__ float rows[kElemThreads * kJoinCols];
+template <int DT, bool ANY>
+__device__ __forceinline__ void join_columns(const Join& J, int64_t i) {
   constexpr int W = kJoinCols;
-  depends_begin();
-  const Join& J = A.job[A.n > 2 && blockIdx.x >= A.job[2].first ? 2 : A.n > 1 && blockIdx.x >= A.job[1].first ? 1 : 0];
-  const int64_t per = (J.cols + W - 1) / W, i = ((int64_t)blockIdx.x - J.first) * kElemThreads + threadIdx.x;
-  int64_t r = 0, c = 0;
-  int n = 0;
-  if (i < J.rows * per) {
-    r = i / per;
-    c = (i - r * per) * W;
-    n = valid_columns(J.cols - c, W);
-  }
-  const float* p = J.part + (n ? r * J.ld_part + c : 0);   // rows are padded to W
+  int64_t r;
+  const Columns<W, ANY> t = deal_columns<W, ANY>(i, J.rows, J.cols, &r);
+  const float* p = J.part + r * J.ld_part;
   float v[W];
-  load_row<QMUON_FP32, W>(p, n ? W : 0, 2, v);
+  t.template load<QMUON_FP32>(p, 2, v);
 #pragma unroll 4
   for (int s = 1; s < J.splits; ++s) {
     float a[W];
-    load_row<QMUON_FP32, W>(p + s * J.rows * J.ld_part, n ? W : 0, 2, a);
+    t.template load<QMUON_FP32>(p + s * J.rows * J.ld_part, 2, a);
 #pragma unroll
     for (int k = 0; k < W; ++k) v[k] += a[k];
   }
-  float* stage = rows + (threadIdx.x >> 5) * 32 * W;
-  if (J.dt == QMUON_BF16) join_rows<QMUON_BF16>(J, r, c, n, v, stage);
-  else if (J.dt == QMUON_FP16) join_rows<QMUON_FP16>(J, r, c, n, v, stage);
-  else join_rows<QMUON_FP32>(J, r, c, n, v, stage);
+  unsigned char* o = static_cast<unsigned char*>(J.out) + r * J.ld * elem_size(DT);
+  if (J.accumulate) {
+    float old[W];
+    t.template load<DT>(o, J.vec, old);
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] += old[k];
+  }
+  t.template store<DT>(o, J.vec, v);
+}
+template <int DT>
+__device__ __forceinline__ void join_one(const Join& J, int64_t i) {
+  if (J.vec) join_columns<DT, false>(J, i);
+  else join_columns<DT, true>(J, i);
+}
+__global__ void __launch_bounds__(kElemThreads) join_kernel(const __grid_constant__ JoinArgs A) {
+  depends_begin();
+  const Join& J = A.job[A.n > 2 && blockIdx.x >= A.job[2].first ? 2 : A.n > 1 && blockIdx.x >= A.job[1].first ? 1 : 0];
+  const int64_t i = ((int64_t)blockIdx.x - J.first) * kElemThreads + threadIdx.x;
+  if (J.dt == QMUON_BF16) join_one<QMUON_BF16>(J, i);
+  else if (J.dt == QMUON_FP16) join_one<QMUON_FP16>(J, i);
+  else join_one<QMUON_FP32>(J, i);
 }
 
 // ---------------------------------------------------------------------------
@@ -816,7 +797,10 @@ void lay_operands(Geometry& G, int64_t rows, int64_t width, int64_t inner, bool 
     if (G.copy_w[i]) lay(G, &G.w[i], (size_t)inner * G.ld_wp * 2);
 }
 
-// `direct`: few rows need no partial sums.
+// `direct`: the product's own kernel may finish a column of gate and up; else their fp32 values go through the workspace
+// to elem_kernel, as split products' do.  The tensor-core kernel's epilogue has 8 warps on an SM and accesses rows in
+// vectors only (written by elements there, the rows of fp16 3001 x 2731 took 45 us); few_kernel writes by elements, but
+// no codes.
 void lay_projections(Geometry& G, int64_t rows, int64_t width, int64_t inner, bool direct) {
   G.ld_fwd = (int64_t)round_up((size_t)inner, 8);
   if (G.few) {
@@ -826,7 +810,7 @@ void lay_projections(Geometry& G, int64_t rows, int64_t width, int64_t inner, bo
   G.tiles_m = (int32_t)ceil_div(rows, kTile);
   G.tiles_n = (int32_t)ceil_div(inner, kInnerTile);
   G.splits = pick_splits((int64_t)G.tiles_m * G.tiles_n, (int)ceil_div(width, kBK), G.pairs);
-  if (G.splits > 1) lay(G, &G.part, (size_t)G.splits * 2 * rows * G.ld_fwd * 4);
+  if (G.splits > 1 || !direct) lay(G, &G.part, (size_t)G.splits * 2 * rows * G.ld_fwd * 4);
 }
 
 Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
@@ -836,7 +820,9 @@ Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
   G.few = c.rows <= kFewRows;
   if (!G.few)
     lay_operands(G, c.rows, c.width, c.inner, !tma_ready(c.x, c.ld_x), !tma_ready(c.w_gate, c.ld_w_gate), !tma_ready(c.w_up, c.ld_w_up));
-  lay_projections(G, c.rows, c.width, c.inner, c.saved != QMUON_SAVE_MXFP8);
+  const bool vectors = vec_class(c.h, c.ld_h, 2) &&
+                       (c.saved != QMUON_SAVE_SAME || (vec_class(c.gate, c.ld_gate, 2) && vec_class(c.up, c.ld_up, 2)));
+  lay_projections(G, c.rows, c.width, c.inner, G.few ? c.saved != QMUON_SAVE_MXFP8 : vectors);
   return G;
 }
 
@@ -857,7 +843,8 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
   lay(G, &G.dup, (size_t)c.rows * G.ld_d * 2);
   G.ld_w = (int64_t)round_up((size_t)c.width, 8);
   const size_t behind = G.total;
-  if (c.saved == QMUON_SAVE_NONE) lay_projections(G, c.rows, c.width, c.inner, false);
+  if (c.saved == QMUON_SAVE_NONE)
+    lay_projections(G, c.rows, c.width, c.inner, !G.few && vec_class(c.dh, c.ld_dh, 2) && (!c.h || vec_class(c.h, c.ld_h, 2)));
   const size_t most = G.total;
   G.total = behind;   // the projections' partial sums are done with when the gradients' begin
   const int kbx = 2 * (int)ceil_div(c.inner, kBK), kbw = (int)ceil_div(c.rows, kBK);
@@ -878,13 +865,15 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
     int64_t best = INT64_MAX;
     for (const int64_t most : {(int64_t)1 << 40, 4 * share, 2 * share, share}) {
       const int64_t sx = tx ? std::min<int64_t>(32, ceil_div(kbx, most)) : 1, sw = tw ? std::min<int64_t>(32, ceil_div(kbw, most)) : 1;
-      const int64_t longest = std::max(tx ? ceil_div(kbx, sx) : 0, tw ? ceil_div(kbw, sw) : 0) + 6;
-      const int64_t cost = std::max(longest, ceil_div(all + 6 * (tx * sx + tw * sw), G.pairs)) + (sx > 1 || sw > 1 ? 16 : 0);
+      const int64_t longest = std::max(tx ? ceil_div(kbx, sx) : 0, tw ? ceil_div(kbw, sw) : 0) + 6, units = tx * sx + tw * sw;
+      const int64_t cost = std::max(longest, ceil_div(units, G.pairs) * (ceil_div(all, units) + 6)) + (sx > 1 || sw > 1 ? 16 : 0);
       if (cost < best) best = cost, G.dx_splits = (int32_t)sx, G.dw_splits = (int32_t)sw;
     }
   }
-  if (c.dx && G.dx_splits > 1) lay(G, &G.part_x, (size_t)G.dx_splits * c.rows * G.ld_w * 4);
-  if (c.dw_gate && G.dw_splits > 1) lay(G, &G.part_w, (size_t)2 * G.dw_splits * c.inner * G.ld_w * 4);
+  const int gs = elem_size(c.grad_dtype);
+  if (c.dx && (G.dx_splits > 1 || !vec_class(c.dx, c.ld_dx, 2))) lay(G, &G.part_x, (size_t)G.dx_splits * c.rows * G.ld_w * 4);
+  if (c.dw_gate && (G.dw_splits > 1 || !vec_class(c.dw_gate, c.ld_dw_gate, gs) || !vec_class(c.dw_up, c.ld_dw_up, gs)))
+    lay(G, &G.part_w, (size_t)2 * G.dw_splits * c.inner * G.ld_w * 4);
   G.total = std::max(G.total, most);
   return G;
 }
@@ -928,13 +917,13 @@ cudaError_t launch_gemm(const GemmArgs& A, int64_t units, int pairs, int dt, cud
 
 template <int DT, int FROM, bool BWD>
 cudaError_t launch_elem_of(const ElemArgs& E, cudaStream_t s) {
-  const int64_t grid = ceil_div(E.A.rows * ceil_div(E.A.inner, kElemCols), kElemThreads);
   const bool vec = (!BWD || E.A.vec_dh) && (FROM != FROM_SAME || E.vec_in) && (!E.A.h || E.A.vec_h) &&
                    (BWD || E.A.saved != QMUON_SAVE_SAME || (E.A.vec_gate && E.A.vec_up));
-  auto go = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid), dim3(kElemThreads), vec ? 0 : kElemRows, s, E); };
-  if (E.A.act == QMUON_ACT_SILU) return go(elem_kernel<DT, QMUON_ACT_SILU, FROM, BWD>);
-  if (E.A.act == QMUON_ACT_GELU) return go(elem_kernel<DT, QMUON_ACT_GELU, FROM, BWD>);
-  return go(elem_kernel<DT, QMUON_ACT_GELU_TANH, FROM, BWD>);
+  const int64_t grid = ceil_div(threads_of(E.A.rows, E.A.inner, kElemCols, !vec), kElemThreads);
+  auto go = [&](auto kernel, auto any) { return launch_dependent(vec ? kernel : any, dim3((unsigned)grid), dim3(kElemThreads), 0, s, E); };
+  if (E.A.act == QMUON_ACT_SILU) return go(elem_kernel<DT, QMUON_ACT_SILU, FROM, BWD, false>, elem_kernel<DT, QMUON_ACT_SILU, FROM, BWD, true>);
+  if (E.A.act == QMUON_ACT_GELU) return go(elem_kernel<DT, QMUON_ACT_GELU, FROM, BWD, false>, elem_kernel<DT, QMUON_ACT_GELU, FROM, BWD, true>);
+  return go(elem_kernel<DT, QMUON_ACT_GELU_TANH, FROM, BWD, false>, elem_kernel<DT, QMUON_ACT_GELU_TANH, FROM, BWD, true>);
 }
 template <int FROM, bool BWD>
 cudaError_t launch_elem(const ElemArgs& E, int dt, cudaStream_t s) {
@@ -943,8 +932,9 @@ cudaError_t launch_elem(const ElemArgs& E, int dt, cudaStream_t s) {
 
 void add_join(JoinArgs& A, int64_t* grid, const float* part, int splits, int64_t rows, int64_t cols, int64_t ld_part, void* out, int64_t ld,
               int dt, int accumulate) {
-  A.job[A.n++] = Join{part, out, rows, cols, ld_part, ld, *grid, splits, vec_class(out, ld, elem_size(dt)), accumulate, dt};
-  *grid += ceil_div(rows * ceil_div(cols, kJoinCols), kElemThreads);
+  const int vec = vec_class(out, ld, elem_size(dt));
+  A.job[A.n++] = Join{part, out, rows, cols, ld_part, ld, *grid, splits, vec, accumulate, dt};
+  *grid += ceil_div(threads_of(rows, cols, kJoinCols, vec == 0), kElemThreads);
 }
 
 template <int DT, int ACT, int NT>
@@ -1210,8 +1200,8 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
     A.vec_dw[0] = vec_class(c->dw_gate, c->ld_dw_gate, gs), A.vec_dw[1] = vec_class(c->dw_up, c->ld_dw_up, gs);
     A.dw_f32 = c->grad_dtype == QMUON_FP32, A.accumulate = c->accumulate != 0;
     A.ld_part = G.ld_w;
-    A.part = c->dx && G.dx_splits > 1 ? reinterpret_cast<float*>(b + G.part_x) : nullptr;
-    A.part_w = c->dw_gate && G.dw_splits > 1 ? reinterpret_cast<float*>(b + G.part_w) : nullptr;
+    A.part = G.part_x ? reinterpret_cast<float*>(b + G.part_x) : nullptr;
+    A.part_w = G.part_w ? reinterpret_cast<float*>(b + G.part_w) : nullptr;
     if (!encode_map(&A.a[0], A.dgate, c->rows, c->inner, G.ld_d, c->dtype) ||
         !encode_map(&A.a[1], A.dup, c->rows, c->inner, G.ld_d, c->dtype))
       return QMUON_ERR_CUDA;

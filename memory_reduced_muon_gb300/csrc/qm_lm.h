@@ -30,6 +30,10 @@ __device__ __forceinline__ void load32b(const void* p, uint32_t (&w)[8]) {
                : "memory");
 }
 
+inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // How an array's rows may be accessed: 2 in 32-byte vectors, 1 in 16-byte ones, 0 by elements.
 inline int vec_class(const void* p, int64_t ld, int es) {
   const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * es);
@@ -97,79 +101,56 @@ __device__ __forceinline__ void store_row(void* p, int n, int vec, const float (
   }
 }
 
-// The same for every lane of a converged warp (p, n: the lane's own, n = 0 for
-// none; vec alike in all of them).  Rows that cannot be accessed in vectors go
-// through `stage`, 32 W fp32 of the warp's own, so that neighbouring lanes
-// access neighbouring elements: 32 lanes that each write a row of their own
-// touch 32 sectors with every 2-byte store.
-template <int W>
-__device__ __forceinline__ int stage_at(int row, int col) {
-  return row * W + (col ^ (row & (W - 1)));   // column k of all rows in different banks (in pairs for W < 32)
-}
-// (Functions of their own: in line, their registers would cost the kernels that reach them only with unaligned rows.)
-template <int DT, int W>
-__device__ __noinline__ void fill_stage(const void* p, int n, float* stage) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
+// The W columns of a row that a thread takes.  Side by side from column c, n of them there: rows on 16 bytes, in vectors
+// (vec not 0).  ANY: rows that start anywhere; columns c, c + 32, ..., n of them there, lane l of the warp's having c + l:
+// neighbouring lanes access neighbouring elements, in which a warp's 2-byte accesses touch 3 sectors (32 if each lane had
+// columns of its own side by side).
+template <int W, bool ANY>
+struct Columns {
+  int64_t c;
+  int n;
+  template <int DT>
+  __device__ __forceinline__ void load(const void* row, int vec, float (&v)[W]) const {
+    if constexpr (ANY) {
 #pragma unroll
-  for (int j0 = 0; j0 < W; j0 += 8) {   // eight at a time: shuffles, accesses of either memory
-    float e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int row = ((j0 + j) * 32 + lane) / W, col = ((j0 + j) * 32 + lane) % W;
-      const int m = __shfl_sync(0xffffffffu, n, row);
-      const void* q = reinterpret_cast<const void*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p), row));
-      e[j] = 0.0f;
-      if (col < m) e[j] = load_elem<DT>(q, col);
+      for (int k = 0; k < W; ++k) v[k] = k < n ? load_elem<DT>(row, c + 32 * k) : 0.0f;
+    } else {
+      load_row<DT, W>(static_cast<const unsigned char*>(row) + c * elem_size(DT), n, vec, v);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) stage[stage_at<W>(((j0 + j) * 32 + lane) / W, ((j0 + j) * 32 + lane) % W)] = e[j];
   }
-  __syncwarp();
-}
-template <int DT, int W>
-__device__ __noinline__ void drain_stage(void* p, int n, const float* stage) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
+  template <int DT>
+  __device__ __forceinline__ void store(void* row, int vec, const float (&v)[W]) const {
+    if constexpr (ANY) {
 #pragma unroll
-  for (int j0 = 0; j0 < W; j0 += 8) {
-    float e[8];
-    int m[8];
-    uintptr_t q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int row = ((j0 + j) * 32 + lane) / W, col = ((j0 + j) * 32 + lane) % W;
-      e[j] = stage[stage_at<W>(row, col)];
-      m[j] = __shfl_sync(0xffffffffu, n, row) - col;
-      q[j] = __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p), row) + col * elem_size(DT);
+      for (int k = 0; k < W; ++k)
+        if (k < n) store_elem<DT>(row, c + 32 * k, v[k]);
+    } else {
+      store_row<DT, W>(static_cast<unsigned char*>(row) + c * elem_size(DT), n, vec, v);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (m[j] > 0) store_elem<DT>(reinterpret_cast<void*>(q[j]), 0, e[j]);
   }
-  __syncwarp();
+};
+__device__ __forceinline__ int valid_columns(int64_t left, int most) { return left >= most ? most : left > 0 ? (int)left : 0; }
+// Thread i's columns, and its row, of rows x cols dealt out to threads (ANY: to warps of a row); no columns behind the last.
+template <int W, bool ANY>
+__device__ __forceinline__ Columns<W, ANY> deal_columns(int64_t i, int64_t rows, int64_t cols, int64_t* row) {
+  Columns<W, ANY> t{0, 0};
+  const int64_t per = ANY ? (cols + 32 * W - 1) / (32 * W) * 32 : (cols + W - 1) / W;
+  *row = 0;
+  if (i < rows * per) {
+    *row = i / per;
+    const int64_t j = i - *row * per;
+    if constexpr (ANY) {
+      t.c = (j >> 5) * (32 * W) + (j & 31);
+      t.n = valid_columns((cols - t.c + 31) >> 5, W);
+    } else {
+      t.c = j * W;
+      t.n = valid_columns(cols - t.c, W);
+    }
+  }
+  return t;
 }
-template <int DT, int W>
-__device__ __forceinline__ void load_rows(const void* p, int n, int vec, float (&v)[W], float* stage) {
-  if (vec) {
-    load_row<DT, W>(p, n, vec, v);
-    return;
-  }
-  fill_stage<DT, W>(p, n, stage);
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int k = 0; k < W; ++k) v[k] = stage[stage_at<W>(lane, k)];
-}
-template <int DT, int W>
-__device__ __forceinline__ void store_rows(void* p, int n, int vec, const float (&v)[W], float* stage) {
-  if (vec) {
-    store_row<DT, W>(p, n, vec, v);
-    return;
-  }
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int k = 0; k < W; ++k) stage[stage_at<W>(lane, k)] = v[k];
-  drain_stage<DT, W>(p, n, stage);
+inline int64_t threads_of(int64_t rows, int64_t cols, int w, bool any) {
+  return rows * (any ? ceil_div(cols, 32 * w) * 32 : ceil_div(cols, w));
 }
 
 // W codes (16 or 32) of an MXFP8 scale of 32, 16-byte aligned (vec: as above): E4M3 to the nearest of v times the power of
@@ -225,9 +206,37 @@ __device__ __forceinline__ void decode_row(const uint8_t* p, int vec, float scal
     v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = c.x, v[4 * i + 3] = c.y;
   }
 }
+// The codes of a row's columns, and their exponents (`row`: the row's codes, `scales`: its exponents, valid where there are
+// columns).  Every lane of the warp calls them.
+template <int W, bool ANY>
+__device__ __forceinline__ void encode_columns(const Columns<W, ANY>& t, uint8_t* row, uint8_t* scales, int vec, const float (&v)[W]) {
+  if constexpr (ANY) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) {   // a scale's 32 columns are the warp's lanes'
+      const float a = k < t.n ? fmaxf(fabsf(v[k]), 0.0f) : 0.0f;   // not negative, no NaN: ordered as integers
+      const int byte = e8m0_of_amax(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a))));
+      if (k >= t.n) continue;
+      row[t.c + 32 * k] = (uint8_t)cvt_e4m3x2(__fmul_rn(v[k], pow2_from_e8m0(byte)), 0.0f);
+      if ((t.c & 31) == 0) scales[(t.c >> 5) + k] = (uint8_t)byte;
+    }
+  } else {
+    const int byte = encode_row<W>(row + t.c, t.n > 0, vec, v);
+    if (t.n > 0 && (t.c & 31) == 0) scales[t.c >> 5] = (uint8_t)byte;
+  }
+}
 // 2^(byte - 127): the subnormal 2^-127 for byte 0, NaN for 255.
 __device__ __forceinline__ float scale_of_e8m0(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+template <int W, bool ANY>
+__device__ __forceinline__ void decode_columns(const Columns<W, ANY>& t, const uint8_t* row, const uint8_t* scales, int vec, float (&v)[W]) {
+  if constexpr (ANY) {
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      v[k] = k < t.n ? __fmul_rn(e4m3x2_to(row[t.c + 32 * k]).x, scale_of_e8m0(scales[(t.c >> 5) + k])) : 0.0f;
+  } else {
+    if (t.n > 0) decode_row<W>(row + t.c, vec, scale_of_e8m0(scales[t.c >> 5]), v);
+  }
 }
 // Rounded to DT as a decoded checkpoint is: bf16 holds every product of a code
 // and a scale down to its subnormals; in fp16 a finite value beyond its range
@@ -240,9 +249,6 @@ __device__ __forceinline__ float decoded(float v) {
   return v;
 }
 
-inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // SMs of the current device; 0 where the query fails.
 inline int num_sms() {
