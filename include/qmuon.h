@@ -738,7 +738,7 @@ typedef enum {
  *   ws            D  256-byte aligned, of qmuon_gated_ffn_workspace_size(ffn);
  *                 qmuon_sync_status reports a wait in the kernel that expired
  * Rows of x and of the weights that do not all start on 16 bytes are copied to
- * the workspace first, but for the projections of 16 rows and fewer.  rows may be 0; rows, width and inner at most 2^28,
+ * the workspace first, but for small projections.  rows may be 0; rows, width and inner at most 2^28,
  * inner * width at most 2^36, rows * inner and rows * width at most 2^38.
  * Sums are taken in an order that depends on the sizes and on the GPU's SM
  * count alone. */

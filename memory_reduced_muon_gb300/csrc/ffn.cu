@@ -520,7 +520,7 @@ struct ElemArgs {
 
 // The workspace's header, by the first CTA of a kernel that is complete before any kernel looks at it.
 __device__ __forceinline__ void clear_header(WsHeader* h) {
-  if (blockIdx.x == 0 && threadIdx.x < kWsHeader / 4) reinterpret_cast<uint32_t*>(h)[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kWsHeader / 4) reinterpret_cast<uint32_t*>(h)[threadIdx.x] = 0u;
 }
 
 // A thread takes 16 columns of a row.  (Of 32, as in the product's epilogue, the 160 registers left 12 warps on an SM:
@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(kElemThreads) join_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 // With few rows the time is the weights' way from DRAM.  A CTA takes 8 columns
 // of gate and the same 8 of up, as the 16 rows of an m16n8k16 product whose 8
-// columns are rows of x (NT such products for 8 NT rows): gate and up of a
+// columns are rows of x (NT such products for 8 NT rows; more rows are other
+// CTAs', grid.y): gate and up of a
 // column meet in one thread.  Its 8 warps take turns over K, 32 at a time: a
 // lane loads 16 bytes of a row of Wg, of Wu and of x at the same columns, in
 // which order K is summed does not matter, so the pieces go straight into the
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) few_kernel(const __grid_consta
   constexpr int kWarps = kFewThreads / 32, U = 2;   // U steps of K at a time
   __shared__ float4 sums[kWarps][NT * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t j = (int64_t)blockIdx.x * kFewCols + g;
+  const int64_t j = (int64_t)blockIdx.x * kFewCols + g, row0 = (int64_t)blockIdx.y * (8 * NT);
   const bool there = j < A.inner;
   const uint16_t* wg = static_cast<const uint16_t*>(F.w[0]) + (there ? j : 0) * F.ld_w[0];
   const uint16_t* wu = static_cast<const uint16_t*>(F.w[1]) + (there ? j : 0) * F.ld_w[1];
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) few_kernel(const __grid_consta
       const int64_t k = (s0 + i * kWarps) * 32 + 8 * t;
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
-        const int row = 8 * m + g;
+        const int64_t row = row0 + 8 * m + g;
         const uint4 x = eight_of<VEC, false>(static_cast<const uint16_t*>(F.x) + (row < A.rows ? row : 0) * F.ld_x, row < A.rows, k, A.width);
         mma_16x8x16<DT>(acc[m], a[i].x, b[i].x, a[i].y, b[i].y, x.x, x.y);
         mma_16x8x16<DT>(acc[m], a[i].z, b[i].z, a[i].w, b[i].w, x.z, x.w);
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) few_kernel(const __grid_consta
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {   // gate and up of column j, rows 2 t and 2 t + 1 of this thread's product
-    const int64_t row = 8 * warp + 2 * t + i;
+    const int64_t row = row0 + 8 * warp + 2 * t + i;
     if (row >= A.rows) break;
     const float gate = i ? v.y : v.x, up = i ? v.w : v.z;
     if (A.part) {   // [gate, up][rows][ld_part]
@@ -784,6 +785,17 @@ struct Geometry {
   bool few = false;                                     // the projections by few_kernel
 };
 
+// Whether few_kernel makes the projections.  Up to 16 rows: one pass over the weights (4096 x 14336 34 us, the CTA pairs
+// 64; 32 rows in one pass 70).  More rows read the weights again for every 16, out of L2, which pays where the pairs' fixed
+// 10 us (tensor memory, a cluster's start, the header's clearing) are the larger part: 64 x 256 x 1024 3.3 us against 10.3,
+// 512 x 512 x 512 8.5 against 12.4, but 512 x 256 x 1024 13.7 against 12.4 and 32 x 2048 x 8192 21.7 against 18.7; with rows
+// off 16 bytes 128 x 256 x 1024 10.2 against 12.4, 256 x 256 x 1024 18.7 against 12.4.
+bool few_rows(int64_t rows, int64_t width, int64_t inner, bool vec) {
+  if (rows <= kFewRows) return true;
+  const int64_t most = vec ? (int64_t)3 << 25 : (int64_t)1 << 25;
+  return rows <= 4096 && inner <= most / rows / width;
+}
+
 // What a call lays out in its workspace, behind the header.
 void lay(Geometry& G, size_t* at, size_t bytes) { *at = G.total, G.total += round_up(bytes, 256); }
 
@@ -817,7 +829,7 @@ Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
   Geometry G;
   G.pairs = pairs;
   G.total = kWsHeader;
-  G.few = c.rows <= kFewRows;
+  G.few = few_rows(c.rows, c.width, c.inner, tma_ready(c.x, c.ld_x) && tma_ready(c.w_gate, c.ld_w_gate) && tma_ready(c.w_up, c.ld_w_up));
   if (!G.few)
     lay_operands(G, c.rows, c.width, c.inner, !tma_ready(c.x, c.ld_x), !tma_ready(c.w_gate, c.ld_w_gate), !tma_ready(c.w_up, c.ld_w_up));
   const bool vectors = vec_class(c.h, c.ld_h, 2) &&
@@ -834,7 +846,8 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
   Geometry G;
   G.pairs = pairs;
   G.total = kWsHeader;
-  G.few = c.rows <= kFewRows;
+  G.few = few_rows(c.rows, c.width, c.inner,
+                   (c.x_scale || tma_ready(c.x, c.ld_x)) && tma_ready(c.w_gate, c.ld_w_gate) && tma_ready(c.w_up, c.ld_w_up));
   const bool w = c.dx || (c.saved == QMUON_SAVE_NONE && !G.few);   // few_kernel reads them as they are
   lay_operands(G, c.rows, c.width, c.inner, needs_x(c) && (c.x_scale || ((c.dw_gate || !G.few) && !tma_ready(c.x, c.ld_x))),
                w && !tma_ready(c.w_gate, c.ld_w_gate), w && !tma_ready(c.w_up, c.ld_w_up));
@@ -939,7 +952,7 @@ void add_join(JoinArgs& A, int64_t* grid, const float* part, int splits, int64_t
 
 template <int DT, int ACT, int NT>
 cudaError_t launch_few_of(const FewArgs& F, bool vec, cudaStream_t s) {
-  const dim3 grid((unsigned)ceil_div(F.A.inner, kFewCols));
+  const dim3 grid((unsigned)ceil_div(F.A.inner, kFewCols), (unsigned)ceil_div(F.A.rows, 8 * NT));
   return vec ? launch_dependent(few_kernel<DT, ACT, NT, true>, grid, dim3(kFewThreads), 0, s, F)
              : launch_dependent(few_kernel<DT, ACT, NT, false>, grid, dim3(kFewThreads), 0, s, F);
 }

@@ -120,10 +120,12 @@ def test_gated_ffn_forward_refusals(L):
     assert call(ws=0) == INV and call(ws=FAKE + 128) == INV
     assert call(dtype=q.QMUON_FP32) == UNS and call(saved=M, inner=97, ld_h=97) == UNS
     assert call(rows=0) == q.QMUON_OK
-    # rows that do not start on 16 bytes are copied, where there are not just a few: the workspace says so
-    size = lambda rows=300, **kw: L.qmuon_gated_ffn_workspace_size(C.byref(_ffn(rows=rows, **kw)))   # noqa: E731
-    assert size() > 0 and size(x=FAKE + 2) >= size() + 300 * 64 * 2 and size(ld_w_up=65) >= size() + 96 * 64 * 2
-    assert size(rows=1, ld_w_up=65) == size(rows=1) > 0
+    # rows that do not start on 16 bytes are copied, but for small products: the workspace says so
+    big = dict(rows=300, width=1024, inner=2048, ld_x=1024, ld_w_gate=1024, ld_w_up=1024, ld_h=2048)
+    size = lambda **kw: L.qmuon_gated_ffn_workspace_size(C.byref(_ffn(**kw)))   # noqa: E731
+    assert size(**big) > 0 and size(**{**big, "x": FAKE + 2}) >= size(**big) + 300 * 1024 * 2
+    assert size(**{**big, "ld_w_up": 1025}) >= size(**big) + 2048 * 1024 * 2
+    assert size(ld_w_up=65) == size() > 0
 
 
 def _grad(**kw):

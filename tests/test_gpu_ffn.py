@@ -32,6 +32,9 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(1, 64, 128, 0, 0), (1, 1, 1, 0, 0), (2, 8, 31, 0, 0), (3, 257, 33, 3, 1), (127, 63, 129, 0, 0), (128, 64, 127, 8, 0),
           (129, 65, 130, 0, 8), (200, 1000, 96, 16, 0), (256, 128, 256, 0, 0), (257, 200, 384, 0, 0), (300, 72, 1001, 5, 3),
           (1, 4096, 640, 0, 0), (17, 1024, 64, 0, 0), (513, 40, 520, 0, 0)]
+# large enough for the tensor-core kernel forward (the smaller ones above go through the cores' registers there)
+LARGE = [(257, 1100, 384, 0, 0), (129, 1001, 301, 3, 1), (300, 72, 2001, 5, 3), (1000, 520, 202, 0, 0), (4097, 72, 33, 0, 0), (4100, 1, 1, 0, 0),
+         (260, 2056, 200, 8, 8)]
 ACTS = ["silu", "gelu", "gelu_tanh"]
 
 
@@ -114,7 +117,7 @@ def _check_forward(shape, dtype, name, saved):
             assert (np.abs(act.decode64(payload, scale) - v) <= half + e).all()
 
 
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + LARGE, ids=str)
 @pytest.mark.parametrize("dtype,name", list(itertools.product(["bf16", "f16"], ACTS)))
 @pytest.mark.parametrize("saved", ["none", "same"])
 def test_forward(shape, dtype, name, saved):
@@ -122,7 +125,7 @@ def test_forward(shape, dtype, name, saved):
 
 
 @pytest.mark.parametrize("shape", [(1, 64, 128, 0, 0), (2, 8, 32, 0, 0), (129, 65, 160, 0, 8), (300, 72, 992, 5, 3), (1, 2048, 64, 0, 0),
-                                   (257, 200, 384, 0, 0)], ids=str)
+                                   (257, 200, 384, 0, 0), (257, 1100, 384, 0, 0), (300, 72, 2016, 5, 3), (4097, 72, 32, 1, 0)], ids=str)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_forward_keeps_8_bits(shape, dtype):
     _check_forward(shape, dtype, "silu", "mxfp8")
@@ -219,7 +222,7 @@ def _backward(shape, dtype, name, saved, x_mxfp8=False, grad_dtype=None, accumul
     return {k: m.t for k, m in out.items()}
 
 
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + LARGE, ids=str)
 @pytest.mark.parametrize("dtype,name,saved", [("bf16", "silu", "none"), ("f16", "gelu", "none"), ("bf16", "gelu_tanh", "same"),
                                               ("f16", "silu", "same"), ("bf16", "gelu", "same"), ("f16", "gelu_tanh", "none")])
 def test_backward(shape, dtype, name, saved):
@@ -227,7 +230,7 @@ def test_backward(shape, dtype, name, saved):
 
 
 @pytest.mark.parametrize("shape", [(1, 64, 128, 0, 0), (2, 32, 32, 0, 0), (129, 64, 160, 0, 8), (300, 96, 992, 5, 3), (1, 2048, 64, 0, 0),
-                                   (257, 224, 384, 0, 0), (1100, 32, 64, 0, 0)], ids=str)
+                                   (257, 224, 384, 0, 0), (1100, 32, 64, 0, 0), (300, 1024, 384, 0, 0), (300, 64, 2016, 5, 3)], ids=str)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("saved,x_mxfp8", [("mxfp8", True), ("mxfp8", False), ("none", True), ("same", True)])
 def test_backward_from_8_bits(shape, dtype, saved, x_mxfp8):
