@@ -191,6 +191,7 @@ __device__ __forceinline__ void move_keys(const SortArgs& A, int64_t first, int 
 // Thread d: the CTA's number of digit d; count[w][d] becomes the number in the warps before w.
 __device__ __forceinline__ uint32_t warps_before(uint16_t (*count)[kDigits]) {
   uint32_t sum = 0;
+#pragma unroll
   for (int w = 0; w < kSortWarps; ++w) {
     const uint32_t k = count[w][threadIdx.x];
     count[w][threadIdx.x] = (uint16_t)sum;
@@ -210,9 +211,8 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* warp_sum) {
   __syncthreads();
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  uint32_t before = incl - v;
-  for (int w = 0; w < warp; ++w) before += warp_sum[w];
-  return before;
+  const uint32_t w = lane < warp ? warp_sum[lane] : 0u;   // the warps before
+  return incl - v + __reduce_add_sync(0xffffffffu, w);
 }
 // Every write of the cluster's CTAs before it is seen by all of them behind it.
 __device__ __forceinline__ void cluster_barrier() {
@@ -240,9 +240,13 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(SortArgs A) 
     A.counts[(int64_t)d * A.n_cta + blockIdx.x] = warps_before(count);
     cluster_barrier();
     uint32_t total = 0, mine = 0;
-    for (int c = 0; c < A.n_cta; ++c) {
+    uint32_t of[kSortCluster];   // all loads at once
+#pragma unroll
+    for (int c = 0; c < kSortCluster; ++c) of[c] = c < A.n_cta ? __ldcg(A.counts + (int64_t)d * A.n_cta + c) : 0u;
+#pragma unroll
+    for (int c = 0; c < kSortCluster; ++c) {
       if (c == (int)blockIdx.x) mine = total;
-      total += __ldcg(A.counts + (int64_t)d * A.n_cta + c);
+      total += of[c];
     }
     base[d] = sum_before(total, warp_sum) + mine;
     __syncthreads();
@@ -391,11 +395,12 @@ __global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
   depends_begin();
   __shared__ int64_t range[2];
   __shared__ uint8_t there[kZeros];
-  if ((int64_t)blockIdx.x >= A.pieces) {
+  const int64_t piece = blockIdx.x;
+  if (piece >= A.pieces) {
     float zero[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) zero[k] = 0.0f;
-    const int64_t r0 = ((int64_t)blockIdx.x - A.pieces) * kZeros;
+    const int64_t r0 = (piece - A.pieces) * kZeros;
     const int rows = (int)(A.zero_rows - r0 < kZeros ? A.zero_rows - r0 : kZeros);
     if (threadIdx.x < 64) {   // the positions of these rows' tokens
       const int warp = threadIdx.x >> 5;
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
     return;
   }
   __shared__ uint2 mine[kPiece + 2];   // the neighbours' keys at both ends
-  const int64_t i0 = (int64_t)blockIdx.x * kPiece;
+  const int64_t i0 = piece * kPiece;
   const int n = (int)(A.n - i0 < kPiece ? A.n - i0 : kPiece);
   if (threadIdx.x < n + 2) {
     const int64_t i = i0 - 1 + threadIdx.x;
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
           write_row<GT, N>(A, key, col, sum);
         } else {
           // slot 0: the run began before this piece (and may go on); slot 1: it begins here and goes on
-          float* p = A.partial + ((int64_t)blockIdx.x * 2 + (before ? 0 : 1)) * A.ldp + col;
+          float* p = A.partial + (piece * 2 + (before ? 0 : 1)) * A.ldp + col;
           store_cols<QMUON_FP32, N>(p, 0, sum);
         }
       }
@@ -468,14 +473,19 @@ template <int GT, int N>
 __global__ void __launch_bounds__(kThreads) join_kernel(SumArgs A) {
   const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
   depends_begin();
-  const int64_t p = blockIdx.x, last = (p + 1) * kPiece - 1;
-  if (last + 1 >= A.n || col >= A.cols) return;
-  const uint32_t key = A.sorted[last].x;
-  if (key >= (uint32_t)A.vocab || A.sorted[last + 1].x != key) return;
-  if (A.sorted[p * kPiece].x == key && p > 0 && A.sorted[p * kPiece - 1].x == key) return;   // it began before
+  const int64_t p = blockIdx.x, last = (p + 1) * kPiece - 1;   // not the last piece: last + 1 is a position
+  if (col >= A.cols) return;
+  // all at once: one way to L2
+  const uint32_t key = A.sorted[last].x, behind = A.sorted[last + 1].x, first = A.sorted[p * kPiece].x;
+  const uint32_t ahead = p > 0 ? A.sorted[p * kPiece - 1].x : 0xFFFFFFFFu;
+  const uint32_t next = p + 2 < A.pieces ? A.sorted[(p + 2) * kPiece].x : 0xFFFFFFFFu;
+  if (key >= (uint32_t)A.vocab || behind != key) return;
+  if (first == key && ahead == key) return;   // it began before
   // the first piece behind it that begins with another key: most runs end in the next one, so the search starts there
-  int64_t lo = p + 2, hi = p + 3, step = 1;
-  while (hi < A.pieces && A.sorted[(hi - 1) * kPiece].x == key) lo = hi, step *= 2, hi += step;
+  int64_t lo = p + 2, hi = p + 2, step = 1;
+  if (next == key)
+    do lo = ++hi, hi += step, step *= 2;
+    while (hi < A.pieces && A.sorted[hi * kPiece].x == key);
   if (hi > A.pieces) hi = A.pieces;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
