@@ -43,6 +43,7 @@ constexpr int kStages = 7;
 constexpr uint32_t kStageBytes = 4 * kBox;         // per CTA: 128 x 64 of A, 128 x 64 of B
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
 constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
+static_assert(kWsHeader == 64 * 4, "clear_kernel's threads");
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
 constexpr int kGroupM = 8;                         // tile rows that run side by side
 
@@ -523,6 +524,14 @@ __device__ __forceinline__ void clear_header(WsHeader* h) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kWsHeader / 4) reinterpret_cast<uint32_t*>(h)[threadIdx.x] = 0u;
 }
 
+// The same as a kernel of its own, for calls that begin with the tensor-core kernel: unlike a memset's, its dependents'
+// start overlaps it.
+__global__ void __launch_bounds__(64) clear_kernel(WsHeader* h) {
+  depends_begin();
+  clear_header(h);
+}
+cudaError_t launch_clear(WsHeader* h, cudaStream_t s) { return launch_dependent(clear_kernel, dim3(1), dim3(64), 0, s, h); }
+
 // A thread takes 16 columns of a row.  (Of 32, as in the product's epilogue, the 160 registers left 12 warps on an SM:
 // 8192 x 14336 from carriers in 214 us.)
 template <int DT, int ACT, int FROM, bool BWD, bool ANY>
@@ -786,13 +795,13 @@ struct Geometry {
 };
 
 // Whether few_kernel makes the projections.  Up to 16 rows: one pass over the weights (4096 x 14336 34 us, the CTA pairs
-// 64; 32 rows in one pass 70).  More rows read the weights again for every 16, out of L2, which pays where the pairs' fixed
-// 10 us (tensor memory, a cluster's start, the header's clearing) are the larger part: 64 x 256 x 1024 3.3 us against 10.3,
-// 512 x 512 x 512 8.5 against 12.4, but 512 x 256 x 1024 13.7 against 12.4 and 32 x 2048 x 8192 21.7 against 18.7; with rows
-// off 16 bytes 128 x 256 x 1024 10.2 against 12.4, 256 x 256 x 1024 18.7 against 12.4.
+// 60; 32 rows in one pass 70).  More rows read the weights again for every 16, out of L2, which pays where the pairs' fixed
+// 6 us (tensor memory, a cluster's start, the header's clearing) are the larger part: 64 x 256 x 1024 3.3 us against 6.6,
+// 128 x 512 x 512 3.5 against 8.0, but 256 x 256 x 1024 7.7 against 7.1 and 64 x 256 x 8192 13.5 against 7.6; with rows
+// off 16 bytes 64 x 256 x 1024 6.6 against 8.0, 128 x 256 x 1024 10.2 against 8.5.
 bool few_rows(int64_t rows, int64_t width, int64_t inner, bool vec) {
   if (rows <= kFewRows) return true;
-  const int64_t most = vec ? (int64_t)3 << 25 : (int64_t)1 << 25;
+  const int64_t most = vec ? (int64_t)1 << 26 : (int64_t)3 << 23;
   return rows <= 4096 && inner <= most / rows / width;
 }
 
@@ -1097,7 +1106,7 @@ extern "C" qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* c, void* 
     if (G.few) {
       e = launch_few(FewArgs{A, x, {w[0], w[1]}, ld_x, {ld_w[0], ld_w[1]}}, c->dtype, s);
     } else {
-      e = cudaMemsetAsync(b, 0, kWsHeader, s);
+      e = launch_clear(A.hdr, s);
       if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, nullptr, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
       if (e != cudaSuccess) return set_error("qmuon_gated_ffn_forward (operands)", e);
       if (!encode_map(&A.a[0], x, c->rows, c->width, ld_x, c->dtype) ||
@@ -1148,7 +1157,7 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
     const void *x = c->x, *w[2] = {c->w_gate, c->w_up};
     int64_t ld_x = c->ld_x, ld_w[2] = {c->ld_w_gate, c->ld_w_up};
     // the header is cleared by the first kernel that needs no wait, where there is one
-    if (c->saved == QMUON_SAVE_NONE && !G.few) e = cudaMemsetAsync(b, 0, kWsHeader, s);
+    if (c->saved == QMUON_SAVE_NONE && !G.few) e = launch_clear(reinterpret_cast<WsHeader*>(b), s);
     const void* w_given[2] = {c->w_gate, c->w_up};
     if (e == cudaSuccess) e = bring_operands(G, b, &x, &ld_x, c->x_scale, w, ld_w, c->rows, c->width, c->inner, c->dtype, s);
     if (e != cudaSuccess) return set_error("qmuon_gated_ffn_backward (operands)", e);
