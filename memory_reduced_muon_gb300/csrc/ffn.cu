@@ -44,7 +44,6 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 256, kBK = 64;
-constexpr int kInnerTile = 128;                    // columns of gate, and of up, in a forward tile
 constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter
 constexpr int kThreads = 64 + 32 * kEpiWarps;      // warp 0 TMA, warp 1 MMA, warps 2.. epilogue
 constexpr int kStages = 7;
@@ -144,7 +143,7 @@ __device__ __forceinline__ void raster(int tile, int tiles_m, int tiles_n, int* 
 __device__ __forceinline__ int blocks_of(int64_t k) { return (int)((k + kBK - 1) / kBK); }
 
 // The i-th unit of CTA pair `pair` out of `pairs`; false behind its last one.
-template <int KIND>
+template <int KIND, int NI>
 __device__ __forceinline__ bool unit_at(const GemmArgs& A, int pair, int pairs, int i, Unit* u) {
   const int64_t first = (int64_t)i * pairs + pair;
   int tm, tn;
@@ -155,7 +154,7 @@ __device__ __forceinline__ bool unit_at(const GemmArgs& A, int pair, int pairs, 
     raster<group_rows(KIND)>(tile, A.tiles_m, A.tiles_n, &tm, &tn);
     u->kind = 0;
     u->m0 = tm * kTile;
-    u->n0 = tn * (KIND == K_GRAD ? kTile : kInnerTile);
+    u->n0 = tn * (KIND == K_GRAD ? kTile : NI);
     const int kb = KIND == K_GRAD ? 2 * blocks_of(A.inner) : blocks_of(A.width);
     u->kb0 = (int)((int64_t)kb * u->split / A.splits);
     u->kb1 = (int)((int64_t)kb * (u->split + 1) / A.splits);
@@ -196,12 +195,12 @@ __device__ __forceinline__ bool unit_at(const GemmArgs& A, int pair, int pairs, 
   return false;
 }
 
-// kind::f16: fp32 accumulator, A and B bf16 or fp16, M = 256, N = 256.
-template <int DT>
+// kind::f16: fp32 accumulator, A and B bf16 or fp16, M = 256, N columns.
+template <int DT, int N>
 __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn) {
   constexpr uint32_t type = DT == QMUON_BF16 ? 1u : 0u;
   return (1u << 4) | (type << 7) | (type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
 // A thread's columns of gate and up: what the forward pass stores.  Every lane of the warp calls this.
@@ -265,8 +264,12 @@ __device__ __forceinline__ const T (&part_of(const T (&v)[M], int q))[N] {
   return *reinterpret_cast<const T(*)[N]>(v + N * q);
 }
 
-template <int KIND, int DT, int ACT>
+// NI: columns of gate, and of up, in a forward tile, 128 or 64 (see pick_tiles).
+template <int KIND, int DT, int ACT, int NI>
 __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ GemmArgs A) {
+  constexpr int N = KIND == K_GRAD ? kTile : 2 * NI;             // columns of an accumulator
+  constexpr int kBoxesB = N / 128;                               // of 64 of them, per CTA and stage
+  constexpr uint32_t kLoadBytes = 2 * (2 + kBoxesB) * kBox;      // of both CTAs per stage
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         if (!mbar_try_wait(empty, parity) && !__all_sync(0xffffffffu, mbar_wait(empty, parity, A.hdr, 0x2100u | KIND))) return false;
         const uint32_t sa = smem0 + s * kStageBytes;
         if (elect_one()) {
-          if (leader) mbar_expect_tx(full0 + 8 * s, 2 * kStageBytes);
+          if (leader) mbar_expect_tx(full0 + 8 * s, kLoadBytes);
           if constexpr (decltype(a_mn)::value) {
             tma_load_2d_pair(sa, ma, bar, am, k0);
             tma_load_2d_pair(sa + kBox, ma, bar, am + 64, k0);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
             tma_load_2d_pair(sa + 3 * kBox, mb, bar, bn + 64, k0);
           } else {
             tma_load_2d_pair(sa + 2 * kBox, mb, bar, k0, bn);
-            tma_load_2d_pair(sa + 3 * kBox, mb, bar, k0, bn + 64);
+            if constexpr (kBoxesB > 1) tma_load_2d_pair(sa + 3 * kBox, mb, bar, k0, bn + 64);
           }
         }
         __syncwarp();
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
       }
       return true;
     };
-    for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+    for (int i = 0; unit_at<KIND, NI>(A, pair, pairs, i, &u); ++i) {
       const int am = u.m0 + 128 * rank;
       bool ok;
       if constexpr (KIND != K_GRAD) {
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         constexpr uint32_t step_a = (amn ? 2048 : 32) >> 4, step_b = (bmn ? 2048 : 32) >> 4;
         const uint64_t first_a = amn ? desc_mnmajor(smem0, 0) : desc_kmajor(smem0, 0);
         const uint64_t first_b = bmn ? desc_mnmajor(smem0 + 2 * kBox, 0) : desc_kmajor(smem0 + 2 * kBox, 0);
-        const uint32_t idesc = instr_desc<DT>(amn, bmn);
+        const uint32_t idesc = instr_desc<DT, N>(amn, bmn);
         for (uint32_t add = 0; n > 0; --n, add = 1) {
           const uint32_t full = full0 + 8 * s;
           if (!mbar_try_wait(full, parity) && !__all_sync(0xffffffffu, mbar_wait(full, parity, A.hdr, 0x2300u | KIND))) return false;
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         return true;
       };
       Unit u;
-      for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+      for (int i = 0; unit_at<KIND, NI>(A, pair, pairs, i, &u); ++i) {
         const int acc = i & 1, use = i >> 1;
         if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * acc, (use - 1) & 1, A.hdr, 0x2500u | KIND))) break;
         tc_fence_after();
@@ -411,14 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_l = cluster_map(tempty0, 0);
     Unit u;
-    for (int i = 0; unit_at<KIND>(A, pair, pairs, i, &u); ++i) {
+    for (int i = 0; unit_at<KIND, NI>(A, pair, pairs, i, &u); ++i) {
       const int64_t r = u.m0 + 128 * rank + quarter * 32 + lane;
       const int acc = i & 1, use = i >> 1;
-      const int64_t c0 = KIND != K_GRAD ? u.n0 + 64 * half : u.n0 + 128 * half;   // this warp's first column
-      uint32_t dh[KIND == K_BWD ? 2 : 1][16];
+      const int64_t c0 = u.n0 + (KIND != K_GRAD ? NI / 2 : 128) * half;   // this warp's first column
+      uint32_t dh[KIND == K_BWD ? NI / 64 : 1][16];
       if (KIND == K_BWD && !A.part) {   // while the tensor cores work
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NI / 64; ++j) {
           const int64_t c = c0 + 32 * j;
           load_dh<DT, 32, false>(A, r, {c, r < A.rows ? valid_columns(A.inner - c, 32) : 0}, dh[j]);
         }
@@ -435,15 +438,15 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
       };
       if (KIND != K_GRAD) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NI / 64; ++j) {
           uint32_t gv[32], uv[32];
           __syncwarp();   // lanes without a row rejoin: tcgen05.ld is warp-collective
-          tmem_ld32_async(t + (uint32_t)(64 * half + 32 * j), gv);
-          tmem_ld32_async(t + (uint32_t)(kInnerTile + 64 * half + 32 * j), uv);
+          tmem_ld32_async(t + (uint32_t)(NI / 2 * half + 32 * j), gv);
+          tmem_ld32_async(t + (uint32_t)(NI + NI / 2 * half + 32 * j), uv);
           tmem_wait_ld();
           tmem_hold(gv);
           tmem_hold(uv);
-          if (j == 1) release();
+          if (j == NI / 64 - 1) release();
           float g[32], v[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) g[k] = __uint_as_float(gv[k]), v[k] = __uint_as_float(uv[k]);
@@ -780,15 +783,26 @@ bool encode_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, in
 // A tensor map reads rows that start on 16 bytes; others are copied to the workspace first.
 bool tma_ready(const void* p, int64_t ld) { return is_aligned(p, 16) && ld % 8 == 0; }
 
-// Splits of a product of `tiles` tiles of `kb` K blocks: the least estimated time, in K blocks of a pair.  A unit's start
-// and epilogue cost about as much as 6 blocks, partial sums another 4 and their second kernel 8.
-int pick_splits(int64_t tiles, int kb, int pairs) {
-  if (tiles >= pairs) return 1;
-  int best = 1;
+// The width of the projections' tiles and the splits of their K blocks: the least estimated time, in K blocks of a pair on
+// a tile of 128 columns.  A unit's start and epilogue cost about as much as 6 blocks, partial sums another 4 and their
+// second kernel 8; a tile of 64 columns has half the epilogue, and blocks of 0.55 (its rows' operand is as large).  Narrow
+// tiles are for what fills the pairs badly: 100 x 4096 x 512 13.2 us against 19.0, 300 x 256 x 8192 10.9 against 11.9, 4000 x
+// 512 x 512 9.4 against 10.3, 64 x 4096 x 14336 46.6 against 48.4; wide ones for the rest: 1024 x 4096 x 14336 123 against 149.
+struct Tiles {
+  int inner, splits;
+};
+Tiles pick_tiles(int64_t rows, int64_t width, int64_t inner, int pairs) {
+  const int64_t kb = ceil_div(width, kBK);
+  Tiles best{128, 1};
   int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= 32 && s <= std::max(1, kb / 4); ++s) {
-    const int64_t cost = ceil_div(tiles * s, pairs) * (ceil_div(kb, s) + 6 + (s > 1 ? 4 : 0)) + (s > 1 ? 8 : 0);
-    if (cost < best_cost) best_cost = cost, best = s;
+  for (const int ni : {128, 64}) {
+    const int64_t tiles = ceil_div(rows, kTile) * ceil_div(inner, ni), block = ni == 128 ? 20 : 11, fixed = ni == 128 ? 120 : 75;
+    const int most = tiles >= pairs ? 1 : (int)std::min<int64_t>(32, std::max<int64_t>(1, kb / 4));
+    for (int s = 1; s <= most; ++s) {
+      const int64_t cost =
+          ceil_div(tiles * s, pairs) * (ceil_div(kb, s) * block + fixed + (s > 1 ? 2 * fixed / 3 : 0)) + (s > 1 ? 160 : 0);
+      if (cost < best_cost) best_cost = cost, best = Tiles{ni, s};
+    }
   }
   return best;
 }
@@ -796,6 +810,7 @@ int pick_splits(int64_t tiles, int kb, int pairs) {
 struct Geometry {
   int pairs = 0;
   int32_t tiles_m = 0, tiles_n = 0, splits = 1;         // forward (or the projections again)
+  int32_t inner_tile = 128;
   int32_t dx_m = 0, dx_n = 0, dx_splits = 1;
   int32_t dw_m = 0, dw_n = 0, dw_splits = 1;
   int64_t ld_fwd = 0, ld_w = 0, ld_d = 0;               // of partial gate/up, of partial dx/dW, of dgate/dup
@@ -840,8 +855,10 @@ void lay_projections(Geometry& G, int64_t rows, int64_t width, int64_t inner, bo
     return;
   }
   G.tiles_m = (int32_t)ceil_div(rows, kTile);
-  G.tiles_n = (int32_t)ceil_div(inner, kInnerTile);
-  G.splits = pick_splits((int64_t)G.tiles_m * G.tiles_n, (int)ceil_div(width, kBK), G.pairs);
+  const Tiles t = pick_tiles(rows, width, inner, G.pairs);
+  G.inner_tile = t.inner;
+  G.tiles_n = (int32_t)ceil_div(inner, t.inner);
+  G.splits = t.splits;
   if (G.splits > 1 || !direct) lay(G, &G.part, (size_t)G.splits * 2 * rows * G.ld_fwd * 4);
 }
 
@@ -933,19 +950,21 @@ cudaError_t launch_pairs(K kernel, const GemmArgs& A, int64_t units, int pairs, 
   return cudaLaunchKernelEx(&cfg, kernel, A);
 }
 
-template <int KIND, int DT>
+template <int KIND, int DT, int NI>
 cudaError_t launch_act(const GemmArgs& A, int64_t units, int pairs, cudaStream_t s) {
-  if constexpr (KIND == K_GRAD) {
-    return launch_pairs(ffn_kernel<K_GRAD, DT, 0>, A, units, pairs, s);
-  } else {
-    if (A.act == QMUON_ACT_SILU) return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_SILU>, A, units, pairs, s);
-    if (A.act == QMUON_ACT_GELU) return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_GELU>, A, units, pairs, s);
-    return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_GELU_TANH>, A, units, pairs, s);
-  }
+  if (A.act == QMUON_ACT_SILU) return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_SILU, NI>, A, units, pairs, s);
+  if (A.act == QMUON_ACT_GELU) return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_GELU, NI>, A, units, pairs, s);
+  return launch_pairs(ffn_kernel<KIND, DT, QMUON_ACT_GELU_TANH, NI>, A, units, pairs, s);
 }
 template <int KIND>
-cudaError_t launch_gemm(const GemmArgs& A, int64_t units, int pairs, int dt, cudaStream_t s) {
-  return dt == QMUON_BF16 ? launch_act<KIND, QMUON_BF16>(A, units, pairs, s) : launch_act<KIND, QMUON_FP16>(A, units, pairs, s);
+cudaError_t launch_projections(const GemmArgs& A, const Geometry& G, int dt, cudaStream_t s) {
+  if (G.inner_tile == 128)
+    return dt == QMUON_BF16 ? launch_act<KIND, QMUON_BF16, 128>(A, A.units, G.pairs, s) : launch_act<KIND, QMUON_FP16, 128>(A, A.units, G.pairs, s);
+  return dt == QMUON_BF16 ? launch_act<KIND, QMUON_BF16, 64>(A, A.units, G.pairs, s) : launch_act<KIND, QMUON_FP16, 64>(A, A.units, G.pairs, s);
+}
+cudaError_t launch_gradients(const GemmArgs& A, int64_t units, int pairs, int dt, cudaStream_t s) {
+  return dt == QMUON_BF16 ? launch_pairs(ffn_kernel<K_GRAD, QMUON_BF16, 0, 128>, A, units, pairs, s)
+                          : launch_pairs(ffn_kernel<K_GRAD, QMUON_FP16, 0, 128>, A, units, pairs, s);
 }
 
 template <int DT, int FROM, bool BWD>
@@ -1124,7 +1143,7 @@ extern "C" qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* c, void* 
           !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
           !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
         return QMUON_ERR_CUDA;
-      e = launch_gemm<K_FWD>(A, A.units, G.pairs, c->dtype, s);
+      e = launch_projections<K_FWD>(A, G, c->dtype, s);
     }
     if (e == cudaSuccess && A.part) {
       ElemArgs E{};
@@ -1193,7 +1212,7 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
             !encode_map(&A.b[0], w[0], c->inner, c->width, ld_w[0], c->dtype) ||
             !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype))
           return QMUON_ERR_CUDA;
-        e = launch_gemm<K_BWD>(A, A.units, G.pairs, c->dtype, s);
+        e = launch_projections<K_BWD>(A, G, c->dtype, s);
       }
       if (e == cudaSuccess && A.part) {
         E.A = A;
@@ -1242,7 +1261,7 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
                   !encode_map(&A.b[1], w[1], c->inner, c->width, ld_w[1], c->dtype)))
       return QMUON_ERR_CUDA;
     if (c->dw_gate && !encode_map(&A.b[2], x, c->rows, c->width, ld_x, c->dtype)) return QMUON_ERR_CUDA;
-    e = launch_gemm<K_GRAD>(A, units_x + units_w, pairs, c->dtype, s);
+    e = launch_gradients(A, units_x + units_w, pairs, c->dtype, s);
     JoinArgs J{};
     int64_t grid = 0;
     if (A.part) add_join(J, &grid, A.part, G.dx_splits, c->rows, c->width, G.ld_w, c->dx, c->ld_dx, c->dtype, 0);
