@@ -783,11 +783,12 @@ bool encode_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, in
 // A tensor map reads rows that start on 16 bytes; others are copied to the workspace first.
 bool tma_ready(const void* p, int64_t ld) { return is_aligned(p, 16) && ld % 8 == 0; }
 
-// The width of the projections' tiles and the splits of their K blocks: the least estimated time, in K blocks of a pair on
-// a tile of 128 columns.  A unit's start and epilogue cost about as much as 6 blocks, partial sums another 4 and their
-// second kernel 8; a tile of 64 columns has half the epilogue, and blocks of 0.55 (its rows' operand is as large).  Narrow
-// tiles are for what fills the pairs badly: 100 x 4096 x 512 13.2 us against 19.0, 300 x 256 x 8192 10.9 against 11.9, 4000 x
-// 512 x 512 9.4 against 10.3, 64 x 4096 x 14336 46.6 against 48.4; wide ones for the rest: 1024 x 4096 x 14336 123 against 149.
+// The width of the projections' tiles and the splits of their K blocks: the least estimated time, in twentieths of a K
+// block of a pair on a tile of 128 columns.  A block of 64 columns takes 12 (its rows' operand is as large), a unit 20 more,
+// the last epilogue 200 or 100, partial sums 40 a unit and 160 for their kernel.  Narrow tiles are for what fills the pairs
+// badly, and for short K, where the last epilogue counts: 100 x 4096 x 512 13.2 us against 19.0, 2000 x 256 x 1024 8.1
+// against 8.8, 4000 x 512 x 512 9.4 against 10.3, 64 x 4096 x 14336 46.6 against 48.4; wide ones for the rest: 300 x 1000 x
+// 3000 16.2 against 18.4, 1024 x 4096 x 14336 123 against 149.
 struct Tiles {
   int inner, splits;
 };
@@ -796,12 +797,12 @@ Tiles pick_tiles(int64_t rows, int64_t width, int64_t inner, int pairs) {
   Tiles best{128, 1};
   int64_t best_cost = INT64_MAX;
   for (const int ni : {128, 64}) {
-    const int64_t tiles = ceil_div(rows, kTile) * ceil_div(inner, ni), block = ni == 128 ? 20 : 11, fixed = ni == 128 ? 120 : 75;
+    const int64_t tiles = ceil_div(rows, kTile) * ceil_div(inner, ni), block = ni == 128 ? 20 : 12, last = ni == 128 ? 200 : 100;
     const int most = tiles >= pairs ? 1 : (int)std::min<int64_t>(32, std::max<int64_t>(1, kb / 4));
     for (int s = 1; s <= most; ++s) {
       const int64_t cost =
-          ceil_div(tiles * s, pairs) * (ceil_div(kb, s) * block + fixed + (s > 1 ? 2 * fixed / 3 : 0)) + (s > 1 ? 160 : 0);
-      if (cost < best_cost) best_cost = cost, best = Tiles{ni, s};
+          ceil_div(tiles * s, pairs) * (ceil_div(kb, s) * block + 20 + (s > 1 ? 40 : 0)) + last + (s > 1 ? 160 : 0);
+      if (cost < (ni == best.inner ? best_cost : best_cost * 9 / 10)) best_cost = cost, best = Tiles{ni, s};   // narrow: only where it is clear
     }
   }
   return best;
