@@ -264,6 +264,12 @@ __device__ __forceinline__ const T (&part_of(const T (&v)[M], int q))[N] {
   return *reinterpret_cast<const T(*)[N]>(v + N * q);
 }
 
+// A wait of a whole warp, whose lanes go on together or not at all: tried in line, then bounded.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, WsHeader* h, unsigned where) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, h, where));
+}
+
 // NI: columns of gate, and of up, in a forward tile, 128 or 64 (see pick_tiles).
 template <int KIND, int DT, int ACT, int NI>
 __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ GemmArgs A) {
@@ -292,7 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     }
     fence_mbar_init();
   }
-  if (warp == 0 && lane < 5) prefetch_map(lane < 2 ? &A.a[lane] : &A.b[lane - 2]);
+  // the tensor maps that this call reads, ahead of the first copies
+  if (KIND != K_GRAD) {
+    if (warp == 0 && lane < 2) prefetch_map(lane == 0 ? &A.a[0] : &A.b[rank]);
+  } else if (warp == 0 && lane < 5) {
+    if (lane < 2) prefetch_map(&A.a[lane]);
+    else if (lane < 4 ? A.units > 0 : A.units_w > 0) prefetch_map(&A.b[lane - 2]);
+  }
   if (warp == 1) {
     tmem_alloc_cg<2>(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_cg<2>();
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     auto load = [&](auto a_mn, auto b_mn, const CUtensorMap* ma, const CUtensorMap* mb, int am, int bn, int k0, int n) -> bool {
       for (; n > 0; --n, ++it, k0 += kBK) {
         const uint32_t empty = empty0 + 8 * s, bar = full_l + 8 * s;
-        if (!mbar_try_wait(empty, parity) && !__all_sync(0xffffffffu, mbar_wait(empty, parity, A.hdr, 0x2100u | KIND))) return false;
+        if (!warp_wait(empty, parity, A.hdr, 0x2100u | KIND)) return false;
         const uint32_t sa = smem0 + s * kStageBytes;
         if (elect_one()) {
           if (leader) mbar_expect_tx(full0 + 8 * s, kLoadBytes);
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         const uint32_t idesc = instr_desc<DT, N>(amn, bmn);
         for (uint32_t add = 0; n > 0; --n, add = 1) {
           const uint32_t full = full0 + 8 * s;
-          if (!mbar_try_wait(full, parity) && !__all_sync(0xffffffffu, mbar_wait(full, parity, A.hdr, 0x2300u | KIND))) return false;
+          if (!warp_wait(full, parity, A.hdr, 0x2300u | KIND)) return false;
           tc_fence_after();
           const uint64_t ad = first_a + (uint32_t)(s * (kStageBytes >> 4)), bd = first_b + (uint32_t)(s * (kStageBytes >> 4));
           if (elect_one()) {
@@ -397,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
       Unit u;
       for (int i = 0; unit_at<KIND, NI>(A, pair, pairs, i, &u); ++i) {
         const int acc = i & 1, use = i >> 1;
-        if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * acc, (use - 1) & 1, A.hdr, 0x2500u | KIND))) break;
+        if (use > 0 && !warp_wait(tempty0 + 8 * acc, (use - 1) & 1, A.hdr, 0x2500u | KIND)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * kTile);
         bool ok;

@@ -407,3 +407,24 @@ def test_calls_on_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for a, b in hs:
         assert torch.equal(a, b)
+
+
+def test_a_recorded_failure_is_reported_and_cleared():
+    rows, width, inner = 300, 1024, 512
+    x, w = torch.ones(rows, width, device="cuda").bfloat16(), torch.ones(inner, width, device="cuda").bfloat16()
+    h = torch.empty(rows, inner, dtype=torch.bfloat16, device="cuda")
+    call = q.gated_ffn(x, w, w, h, rows, width, inner, "bf16")
+    ws = torch.empty(q.qmuon_gated_ffn_workspace_size(call), dtype=torch.uint8, device="cuda")
+    q.qmuon_gated_ffn_forward(call, ws)
+    want = h.clone()
+    ws[:8].view(torch.int32).copy_(torch.tensor([q.QMUON_ERR_TIMEOUT, 0x2300], dtype=torch.int32))    # as a kernel records it
+    with pytest.raises(q.QmuonError) as e:
+        q.qmuon_sync_status(ws)
+    assert e.value.status == q.QMUON_ERR_TIMEOUT
+    q.qmuon_sync_status(ws)
+    # a record that nobody read does not stop the next call
+    ws[:4].view(torch.int32).fill_(q.QMUON_ERR_TIMEOUT)
+    h.fill_(0.0)
+    q.qmuon_gated_ffn_forward(call, ws)
+    q.qmuon_sync_status(ws)
+    assert torch.equal(h, want)
