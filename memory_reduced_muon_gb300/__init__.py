@@ -853,6 +853,28 @@ def _tokens(x, n: int, bits: int, where: str):
     return _array(x, None, n, where, "tokens"), bits
 
 
+_device = None   # the current device's index, where torch has it without a call of its own
+
+
+def _current_device() -> int:
+    global _device
+    if _device is None:
+        import torch
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device()
+
+
+def _here(where: str, *arrays):
+    """Tensors lie on the current device, on which the call's kernels run (after the checks that they are on a GPU)."""
+    device = None
+    for x in arrays:
+        if x is not None and not isinstance(x, int):
+            if device is None:
+                device = _current_device()
+            if x.get_device() != device:
+                _refuse(x, where, "every array", f"on the current device, cuda:{device}")
+
+
 def _call(where: str, packed, *args):
     st = (_bytes_entries.get(where) or _by_bytes(where))(packed, *args)
     if st != QMUON_OK:
@@ -873,6 +895,7 @@ def qmuon_embedding_forward(table, tokens, out, n_tokens: int, vocab: int, cols:
                             dtype, bits, 0)
     except (struct.error, OverflowError) as e:
         raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    _here(where, table, tokens, out)
     _call(where, packed, _raw_stream() if stream is None and _raw_stream else _stream(stream))
 
 
@@ -895,6 +918,7 @@ def qmuon_embedding_backward(dout, tokens, dtable, n_tokens: int, vocab: int, co
                                  ld_dout, ld_dtable, scale, dtype, grad_dtype, bits, 1 if accumulate else 0, 0)
     except (struct.error, OverflowError) as e:
         raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    _here(where, dout, tokens, dtable, ws)
     _call(where, packed, _on_gpu(ws, where, "ws"), _nbytes(ws) if ws_bytes is None else int(ws_bytes),
           _raw_stream() if stream is None and _raw_stream else _stream(stream))
 
@@ -908,6 +932,7 @@ def _mxfp8(where: str, x, payload, scale_inv, rows: int, cols: int, dtype, ld_x:
                         _bytes(scale_inv, rows * (cols // 32), where, "scale_inv"), rows, cols, ld_x, dtype, 0)
     except (struct.error, OverflowError) as e:
         raise QmuonError(QMUON_ERR_INVALID_ARGUMENT, where, str(e)) from None
+    _here(where, x, payload, scale_inv)
     _call(where, packed, _raw_stream() if stream is None and _raw_stream else _stream(stream))
 
 
@@ -959,6 +984,7 @@ def qmuon_gated_ffn_workspace_size(ffn: qmuon_gated_ffn) -> int:
 
 def qmuon_gated_ffn_forward(ffn: qmuon_gated_ffn, ws, ws_bytes: Optional[int] = None, stream=None):
     where = "qmuon_gated_ffn_forward"
+    _here(where, ws, *getattr(ffn, "_keep", ()))
     st = (_lib_handle or lib()).qmuon_gated_ffn_forward(C.byref(ffn), _on_gpu(ws, where, "ws"),
                                                         _nbytes(ws) if ws_bytes is None else int(ws_bytes),
                                                         _raw_stream() if stream is None and _raw_stream else _stream(stream))
@@ -1009,6 +1035,7 @@ def qmuon_gated_ffn_backward_workspace_size(ffn: qmuon_gated_ffn_grad) -> int:
 
 def qmuon_gated_ffn_backward(ffn: qmuon_gated_ffn_grad, ws, ws_bytes: Optional[int] = None, stream=None):
     where = "qmuon_gated_ffn_backward"
+    _here(where, ws, *getattr(ffn, "_keep", ()))
     st = (_lib_handle or lib()).qmuon_gated_ffn_backward(C.byref(ffn), _on_gpu(ws, where, "ws"),
                                                          _nbytes(ws) if ws_bytes is None else int(ws_bytes),
                                                          _raw_stream() if stream is None and _raw_stream else _stream(stream))

@@ -428,3 +428,19 @@ def test_a_recorded_failure_is_reported_and_cleared():
     q.qmuon_gated_ffn_forward(call, ws)
     q.qmuon_sync_status(ws)
     assert torch.equal(h, want)
+
+
+def test_arrays_of_another_device_are_refused(monkeypatch):
+    """The calls run on the current device; with one GPU here, the current one is said to be another."""
+    t = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    tokens, byte = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    call = q.gated_ffn(t, t, t, torch.empty(4, 4, dtype=torch.bfloat16, device="cuda"), 4, 64, 4, "bf16")
+    grad = q.gated_ffn_grad(torch.empty(4, 4, dtype=torch.bfloat16, device="cuda"), t, t, t, t.clone(), None, None, 4, 64, 4, "bf16")
+    monkeypatch.setattr(q, "_device", lambda: 1)
+    for f in (lambda: q.qmuon_embedding_forward(t, tokens, t.clone(), 4, 4, 64, "bf16"),
+              lambda: q.qmuon_embedding_backward(t, tokens, t.clone(), 4, 4, 64, "bf16", byte, ws_bytes=1 << 20),
+              lambda: q.qmuon_mxfp8_encode(t, byte, byte, 4, 64, "bf16"), lambda: q.qmuon_mxfp8_decode(byte, byte, t, 4, 64, "bf16"),
+              lambda: q.qmuon_gated_ffn_forward(call, byte), lambda: q.qmuon_gated_ffn_backward(grad, byte)):
+        with pytest.raises(q.QmuonError) as e:
+            f()
+        assert e.value.status == q.QMUON_ERR_INVALID_ARGUMENT and "current device" in str(e.value)
