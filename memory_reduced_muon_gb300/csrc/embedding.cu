@@ -467,14 +467,16 @@ __global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
   }
 }
 
-// The runs that cross pieces: CTA (piece, slab) adds up the run that begins in its piece and goes on behind it.  The
-// pieces' sums are added in four interleaved chains (piece j in chain j mod 4), then the chains in order.
+// The runs that cross pieces: CTA (piece, slab) adds up the run that begins in its piece and goes on behind it.  Warp w
+// takes the run's pieces w, w + 8, ... in order, 4 at a time on their way, and the warps' sums are added in order: a token
+// that is most of a batch has thousands of pieces.
+constexpr int kJoinWarps = 8;
 template <int GT, int N>
-__global__ void __launch_bounds__(kThreads) join_kernel(SumArgs A) {
-  const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SumArgs A) {
+  __shared__ float sums[kJoinWarps][32][N];
+  const int warp = threadIdx.y;
   depends_begin();
   const int64_t p = blockIdx.x, last = (p + 1) * kPiece - 1;   // not the last piece: last + 1 is a position
-  if (col >= A.cols) return;
   // all at once: one way to L2
   const uint32_t key = A.sorted[last].x, behind = A.sorted[last + 1].x, first = A.sorted[p * kPiece].x;
   const uint32_t ahead = p > 0 ? A.sorted[p * kPiece - 1].x : 0xFFFFFFFFu;
@@ -492,32 +494,43 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SumArgs A) {
     if (A.sorted[mid * kPiece].x == key) lo = mid + 1;
     else hi = mid;
   }
-  float chain[4][N];
+  for (int64_t slab = (int64_t)blockIdx.y * 32 * N; slab < A.cols; slab += (int64_t)gridDim.y * 32 * N) {
+    const int64_t col = slab + threadIdx.x * N;
+    const bool there = col < A.cols;
+    float sum[N];
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+    for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+    if (there) {
+      if (warp == 0) load_cols<QMUON_FP32, N>(A.partial, (p * 2 + 1) * A.ldp + col, sum);
+      for (int64_t j = p + 1 + warp; j < lo; j += 4 * kJoinWarps) {
+        float v[4][N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) chain[c][k] = 0.0f;
-  load_cols<QMUON_FP32, N>(A.partial, (p * 2 + 1) * A.ldp + col, chain[0]);
-  for (int64_t j = p + 1; j < lo; j += 4) {
-    float v[4][N];
+        for (int c = 0; c < 4; ++c) {
+          if (j + c * kJoinWarps < lo) {
+            load_cols<QMUON_FP32, N>(A.partial, (j + c * kJoinWarps) * 2 * A.ldp + col, v[c]);
+          } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (j + c < lo) {
-        load_cols<QMUON_FP32, N>(A.partial, (j + c) * 2 * A.ldp + col, v[c]);
-      } else {
+            for (int k = 0; k < N; ++k) v[c][k] = 0.0f;
+          }
+        }
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[c][k] = 0.0f;
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < N; ++k) sum[k] += v[c][k];
       }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int k = 0; k < N; ++k) sums[warp][threadIdx.x][k] = sum[k];
+    __syncthreads();
+    if (warp == 0 && there) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) chain[c][k] += v[c][k];
+      for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] += sums[w][threadIdx.x][k];
+      write_row<GT, N>(A, key, col, sum);
+    }
+    __syncthreads();
   }
-  float sum[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) sum[k] = (chain[0][k] + chain[1][k]) + (chain[2][k] + chain[3][k]);
-  write_row<GT, N>(A, key, col, sum);
 }
 
 struct Layout {
@@ -575,7 +588,8 @@ cudaError_t launch_sums(const SumArgs& A, cudaStream_t s) {
   const int64_t zeros = ceil_div(A.zero_rows, kZeros);
   const int threads = (int)std::min<int64_t>(kThreads, round_up((size_t)ceil_div(A.cols, N), 32));
   cudaError_t e = launch_dependent(sum_kernel<DT, GT, N>, dim3((unsigned)(A.pieces + zeros), slabs), dim3(std::max(threads, 64)), 0, s, A);
-  if (e == cudaSuccess && A.pieces > 1) e = launch_dependent(join_kernel<GT, N>, dim3(A.pieces - 1, slabs), dim3(std::max(threads, 64)), 0, s, A);
+  if (e == cudaSuccess && A.pieces > 1)
+    e = launch_dependent(join_kernel<GT, N>, dim3(A.pieces - 1, (unsigned)std::min<int64_t>(ceil_div(A.cols, (int64_t)32 * N), 4096)), dim3(32, kJoinWarps), 0, s, A);
   return e;
 }
 template <int DT>

@@ -143,6 +143,21 @@ def test_gradient_of_many_tokens(n, vocab, kind):
     _backward(n, vocab, 8, 0, 0, "f32", "f32", kind, 64, False)
 
 
+def test_gradient_of_very_wide_rows():
+    """More columns than a grid's second dimension has slabs of 32, by elements and by vectors."""
+    for cols, dtype in ((4200000 - 5701, "f32"), (4194304, "bf16")):
+        n, vocab = 70, 2
+        tokens = torch.cat([torch.zeros(66, dtype=torch.int64), torch.ones(4, dtype=torch.int64)]).cuda()
+        dout = torch.ones(n, cols, dtype=DT[dtype], device="cuda")
+        grad = torch.full((vocab, cols), 7.0, dtype=DT[dtype], device="cuda")
+        ws = torch.empty(q.qmuon_embedding_workspace_size(n, vocab, cols), dtype=torch.uint8, device="cuda")
+        q.qmuon_embedding_backward(dout, tokens, grad, n, vocab, cols, dtype, ws)
+        assert bool((grad[0] == 66).all()) and bool((grad[1] == 4).all())
+        out = torch.empty(n, cols, dtype=DT[dtype], device="cuda")
+        q.qmuon_embedding_forward(grad, tokens, out, n, vocab, cols, dtype, scale=0.5)
+        assert bool((out[:66] == 33).all()) and bool((out[66:] == 2).all())
+
+
 def test_gradient_of_no_tokens():
     for accumulate in (False, True):
         _backward(0, 70, 72, 8, 0, "bf16", "bf16", "all", 64, accumulate)
