@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(SortArgs A) {
 // sums
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 32;    // sorted positions of a piece
-constexpr int kZeros = 16;    // rows of a CTA that looks for rows without a token
+constexpr int kZeros = 16;    // rows of a CTA that looks for rows without a token (102400 x 4096 bf16 166 us; 8 rows 173, 32 168)
 
 struct SumArgs {
   const uint2* sorted;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
 #pragma unroll
   for (int k = 0; k < N; ++k) sum[k] = 0.0f;
   bool before = mine[0].x == mine[1].x;   // the run began in an earlier piece
-  constexpr int U = 4;                    // rows in flight
+  constexpr int U = N == 1 ? 16 : 4;      // rows in flight (single columns: 4 rows 195 us, 16 180, for 65536 x 1001 fp32)
   for (int j0 = 0; j0 < n; j0 += U) {
     float v[U][N];
 #pragma unroll
