@@ -767,7 +767,12 @@ QMUON_API qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* ffn, void*
  *   dgate = dh * up * act'(gate)    dup = dh * act(gate)
  *   dx = dgate Wg + dup Wu          dWg = dgate^T x       dWu = dup^T x
  * dgate and dup are rounded to dtype before the products; dx, dWg and dWu once
- * more at the end.
+ * more at the end.  In fp16 the two are held times a power of two, for which
+ * dh's largest finite magnitude becomes 1/4 or more and the products' sums are
+ * divided by it again: below 2^-12 of that magnitude they lose bits, to 2^-23
+ * of it (times up act' and act).  Where one leaves fp16's range, as with up act'
+ * or act beyond 1.3e5, or with a magnitude of 1/4 or more (held as it is) and a
+ * product beyond 65504, it is infinite.
  *   x, x_scale   x_scale NULL: x as in the forward pass;  else x is an MXFP8
  *                carrier (codes, 16-byte aligned, and exponents; width % 32 != 0
  *                is QMUON_ERR_UNSUPPORTED), decoded as qmuon_mxfp8_decode does;

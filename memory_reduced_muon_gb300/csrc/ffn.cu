@@ -16,7 +16,11 @@
 // The gradients dgate and dup are rounded to the type of the activations before
 // the products that read them (tensor cores take 16-bit operands of one type).
 // Their roundings are independent of the result's own and as large, relative to
-// its norm: in bf16 the results are off by 0.0024 instead of 0.0017.
+// its norm: in bf16 the results are off by 0.0024 instead of 0.0017.  fp16 has
+// no room for small ones (dh of 1e-5 would leave a weight's gradient off by 3%
+// of its norm), so there both are held times a power of two, one for the call,
+// that dh's largest magnitude sets (dh_scale), and the products' sums are
+// divided by it, which is exact.
 //
 // Few tiles: the K range is split over units, whose fp32 partial sums go
 // through the workspace and a second kernel that adds them in order.  Few rows,
@@ -109,6 +113,8 @@ struct GemmArgs {
   int64_t ld_h, ld_gate, ld_up;
   const void* dh;            // backward
   int64_t ld_dh;
+  const uint32_t* dh_max;    // fp16: dh_max_kernel's `dh_parts` maxima
+  int32_t dh_parts;
   void *dgate, *dup;
   int64_t ld_d;
   // gradients
@@ -221,15 +227,31 @@ __device__ __forceinline__ void finish_forward(const GemmArgs& A, int64_t r, con
     encode_columns(t, static_cast<uint8_t*>(A.up) + e, A.up_scale + (e >> 5), A.vec_up, u);
   }
 }
+// The power of two that dgate and dup are held times: 1 but in fp16, where dh's largest finite magnitude is brought to
+// [1/4, 1/2) if it lies below.  What is 2^-12 of it keeps all of its bits, and a smaller value is off by 2^-23 of it at most
+// (times up act' or act); 1.3e5 times it still fits.  Never below 1: nothing is held with fewer bits than without.  Every
+// lane of the warp calls this.
+struct DhScale {
+  float times, back;   // and its inverse
+};
+template <int DT>
+__device__ __forceinline__ DhScale dh_scale(const GemmArgs& A) {
+  if constexpr (DT != QMUON_FP16) return {1.0f, 1.0f};
+  uint32_t m = 0;   // of fp32, not negative: ordered as integers
+  for (int i = threadIdx.x & 31; i < A.dh_parts; i += 32) m = max(m, A.dh_max[i]);
+  const uint32_t e = __reduce_max_sync(0xffffffffu, m) >> 23;   // 103 at least, or 0 for zero
+  if (e == 0 || e >= 125) return {1.0f, 1.0f};
+  return {__uint_as_float((252 - e) << 23), __uint_as_float((e + 2) << 23)};
+}
 // The same of the backward pass, from dh's words: dgate and dup for the products, and h again.
 template <int DT, int ACT, int W, bool ANY>
 __device__ __forceinline__ void finish_backward(const GemmArgs& A, int64_t r, const Columns<W, ANY>& t, const float (&g)[W],
-                                                const float (&u)[W], const uint32_t (&dh)[W / 2]) {
+                                                const float (&u)[W], const uint32_t (&dh)[W / 2], DhScale scale) {
   float h[W], dg[W], du[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const float2 a = act_and_slope<ACT>(g[i]), d = unpack2<DT>(dh[i >> 1]);
-    const float x = i & 1 ? d.y : d.x;
+    const float x = (i & 1 ? d.y : d.x) * scale.times;   // exact
     h[i] = a.x * u[i];
     dg[i] = x * u[i] * a.y;
     du[i] = x * a.x;
@@ -425,6 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     // ---- epilogue: warps 2..9; TMEM lane quarter = warp % 4 ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_l = cluster_map(tempty0, 0);
+    DhScale scale{1.0f, 1.0f};
+    if constexpr (KIND != K_FWD) scale = dh_scale<DT>(A);
     Unit u;
     for (int i = 0; unit_at<KIND, NI>(A, pair, pairs, i, &u); ++i) {
       const int64_t r = u.m0 + 128 * rank + quarter * 32 + lane;
@@ -476,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 #pragma unroll
             for (int q = 0; q < 2; ++q)
               finish_backward<DT, ACT, 16, false>(A, r, {c + 16 * q, valid_columns(n - 16 * q, 16)}, part_of<16>(g, q),
-                                                  part_of<16>(v, q), part_of<8>(dh[j], q));
+                                                  part_of<16>(v, q), part_of<8>(dh[j], q), scale);
           }
         }
       } else {
@@ -489,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
           if (j == 3) release();
           float v[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(av[k]);
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(av[k]) * scale.back;
           const int64_t c = c0 + 32 * j;
           const int n = r < rows ? valid_columns(A.width - c, 32) : 0;
           float* part = u.kind == 0 ? A.part : A.part_w;
@@ -591,9 +615,49 @@ __global__ void __launch_bounds__(kElemThreads) elem_kernel(const __grid_constan
     decode_columns(t, static_cast<const uint8_t*>(E.gate) + e, E.gate_scale + (e >> 5), E.vec_in, g);
     decode_columns(t, static_cast<const uint8_t*>(E.up) + e, E.up_scale + (e >> 5), E.vec_in, u);
   }
-  if constexpr (BWD) finish_backward<DT, ACT, W, ANY>(A, r, t, g, u, dh);
+  if constexpr (BWD) finish_backward<DT, ACT, W, ANY>(A, r, t, g, u, dh, dh_scale<DT>(A));
   else finish_forward<DT, ACT, W, ANY>(A, r, t, g, u);
 }
+
+// The largest finite magnitude of dh (fp16), one maximum per CTA as the bits of an fp32: a pass over dh of its own, before
+// anything can be rounded.  2 to 3 us of a small call (2048 x 256 x 1024 18 -> 21), about 40 of 8192 x 14336's 2400.
+constexpr int kMaxThreads = 1024, kMaxCols = 16, kMaxUnroll = 2;
+struct MaxArgs {
+  const void* dh;
+  int64_t rows, inner, ld, threads;
+  int32_t vec;
+  uint32_t* out;
+};
+template <bool ANY>
+__global__ void __launch_bounds__(kMaxThreads) dh_max_kernel(MaxArgs A) {
+  constexpr int W = kMaxCols;
+  __shared__ uint32_t warp_max[kMaxThreads / 32];
+  depends_begin();
+  uint32_t m = 0;
+  const int64_t step = (int64_t)gridDim.x * kMaxThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kMaxThreads + threadIdx.x; i < A.threads; i += kMaxUnroll * step) {
+    float v[kMaxUnroll][W];
+#pragma unroll
+    for (int k = 0; k < kMaxUnroll; ++k) {
+      int64_t r;
+      const Columns<W, ANY> t = deal_columns<W, ANY>(i + k * step, A.rows, A.inner, &r);
+      t.template load<QMUON_FP16>(static_cast<const unsigned char*>(A.dh) + r * A.ld * 2, A.vec, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kMaxUnroll; ++k)
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        if (fabsf(v[k][j]) <= 65504.0f) m = max(m, __float_as_uint(fabsf(v[k][j])));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = __reduce_max_sync(0xffffffffu, warp_max[threadIdx.x]);
+    if (threadIdx.x == 0) A.out[blockIdx.x] = m;
+  }
+}
+static_assert(kMaxThreads == 32 * 32, "a warp reduces the warps' maxima");
 
 // Sums of split products, rows x cols of [splits][rows][ld_part], to the type of the result; the products of a call
 // together in one launch.
@@ -827,7 +891,7 @@ struct Geometry {
   int32_t dx_m = 0, dx_n = 0, dx_splits = 1;
   int32_t dw_m = 0, dw_n = 0, dw_splits = 1;
   int64_t ld_fwd = 0, ld_w = 0, ld_d = 0;               // of partial gate/up, of partial dx/dW, of dgate/dup
-  size_t dgate = 0, dup = 0, x = 0, w[2] = {0, 0}, part = 0, part_x = 0, part_w = 0, total = 0;
+  size_t dgate = 0, dup = 0, dh_max = 0, x = 0, w[2] = {0, 0}, part = 0, part_x = 0, part_w = 0, total = 0;
   int64_t ld_x = 0, ld_wp = 0;
   bool copy_x = false, copy_w[2] = {false, false};
   bool few = false;                                     // the projections by few_kernel
@@ -904,6 +968,7 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
   G.ld_d = (int64_t)round_up((size_t)c.inner, 16);
   lay(G, &G.dgate, (size_t)c.rows * G.ld_d * 2);
   lay(G, &G.dup, (size_t)c.rows * G.ld_d * 2);
+  if (c.dtype == QMUON_FP16) lay(G, &G.dh_max, (size_t)2 * G.pairs * 4);
   G.ld_w = (int64_t)round_up((size_t)c.width, 8);
   const size_t behind = G.total;
   if (c.saved == QMUON_SAVE_NONE)
@@ -1020,6 +1085,16 @@ cudaError_t launch_few(const FewArgs& F, int dt, cudaStream_t s) {
     return F.A.act == QMUON_ACT_GELU ? launch_few_act<DT, QMUON_ACT_GELU>(F, s) : launch_few_act<DT, QMUON_ACT_GELU_TANH>(F, s);
   };
   return dt == QMUON_BF16 ? of(std::integral_constant<int, QMUON_BF16>{}) : of(std::integral_constant<int, QMUON_FP16>{});
+}
+
+// dh's maxima, of at most `most` CTAs; their number in A.
+cudaError_t launch_dh_max(GemmArgs& A, uint32_t* out, int most, cudaStream_t s) {
+  const bool any = A.vec_dh == 0;
+  const int64_t threads = threads_of(A.rows, A.inner, kMaxCols, any);
+  A.dh_max = out;
+  A.dh_parts = (int32_t)std::min<int64_t>(most, ceil_div(threads, kMaxThreads * kMaxUnroll));
+  const MaxArgs M{A.dh, A.rows, A.inner, A.ld_dh, threads, A.vec_dh, out};
+  return launch_dependent(any ? dh_max_kernel<true> : dh_max_kernel<false>, dim3((unsigned)A.dh_parts), dim3(kMaxThreads), 0, s, M);
 }
 
 // The operands as the tensor maps read them: the caller's arrays, or aligned copies in the workspace.
@@ -1212,6 +1287,8 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
     A.dgate = b + G.dgate, A.dup = b + G.dup, A.ld_d = G.ld_d;
     A.act = c->act, A.saved = c->saved;
     A.hdr = reinterpret_cast<WsHeader*>(b);
+    if (c->dtype == QMUON_FP16) e = launch_dh_max(A, reinterpret_cast<uint32_t*>(b + G.dh_max), 2 * G.pairs, s);
+    if (e != cudaSuccess) return set_error("qmuon_gated_ffn_backward (launch)", e);
     ElemArgs E{};
     if (c->saved == QMUON_SAVE_NONE) {   // gate and up again
       A.tiles_m = G.tiles_m, A.tiles_n = G.tiles_n, A.splits = G.splits;
