@@ -952,6 +952,11 @@ Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
   return G;
 }
 
+// The most K blocks of a unit, 5.4e8 cycles of the tensor cores: the epilogue waits for all of them at once, and its wait
+// is bounded (kWaitCycles, 4e9).  dx over 2^28 columns of dgate and of dup, 2^23 blocks, would outlast it in one piece.
+constexpr int kMaxBlocks = 1 << 20;
+static_assert((long long)kMaxBlocks * 512 * 4 < kWaitCycles, "a unit ends long before its wait does");
+
 // What the backward pass reads besides dh and what was saved.
 bool needs_x(const qmuon_gated_ffn_grad& c) { return c.dw_gate || c.saved == QMUON_SAVE_NONE; }
 bool needs_weights(const qmuon_gated_ffn_grad& c) { return c.dx || c.saved == QMUON_SAVE_NONE; }
@@ -998,6 +1003,8 @@ Geometry backward_geometry(const qmuon_gated_ffn_grad& c, int pairs) {
       if (cost < best) best = cost, G.dx_splits = (int32_t)sx, G.dw_splits = (int32_t)sw;
     }
   }
+  G.dx_splits = std::max(G.dx_splits, (int32_t)ceil_div(kbx, kMaxBlocks));
+  G.dw_splits = std::max(G.dw_splits, (int32_t)ceil_div(kbw, kMaxBlocks));
   const int gs = elem_size(c.grad_dtype);
   if (c.dx && (G.dx_splits > 1 || !vec_class(c.dx, c.ld_dx, 2))) lay(G, &G.part_x, (size_t)G.dx_splits * c.rows * G.ld_w * 4);
   if (c.dw_gate && (G.dw_splits > 1 || !vec_class(c.dw_gate, c.ld_dw_gate, gs) || !vec_class(c.dw_up, c.ld_dw_up, gs)))
