@@ -373,9 +373,8 @@ __device__ __forceinline__ void write_row(const SumArgs& A, int64_t row, int64_t
   store_cols<GT, N>(A.dtable, e, v);
 }
 
-// The first sorted position whose key is not below `key`, by a whole warp.
-__device__ __forceinline__ int64_t first_at_least(const uint2* sorted, int64_t n, uint32_t key, int lane) {
-  int64_t lo = 0, hi = n;   // lies in [lo, hi]
+// The first sorted position in [lo, hi) whose key is not below `key`, or hi, by a whole warp.
+__device__ __forceinline__ int64_t first_at_least(const uint2* sorted, int64_t lo, int64_t hi, uint32_t key, int lane) {
   while (lo < hi) {
     const int64_t step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step - 1;
     const uint32_t less = __ballot_sync(0xffffffffu, i < hi && sorted[i].x < key);   // ascending: a run of low lanes
@@ -404,12 +403,21 @@ __global__ void __launch_bounds__(kThreads, 4) sum_kernel(SumArgs A) {
     const int rows = (int)(A.zero_rows - r0 < kZeros ? A.zero_rows - r0 : kZeros);
     if (threadIdx.x < 64) {   // the positions of these rows' tokens
       const int warp = threadIdx.x >> 5;
-      const int64_t at = first_at_least(A.sorted, A.n, (uint32_t)(r0 + (warp ? rows : 0)), threadIdx.x & 31);
+      const int64_t at = first_at_least(A.sorted, 0, A.n, (uint32_t)(r0 + (warp ? rows : 0)), threadIdx.x & 31);
       if ((threadIdx.x & 31) == 0) range[warp] = at;
       if (threadIdx.x < kZeros) there[threadIdx.x] = 0;
     }
     __syncthreads();
-    for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) there[A.sorted[i].x - (uint32_t)r0] = 1;
+    if (range[1] - range[0] <= (int64_t)kZeros * blockDim.x) {
+      for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) there[A.sorted[i].x - (uint32_t)r0] = 1;
+    } else {   // frequent tokens: a search per row, whose work does not grow with their number (2^20 tokens, 95% of them one,
+               // 102400 x 64 bf16 3.45 -> 1.81 ms)
+      for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
+        const uint32_t key = (uint32_t)(r0 + r);
+        const int64_t at = first_at_least(A.sorted, range[0], range[1], key, threadIdx.x & 31);
+        if ((threadIdx.x & 31) == 0 && at < range[1]) there[r] = A.sorted[at].x == key;
+      }
+    }
     __syncthreads();
     if (col >= A.cols) return;
 #pragma unroll 4
