@@ -738,8 +738,10 @@ typedef enum {
  *   ws            D  256-byte aligned, of qmuon_gated_ffn_workspace_size(ffn);
  *                 qmuon_sync_status reports a wait in the kernel that expired
  * Rows of x and of the weights that do not all start on 16 bytes are copied to
- * the workspace first, but for small projections.  rows may be 0; rows, width and inner at most 2^28,
- * inner * width at most 2^36, rows * inner and rows * width at most 2^38.
+ * the workspace first, but for small projections.  rows may be 0 (nothing is
+ * launched, and ws, which may be NULL, is neither read nor written: its header
+ * says nothing of such a call); rows, width and inner at most 2^28, inner *
+ * width at most 2^36, rows * inner and rows * width at most 2^38.
  * Sums are taken in an order that depends on the sizes and on the GPU's SM
  * count alone. */
 typedef struct {
@@ -788,7 +790,8 @@ QMUON_API qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* ffn, void*
  *                follows it, or NULL
  *   ws           D  256-byte aligned, of qmuon_gated_ffn_backward_workspace_size
  * One of dx, dw_gate and h at least.  With no rows the weights' gradients are
- * zero, or left alone where they accumulate. */
+ * zero, or left alone where they accumulate, and ws is neither read nor
+ * written. */
 typedef struct {
   const void* dh;
   const void* x;
