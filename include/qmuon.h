@@ -742,8 +742,10 @@ typedef enum {
  * launched, and ws, which may be NULL, is neither read nor written: its header
  * says nothing of such a call); rows, width and inner at most 2^28, inner *
  * width at most 2^36, rows * inner and rows * width at most 2^38.
- * Sums are taken in an order that depends on the sizes and on the GPU's SM
- * count alone. */
+ * Sums are taken in an order that depends on the sizes, on whether the rows of
+ * x, w_gate and w_up start on 16 bytes, and on the GPU's SM count alone: small
+ * projections of other rows go to another kernel, whose results may differ in
+ * their last bits. */
 typedef struct {
   const void* x;
   const void* w_gate;
@@ -791,7 +793,10 @@ QMUON_API qmuon_status qmuon_gated_ffn_forward(const qmuon_gated_ffn* ffn, void*
  *   ws           D  256-byte aligned, of qmuon_gated_ffn_backward_workspace_size
  * One of dx, dw_gate and h at least.  With no rows the weights' gradients are
  * zero, or left alone where they accumulate, and ws is neither read nor
- * written. */
+ * written.  Sums are taken in an order as in the forward pass; rows of an x
+ * that is a carrier count as starting on 16 bytes, so that gate and up, where
+ * they are computed again, may differ from the forward pass's in their last
+ * bits. */
 typedef struct {
   const void* dh;
   const void* x;
