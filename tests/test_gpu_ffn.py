@@ -29,6 +29,8 @@ from test_gpu_embedding import DT, TINY, U, UT, Matrix, _np
 pytestmark = pytest.mark.gpu
 
 # rows, width, inner, pad, off: every edge of the tiles of 256 x 128, of the 64 columns of a block of K, splits of K and none
+# (of the gradients' products, that is: the projections of all of these are small enough for the cores' registers; those on
+# the tensor cores are tested at LARGE, and by their tiles in test_gpu_ffn_tiles.py)
 SHAPES = [(1, 64, 128, 0, 0), (1, 1, 1, 0, 0), (2, 8, 31, 0, 0), (3, 257, 33, 3, 1), (127, 63, 129, 0, 0), (128, 64, 127, 8, 0),
           (129, 65, 130, 0, 8), (200, 1000, 96, 16, 0), (256, 128, 256, 0, 0), (257, 200, 384, 0, 0), (300, 72, 1001, 5, 3),
           (1, 4096, 640, 0, 0), (17, 1024, 64, 0, 0), (513, 40, 520, 0, 0)]
