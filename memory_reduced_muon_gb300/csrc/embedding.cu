@@ -125,6 +125,9 @@ cudaError_t launch_lookup(const LookupArgs& A, int sms, cudaStream_t s) {
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRounds = 16, kSortKeys = kSortThreads * kRounds;
 constexpr int kSortCluster = 8, kClusterKeys = kSortWarps * 64;   // a CTA's keys before the cluster grows
+// Of the table's last rows, written meanwhile: what a few SMs' sorting time has room for.  In us, of bf16 with 16384 tokens,
+// none / 16 / 32 / 64 / 96 / 128 MB: 102400 x 4096 177 / 177 / 175 / 171 / 174 / 177, 50000 x 1000 56 / 55 / 55 / 52 / 58 / 58,
+// 400000 x 64 52 / 44 / 38 / 36 / 36 / 36; 65536 tokens, 102400 x 1024 121 / 122 / 122 / 121 / 120 / 118.
 constexpr int64_t kFillBytes = (int64_t)64 << 20;
 static_assert(kSortThreads == kDigits, "a thread per digit");
 
@@ -141,7 +144,7 @@ struct SortArgs {
   // cluster_sort_kernel, CTAs behind the first cluster: zeros to the last `fill` rows of the table's gradient
   unsigned char* table;
   int64_t fill, ld_bytes;
-  int32_t vecs;          // of 16 bytes in a row
+  int32_t vecs, across;  // of 16 bytes in a row; threads of a row, a power of two up to a CTA's
 };
 
 __device__ __forceinline__ uint2 key_of(const SortArgs& A, int64_t i) {
@@ -226,9 +229,11 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(SortArgs A) 
   const int64_t first = ((int64_t)blockIdx.x * kSortWarps + warp) * A.share;
   depends_begin();
   if ((int)blockIdx.x >= A.n_cta) {
-    const int others = gridDim.x - A.n_cta;
-    for (int64_t r = A.vocab - A.fill + (blockIdx.x - A.n_cta); r < A.vocab; r += others)
-      for (int i = d; i < A.vecs; i += kSortThreads) *reinterpret_cast<uint4*>(A.table + r * A.ld_bytes + 16 * (int64_t)i) = make_uint4(0u, 0u, 0u, 0u);
+    // rows of less than a CTA's vectors share it (one row at a time, 400000 x 64 bf16 took 738 us, 50000 x 1000 96)
+    const int down = kSortThreads / A.across;
+    const int64_t step = (int64_t)(gridDim.x - A.n_cta) * down;
+    for (int64_t r = A.vocab - A.fill + (int64_t)(blockIdx.x - A.n_cta) * down + d / A.across; r < A.vocab; r += step)
+      for (int i = d & (A.across - 1); i < A.vecs; i += A.across) *reinterpret_cast<uint4*>(A.table + r * A.ld_bytes + 16 * (int64_t)i) = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
   for (int pass = 0; pass < A.passes; ++pass) {
@@ -676,6 +681,7 @@ extern "C" qmuon_status qmuon_embedding_backward(const qmuon_embedding_grad* c, 
           A.fill = std::min(c->vocab, kFillBytes / bytes);
           A.ld_bytes = c->ld_dtable * gs;
           A.vecs = (int32_t)(bytes / 16);
+          for (A.across = 1; A.across < A.vecs && A.across < kSortThreads;) A.across *= 2;
           zero_rows -= A.fill;
         }
         e = launch_cluster(A, sms, s);
