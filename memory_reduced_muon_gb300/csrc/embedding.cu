@@ -11,7 +11,8 @@
 // and are added in fp32 in that order, kPiece positions at a time.  A piece
 // whose run of a token neither begins before it nor goes on behind it writes
 // its row itself; runs that cross pieces leave fp32 partial sums, which a second
-// kernel adds in the pieces' order.  No atomics touch a result.
+// kernel adds: warp w those of the run's pieces w, w + 8, ..., then the warps'
+// sums.  No atomics touch a result.
 #include <algorithm>
 
 #include "qm_lm.h"

@@ -65,7 +65,8 @@ __host__ __device__ constexpr int group_rows(int kind) { return kind == K_GRAD ?
 // ---------------------------------------------------------------------------
 // activations
 // ---------------------------------------------------------------------------
-// The logistic function; 0 and 1 at the ends, NaN for NaN.
+// The logistic function; 0 and 1 at the ends, NaN for NaN.  Already 0 from -87.4 down, where the quotient's divisor passes
+// 2^126 and the true value 1.2e-38: silu and its slope lack 1e-36 there.
 __device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 template <int ACT>

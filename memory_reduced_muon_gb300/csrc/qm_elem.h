@@ -1,4 +1,5 @@
-// Device helpers shared by update.cu, adamw.cu and rmsnorm.cu: widening and
+// Device helpers shared by update.cu, adamw.cu, rmsnorm.cu and, through qm_lm.h,
+// embedding.cu, mxfp8.cu and ffn.cu: widening and
 // rounding between the stored types and fp32, 16-byte vectors, packed fp32
 // pairs, E4M3 codes and E8M0 scales, asynchronous copies, dependent launches,
 // and the Philox generator under round keys made on the host.
