@@ -1295,7 +1295,7 @@ extern "C" qmuon_status qmuon_gated_ffn_backward(const qmuon_gated_ffn_grad* c, 
     A.dgate = b + G.dgate, A.dup = b + G.dup, A.ld_d = G.ld_d;
     A.act = c->act, A.saved = c->saved;
     A.hdr = reinterpret_cast<WsHeader*>(b);
-    if (c->dtype == QMUON_FP16) e = launch_dh_max(A, reinterpret_cast<uint32_t*>(b + G.dh_max), 2 * G.pairs, s);
+    if (c->dtype == QMUON_FP16 && (c->dx || c->dw_gate)) e = launch_dh_max(A, reinterpret_cast<uint32_t*>(b + G.dh_max), 2 * G.pairs, s);
     if (e != cudaSuccess) return set_error("qmuon_gated_ffn_backward (launch)", e);
     ElemArgs E{};
     if (c->saved == QMUON_SAVE_NONE) {   // gate and up again
