@@ -860,6 +860,11 @@ bool encode_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, in
 // A tensor map reads rows that start on 16 bytes; others are copied to the workspace first.
 bool tma_ready(const void* p, int64_t ld) { return is_aligned(p, 16) && ld % 8 == 0; }
 
+// The most K blocks of a unit, 5.4e8 cycles of the tensor cores: the epilogue waits for all of them at once, and its wait
+// is bounded (kWaitCycles, 4e9).  dx over 2^28 columns of dgate and of dup, 2^23 blocks, would outlast it in one piece.
+constexpr int kMaxBlocks = 1 << 20;
+static_assert((long long)kMaxBlocks * 512 * 4 < kWaitCycles, "a unit ends long before its wait does");
+
 // The width of the projections' tiles and the splits of their K blocks: the least estimated time, in twentieths of a K
 // block of a pair on a tile of 128 columns.  A block of 64 columns takes 12 (its rows' operand is as large), a unit 20 more,
 // the last epilogue 200 or 100, partial sums 40 a unit and 160 for their kernel.  Narrow tiles are for what fills the pairs
@@ -875,8 +880,9 @@ Tiles pick_tiles(int64_t rows, int64_t width, int64_t inner, int pairs) {
   int64_t best_cost = INT64_MAX;
   for (const int ni : {128, 64}) {
     const int64_t tiles = ceil_div(rows, kTile) * ceil_div(inner, ni), block = ni == 128 ? 20 : 12, last = ni == 128 ? 200 : 100;
-    const int most = tiles >= pairs ? 1 : (int)std::min<int64_t>(32, std::max<int64_t>(1, kb / 4));
-    for (int s = 1; s <= most; ++s) {
+    const int least = (int)ceil_div(kb, kMaxBlocks);
+    const int most = tiles >= pairs ? least : (int)std::min<int64_t>(32, std::max<int64_t>(1, kb / 4));
+    for (int s = least; s <= most; ++s) {
       const int64_t cost =
           ceil_div(tiles * s, pairs) * (ceil_div(kb, s) * block + 20 + (s > 1 ? 40 : 0)) + last + (s > 1 ? 160 : 0);
       if (cost < (ni == best.inner ? best_cost : best_cost * 9 / 10)) best_cost = cost, best = Tiles{ni, s};   // narrow: only where it is clear
@@ -952,11 +958,6 @@ Geometry forward_geometry(const qmuon_gated_ffn& c, int pairs) {
   lay_projections(G, c.rows, c.width, c.inner, G.few ? c.saved != QMUON_SAVE_MXFP8 : vectors);
   return G;
 }
-
-// The most K blocks of a unit, 5.4e8 cycles of the tensor cores: the epilogue waits for all of them at once, and its wait
-// is bounded (kWaitCycles, 4e9).  dx over 2^28 columns of dgate and of dup, 2^23 blocks, would outlast it in one piece.
-constexpr int kMaxBlocks = 1 << 20;
-static_assert((long long)kMaxBlocks * 512 * 4 < kWaitCycles, "a unit ends long before its wait does");
 
 // What the backward pass reads besides dh and what was saved.
 bool needs_x(const qmuon_gated_ffn_grad& c) { return c.dw_gate || c.saved == QMUON_SAVE_NONE; }

@@ -41,6 +41,16 @@ def test_long_sums_have_room_for_their_pieces():
     assert _size(rows, 64, 64) - _size(rows, 64, 64, dw=False) >= 2 * 4 * 64 * 64 * 4
 
 
+def test_long_projections_have_room_for_their_pieces():
+    # 16 x 8 tiles of 256 x 128 and more are enough for all CTA pairs (76 here); K of 2^20 + 1 blocks
+    rows, inner, width = 4032, 1000, (1 << 26) + 64
+    c = q.qmuon_gated_ffn(*[FAKE] * 4, *[None] * 4, rows, width, inner, width, width, width, inner, inner, inner, q.QMUON_ACT_SILU,
+                          q.QMUON_BF16, q.QMUON_SAVE_NONE, 0)
+    assert q.lib().qmuon_gated_ffn_workspace_size(C.byref(c)) == 256 + 2 * 2 * rows * inner * 4
+    c.width = c.ld_x = c.ld_w_gate = c.ld_w_up = 1 << 26
+    assert q.lib().qmuon_gated_ffn_workspace_size(C.byref(c)) == 256
+
+
 @pytest.mark.gpu
 def test_longest_sum():
     """dx of one row over 2^28 columns, beside weights' gradients of as many tiles: whole numbers, whose sums are exact."""
